@@ -44,6 +44,18 @@ class KdaLayerGates(ctypes.Structure):
                 ("norm_weight", ctypes.c_void_p), ("norm_eps", ctypes.c_float)]
 
 
+class KdaScanDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("H", ctypes.c_int), ("d", ctypes.c_int),
+                ("num_seqs", ctypes.c_int), ("dtype", ctypes.c_int), ("gate_dtype", ctypes.c_int),
+                ("write", ctypes.c_int), ("validate", ctypes.c_int)]
+
+
+class KdaNormDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("width", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("res_dtype", ctypes.c_int), ("post_norm", ctypes.c_int), ("post_eps", ctypes.c_float),
+                ("pre_eps", ctypes.c_float)]
+
+
 class KdaError(RuntimeError):
     def __init__(self, status: int, fn: str, detail: str = ""):
         self.status = status
@@ -99,6 +111,21 @@ def load() -> ctypes.CDLL:
         lib.kda_affine_compose.argtypes = [ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                            P, P, P, P]
         lib.kda_affine_compose.restype = ctypes.c_int
+        S, Z = ctypes.POINTER(KdaScanDesc), ctypes.POINTER(ctypes.c_size_t)
+        F = ctypes.c_float
+        lib.kda_scan_states_size.argtypes = [S, Z]
+        lib.kda_scan_fwd.argtypes = [S, P, P, P, F, P, P, P, P, P, P]
+        lib.kda_scan_bwd_workspace_size.argtypes = [S, ctypes.c_int, ctypes.c_int, Z]
+        lib.kda_scan_bwd.argtypes = [S, P, P, P, F, P, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
+        lib.kda_scan_step.argtypes = [S, P, P, P, F, P, P, P, P]
+        NP = ctypes.POINTER(KdaNormDesc)
+        lib.kda_block_norm_fwd.argtypes = [NP, P, P, P, P, P, P, P, P, P]
+        lib.kda_block_norm_bwd_workspace_size.argtypes = [NP, Z]
+        lib.kda_block_norm_bwd.argtypes = [NP, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
+        for fn in (lib.kda_scan_states_size, lib.kda_scan_fwd, lib.kda_scan_bwd_workspace_size, lib.kda_scan_bwd,
+                   lib.kda_scan_step, lib.kda_block_norm_fwd, lib.kda_block_norm_bwd_workspace_size,
+                   lib.kda_block_norm_bwd):
+            fn.restype = ctypes.c_int
         lib.kda_status_string.argtypes = [ctypes.c_int]
         lib.kda_status_string.restype = ctypes.c_char_p
         lib.kda_last_cuda_error.argtypes = []
@@ -410,3 +437,306 @@ def kda_affine_compose(pairs, initial_state=None, entry_states=None, *, stream=N
                                 _ptr(entry_states), _stream_handle(stream, pairs.device))
     _check(st, "kda_affine_compose")
     return entry_states
+
+
+# ------------------------------------------------ gated linear recurrence, norms
+
+WRITES = {"one": 0, "complement": 1}
+
+
+def _addr(t: Optional[torch.Tensor]):
+    """A tensor's address for the C call.  One without elements may have none;
+    the library reads nothing through it but refuses NULL, so it gets a
+    non-null stand-in."""
+    if t is None:
+        return None
+    if not t.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    return t.data_ptr() or 256
+
+
+def _expect(name, t, shape, dtype, dev):
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, not {t.device}")
+
+
+class _Launch:
+    """The device and stream of one call.  On a stream other than the current
+    one, new tensors come from that stream's memory, and every tensor of the
+    call is kept from reuse until both streams are done with it."""
+
+    def __init__(self, dev, stream, tensors):
+        if dev.type != "cuda":
+            raise ValueError(f"tensors must be on a CUDA device, not {dev}")
+        current = torch.cuda.current_stream(dev)
+        self.stream = current if stream is None else stream
+        self.side = self.stream != current
+        self.current, self.tensors, self.guard = current, tensors, None
+        if self.side:
+            if self.stream.device != dev:
+                raise ValueError(f"the stream must be on {dev}, not {self.stream.device}")
+            self.guard = torch.cuda.stream(self.stream)
+        elif dev.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(dev)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self.stream.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+    def keep(self, *new):
+        if self.side:
+            for t in self.tensors:
+                if t is not None:
+                    t.record_stream(self.stream)
+            for t in new:
+                if t is not None:
+                    t.record_stream(self.current)
+
+
+def _scan_desc(x, decay, A_log, initial_state, cu_seqlens, write, B, validate):
+    """Checked descriptor, (sequences, tokens) and the [N, H, d] state shape."""
+    if x.dim() not in (3, 4):
+        raise ValueError("x must be [tokens, H, d] or [B, T, H, d]")
+    if write not in WRITES:
+        raise ValueError(f"write must be one of {sorted(WRITES)}")
+    dev = x.device
+    H, dd = x.shape[-2:]
+    tokens = x.shape[0] if x.dim() == 3 else x.shape[0] * x.shape[1]
+    batch = x.shape[0] if x.dim() == 4 else (1 if B is None else B)
+    if B is not None and (B != batch or B <= 0 or tokens % B):
+        raise ValueError(f"{tokens} tokens are no batch of {B} sequences")
+    if A_log is None:
+        _expect("decay", decay, x.shape, decay.dtype, dev)
+    else:
+        _expect("decay", decay, x.shape, x.dtype, dev)
+        _expect("A_log", A_log, (H,), torch.float32, dev)
+    d = KdaScanDesc()
+    if cu_seqlens is not None:
+        if batch != 1:
+            raise ValueError("cu_seqlens needs B = 1")
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+            raise ValueError("cu_seqlens must be [N + 1] with N >= 1")
+        _expect("cu_seqlens", cu_seqlens, cu_seqlens.shape, torch.int32, dev)
+        d.num_seqs = cu_seqlens.numel() - 1
+    d.B, d.T, d.H, d.d = batch, (tokens // batch if batch else 0), H, dd
+    d.dtype, d.gate_dtype = _dt(x), _dt(decay)
+    d.write, d.validate = WRITES[write], int(bool(validate))
+    state = (d.num_seqs or batch, H, dd)
+    _expect("initial_state", initial_state, state, torch.float32, dev)
+    return d, state
+
+
+def kda_scan_states_size(desc: KdaScanDesc) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().kda_scan_states_size(ctypes.byref(desc), ctypes.byref(n)), "kda_scan_states_size")
+    return n.value
+
+
+def kda_scan_fwd(x, decay, A_log=None, g_min=-5.0, initial_state=None, cu_seqlens=None, out=None, final_state=None,
+                 states=None, *, write="one", validate=False, want_final_state=True, want_states=False, B=None,
+                 stream=None):
+    """Gated linear recurrence h_t = alpha_t h_{t-1} + w_t x_t through the C ABI.
+
+    x, decay: [tokens, H, d] (or [B, T, H, d]); decay is log_alpha (fp32 or
+    bf16), or with A_log ([H] fp32) the decay logits z in x's dtype;
+    initial_state: [N, H, d] fp32 or None; write: "one" (w = 1) or
+    "complement" (w = 1 - alpha).  Returns (out, final_state), and with
+    want_states (or a `states` buffer) a third, the states for kda_scan_bwd."""
+    lib = load()
+    dev = x.device
+    d, state = _scan_desc(x, decay, A_log, initial_state, cu_seqlens, write, B, validate)
+    _expect("out", out, x.shape, x.dtype, dev)
+    _expect("final_state", final_state, state, torch.float32, dev)
+    launch = _Launch(dev, stream, (x, decay, A_log, initial_state, cu_seqlens, out, final_state, states))
+    with launch as handle:
+        if want_states or states is not None:
+            n = kda_scan_states_size(d) // 4
+            if states is None:
+                states = torch.empty(n, dtype=torch.float32, device=dev)
+            _expect("states", states, (n,), torch.float32, dev)
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        if final_state is None and want_final_state:
+            final_state = torch.empty(state, dtype=torch.float32, device=dev)
+        st = lib.kda_scan_fwd(ctypes.byref(d), _addr(x), _addr(decay), _addr(A_log), g_min, _addr(initial_state),
+                              _addr(cu_seqlens), _addr(out), _addr(final_state), _addr(states), handle)
+    _check(st, "kda_scan_fwd")
+    launch.keep(out, final_state, states)
+    return (out, final_state) if states is None else (out, final_state, states)
+
+
+def kda_scan_bwd(x, decay, d_out, A_log=None, g_min=-5.0, initial_state=None, d_final_state=None, cu_seqlens=None,
+                 states=None, *, write="one", validate=False, want_d_initial_state=True, B=None, stream=None,
+                 workspace=None, grads=None):
+    """Gradients of kda_scan_fwd through the C ABI for
+    L = sum <d_out, out> + <d_final_state, final_state>.
+
+    states: what kda_scan_fwd(..., want_states=True) returned for the same
+    arguments, or None (they are rebuilt).  Returns a dict: dx (x's dtype),
+    d_decay (decay's dtype), dA_log ([H] fp32; None without A_log) and
+    d_initial_state (fp32; None unless wanted).  Rows behind the last sequence
+    of cu_seqlens are not written.  `grads` may pass that dict preallocated."""
+    lib = load()
+    dev = x.device
+    d, state = _scan_desc(x, decay, A_log, initial_state, cu_seqlens, write, B, validate)
+    _expect("d_out", d_out, x.shape, x.dtype, dev)
+    _expect("d_final_state", d_final_state, state, torch.float32, dev)
+    if states is not None:
+        _expect("states", states, (kda_scan_states_size(d) // 4,), torch.float32, dev)
+    given = tuple((grads or {}).values())
+    launch = _Launch(dev, stream, (x, decay, A_log, initial_state, d_out, d_final_state, cu_seqlens, states,
+                                   workspace) + given)
+    with launch as handle:
+        if grads is None:
+            grads = dict(dx=torch.empty(x.shape, dtype=x.dtype, device=dev),
+                         d_decay=torch.empty(x.shape, dtype=decay.dtype, device=dev),
+                         dA_log=None if A_log is None else torch.empty(A_log.shape, dtype=torch.float32, device=dev),
+                         d_initial_state=(torch.empty(state, dtype=torch.float32, device=dev)
+                                          if want_d_initial_state else None))
+        else:
+            _expect("dx", grads["dx"], x.shape, x.dtype, dev)
+            _expect("d_decay", grads["d_decay"], x.shape, decay.dtype, dev)
+            _expect("dA_log", grads.get("dA_log"), (d.H,), torch.float32, dev)
+            _expect("d_initial_state", grads.get("d_initial_state"), state, torch.float32, dev)
+        if workspace is None:
+            n = ctypes.c_size_t(0)
+            _check(lib.kda_scan_bwd_workspace_size(ctypes.byref(d), int(A_log is not None), int(states is not None),
+                                                   ctypes.byref(n)), "kda_scan_bwd_workspace_size")
+            if n.value:
+                workspace = torch.empty(n.value, dtype=torch.uint8, device=dev)
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        st = lib.kda_scan_bwd(ctypes.byref(d), _addr(x), _addr(decay), _addr(A_log), g_min, _addr(initial_state),
+                              _addr(cu_seqlens), _addr(states), _addr(d_out), _addr(d_final_state),
+                              _addr(grads["dx"]), _addr(grads["d_decay"]), _addr(grads.get("dA_log")),
+                              _addr(grads.get("d_initial_state")), _addr(workspace), ws_bytes, handle)
+    _check(st, "kda_scan_bwd")
+    launch.keep(*grads.values())
+    return grads
+
+
+def kda_scan_step(x, decay, state_in, A_log=None, g_min=-5.0, state_out=None, out=None, *, write="one",
+                  validate=False, stream=None):
+    """One token of kda_scan_fwd for N sequences: x, decay [N, H, d], state_in
+    [N, H, d] fp32.  The new state goes to state_out (None: in place of
+    state_in).  Returns (out, state_out)."""
+    lib = load()
+    dev = x.device
+    if x.dim() != 3 or x.shape[0] == 0:
+        raise ValueError("x must be [N, H, d] with N >= 1")
+    d, state = _scan_desc(x, decay, A_log, state_in, None, write, x.shape[0], validate)
+    if state_out is None:
+        state_out = state_in
+    _expect("state_out", state_out, state, torch.float32, dev)
+    _expect("out", out, x.shape, x.dtype, dev)
+    launch = _Launch(dev, stream, (x, decay, A_log, state_in, state_out, out))
+    with launch as handle:
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        st = lib.kda_scan_step(ctypes.byref(d), _addr(x), _addr(decay), _addr(A_log), g_min, _addr(state_in),
+                               _addr(state_out), _addr(out), handle)
+    _check(st, "kda_scan_step")
+    launch.keep(out)
+    return out, state_out
+
+
+def _norm_desc(y, residual, gate, post_norm, post_weight, scale, pre_weight, post_eps, pre_eps):
+    if y.dim() < 1 or y.shape[-1] < 1:
+        raise ValueError("y must be [..., width] with width >= 1")
+    dev, width = y.device, y.shape[-1]
+    _expect("residual", residual, y.shape, y.dtype if residual is None else residual.dtype, dev)
+    _expect("gate", gate, y.shape, y.dtype, dev)
+    for name, t in (("post_weight", post_weight), ("scale", scale), ("pre_weight", pre_weight)):
+        _expect(name, t, (width,), torch.float32, dev)
+    d = KdaNormDesc()
+    d.rows, d.width = y.numel() // width, width
+    d.dtype = _dt(y)
+    d.res_dtype = d.dtype if residual is None else _dt(residual)
+    d.post_norm, d.post_eps, d.pre_eps = int(bool(post_norm)), post_eps, pre_eps
+    return d
+
+
+def kda_block_norm_fwd(y, residual=None, gate=None, *, post_norm=True, post_weight=None, scale=None, pre_weight=None,
+                       post_eps=1e-6, pre_eps=1e-6, want_out=True, want_normed=False, out=None, normed=None,
+                       stream=None):
+    """Norms before and after a block through the C ABI, per row of y [..., width]:
+
+        out    = residual + scale * sigmoid(gate) * RMSNorm(y; post_weight, post_eps)
+        normed = RMSNorm(out; pre_weight, pre_eps)
+
+    Every part is optional: post_norm=False leaves y as it is, None weights
+    and scale are ones, no gate is 1, no residual is 0.  gate has y's dtype;
+    residual (fp32 or bf16) sets out's.  Returns (out, normed), None for the
+    one not wanted; out may be `residual` itself (update in place)."""
+    lib = load()
+    dev = y.device
+    d = _norm_desc(y, residual, gate, post_norm, post_weight, scale, pre_weight, post_eps, pre_eps)
+    odt = y.dtype if residual is None else residual.dtype
+    _expect("out", out, y.shape, odt, dev)
+    _expect("normed", normed, y.shape, y.dtype, dev)
+    launch = _Launch(dev, stream, (y, residual, gate, post_weight, scale, pre_weight, out, normed))
+    with launch as handle:
+        if out is None and want_out:
+            out = torch.empty(y.shape, dtype=odt, device=dev)
+        if normed is None and want_normed:
+            normed = torch.empty(y.shape, dtype=y.dtype, device=dev)
+        st = lib.kda_block_norm_fwd(ctypes.byref(d), _addr(y), _addr(residual), _addr(gate), _addr(post_weight),
+                                    _addr(scale), _addr(pre_weight), _addr(out), _addr(normed), handle)
+    _check(st, "kda_block_norm_fwd")
+    launch.keep(out, normed)
+    return out, normed
+
+
+def kda_block_norm_bwd(y, d_out, d_normed=None, residual=None, gate=None, *, post_norm=True, post_weight=None,
+                       scale=None, pre_weight=None, post_eps=1e-6, pre_eps=1e-6, stream=None, workspace=None,
+                       grads=None):
+    """Gradients of kda_block_norm_fwd through the C ABI for
+    L = <d_out, out> + <d_normed, normed> (either may be None).  Returns a dict:
+    d_y, d_residual, d_gate in the dtypes of their tensors, d_post_weight,
+    d_scale, d_pre_weight in fp32; None for each input that was not given.
+    `grads` may pass that dict preallocated: then the entries it holds (d_y
+    and, with a gate, d_gate are required) are written."""
+    lib = load()
+    dev = y.device
+    d = _norm_desc(y, residual, gate, post_norm, post_weight, scale, pre_weight, post_eps, pre_eps)
+    rdt, width = (y.dtype if residual is None else residual.dtype), y.shape[-1]
+    _expect("d_out", d_out, y.shape, rdt, dev)
+    _expect("d_normed", d_normed, y.shape, y.dtype, dev)
+    given = tuple((grads or {}).values())
+    launch = _Launch(dev, stream, (y, residual, gate, post_weight, scale, pre_weight, d_out, d_normed, workspace)
+                     + given)
+    with launch as handle:
+        if grads is None:
+            new = lambda like: None if like is None else torch.empty(like.shape, dtype=like.dtype, device=dev)  # noqa: E731
+            grads = dict(d_y=new(y), d_residual=new(residual), d_gate=new(gate), d_post_weight=new(post_weight),
+                         d_scale=new(scale), d_pre_weight=None if d_normed is None else new(pre_weight))
+        else:
+            for name, dt in (("d_y", y.dtype), ("d_residual", rdt), ("d_gate", y.dtype)):
+                _expect(name, grads.get(name), y.shape, dt, dev)
+            for name in ("d_post_weight", "d_scale", "d_pre_weight"):
+                _expect(name, grads.get(name), (width,), torch.float32, dev)
+        if workspace is None:
+            n = ctypes.c_size_t(0)
+            _check(lib.kda_block_norm_bwd_workspace_size(ctypes.byref(d), ctypes.byref(n)),
+                   "kda_block_norm_bwd_workspace_size")
+            if n.value:
+                workspace = torch.empty(n.value, dtype=torch.uint8, device=dev)
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        g = {k: _addr(grads.get(k)) for k in ("d_y", "d_residual", "d_gate", "d_post_weight", "d_scale", "d_pre_weight")}
+        st = lib.kda_block_norm_bwd(ctypes.byref(d), _addr(y), _addr(residual), _addr(gate), _addr(post_weight),
+                                    _addr(scale), _addr(pre_weight), _addr(d_out), _addr(d_normed), g["d_y"],
+                                    g["d_residual"], g["d_gate"], g["d_post_weight"], g["d_scale"],
+                                    g["d_pre_weight"], _addr(workspace), ws_bytes, handle)
+    _check(st, "kda_block_norm_bwd")
+    launch.keep(*grads.values())
+    return grads

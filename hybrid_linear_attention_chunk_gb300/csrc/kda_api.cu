@@ -320,6 +320,140 @@ kda_status run_decode(const kda_decode_desc *d, const kda_layer_gates *lg, const
   return KDA_OK;
 }
 
+// --------------------------------------------- gated linear recurrence, norms
+
+// No output may overlap an input or another output, but for the listed pairs
+// (in, out) that may be the same buffer.
+bool aliased(const Range *in, int n_in, const Range *out, int n_out, int same_in = -1, int same_out = -1) {
+  for (int o = 0; o < n_out; ++o) {
+    for (int i = 0; i < n_in; ++i) {
+      if (i == same_in && o == same_out && in[i].lo == out[o].lo && in[i].hi == out[o].hi) continue;
+      if (overlap(in[i], out[o])) return true;
+    }
+    for (int p = 0; p < o; ++p)
+      if (overlap(out[p], out[o])) return true;
+  }
+  return false;
+}
+
+// Sizes and types of a scan descriptor.
+kda_status scan_sizes(const kda_scan_desc *d, bool logits, bool varlen, ScanArgs *a) {
+  if (!dtype_ok(d->dtype) || (!logits && !dtype_ok(d->gate_dtype))) return KDA_ERR_DTYPE;
+  if (d->write != KDA_WRITE_ONE && d->write != KDA_WRITE_COMPLEMENT) return KDA_ERR_SHAPE;
+  if (d->B <= 0 || d->T < 0 || d->H <= 0 || d->d <= 0 || d->num_seqs < 0) return KDA_ERR_SHAPE;
+  if (varlen ? (d->B != 1 || d->num_seqs <= 0) : d->num_seqs != 0) return KDA_ERR_SHAPE;
+  const long long D = (long long)d->H * d->d, tokens = (long long)d->B * d->T;
+  const long long N = varlen ? d->num_seqs : d->B;
+  if (D >= (1LL << 31) || tokens >= (1LL << 31) - 64 || N * D >= (1LL << 36) || tokens * D >= (1LL << 44))
+    return KDA_ERR_SHAPE;
+  a->N = (int)N;
+  a->T_total = (int)tokens;
+  a->T_seq = varlen ? 0 : d->T;
+  a->H = d->H;
+  a->d = d->d;
+  a->D = (int)D;
+  a->t = d->dtype;
+  a->gate = logits ? d->dtype : d->gate_dtype;
+  a->complement = d->write == KDA_WRITE_COMPLEMENT;
+  a->x = a->g = nullptr;
+  a->A_log = nullptr;
+  a->g_min = 0.f;
+  a->s0 = nullptr;
+  a->cu = nullptr;
+  a->o = nullptr;
+  a->sT = a->states = nullptr;
+  return KDA_OK;
+}
+
+// The inputs that every scan call shares.
+kda_status check_scan(const kda_scan_desc *d, const void *x, const void *decay, const float *A_log, float g_min,
+                      const float *s0, const int32_t *cu, ScanArgs *a) {
+  if (!d || !x || !decay) return KDA_ERR_NULL;
+  kda_status st = scan_sizes(d, A_log != nullptr, cu != nullptr, a);
+  if (st != KDA_OK) return st;
+  if (A_log && !(g_min >= kLogDecayFloor && g_min < 0.f)) return KDA_ERR_RANGE;
+  a->x = x;
+  a->g = decay;
+  a->A_log = A_log;
+  a->g_min = g_min;
+  a->s0 = s0;
+  a->cu = cu;
+  if (!aligned_to(x, esize(a->t)) || !aligned_to(decay, esize(a->gdt())) || !aligned_to(A_log, 4) ||
+      !aligned_to(s0, 4) || !aligned_to(cu, 4))
+    return KDA_ERR_ALIGN;
+  return KDA_OK;
+}
+
+Range scan_span(const ScanArgs &a, const void *p, kda_dtype t) {
+  return span(p, p ? (size_t)a.T_total * a.D * esize(t) : 0);
+}
+
+Range chain_span(const ScanArgs &a, const void *p) { return span(p, p ? (size_t)a.N * a.D * 4 : 0); }
+
+kda_status validate_scan(const kda_scan_desc *d, const ScanArgs &a, cudaStream_t s) {
+  if (!d->validate) return KDA_OK;
+  return run_validation(s, [&](int *flag) { return launch_validate_scan(a, flag, s); });
+}
+
+kda_status check_norm(const kda_norm_desc *d, const void *y, const void *residual, const void *gate,
+                      const float *post_weight, const float *scale, const float *pre_weight, NormArgs *a) {
+  if (!d || !y) return KDA_ERR_NULL;
+  if (!dtype_ok(d->dtype) || !dtype_ok(d->res_dtype)) return KDA_ERR_DTYPE;
+  if (!residual && d->res_dtype != d->dtype) return KDA_ERR_DTYPE;
+  if (d->rows < 0 || d->rows >= (1LL << 31) || d->width < 1 || d->width > KDA_NORM_MAX_WIDTH) return KDA_ERR_SHAPE;
+  if (post_weight && !d->post_norm) return KDA_ERR_UNSUPPORTED;
+  if ((d->post_norm && !(d->post_eps >= 0.f)) || !(d->pre_eps >= 0.f)) return KDA_ERR_RANGE;
+  if (!aligned_to(y, esize(d->dtype)) || !aligned_to(residual, esize(d->res_dtype)) ||
+      !aligned_to(gate, esize(d->dtype)) || !aligned_to(post_weight, 4) || !aligned_to(scale, 4) ||
+      !aligned_to(pre_weight, 4))
+    return KDA_ERR_ALIGN;
+  a->rows = d->rows;
+  a->width = d->width;
+  a->t = d->dtype;
+  a->rt = d->res_dtype;
+  a->post = d->post_norm != 0;
+  a->e1 = d->post_eps;
+  a->e2 = d->pre_eps;
+  a->y = y;
+  a->res = residual;
+  a->gate = gate;
+  a->w1 = post_weight;
+  a->sc = scale;
+  a->w2 = pre_weight;
+  a->out = a->normed = nullptr;
+  return KDA_OK;
+}
+
+Range rows_span(const NormArgs &a, const void *p, kda_dtype t) {
+  return span(p, p ? (size_t)a.rows * a.width * esize(t) : 0);
+}
+
+Range width_span(const NormArgs &a, const float *p) { return span(p, p ? (size_t)a.width * 4 : 0); }
+
+// A workspace of `need` bytes: the caller's, or one allocated on s around `run`.
+template <class Run>
+kda_status with_workspace(void *ws, size_t ws_bytes, size_t need, cudaStream_t s, Run run) {
+  if (ws) {
+    if (ws_bytes < need) return KDA_ERR_SHAPE;
+    if (!aligned16(ws)) return KDA_ERR_ALIGN;
+  }
+  cudaError_t e;
+  if (ws || need == 0) {
+    e = run(ws);
+  } else {
+    void *tmp = nullptr;
+    e = cudaMallocAsync(&tmp, need, s);
+    if (e == cudaSuccess) {
+      e = run(tmp);
+      const cudaError_t ef = cudaFreeAsync(tmp, s);
+      if (e == cudaSuccess) e = ef;
+    }
+  }
+  return e == cudaSuccess ? KDA_OK : cuda_fail(e);
+}
+
+size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
+
 }  // namespace
 
 cudaError_t launch_validate_prefill(const PrefillArgs &a, int *d_flag, cudaStream_t s) {
@@ -553,6 +687,171 @@ kda_status kda_chunk_bwd(const kda_chunk_desc *desc, const void *q, const void *
   }
   if (e != cudaSuccess) return cuda_fail(e);
   return KDA_OK;
+}
+
+kda_status kda_scan_states_size(const kda_scan_desc *desc, size_t *bytes) {
+  if (!desc || !bytes) return KDA_ERR_NULL;
+  *bytes = 0;
+  ScanArgs a;
+  const kda_status st = scan_sizes(desc, true, desc->num_seqs > 0, &a);
+  if (st != KDA_OK) return st;
+  *bytes = scan_states_bytes(a);
+  return KDA_OK;
+}
+
+kda_status kda_scan_fwd(const kda_scan_desc *desc, const void *x, const void *decay, const float *A_log,
+                        float g_min, const float *initial_state, const int32_t *cu_seqlens, void *out,
+                        float *final_state, float *states, kda_stream_t stream) {
+  if (!out) return KDA_ERR_NULL;
+  ScanArgs a;
+  kda_status st = check_scan(desc, x, decay, A_log, g_min, initial_state, cu_seqlens, &a);
+  if (st != KDA_OK) return st;
+  if (!aligned_to(out, esize(a.t)) || !aligned_to(final_state, 4) || !aligned_to(states, 4)) return KDA_ERR_ALIGN;
+  const Range in[] = {scan_span(a, x, a.t), scan_span(a, decay, a.gdt()), span(A_log, A_log ? (size_t)a.H * 4 : 0),
+                      span(cu_seqlens, cu_seqlens ? (size_t)(a.N + 1) * 4 : 0), chain_span(a, initial_state)};
+  const Range outs[] = {scan_span(a, out, a.t), span(states, states ? scan_states_bytes(a) : 0),
+                        chain_span(a, final_state)};
+  if (aliased(in, 5, outs, 3, 4, 2)) return KDA_ERR_ALIAS;
+  a.o = out;
+  a.sT = final_state;
+  a.states = states;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  st = validate_scan(desc, a, s);
+  if (st != KDA_OK) return st;
+  const cudaError_t e = launch_scan_fwd(a, s);
+  return e == cudaSuccess ? KDA_OK : cuda_fail(e);
+}
+
+kda_status kda_scan_bwd_workspace_size(const kda_scan_desc *desc, int logits, int have_states, size_t *bytes) {
+  if (!desc || !bytes) return KDA_ERR_NULL;
+  *bytes = 0;
+  ScanArgs a;
+  const kda_status st = scan_sizes(desc, logits != 0, desc->num_seqs > 0, &a);
+  if (st != KDA_OK) return st;
+  *bytes = (have_states ? 0 : round256(scan_states_bytes(a))) + (logits ? round256(scan_dA_bytes(a)) : 0);
+  return KDA_OK;
+}
+
+kda_status kda_scan_bwd(const kda_scan_desc *desc, const void *x, const void *decay, const float *A_log,
+                        float g_min, const float *initial_state, const int32_t *cu_seqlens,
+                        const float *states, const void *d_out, const float *d_final_state, void *dx,
+                        void *d_decay, float *dA_log, float *d_initial_state, void *workspace,
+                        size_t workspace_bytes, kda_stream_t stream) {
+  if (!d_out || !dx || !d_decay || (A_log && !dA_log)) return KDA_ERR_NULL;
+  if (dA_log && !A_log) return KDA_ERR_UNSUPPORTED;
+  ScanArgs a;
+  kda_status st = check_scan(desc, x, decay, A_log, g_min, initial_state, cu_seqlens, &a);
+  if (st != KDA_OK) return st;
+  if (!aligned_to(d_out, esize(a.t)) || !aligned_to(dx, esize(a.t)) || !aligned_to(d_decay, esize(a.gdt())) ||
+      !aligned_to(states, 4) || !aligned_to(d_final_state, 4) || !aligned_to(dA_log, 4) ||
+      !aligned_to(d_initial_state, 4))
+    return KDA_ERR_ALIGN;
+  size_t need = 0;
+  st = kda_scan_bwd_workspace_size(desc, A_log != nullptr, states != nullptr, &need);
+  if (st != KDA_OK) return st;
+  const Range in[] = {scan_span(a, x, a.t), scan_span(a, decay, a.gdt()), span(A_log, A_log ? (size_t)a.H * 4 : 0),
+                      span(cu_seqlens, cu_seqlens ? (size_t)(a.N + 1) * 4 : 0), chain_span(a, initial_state),
+                      span(states, states ? scan_states_bytes(a) : 0), scan_span(a, d_out, a.t),
+                      chain_span(a, d_final_state)};
+  const Range outs[] = {scan_span(a, dx, a.t), scan_span(a, d_decay, a.gdt()),
+                        span(dA_log, dA_log ? (size_t)a.H * 4 : 0), chain_span(a, d_initial_state),
+                        span(workspace, workspace ? workspace_bytes : 0)};
+  if (aliased(in, 8, outs, 5)) return KDA_ERR_ALIAS;
+  if (workspace && workspace_bytes < need) return KDA_ERR_SHAPE;
+  if (workspace && !aligned16(workspace)) return KDA_ERR_ALIGN;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  st = validate_scan(desc, a, s);
+  if (st != KDA_OK) return st;
+  const ScanBwdIo io{d_out, d_final_state, dx, d_decay, dA_log, d_initial_state};
+  return with_workspace(workspace, workspace_bytes, need, s, [&](void *ws) {
+    ScanArgs b = a;
+    char *p = static_cast<char *>(ws);
+    b.states = const_cast<float *>(states);
+    if (!states) {
+      b.states = reinterpret_cast<float *>(p);
+      p += round256(scan_states_bytes(a));
+      const cudaError_t e = launch_scan_states(b, s);
+      if (e != cudaSuccess) return e;
+    }
+    return launch_scan_bwd(b, io, reinterpret_cast<float *>(p), s);
+  });
+}
+
+kda_status kda_scan_step(const kda_scan_desc *desc, const void *x, const void *decay, const float *A_log,
+                         float g_min, const float *state_in, float *state_out, void *out, kda_stream_t stream) {
+  if (!desc || !out || !state_in || !state_out) return KDA_ERR_NULL;
+  if (desc->T != 1) return KDA_ERR_SHAPE;
+  ScanArgs a;
+  kda_status st = check_scan(desc, x, decay, A_log, g_min, state_in, nullptr, &a);
+  if (st != KDA_OK) return st;
+  if (!aligned_to(out, esize(a.t)) || !aligned_to(state_out, 4)) return KDA_ERR_ALIGN;
+  const Range in[] = {scan_span(a, x, a.t), scan_span(a, decay, a.gdt()), span(A_log, A_log ? (size_t)a.H * 4 : 0),
+                      chain_span(a, state_in)};
+  const Range outs[] = {scan_span(a, out, a.t), chain_span(a, state_out)};
+  if (aliased(in, 4, outs, 2, 3, 1)) return KDA_ERR_ALIAS;
+  a.o = out;
+  a.sT = state_out;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  st = validate_scan(desc, a, s);
+  if (st != KDA_OK) return st;
+  const cudaError_t e = launch_scan_step(a, s);
+  return e == cudaSuccess ? KDA_OK : cuda_fail(e);
+}
+
+kda_status kda_block_norm_fwd(const kda_norm_desc *desc, const void *y, const void *residual, const void *gate,
+                              const float *post_weight, const float *scale, const float *pre_weight, void *out,
+                              void *normed, kda_stream_t stream) {
+  NormArgs a;
+  const kda_status st = check_norm(desc, y, residual, gate, post_weight, scale, pre_weight, &a);
+  if (st != KDA_OK) return st;
+  if (!out && !normed) return KDA_ERR_NULL;
+  if (pre_weight && !normed) return KDA_ERR_UNSUPPORTED;
+  if (!aligned_to(out, esize(a.rt)) || !aligned_to(normed, esize(a.t))) return KDA_ERR_ALIGN;
+  const Range in[] = {rows_span(a, y, a.t), rows_span(a, residual, a.rt), rows_span(a, gate, a.t),
+                      width_span(a, post_weight), width_span(a, scale), width_span(a, pre_weight)};
+  const Range outs[] = {rows_span(a, out, a.rt), rows_span(a, normed, a.t)};
+  if (aliased(in, 6, outs, 2, 1, 0)) return KDA_ERR_ALIAS;
+  a.out = out;
+  a.normed = normed;
+  const cudaError_t e = launch_norm_fwd(a, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? KDA_OK : cuda_fail(e);
+}
+
+kda_status kda_block_norm_bwd_workspace_size(const kda_norm_desc *desc, size_t *bytes) {
+  if (!desc || !bytes) return KDA_ERR_NULL;
+  *bytes = 0;
+  if (desc->rows < 0 || desc->rows >= (1LL << 31) || desc->width < 1 || desc->width > KDA_NORM_MAX_WIDTH)
+    return KDA_ERR_SHAPE;
+  *bytes = norm_bwd_workspace_bytes(desc->width);
+  return KDA_OK;
+}
+
+kda_status kda_block_norm_bwd(const kda_norm_desc *desc, const void *y, const void *residual, const void *gate,
+                              const float *post_weight, const float *scale, const float *pre_weight,
+                              const void *d_out, const void *d_normed, void *d_y, void *d_residual, void *d_gate,
+                              float *d_post_weight, float *d_scale, float *d_pre_weight, void *workspace,
+                              size_t workspace_bytes, kda_stream_t stream) {
+  NormArgs a;
+  kda_status st = check_norm(desc, y, residual, gate, post_weight, scale, pre_weight, &a);
+  if (st != KDA_OK) return st;
+  if ((!d_out && !d_normed) || !d_y || (gate && !d_gate)) return KDA_ERR_NULL;
+  if ((d_post_weight && !a.post) || (d_pre_weight && !d_normed)) return KDA_ERR_NULL;
+  if ((d_gate && !gate) || (d_residual && !residual)) return KDA_ERR_UNSUPPORTED;
+  if (!aligned_to(d_out, esize(a.rt)) || !aligned_to(d_normed, esize(a.t)) || !aligned_to(d_y, esize(a.t)) ||
+      !aligned_to(d_residual, esize(a.rt)) || !aligned_to(d_gate, esize(a.t)) || !aligned_to(d_post_weight, 4) ||
+      !aligned_to(d_scale, 4) || !aligned_to(d_pre_weight, 4))
+    return KDA_ERR_ALIGN;
+  const Range in[] = {rows_span(a, y, a.t), rows_span(a, residual, a.rt), rows_span(a, gate, a.t),
+                      width_span(a, post_weight), width_span(a, scale), width_span(a, pre_weight),
+                      rows_span(a, d_normed, a.t), rows_span(a, d_out, a.rt)};
+  const Range outs[] = {rows_span(a, d_y, a.t), rows_span(a, d_gate, a.t), width_span(a, d_post_weight),
+                        width_span(a, d_scale), width_span(a, d_pre_weight),
+                        span(workspace, workspace ? workspace_bytes : 0), rows_span(a, d_residual, a.rt)};
+  if (aliased(in, 8, outs, 7, 7, 6)) return KDA_ERR_ALIAS;
+  const NormBwdIo io{d_out, d_normed, d_y, d_residual, d_gate, d_post_weight, d_scale, d_pre_weight};
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return with_workspace(workspace, workspace_bytes, norm_bwd_workspace_bytes(a.width), s,
+                        [&](void *ws) { return launch_norm_bwd(a, io, ws, s); });
 }
 
 const char *kda_status_string(kda_status s) {

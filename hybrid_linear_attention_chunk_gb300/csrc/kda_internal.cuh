@@ -142,6 +142,64 @@ cudaError_t launch_affine_compose(int N, int H, int P, const float *s0, const fl
 cudaError_t launch_validate_prefill(const PrefillArgs &a, int *d_flag, cudaStream_t s);
 cudaError_t launch_validate_decode(const DecodeArgs &a, int *d_flag, cudaStream_t s);
 
+// Gated linear recurrence (kda_scan.cu).  Channel c of the D = H d channels is
+// a chain; tokens are rows of D elements.
+struct ScanArgs {
+  int N;        // sequences
+  int T_total;  // tokens in the packed buffer
+  int T_seq;    // tokens per sequence when cu == nullptr
+  int H, d, D;
+  kda_dtype t, gate;         // x / out and their gradients; log_alpha
+  bool complement;           // w = 1 - alpha (else 1)
+  const void *x, *g;
+  const float *A_log;        // nullable: g holds log_alpha; else decay logits of dtype t
+  float g_min;
+  const float *s0;           // nullable
+  const int32_t *cu;         // nullable
+  void *o;
+  float *sT;                 // nullable
+  float *states;             // nullable: the state before every kScanTile-th token
+  __host__ __device__ kda_dtype gdt() const { return A_log ? t : gate; }
+};
+struct ScanBwdIo {
+  const void *dO;
+  const float *dST;          // nullable
+  void *dx, *dg;
+  float *dA, *ds0;           // nullable
+};
+constexpr int kScanTile = KDA_SCAN_TILE;
+// Slots of the `states` buffer.  Sequence n's tile j has slot bos / 16 + n + j:
+// a sequence of len tokens has ceil(len / 16) <= floor((bos + len) / 16) -
+// floor(bos / 16) + 1 tiles, so the slots of two sequences never meet.
+inline size_t scan_state_slots(const ScanArgs &a) { return (size_t)a.T_total / kScanTile + a.N; }
+inline size_t scan_states_bytes(const ScanArgs &a) { return scan_state_slots(a) * a.D * sizeof(float); }
+size_t scan_dA_bytes(const ScanArgs &a);  // per-chain partials of dA_log
+cudaError_t launch_scan_fwd(const ScanArgs &a, cudaStream_t s);
+cudaError_t launch_scan_states(const ScanArgs &a, cudaStream_t s);  // a.states alone
+cudaError_t launch_scan_bwd(const ScanArgs &a, const ScanBwdIo &io, float *dA_part, cudaStream_t s);
+cudaError_t launch_scan_step(const ScanArgs &a, cudaStream_t s);    // T_seq = 1, sT the state out
+cudaError_t launch_validate_scan(const ScanArgs &a, int *d_flag, cudaStream_t s);
+
+// Norms around a block (kda_norm.cu).
+struct NormArgs {
+  long long rows;
+  int width;
+  kda_dtype t, rt;           // y / gate / normed; residual / out
+  bool post;
+  float e1, e2;
+  const void *y, *res, *gate;
+  const float *w1, *sc, *w2;
+  void *out, *normed;
+};
+struct NormBwdIo {
+  const void *dout, *dn;
+  void *dy, *dres, *dgate;
+  float *dw1, *dsc, *dw2;
+};
+size_t norm_bwd_workspace_bytes(int width);
+cudaError_t launch_norm_fwd(const NormArgs &a, cudaStream_t s);
+cudaError_t launch_norm_bwd(const NormArgs &a, const NormBwdIo &io, void *ws, cudaStream_t s);
+
 // ---------------------------------------------------------------- device helpers
 
 __device__ __forceinline__ float ld_elem(const void *p, size_t i, kda_dtype t) {

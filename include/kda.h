@@ -1,6 +1,7 @@
 /*
  * kda.h - C ABI of libkda.so: Kimi Delta Attention (KDA) chunked prefill and
- * decode step on one GB300 (sm_103a).
+ * decode step on one GB300 (sm_103a), the gated linear recurrence, and the
+ * norms around a block.
  *
  * Cited page: "Kimi K3：从 3T 稀疏预训练到百万 Token Agent 的端到端扩展"
  * (liuzhao09.github.io/papers/kimi-k3), [K3-notes] below.
@@ -313,6 +314,181 @@ kda_status kda_chunk_bwd(const kda_chunk_desc *desc, const void *q, const void *
                          float *dq, float *dk, float *dv, float *dlog_alpha, float *dbeta,
                          float *d_initial_state, void *workspace, size_t workspace_bytes,
                          kda_stream_t stream);
+
+/*
+ * Gated linear recurrence.  The recurrence without its key: every channel of
+ * every head is a chain of its own,
+ *     h_t = alpha_t h_{t-1} + w_t x_t,     out_t = h_t,     alpha_t = exp(g_t)
+ *     w_t = 1              (KDA_WRITE_ONE)
+ *     w_t = 1 - alpha_t    (KDA_WRITE_COMPLEMENT: h is a running mean of x)
+ * with the log-decay g given, or formed from decay logits z by the layer's
+ * decay gate (see kda_layer_gates), g = g_min Sigmoid(exp(A_h) z).
+ *
+ * Conventions shared by kda_scan_fwd, kda_scan_bwd and kda_scan_step
+ *  - [tokens, H, d] tensors are token-major and dense, as kda_chunk_fwd's;
+ *    H and d are any positive sizes with H * d < 2^31, and tokens is any size.
+ *  - x, out and their gradients have dtype `dtype`.  `decay` is log_alpha in
+ *    `gate_dtype` when A_log is NULL, and z in `dtype` otherwise (g_min is then
+ *    in [-5, 0), KDA_ERR_RANGE otherwise).
+ *  - Pointers need their element's alignment; tensors that are all 16-byte
+ *    aligned with H * d a multiple of 4 run vectorised, others elementwise,
+ *    with the same results up to rounding.
+ *  - Arithmetic is fp32, states and state gradients are fp32; out, dx and
+ *    d_decay are rounded once.  Results are deterministic.
+ *  - log_alpha is any value <= 0; -inf is alpha = 0 and forgets the state.  z is
+ *    any value; at +-inf its gradient is 0.  A non-finite x, state or gradient
+ *    makes what follows of its own chain non-finite, and no other chain.
+ *    Validate mode returns KDA_ERR_RANGE for a log_alpha above 0 or NaN, a NaN
+ *    z, a non-finite A_log, or cu_seqlens that do not start at 0 or that
+ *    decrease or pass the token count.  (Without it such cu_seqlens are clamped
+ *    to the tensors, so no call reads or writes outside them.)
+ *  - cu_seqlens may end before the last token: rows behind the last sequence
+ *    are neither read nor written.
+ */
+typedef enum { KDA_WRITE_ONE = 0, KDA_WRITE_COMPLEMENT = 1 } kda_scan_write;
+
+/* Tokens between two of the states kda_scan_fwd keeps for kda_scan_bwd. */
+#define KDA_SCAN_TILE 16
+
+typedef struct {
+  int B;          /* batch; must be 1 when cu_seqlens is given                */
+  int T;          /* tokens per sequence, or total tokens when varlen          */
+  int H, d;       /* heads, channels per head                                  */
+  int num_seqs;   /* varlen: number of sequences N; 0 when cu_seqlens is NULL  */
+  kda_dtype dtype;      /* x, out, d_out, dx; z and its gradient               */
+  kda_dtype gate_dtype; /* log_alpha and its gradient (ignored with A_log)     */
+  kda_scan_write write;
+  int validate;   /* 1: range-check inputs first (synchronises the stream)     */
+} kda_scan_desc;
+
+/* Bytes of the `states` buffer of kda_scan_fwd and kda_scan_bwd. */
+kda_status kda_scan_states_size(const kda_scan_desc *desc, size_t *bytes);
+
+/*
+ * kda_scan_fwd
+ *   x             [tokens, H, d] dtype
+ *   decay         [tokens, H, d] log_alpha or z
+ *   A_log         [H] fp32 device, or NULL
+ *   initial_state [Nseq, H, d] fp32, or NULL for zeros
+ *   cu_seqlens    [N+1] int32, or NULL for B x T
+ *   out           [tokens, H, d] dtype, written
+ *   final_state   [Nseq, H, d] fp32, or NULL (written); may equal initial_state
+ *   states        kda_scan_states_size bytes, or NULL (written): the state
+ *                 before every KDA_SCAN_TILE-th token of each sequence, in the
+ *                 library's own order, for kda_scan_bwd on the same arguments
+ * An empty sequence leaves its final state equal to its initial state.  Outputs
+ * may alias nothing else (KDA_ERR_ALIAS).
+ */
+kda_status kda_scan_fwd(const kda_scan_desc *desc, const void *x, const void *decay, const float *A_log,
+                        float g_min, const float *initial_state, const int32_t *cu_seqlens, void *out,
+                        float *final_state, float *states, kda_stream_t stream);
+
+/*
+ * kda_scan_bwd - gradients of kda_scan_fwd for
+ * L = sum_t <d_out_t, out_t> + sum_n <d_final_state_n, h_T(n)>:
+ *     D_t = d_out_t + alpha_{t+1} D_{t+1}   (D_T also gets d_final_state)
+ *     dx_t = w_t D_t,    dg_t = alpha_t D_t (h_{t-1} - [x_t with COMPLEMENT])
+ *     d_initial_state = alpha_1 D_1
+ *     dz = dg g (1 - g / g_min) exp(A_h),    dA_log_h = sum z dz
+ *   states          what kda_scan_fwd stored, or NULL: then a forward pass
+ *                   inside the call rebuilds them
+ *   d_out           [tokens, H, d] dtype
+ *   d_final_state   [Nseq, H, d] fp32, or NULL for zero
+ *   dx              [tokens, H, d] dtype, written
+ *   d_decay         [tokens, H, d] decay's dtype, written: dlog_alpha or dz
+ *   dA_log          [H] fp32, written; required with A_log and NULL without
+ *   d_initial_state [Nseq, H, d] fp32, or NULL
+ *   workspace       kda_scan_bwd_workspace_size bytes (16-byte aligned; with
+ *                   `states` given the size is smaller), or NULL: then a call
+ *                   that needs some allocates it stream-ordered
+ * Rows behind the last sequence get no gradient and add nothing to dA_log.
+ */
+kda_status kda_scan_bwd_workspace_size(const kda_scan_desc *desc, int logits, int have_states, size_t *bytes);
+kda_status kda_scan_bwd(const kda_scan_desc *desc, const void *x, const void *decay, const float *A_log,
+                        float g_min, const float *initial_state, const int32_t *cu_seqlens,
+                        const float *states, const void *d_out, const float *d_final_state, void *dx,
+                        void *d_decay, float *dA_log, float *d_initial_state, void *workspace,
+                        size_t workspace_bytes, kda_stream_t stream);
+
+/*
+ * kda_scan_step - one token for B sequences (desc: T = 1, num_seqs = 0).
+ *   x, decay, out [B, H, d];  state_in, state_out [B, H, d] fp32, state_out
+ *   written; state_out may equal state_in (update in place).
+ */
+kda_status kda_scan_step(const kda_scan_desc *desc, const void *x, const void *decay, const float *A_log,
+                         float g_min, const float *state_in, float *state_out, void *out, kda_stream_t stream);
+
+/*
+ * Norms before and after a block, fused with its gate and residual scale.  Per
+ * row of `width` channels (a token; or a token's head, then width = dv and the
+ * result is the KDA output equation, see kda_layer_gates):
+ *     u      = RMSNorm(y; post_weight, post_eps)        (post_norm; else y)
+ *     b      = Sigmoid(gate) o u                        (gate given; else u)
+ *     out    = residual + scale o b                     (missing parts: 0, 1)
+ *     normed = RMSNorm(out; pre_weight, pre_eps)        (the next block's input)
+ *     RMSNorm(a; w, e)_j = a_j w_j / sqrt(mean_j a_j^2 + e)
+ * Conventions
+ *  - y, gate and normed (and their gradients) have dtype `dtype`; residual and
+ *    out (and theirs) `res_dtype`, which equals dtype when residual is NULL.
+ *    Weights, scale and their gradients are fp32 [width].
+ *  - 0 <= rows, 1 <= width <= KDA_NORM_MAX_WIDTH.  Rows are dense.  Pointers need
+ *    their element's alignment; 16-byte aligned tensors of a width that is a
+ *    multiple of 8 run vectorised.
+ *  - Arithmetic is fp32 (mean squares too: a row's squares must not overflow)
+ *    and each output is rounded once; normed is formed from the unrounded out.
+ *    A row of zeros gives zeros when eps > 0.  Results are deterministic.
+ */
+#define KDA_NORM_MAX_WIDTH 8192
+
+typedef struct {
+  int64_t rows;
+  int width;
+  kda_dtype dtype, res_dtype;
+  int post_norm;  /* 1: RMSNorm of y                                           */
+  float post_eps; /* >= 0, used with post_norm                                 */
+  float pre_eps;  /* >= 0, used with normed / d_normed                         */
+} kda_norm_desc;
+
+/*
+ * kda_block_norm_fwd
+ *   y           [rows, width] dtype
+ *   residual    [rows, width] res_dtype, or NULL
+ *   gate        [rows, width] dtype (logits), or NULL
+ *   post_weight [width] fp32, or NULL for ones (must be NULL without post_norm)
+ *   scale       [width] fp32, or NULL for ones
+ *   pre_weight  [width] fp32, or NULL for ones (must be NULL without normed)
+ *   out         [rows, width] res_dtype, or NULL when not wanted; may equal
+ *               residual (update in place)
+ *   normed      [rows, width] dtype, or NULL when not wanted (one of the two
+ *               outputs is required)
+ * Outputs may alias nothing else (KDA_ERR_ALIAS).
+ */
+kda_status kda_block_norm_fwd(const kda_norm_desc *desc, const void *y, const void *residual, const void *gate,
+                              const float *post_weight, const float *scale, const float *pre_weight, void *out,
+                              void *normed, kda_stream_t stream);
+
+/*
+ * kda_block_norm_bwd - gradients of L = <d_out, out> + <d_normed, normed>, from
+ * the forward's inputs (the forward is recomputed).
+ *   d_out       [rows, width] res_dtype, or NULL for zero
+ *   d_normed    [rows, width] dtype, or NULL for zero (one of them is required);
+ *               pre_weight is not read without it
+ *   d_y         [rows, width] dtype, written
+ *   d_residual  [rows, width] res_dtype, or NULL; may equal d_out
+ *   d_gate      [rows, width] dtype; given exactly when gate is
+ *   d_post_weight, d_scale, d_pre_weight  [width] fp32, each or NULL; sums over
+ *               the rows (zeros when rows = 0).  d_post_weight needs post_norm,
+ *               d_pre_weight needs d_normed (KDA_ERR_NULL otherwise); the
+ *               gradient of an absent (all ones) weight or scale may be asked for
+ *   workspace   kda_block_norm_bwd_workspace_size bytes, 16-byte aligned, or
+ *               NULL: then a call that needs some allocates it stream-ordered
+ */
+kda_status kda_block_norm_bwd_workspace_size(const kda_norm_desc *desc, size_t *bytes);
+kda_status kda_block_norm_bwd(const kda_norm_desc *desc, const void *y, const void *residual, const void *gate,
+                              const float *post_weight, const float *scale, const float *pre_weight,
+                              const void *d_out, const void *d_normed, void *d_y, void *d_residual, void *d_gate,
+                              float *d_post_weight, float *d_scale, float *d_pre_weight, void *workspace,
+                              size_t workspace_bytes, kda_stream_t stream);
 
 /* Static description of a status code (never NULL). */
 const char *kda_status_string(kda_status status);
