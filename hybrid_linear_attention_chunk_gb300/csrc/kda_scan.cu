@@ -1,156 +1,102 @@
-// Gated linear recurrence: h_t = alpha_t h_{t-1} + w_t x_t per channel, its
-// backward, and the single-token step (formulas in include/kda.h).
+// Gated linear recurrence: forward scan and single-token step (formulas in
+// include/kda.h, numerics in kda_scan.cuh).
 //
-// Numerics.  With alpha near 1 (a memory of thousands of tokens) rounding
-// alpha to fp32 costs up to 3e-8 / (1 - alpha) of the state, the same way at
-// every token of a constant decay.  So a step uses expm1: h' = h + (e h + u)
-// with e = expm1(g), whose rounding error is relative to 1 - alpha; for
-// g <= -ln 2 it uses alpha itself, so that a strong decay (alpha = 0 at the
-// least) leaves nothing of h behind.  Everything is fp32.
-#include "kda_internal.cuh"
+// The scan.  A chain (one channel of one sequence) is serial, and a batch has
+// too few chains to keep HBM busy, so time is split.  A warp takes a tile of 16
+// tokens x 64 channels (2 per lane) straight into registers, reduces it to
+// (log-sum of g, what the tile adds to a zero state), and once the state that
+// enters the tile is known runs the same 16 steps again from it: one read of
+// the inputs, one write of the output.  Eight warps hold 128 consecutive tokens
+// of a round; their pairs meet in shared memory.  When there are few chain
+// blocks, the CTAs of a cluster take consecutive 128-token spans of a round and
+// exchange their pairs through distributed shared memory.  Joining pairs in
+// the recurrence's order (never as a tree over several states) keeps the error
+// of a token-by-token run and makes results the same from run to run.
+#include <initializer_list>
+
+#include "kda_scan.cuh"
 
 namespace kda {
 namespace {
 
-constexpr float kNearOne = -0.6931472f;  // expm1 form above, exp form below
-
-struct Decay {
-  float c;     // expm1(g) or alpha
-  bool near_;
-  __device__ __forceinline__ float alpha() const { return near_ ? 1.f + c : c; }
-  __device__ __forceinline__ float one_minus() const { return near_ ? -c : 1.f - c; }
-  // alpha h + u
-  __device__ __forceinline__ float apply(float h, float u) const {
-    const float r = fmaf(c, h, u);
-    return near_ ? h + r : r;
-  }
-};
-
-__device__ __forceinline__ Decay decay_of(float g) {
-  Decay d;
-  d.near_ = g > kNearOne;
-  d.c = d.near_ ? expm1f(g) : expf(g);
-  return d;
-}
-
-// g = g_min Sigmoid(s z); slope = dg/dz.  The exponential's argument is capped
-// (a NaN passes), past which Sigmoid is below 1e-34: e / (1 + e) stays finite.
-__device__ __forceinline__ float gate_of(float z, float s, float g_min, float *slope) {
-  const float v = -s * z;
-  const float e = expf(v > 80.f ? 80.f : v);
-  const float r = 1.f / (1.f + e);
-  const float g = g_min * r;
-  if (slope) *slope = g * (e * r) * s;
-  return g;
-}
-
-__device__ __forceinline__ void scan_range(const ScanArgs &a, int n, int &bos, int &eos) {
-  if (a.cu) {  // clamped: cu_seqlens that break their precondition reach no other memory
-    bos = min(max(a.cu[n], 0), a.T_total);
-    eos = min(max(a.cu[n + 1], bos), a.T_total);
-  } else {
-    bos = n * a.T_seq;
-    eos = bos + a.T_seq;
-  }
-}
-
-constexpr int kThreads = 128;
-
-// One thread per chain.
-__global__ void __launch_bounds__(kThreads) scan_fwd_kernel(ScanArgs a) {
-  const int cblocks = (a.D + kThreads - 1) / kThreads;
-  const int c = (int)(blockIdx.x % cblocks) * kThreads + threadIdx.x, n = blockIdx.x / cblocks;
-  if (c >= a.D) return;
+template <typename X, typename G, bool kLogit, bool kComp, int V>
+__global__ void __launch_bounds__(kScanThreads, 3) scan_fwd_kernel(ScanArgs a, int cblocks) {
+  __shared__ ScanJoin<V> sh;
+  const unsigned ranks = cluster_size(), rank = cluster_rank();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int block = blockIdx.x / ranks, n = block / cblocks;
+  const int c = (block % cblocks) * 32 * V + lane * V;
+  const bool live = c < a.D;  // (D is a multiple of V)
   int bos, eos;
   scan_range(a, n, bos, eos);
+  const X *x = static_cast<const X *>(a.x) + c;
+  const G *dec = static_cast<const G *>(a.g) + c;
+  X *out = static_cast<X *>(a.o);
   const size_t chain = (size_t)n * a.D + c;
-  const float scale = a.A_log ? expf(a.A_log[c / a.d]) : 0.f;
-  float h = a.s0 ? a.s0[chain] : 0.f;
-  size_t slot = (size_t)(bos / kScanTile) + n;
-  for (int t = bos; t < eos; ++t) {
-    if (a.states && (t - bos) % kScanTile == 0) a.states[slot++ * a.D + c] = h;
-    const size_t i = (size_t)t * a.D + c;
-    float g = ld_elem(a.g, i, a.gdt());
-    if (a.A_log) g = gate_of(g, scale, a.g_min, nullptr);
-    const Decay dc = decay_of(g);
-    const float x = ld_elem(a.x, i, a.t);
-    h = dc.apply(h, a.complement ? dc.one_minus() * x : x);
-    if (a.o) st_elem(a.o, i, h, a.t);
+  float carry[V], ns[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    carry[i] = live && a.s0 ? a.s0[chain + i] : 0.f;
+    ns[i] = kLogit && live ? -kLog2e * expf(a.A_log[(c + i) / a.d]) : 0.f;
   }
-  if (a.sT) a.sT[chain] = h;
-}
-
-// One thread per chain: tiles from the last to the first, each rerun forward
-// from its stored state.
-__global__ void __launch_bounds__(kThreads) scan_bwd_kernel(ScanArgs a, ScanBwdIo io, float *dA_part) {
-  const int cblocks = (a.D + kThreads - 1) / kThreads;
-  const int c = (int)(blockIdx.x % cblocks) * kThreads + threadIdx.x, n = blockIdx.x / cblocks;
-  if (c >= a.D) return;
-  int bos, eos;
-  scan_range(a, n, bos, eos);
-  const size_t chain = (size_t)n * a.D + c;
-  const float scale = a.A_log ? expf(a.A_log[c / a.d]) : 0.f;
-  float carry = io.dST ? io.dST[chain] : 0.f;  // gradient of the state that leaves token t
-  float dA = 0.f;
-  const int tiles = (eos - bos + kScanTile - 1) / kScanTile;
-  for (int j = tiles - 1; j >= 0; --j) {
-    const int t0 = bos + j * kScanTile, len = min(kScanTile, eos - t0);
-    float prev[kScanTile];
-    float h = a.states[((size_t)(bos / kScanTile) + n + j) * a.D + c];
-    for (int i = 0; i < len; ++i) {
-      prev[i] = h;
-      const size_t at = (size_t)(t0 + i) * a.D + c;
-      float g = ld_elem(a.g, at, a.gdt());
-      if (a.A_log) g = gate_of(g, scale, a.g_min, nullptr);
-      const Decay dc = decay_of(g);
-      const float x = ld_elem(a.x, at, a.t);
-      h = dc.apply(h, a.complement ? dc.one_minus() * x : x);
+  int par = 0;
+  for (int t0 = bos; t0 < eos; t0 += kScanSpan * (int)ranks, par ^= 1) {
+    const int t = t0 + (int)rank * kScanSpan + warp * kScanTile;
+    const int len = live ? min(max(eos - t, 0), kScanTile) : 0;
+    Pack<X, V> xs[kScanTile];
+    Pack<G, V> gs[kScanTile];
+#pragma unroll
+    for (int j = 0; j < kScanTile; ++j) {
+      xs[j].zero();
+      gs[j].zero();
+      if (j < len) {
+        gs[j].load(dec + (size_t)(t + j) * a.D);
+        xs[j].load(x + (size_t)(t + j) * a.D);
+      }
     }
-    float dA_tile = 0.f;
-    for (int i = len - 1; i >= 0; --i) {
-      const size_t at = (size_t)(t0 + i) * a.D + c;
-      const float z = ld_elem(a.g, at, a.gdt());
-      float slope = 1.f;
-      const float g = a.A_log ? gate_of(z, scale, a.g_min, &slope) : z;
-      const Decay dc = decay_of(g);
-      const float x = ld_elem(a.x, at, a.t);
-      const float D = ld_elem(io.dO, at, a.t) + carry;
-      st_elem(io.dx, at, a.complement ? dc.one_minus() * D : D, a.t);
-      const float dg = dc.alpha() * D * (a.complement ? prev[i] - x : prev[i]) * slope;
-      st_elem(io.dg, at, dg, a.gdt());
-      if (a.A_log && !isinf(z)) dA_tile += dg * z;  // (dg is 0 at z = +-inf)
-      carry = dc.apply(D, 0.f);
+    // tile summary; tokens past the end have alpha = 1 and add nothing
+    float code[kScanTile][V], g[V], add[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) g[i] = add[i] = 0.f;
+#pragma unroll
+    for (int j = 0; j < kScanTile; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        float gv = gs[j].get(i);
+        if (kLogit) gv = j < len ? gate_code(gv, ns[i], a.g_min) : 0.f;
+        code[j][i] = decay_code(gv);
+        g[i] += gv;
+        add[i] = scan_token<kComp>(code[j][i], add[i], xs[j].get(i));
+      }
+    float h[V];
+    sh.join(par, warp, lane, rank, ranks, g, add, carry, h);
+    if (a.states && len > 0) {
+      const size_t slot = (size_t)(bos / kScanTile) + n + (t - bos) / kScanTile;
+      store<V>(a.states + slot * a.D + c, h);
     }
-    dA += dA_tile;
+    if (out) {
+#pragma unroll
+      for (int j = 0; j < kScanTile; ++j) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) h[i] = scan_token<kComp>(code[j][i], h[i], xs[j].get(i));
+        if (j < len) store<V>(out + (size_t)(t + j) * a.D + c, h);
+      }
+    }
   }
-  if (io.ds0) io.ds0[chain] = carry;
-  if (a.A_log) dA_part[chain] = dA;
+  if (a.sT && live && rank == 0 && warp == 0)
+#pragma unroll
+    for (int i = 0; i < V; ++i) a.sT[chain + i] = carry[i];
 }
 
-// dA_log[h]: the sum of the partials [rows][D] over rows and the head's channels.
-__global__ void __launch_bounds__(256) scan_dA_kernel(const float *part, int rows, int D, int d, float *dA) {
-  const int h = blockIdx.x;
-  const long long total = (long long)rows * d;
-  double s = 0.0;
-  for (long long i = threadIdx.x; i < total; i += 256) s += part[(size_t)(i / d) * D + (size_t)h * d + i % d];
-  __shared__ double sh[256];
-  sh[threadIdx.x] = s;
-  __syncthreads();
-  for (int k = 128; k > 0; k >>= 1) {
-    if (threadIdx.x < k) sh[threadIdx.x] += sh[threadIdx.x + k];
-    __syncthreads();
-  }
-  if (threadIdx.x == 0) dA[h] = (float)sh[0];
-}
+constexpr int kStepThreads = 128;
 
-__global__ void __launch_bounds__(kThreads) scan_step_kernel(ScanArgs a) {
-  const size_t i = (size_t)blockIdx.x * kThreads + threadIdx.x;
+__global__ void __launch_bounds__(kStepThreads) scan_step_kernel(ScanArgs a) {
+  const size_t i = (size_t)blockIdx.x * kStepThreads + threadIdx.x;
   if (i >= (size_t)a.N * a.D) return;
   float g = ld_elem(a.g, i, a.gdt());
-  if (a.A_log) g = gate_of(g, expf(a.A_log[(i % a.D) / a.d]), a.g_min, nullptr);
-  const Decay dc = decay_of(g);
-  const float x = ld_elem(a.x, i, a.t);
-  const float h = dc.apply(a.s0[i], a.complement ? dc.one_minus() * x : x);
+  if (a.A_log) g = gate_code(g, -kLog2e * expf(a.A_log[(i % a.D) / a.d]), a.g_min);
+  const float c = decay_code(g), x = ld_elem(a.x, i, a.t);
+  const float h = a.complement ? scan_token<true>(c, a.s0[i], x) : scan_token<false>(c, a.s0[i], x);
   a.sT[i] = h;
   st_elem(a.o, i, h, a.t);
 }
@@ -175,15 +121,48 @@ __global__ void __launch_bounds__(256) validate_scan_kernel(ScanArgs a, int *fla
   if (bad) atomicOr(flag, bad);
 }
 
+template <typename X, typename G, bool kLogit, bool kComp, int V>
+cudaError_t fwd_v(const ScanArgs &a, cudaStream_t s) {
+  const int cblocks = (a.D + 32 * V - 1) / (32 * V), ranks = scan_cluster(a, 32 * V);
+  const long long blocks = (long long)cblocks * a.N * ranks;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(kScanThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = ranks;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, scan_fwd_kernel<X, G, kLogit, kComp, V>, a, cblocks);
+}
+
+template <typename X, typename G, bool kLogit>
+cudaError_t fwd_t(const ScanArgs &a, cudaStream_t s) {
+  const bool pairs = scan_pairs(a.D, {a.x, a.g, a.o, a.states});
+  if (a.complement) return pairs ? fwd_v<X, G, kLogit, true, 2>(a, s) : fwd_v<X, G, kLogit, true, 1>(a, s);
+  return pairs ? fwd_v<X, G, kLogit, false, 2>(a, s) : fwd_v<X, G, kLogit, false, 1>(a, s);
+}
+
 }  // namespace
 
-size_t scan_dA_bytes(const ScanArgs &a) { return (size_t)a.N * a.D * sizeof(float); }
-
-static unsigned scan_blocks(const ScanArgs &a) { return (unsigned)((size_t)((a.D + kThreads - 1) / kThreads) * a.N); }
+// A cluster grows until the grid fills the 152 SMs three times over or a round
+// covers the average sequence.
+int scan_cluster(const ScanArgs &a, int channels) {
+  const long long blocks = (long long)((a.D + channels - 1) / channels) * a.N;
+  const long long tokens = a.T_total / a.N;
+  int r = 1;
+  while (r < kScanMaxCluster && blocks * r < 3 * 152 && (long long)r * kScanSpan < tokens) r *= 2;
+  return r;
+}
 
 cudaError_t launch_scan_fwd(const ScanArgs &a, cudaStream_t s) {
-  scan_fwd_kernel<<<scan_blocks(a), kThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  using B = __nv_bfloat16;
+  if (a.A_log) return a.t == KDA_BF16 ? fwd_t<B, B, true>(a, s) : fwd_t<float, float, true>(a, s);
+  if (a.t == KDA_BF16) return a.gate == KDA_BF16 ? fwd_t<B, B, false>(a, s) : fwd_t<B, float, false>(a, s);
+  return a.gate == KDA_BF16 ? fwd_t<float, B, false>(a, s) : fwd_t<float, float, false>(a, s);
 }
 
 cudaError_t launch_scan_states(const ScanArgs &a, cudaStream_t s) {
@@ -193,19 +172,9 @@ cudaError_t launch_scan_states(const ScanArgs &a, cudaStream_t s) {
   return launch_scan_fwd(b, s);
 }
 
-cudaError_t launch_scan_bwd(const ScanArgs &a, const ScanBwdIo &io, float *dA_part, cudaStream_t s) {
-  scan_bwd_kernel<<<scan_blocks(a), kThreads, 0, s>>>(a, io, dA_part);
-  cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess && a.A_log) {
-    scan_dA_kernel<<<a.H, 256, 0, s>>>(dA_part, a.N, a.D, a.d, io.dA);
-    e = cudaGetLastError();
-  }
-  return e;
-}
-
 cudaError_t launch_scan_step(const ScanArgs &a, cudaStream_t s) {
   const size_t n = (size_t)a.N * a.D;
-  scan_step_kernel<<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, s>>>(a);
+  scan_step_kernel<<<(unsigned)((n + kStepThreads - 1) / kStepThreads), kStepThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
