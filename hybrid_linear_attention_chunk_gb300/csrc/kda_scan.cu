@@ -20,72 +20,91 @@ namespace kda {
 namespace {
 
 template <typename X, typename G, bool kLogit, bool kComp, int V>
-__global__ void __launch_bounds__(kScanThreads, 3) scan_fwd_kernel(ScanArgs a, int cblocks) {
+__global__ void __launch_bounds__(kScanThreads, 2) scan_fwd_kernel(ScanArgs a, int cblocks) {
   __shared__ ScanJoin<V> sh;
-  const unsigned ranks = cluster_size(), rank = cluster_rank();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int block = blockIdx.x / ranks, n = block / cblocks;
-  const int c = (block % cblocks) * 32 * V + lane * V;
-  const bool live = c < a.D;  // (D is a multiple of V)
+  const int ranks = (int)cluster_size(), rank = (int)cluster_rank();
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int block = blockIdx.x / ranks, n = block / cblocks, c0 = (block % cblocks) * 32 * V;
+  const int c = c0 + lane * V, D = a.D;
+  const bool live = c < D, whole = c0 + 32 * V <= D;  // (D is a multiple of V)
   int bos, eos;
   scan_range(a, n, bos, eos);
-  const X *x = static_cast<const X *>(a.x) + c;
-  const G *dec = static_cast<const G *>(a.g) + c;
-  X *out = static_cast<X *>(a.o);
-  const size_t chain = (size_t)n * a.D + c;
-  float carry[V], ns[V];
+  const size_t chain = (size_t)n * D + c;
+  float h[V], state[V], ns[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    carry[i] = live && a.s0 ? a.s0[chain + i] : 0.f;
+    h[i] = state[i] = live && a.s0 ? a.s0[chain + i] : 0.f;
     ns[i] = kLogit && live ? -kLog2e * expf(a.A_log[(c + i) / a.d]) : 0.f;
   }
+  if (ranks == 1 && warp == kScanWarps - 1)
+#pragma unroll
+    for (int i = 0; i < V; ++i) sh.carry[0][lane * V + i] = h[i];
+
+  if (ranks > 1) cluster_sync_all();  // every CTA has started before another stores in it
+
+  Pack<X, V> xs[kScanTile], xn[kScanTile];
+  Pack<G, V> gs[kScanTile];
+  int t = bos + rank * kScanSpan + warp * kScanTile;
+  // a token past the end has alpha = 1 (z = -inf) and adds nothing
+  auto fetch = [&](int at, Pack<X, V>(&xv)[kScanTile], Pack<G, V>(&gv)[kScanTile]) {
+    const int left = eos - at;
+    const bool full = whole && left >= kScanTile;
+    load_tile<G, V>(gv, a.g, D, at, (unsigned)(c * sizeof(G)), live ? left : 0, full, kLogit ? -INFINITY : 0.f);
+    load_tile<X, V>(xv, a.x, D, at, (unsigned)(c * sizeof(X)), live ? left : 0, full, 0.f);
+  };
+  fetch(t, xs, gs);
   int par = 0;
-  for (int t0 = bos; t0 < eos; t0 += kScanSpan * (int)ranks, par ^= 1) {
-    const int t = t0 + (int)rank * kScanSpan + warp * kScanTile;
-    const int len = live ? min(max(eos - t, 0), kScanTile) : 0;
-    Pack<X, V> xs[kScanTile];
-    Pack<G, V> gs[kScanTile];
+  for (int t0 = bos; t0 < eos; t0 += kScanSpan * ranks, t += kScanSpan * ranks, par ^= 1) {
+    float code[kScanTile][V], logs[V];
+    Span<V> mine;
 #pragma unroll
-    for (int j = 0; j < kScanTile; ++j) {
-      xs[j].zero();
-      gs[j].zero();
-      if (j < len) {
-        gs[j].load(dec + (size_t)(t + j) * a.D);
-        xs[j].load(x + (size_t)(t + j) * a.D);
-      }
-    }
-    // tile summary; tokens past the end have alpha = 1 and add nothing
-    float code[kScanTile][V], g[V], add[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) g[i] = add[i] = 0.f;
+    for (int i = 0; i < V; ++i) logs[i] = mine.add[i] = 0.f;
 #pragma unroll
     for (int j = 0; j < kScanTile; ++j)
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        float gv = gs[j].get(i);
-        if (kLogit) gv = j < len ? gate_code(gv, ns[i], a.g_min) : 0.f;
-        code[j][i] = decay_code(gv);
-        g[i] += gv;
-        add[i] = scan_token<kComp>(code[j][i], add[i], xs[j].get(i));
+        const float g = kLogit ? gate_code(gs[j].get(i), ns[i], a.g_min) : gs[j].get(i);
+        code[j][i] = decay_code(g);
+        logs[i] += g;
       }
-    float h[V];
-    sh.join(par, warp, lane, rank, ranks, g, add, carry, h);
-    if (a.states && len > 0) {
+    // the next round's loads run under the rest of this round
+    fetch(t + kScanSpan * ranks, xn, gs);
+#pragma unroll
+    for (int j = 0; j < kScanTile; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) mine.add[i] = scan_token<kComp>(code[j][i], mine.add[i], xs[j].get(i));
+#pragma unroll
+    for (int i = 0; i < V; ++i) mine.c[i] = decay_code(logs[i]);
+    if (ranks == 1) join_one<V>(sh, par, warp, lane, mine, h);
+    else join_cluster<V>(sh, par, warp, lane, rank, ranks, mine, logs, state, h);
+    const int left = live ? eos - t : 0;
+    if (a.states && left > 0) {
       const size_t slot = (size_t)(bos / kScanTile) + n + (t - bos) / kScanTile;
-      store<V>(a.states + slot * a.D + c, h);
+      store<V>(a.states + slot * D + c, h);
     }
-    if (out) {
+    char *o = static_cast<char *>(a.o) + ((size_t)t * D + c) * sizeof(X);
+    const size_t row = (size_t)D * sizeof(X);
+    const int rows = a.o ? left : 0;
 #pragma unroll
-      for (int j = 0; j < kScanTile; ++j) {
+    for (int j = 0; j < kScanTile; ++j, o += row) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) h[i] = scan_token<kComp>(code[j][i], h[i], xs[j].get(i));
-        if (j < len) store<V>(out + (size_t)(t + j) * a.D + c, h);
-      }
+      for (int i = 0; i < V; ++i) h[i] = scan_token<kComp>(code[j][i], h[i], xs[j].get(i));
+      if (j < rows) store<V>(reinterpret_cast<X *>(o), h);
     }
+    if (ranks == 1) {
+      if (warp == kScanWarps - 1)
+#pragma unroll
+        for (int i = 0; i < V; ++i) sh.carry[par ^ 1][lane * V + i] = h[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) h[i] = state[i];
+    }
+#pragma unroll
+    for (int j = 0; j < kScanTile; ++j) xs[j] = xn[j];
   }
-  if (a.sT && live && rank == 0 && warp == 0)
+  if (a.sT && live && rank == 0 && warp == kScanWarps - 1)
 #pragma unroll
-    for (int i = 0; i < V; ++i) a.sT[chain + i] = carry[i];
+    for (int i = 0; i < V; ++i) a.sT[chain + i] = h[i];
 }
 
 constexpr int kStepThreads = 128;

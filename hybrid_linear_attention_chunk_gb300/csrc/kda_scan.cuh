@@ -40,14 +40,14 @@ __device__ __forceinline__ float fast_rcp(float x) {
   return r;
 }
 
-// expm1 on (-1/8, 0] by its series through g^5: the next term is 4.3e-8 of the
-// first, below half a step.
+// expm1(g) on (-1/8, 0] as g + g^2 q(g), q the quadratic with the least maximum
+// relative error there (a reweighted least-squares fit to the series): 1.8e-8
+// of the value, a third of half a step.
 __device__ __forceinline__ float decay_code(float g) {
   g = at_most_zero(g);
-  float p = fmaf(g, 1.f / 120.f, 1.f / 24.f);
-  p = fmaf(g, p, 1.f / 6.f);
-  p = fmaf(g, p, 0.5f);
-  p = fmaf(g * g, p, g);
+  float q = fmaf(g, 0.03972300514578819f, 0.16652730107307434f);
+  q = fmaf(g, q, 0.4999971389770508f);
+  const float p = fmaf(g * g, q, g);
   return g > kNearOne ? -fabsf(p) : fast_exp2(g * kLog2e);
 }
 
@@ -85,35 +85,50 @@ __device__ __forceinline__ void scan_range(const ScanArgs &a, int n, int &bos, i
 
 // V consecutive elements as they lie in memory, and their fp32 values.
 template <typename T, int V> struct Pack;
-template <int V> struct Pack<float, V> {
-  float v[V];
-  __device__ __forceinline__ void load(const float *p) {
-    if (V == 2) {
-      const float2 t = __ldcs(reinterpret_cast<const float2 *>(p));
-      v[0] = t.x;
-      v[V - 1] = t.y;
-    } else {
-      v[0] = __ldcs(p);
-    }
-  }
-  __device__ __forceinline__ float get(int i) const { return v[i]; }
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = 0.f;
-  }
+template <> struct Pack<float, 2> {
+  float2 v;
+  __device__ __forceinline__ void load(const void *p) { v = __ldcs(static_cast<const float2 *>(p)); }
+  __device__ __forceinline__ float get(int i) const { return i ? v.y : v.x; }
+  __device__ __forceinline__ void fill(float f) { v = make_float2(f, f); }
+};
+template <> struct Pack<float, 1> {
+  float v;
+  __device__ __forceinline__ void load(const void *p) { v = __ldcs(static_cast<const float *>(p)); }
+  __device__ __forceinline__ float get(int) const { return v; }
+  __device__ __forceinline__ void fill(float f) { v = f; }
 };
 template <> struct Pack<__nv_bfloat16, 2> {
   unsigned v;
-  __device__ __forceinline__ void load(const __nv_bfloat16 *p) { v = __ldcs(reinterpret_cast<const unsigned *>(p)); }
+  __device__ __forceinline__ void load(const void *p) { v = __ldcs(static_cast<const unsigned *>(p)); }
   __device__ __forceinline__ float get(int i) const { return __uint_as_float(i ? v & 0xffff0000u : v << 16); }
-  __device__ __forceinline__ void zero() { v = 0u; }
+  __device__ __forceinline__ void fill(float f) { v = __float_as_uint(f) | __float_as_uint(f) >> 16; }  // f exact in bf16
 };
 template <> struct Pack<__nv_bfloat16, 1> {
   unsigned short v;
-  __device__ __forceinline__ void load(const __nv_bfloat16 *p) { v = __ldcs(reinterpret_cast<const unsigned short *>(p)); }
+  __device__ __forceinline__ void load(const void *p) { v = __ldcs(static_cast<const unsigned short *>(p)); }
   __device__ __forceinline__ float get(int) const { return __uint_as_float((unsigned)v << 16); }
-  __device__ __forceinline__ void zero() { v = 0; }
+  __device__ __forceinline__ void fill(float f) { v = (unsigned short)(__float_as_uint(f) >> 16); }
 };
+
+// A warp's tile of one array: tokens t .. t + 15, `col` the lane's byte offset
+// in a row.  The row pointers are the same in a whole warp.  Tokens past `len`
+// get `pad`.
+template <typename T, int V>
+__device__ __forceinline__ void load_tile(Pack<T, V> (&v)[kScanTile], const void *base, int D, int t, unsigned col,
+                                          int len, bool full, float pad) {
+  const size_t row = (size_t)D * sizeof(T);
+  const char *p = static_cast<const char *>(base) + (size_t)t * row;
+  if (full) {
+#pragma unroll
+    for (int j = 0; j < kScanTile; ++j, p += row) v[j].load(p + col);
+  } else {
+#pragma unroll
+    for (int j = 0; j < kScanTile; ++j, p += row) {
+      v[j].fill(pad);
+      if (j < len) v[j].load(p + col);
+    }
+  }
+}
 
 template <int V> __device__ __forceinline__ void store(float *p, const float *v) {
   if (V == 2) *reinterpret_cast<float2 *>(p) = make_float2(v[0], v[V - 1]);
@@ -150,11 +165,17 @@ __device__ __forceinline__ unsigned cluster_size() {
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Stores two floats at the same shared-memory place of CTA `rank`.
-__device__ __forceinline__ void store_remote(void *local, unsigned rank, float x, float y) {
-  unsigned addr = (unsigned)__cvta_generic_to_shared(local), remote;
+// Stores at the same shared-memory place of CTA `rank`.
+template <typename T>
+__device__ __forceinline__ void store_remote(T *local, int rank, const T &v) {
+  const unsigned addr = (unsigned)__cvta_generic_to_shared(local);
+  unsigned remote;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(addr), "r"(rank));
-  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(remote), "f"(x), "f"(y) : "memory");
+  const float *f = reinterpret_cast<const float *>(&v);
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(T) / 8); ++i)
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(remote + 8 * i), "f"(f[2 * i]), "f"(f[2 * i + 1])
+                 : "memory");
 }
 
 constexpr int kScanWarps = 8;                               // warps of a CTA
@@ -162,67 +183,73 @@ constexpr int kScanThreads = 32 * kScanWarps;
 constexpr int kScanSpan = kScanWarps * kScanTile;           // tokens of a CTA in one round
 constexpr int kScanMaxCluster = 8;
 
-// Joins the spans of one round.  Every warp gives the decay code c and log-sum
-// G of its tile and what the tile adds (B) per channel, in the order the
-// recurrence runs (warp 0 of CTA 0 first); each thread gets back the state that
-// enters its warp's tile, and `carry` becomes the state that leaves the round.
-template <int V>
-struct ScanJoin {
-  float2 tile[2][kScanWarps][32 * V];          // (c, B)
-  float G[2][kScanWarps][32 * V];
-  float2 cta[2][kScanMaxCluster][32 * V];      // (c, B) of whole CTAs
-
-  __device__ __forceinline__ void join(int par, int warp, int lane, unsigned rank, unsigned ranks,
-                                       const float (&g)[V], const float (&b)[V], float (&carry)[V],
-                                       float (&entry)[V]) {
+// What a span of tokens does to the state, per channel of a lane: the decay
+// code of its log-sum, and what it adds.
+template <int V> struct __align__(8 * V) Span {
+  float c[V], add[V];
+  __device__ __forceinline__ void run(float (&h)[V]) const {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      tile[par][warp][lane * V + i] = make_float2(decay_code(g[i]), b[i]);
-      if (ranks > 1) G[par][warp][lane * V + i] = g[i];
-    }
-    __syncthreads();
-    if (ranks > 1) {
-      if (warp == 0) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          float sum = 0.f, add = 0.f;
-#pragma unroll
-          for (int w = 0; w < kScanWarps; ++w) {
-            const float2 t = tile[par][w][lane * V + i];
-            sum += G[par][w][lane * V + i];
-            add = decay_apply(t.x, add, t.y);
-          }
-          const float c = decay_code(sum);
-          for (unsigned r = 0; r < ranks; ++r) store_remote(&cta[par][rank][lane * V + i], r, c, add);
-        }
-      }
-      cluster_sync_all();
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        entry[i] = carry[i];
-        for (unsigned r = 0; r < ranks; ++r) {
-          if (r == rank) entry[i] = carry[i];
-          const float2 t = cta[par][r][lane * V + i];
-          carry[i] = decay_apply(t.x, carry[i], t.y);
-        }
-        for (int w = 0; w < warp; ++w) {
-          const float2 t = tile[par][w][lane * V + i];
-          entry[i] = decay_apply(t.x, entry[i], t.y);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-#pragma unroll
-        for (int w = 0; w < kScanWarps; ++w) {
-          if (w == warp) entry[i] = carry[i];
-          const float2 t = tile[par][w][lane * V + i];
-          carry[i] = decay_apply(t.x, carry[i], t.y);
-        }
-      }
-    }
+    for (int i = 0; i < V; ++i) h[i] = decay_apply(c[i], h[i], add[i]);
   }
 };
+
+// Joins the tiles of one round, in the order the recurrence runs (warp 0 of
+// CTA 0 first).  Tile by tile each warp runs the state that entered the round
+// through the spans before its own.
+//   One CTA: the last warp leaves the state that enters the next round in
+//   `carry`, which the others read after the next round's barrier.
+//   A cluster: warp 0 joins its CTA's eight tiles into one span and stores it
+//   in every CTA; each thread keeps the round's state in registers.
+// Two buffers: a round's spans are read until the next round's barrier.
+template <int V>
+struct ScanJoin {
+  Span<V> tile[2][kScanWarps][32];
+  Span<V> cta[2][kScanMaxCluster][32];
+  float logs[2][kScanWarps][32 * V];
+  float carry[2][32 * V];
+};
+
+template <int V>
+__device__ __forceinline__ void join_one(ScanJoin<V> &sh, int par, int warp, int lane, const Span<V> &mine,
+                                         float (&entry)[V]) {
+  sh.tile[par][warp][lane] = mine;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < V; ++i) entry[i] = sh.carry[par][lane * V + i];
+  for (int w = 0; w < warp; ++w) sh.tile[par][w][lane].run(entry);
+}
+
+template <int V>
+__device__ __forceinline__ void join_cluster(ScanJoin<V> &sh, int par, int warp, int lane, int rank, int ranks,
+                                             const Span<V> &mine, const float (&logs)[V], float (&state)[V],
+                                             float (&entry)[V]) {
+  sh.tile[par][warp][lane] = mine;
+#pragma unroll
+  for (int i = 0; i < V; ++i) sh.logs[par][warp][lane * V + i] = logs[i];
+  __syncthreads();
+  if (warp == 0) {
+    float sum[V] = {}, add[V] = {};
+#pragma unroll
+    for (int w = 0; w < kScanWarps; ++w) {
+      sh.tile[par][w][lane].run(add);
+#pragma unroll
+      for (int i = 0; i < V; ++i) sum[i] += sh.logs[par][w][lane * V + i];
+    }
+    Span<V> all;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      all.c[i] = decay_code(sum[i]);
+      all.add[i] = add[i];
+    }
+    for (int r = 0; r < ranks; ++r) store_remote(&sh.cta[par][rank][lane], r, all);
+  }
+  cluster_sync_all();
+  for (int r = 0; r < rank; ++r) sh.cta[par][r][lane].run(state);
+#pragma unroll
+  for (int i = 0; i < V; ++i) entry[i] = state[i];
+  for (int r = rank; r < ranks; ++r) sh.cta[par][r][lane].run(state);
+  for (int w = 0; w < warp; ++w) sh.tile[par][w][lane].run(entry);
+}
 
 // Whether every given pointer allows 2-element accesses on rows of D elements.
 inline bool scan_pairs(int D, std::initializer_list<const void *> ptrs) {
