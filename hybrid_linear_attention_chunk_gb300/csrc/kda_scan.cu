@@ -3,15 +3,17 @@
 //
 // The scan.  A chain (one channel of one sequence) is serial, and a batch has
 // too few chains to keep HBM busy, so time is split.  A warp takes a tile of 16
-// tokens x 64 channels (2 per lane) straight into registers, reduces it to
-// (log-sum of g, what the tile adds to a zero state), and once the state that
-// enters the tile is known runs the same 16 steps again from it: one read of
-// the inputs, one write of the output.  Eight warps hold 128 consecutive tokens
-// of a round; their pairs meet in shared memory.  When there are few chain
-// blocks, the CTAs of a cluster take consecutive 128-token spans of a round and
-// exchange their pairs through distributed shared memory.  Joining pairs in
-// the recurrence's order (never as a tree over several states) keeps the error
-// of a token-by-token run and makes results the same from run to run.
+// tokens x 64 channels (2 per lane) straight into registers and scans it from a
+// zero state, keeping each token's sum and product of alphas; once the state
+// that enters the tile is known, a token's output is sum + product * state: one
+// read of the inputs, one write of the output.  Eight warps hold 128 consecutive
+// tokens of a round; what their tiles do to a state meets in shared memory.
+// When there are few chain blocks, the CTAs of a cluster take consecutive
+// 128-token spans of a round and exchange theirs through distributed shared
+// memory.  A state passes through the tiles in the recurrence's order, so it
+// keeps the error of a token-by-token run and is the same from run to run.
+// The loads of the next round are issued as soon as the raw inputs have been
+// used, so they are in flight under the join and the stores.
 #include <initializer_list>
 
 #include "kda_scan.cuh"
@@ -34,7 +36,7 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_fwd_kernel(ScanArgs a, i
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     h[i] = state[i] = live && a.s0 ? a.s0[chain + i] : 0.f;
-    ns[i] = kLogit && live ? -kLog2e * expf(a.A_log[(c + i) / a.d]) : 0.f;
+    ns[i] = kLogit && live ? gate_scale(a.A_log[(c + i) / a.d]) : -1.f;
   }
   if (ranks == 1 && warp == kScanWarps - 1)
 #pragma unroll
@@ -42,7 +44,7 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_fwd_kernel(ScanArgs a, i
 
   if (ranks > 1) cluster_sync_all();  // every CTA has started before another stores in it
 
-  Pack<X, V> xs[kScanTile], xn[kScanTile];
+  Pack<X, V> xs[kScanTile];
   Pack<G, V> gs[kScanTile];
   int t = bos + rank * kScanSpan + warp * kScanTile;
   // a token past the end has alpha = 1 (z = -inf) and adds nothing
@@ -55,26 +57,32 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_fwd_kernel(ScanArgs a, i
   fetch(t, xs, gs);
   int par = 0;
   for (int t0 = bos; t0 < eos; t0 += kScanSpan * ranks, t += kScanSpan * ranks, par ^= 1) {
-    float code[kScanTile][V], logs[V];
+    // from a zero state: sum[j] the state after token j, keep[j] the product of
+    // the alphas up to it
+    float keep[kScanTile][V], sum[kScanTile][V], logs[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      logs[i] = 0.f;
+      float k = 1.f, u = 0.f;
+#pragma unroll
+      for (int j = 0; j < kScanTile; ++j) {
+        const float g = kLogit ? gate_code(gs[j].get(i), ns[i], a.g_min) : at_most_zero(gs[j].get(i));
+        const float al = alpha_of(g), x = xs[j].get(i);
+        logs[i] += g;
+        k *= al;
+        u = fmaf(al, u, kComp ? one_minus(g, al) * x : x);
+        keep[j][i] = k;
+        sum[j][i] = u;
+      }
+    }
+    // the next round's loads run under the rest of this round
+    fetch(t + kScanSpan * ranks, xs, gs);
     Span<V> mine;
 #pragma unroll
-    for (int i = 0; i < V; ++i) logs[i] = mine.add[i] = 0.f;
-#pragma unroll
-    for (int j = 0; j < kScanTile; ++j)
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float g = kLogit ? gate_code(gs[j].get(i), ns[i], a.g_min) : gs[j].get(i);
-        code[j][i] = decay_code(g);
-        logs[i] += g;
-      }
-    // the next round's loads run under the rest of this round
-    fetch(t + kScanSpan * ranks, xn, gs);
-#pragma unroll
-    for (int j = 0; j < kScanTile; ++j)
-#pragma unroll
-      for (int i = 0; i < V; ++i) mine.add[i] = scan_token<kComp>(code[j][i], mine.add[i], xs[j].get(i));
-#pragma unroll
-    for (int i = 0; i < V; ++i) mine.c[i] = decay_code(logs[i]);
+    for (int i = 0; i < V; ++i) {
+      mine.c[i] = decay_code(logs[i]);
+      mine.add[i] = sum[kScanTile - 1][i];
+    }
     if (ranks == 1) join_one<V>(sh, par, warp, lane, mine, h);
     else join_cluster<V>(sh, par, warp, lane, rank, ranks, mine, logs, state, h);
     const int left = live ? eos - t : 0;
@@ -87,11 +95,13 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_fwd_kernel(ScanArgs a, i
     const int rows = a.o ? left : 0;
 #pragma unroll
     for (int j = 0; j < kScanTile; ++j, o += row) {
+      float v[V];
 #pragma unroll
-      for (int i = 0; i < V; ++i) h[i] = scan_token<kComp>(code[j][i], h[i], xs[j].get(i));
-      if (j < rows) store<V>(reinterpret_cast<X *>(o), h);
+      for (int i = 0; i < V; ++i) v[i] = fmaf(keep[j][i], h[i], sum[j][i]);
+      if (j < rows) store<V>(reinterpret_cast<X *>(o), v);
     }
     if (ranks == 1) {
+      mine.run(h);
       if (warp == kScanWarps - 1)
 #pragma unroll
         for (int i = 0; i < V; ++i) sh.carry[par ^ 1][lane * V + i] = h[i];
@@ -99,8 +109,6 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_fwd_kernel(ScanArgs a, i
 #pragma unroll
       for (int i = 0; i < V; ++i) h[i] = state[i];
     }
-#pragma unroll
-    for (int j = 0; j < kScanTile; ++j) xs[j] = xn[j];
   }
   if (a.sT && live && rank == 0 && warp == kScanWarps - 1)
 #pragma unroll
@@ -113,9 +121,10 @@ __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(ScanArgs a) {
   const size_t i = (size_t)blockIdx.x * kStepThreads + threadIdx.x;
   if (i >= (size_t)a.N * a.D) return;
   float g = ld_elem(a.g, i, a.gdt());
-  if (a.A_log) g = gate_code(g, -kLog2e * expf(a.A_log[(i % a.D) / a.d]), a.g_min);
-  const float c = decay_code(g), x = ld_elem(a.x, i, a.t);
-  const float h = a.complement ? scan_token<true>(c, a.s0[i], x) : scan_token<false>(c, a.s0[i], x);
+  if (a.A_log) g = gate_code(g, gate_scale(a.A_log[(i % a.D) / a.d]), a.g_min);
+  g = at_most_zero(g);
+  const float x = ld_elem(a.x, i, a.t);
+  const float h = decay_apply(decay_code(g), a.s0[i], a.complement ? one_minus(g, alpha_of(g)) * x : x);
   a.sT[i] = h;
   st_elem(a.o, i, h, a.t);
 }

@@ -3,13 +3,16 @@
 //
 // Numerics.  With alpha near 1 (a memory of thousands of tokens) rounding
 // alpha to fp32 costs up to 3e-8 / (1 - alpha) of the state, the same way at
-// every token of a constant decay.  So for g > -1/8 a step uses
-// h' = h + (e h + u) with e = expm1(g), whose rounding error is relative to
-// 1 - alpha, and below that alpha itself, so that a strong decay (alpha = 0 at
-// the least) leaves nothing of h behind.  Everything is fp32.
+// every token of a constant decay.  So the decay of a whole 16-token tile, by
+// which a state is carried on, comes from the sum of its logs: h' = h + (e h + B)
+// with e = expm1(sum g) when sum g > -1/8, whose rounding error is relative to
+// 1 - alpha, and alpha itself below that, so that a strong decay (alpha = 0 at
+// the least) leaves nothing of h behind.  Inside a tile the products of up to 16
+// rounded alphas are off by at most 16 roundings, of the tile's own sums alone.
+// w = 1 - alpha comes from expm1(g) too.  Everything is fp32.
 //
-// A decay is one float c: the sign bit set means c = e (e <= 0; -0 for g = 0),
-// clear means c = alpha.
+// The decay of a tile or span is one float c: the sign bit set means c = e
+// (e <= 0; -0 for a sum of 0), clear means c = alpha.
 #pragma once
 
 #include "kda_internal.cuh"
@@ -43,16 +46,15 @@ __device__ __forceinline__ float fast_rcp(float x) {
 // expm1(g) on (-1/8, 0] as g + g^2 q(g), q the quadratic with the least maximum
 // relative error there (a reweighted least-squares fit to the series): 1.8e-8
 // of the value, a third of half a step.
-__device__ __forceinline__ float decay_code(float g) {
-  g = at_most_zero(g);
+__device__ __forceinline__ float expm1_near(float g) {
   float q = fmaf(g, 0.03972300514578819f, 0.16652730107307434f);
   q = fmaf(g, q, 0.4999971389770508f);
-  const float p = fmaf(g * g, q, g);
-  return g > kNearOne ? -fabsf(p) : fast_exp2(g * kLog2e);
+  return fmaf(g * g, q, g);
 }
 
-__device__ __forceinline__ float decay_alpha(float c) { return is_near(c) ? 1.f + c : c; }
-__device__ __forceinline__ float decay_one_minus(float c) { return is_near(c) ? -c : 1.f - c; }
+__device__ __forceinline__ float decay_code(float g) {
+  return g > kNearOne ? -fabsf(expm1_near(g)) : fast_exp2(g * kLog2e);
+}
 
 // alpha h + u
 __device__ __forceinline__ float decay_apply(float c, float h, float u) {
@@ -61,12 +63,14 @@ __device__ __forceinline__ float decay_apply(float c, float h, float u) {
   return r;
 }
 
-// One token: alpha h + w x; with w = 1 - alpha it is h + e (h - x) = x + alpha (h - x).
-template <bool kComp>
-__device__ __forceinline__ float scan_token(float c, float h, float x) {
-  if (!kComp) return decay_apply(c, h, x);
-  return fmaf(c, h - x, is_near(c) ? h : x);
+// alpha and w of one token from its g <= 0.
+__device__ __forceinline__ float alpha_of(float g) { return fast_exp2(g * kLog2e); }
+__device__ __forceinline__ float one_minus(float g, float alpha) {
+  return g > kNearOne ? -expm1_near(g) : 1.f - alpha;
 }
+
+// -exp(A) log2(e), never 0: the product with z = -inf, a masked token, stays inf.
+__device__ __forceinline__ float gate_scale(float A_log) { return fminf(-kLog2e * expf(A_log), -1e-37f); }
 
 // g = g_min Sigmoid(s z) from z and ns = -s log2(e); 2^x = inf gives g = -0.
 __device__ __forceinline__ float gate_code(float z, float ns, float g_min) {

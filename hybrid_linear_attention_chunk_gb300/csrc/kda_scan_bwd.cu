@@ -40,9 +40,9 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_kernel(ScanArgs a, ScanBwdI
       float g = ld_elem(a.g, at, a.gdt());
       float sl;
       if (a.A_log) g = gate_slope(g, scale, a.g_min, &sl);
-      const float dc = decay_code(g);
+      const float al = alpha_of(g);
       const float x = ld_elem(a.x, at, a.t);
-      h = decay_apply(dc, h, a.complement ? decay_one_minus(dc) * x : x);
+      h = decay_apply(decay_code(g), h, a.complement ? one_minus(g, al) * x : x);
     }
     float dA_tile = 0.f;
     for (int i = len - 1; i >= 0; --i) {
@@ -50,14 +50,14 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_kernel(ScanArgs a, ScanBwdI
       const float z = ld_elem(a.g, at, a.gdt());
       float slope = 1.f;
       const float g = a.A_log ? gate_slope(z, scale, a.g_min, &slope) : z;
-      const float dc = decay_code(g);
+      const float al = alpha_of(g);
       const float x = ld_elem(a.x, at, a.t);
       const float D = ld_elem(io.dO, at, a.t) + carry;
-      st_elem(io.dx, at, a.complement ? decay_one_minus(dc) * D : D, a.t);
-      const float dg = decay_alpha(dc) * D * (a.complement ? prev[i] - x : prev[i]) * slope;
+      st_elem(io.dx, at, a.complement ? one_minus(g, al) * D : D, a.t);
+      const float dg = al * D * (a.complement ? prev[i] - x : prev[i]) * slope;
       st_elem(io.dg, at, dg, a.gdt());
       if (a.A_log && !isinf(z)) dA_tile += dg * z;  // (dg is 0 at z = +-inf)
-      carry = decay_apply(dc, D, 0.f);
+      carry = decay_apply(decay_code(g), D, 0.f);
     }
     dA += dA_tile;
   }
