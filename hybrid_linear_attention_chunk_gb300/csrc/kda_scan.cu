@@ -21,84 +21,101 @@
 namespace kda {
 namespace {
 
+template <typename X, typename G, bool kLogit, int V>
+struct FwdSmem {
+  static constexpr int kWarpBytes = 2 * (Tile<X, V, false>::kBytes + Tile<G, V, kLogit>::kBytes);
+  static constexpr int kBytes = (int)sizeof(ScanJoin<V>) + kScanWarps * kWarpBytes;
+};
+
 template <typename X, typename G, bool kLogit, bool kComp, int V>
-__global__ void __launch_bounds__(kScanThreads, 2) scan_fwd_kernel(ScanArgs a, int cblocks) {
-  __shared__ ScanJoin<V> sh;
+__global__ void __launch_bounds__(kScanThreads, FwdSmem<X, G, kLogit, V>::kBytes <= 115712 ? 2 : 1)
+scan_fwd_kernel(ScanArgs a, int cblocks) {
+  extern __shared__ __align__(128) char smem[];
+  ScanJoin<V> &sh = *reinterpret_cast<ScanJoin<V> *>(smem);
   const int ranks = (int)cluster_size(), rank = (int)cluster_rank();
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int block = blockIdx.x / ranks, n = block / cblocks, c0 = (block % cblocks) * 32 * V;
   const int c = c0 + lane * V, D = a.D;
-  const bool live = c < D, whole = c0 + 32 * V <= D;  // (D is a multiple of V)
+  const bool live = c < D;  // (with V = 2, D is a multiple of 4)
   int bos, eos;
   scan_range(a, n, bos, eos);
   const size_t chain = (size_t)n * D + c;
-  float h[V], state[V], ns[V];
+  const Gate<kLogit, V> gate(a, c, live);
+  float h[V], state[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    h[i] = state[i] = live && a.s0 ? a.s0[chain + i] : 0.f;
-    ns[i] = kLogit && live ? gate_scale(a.A_log[(c + i) / a.d]) : -1.f;
-  }
+  for (int i = 0; i < V; ++i) h[i] = state[i] = live && a.s0 ? a.s0[chain + i] : 0.f;
   if (ranks == 1 && warp == kScanWarps - 1)
 #pragma unroll
     for (int i = 0; i < V; ++i) sh.carry[0][lane * V + i] = h[i];
-
   if (ranks > 1) cluster_sync_all();  // every CTA has started before another stores in it
 
-  Pack<X, V> xs[kScanTile];
-  Pack<G, V> gs[kScanTile];
+  Tile<X, V, false> xs;
+  Tile<G, V, kLogit> gs;
+  if constexpr (V == 2) {
+    char *mine = smem + sizeof(ScanJoin<V>) + warp * FwdSmem<X, G, kLogit, V>::kWarpBytes;
+    xs.buf = reinterpret_cast<X *>(mine);
+    gs.buf = reinterpret_cast<G *>(mine + 2 * Tile<X, V, false>::kBytes);
+  }
+  const int step = kScanSpan * ranks;
   int t = bos + rank * kScanSpan + warp * kScanTile;
   // a token past the end has alpha = 1 (z = -inf) and adds nothing
-  auto fetch = [&](int at, Pack<X, V>(&xv)[kScanTile], Pack<G, V>(&gv)[kScanTile]) {
-    const int left = eos - at;
-    const bool full = whole && left >= kScanTile;
-    load_tile<G, V>(gv, a.g, D, at, (unsigned)(c * sizeof(G)), live ? left : 0, full, kLogit ? -INFINITY : 0.f);
-    load_tile<X, V>(xv, a.x, D, at, (unsigned)(c * sizeof(X)), live ? left : 0, full, 0.f);
+  auto fetch = [&](int stage, int at) {
+    gs.issue(stage, a.g, D, at, c0, eos - at, lane);
+    xs.issue(stage, a.x, D, at, c0, eos - at, lane);
+    if (V == 2) copies_commit();
   };
-  fetch(t, xs, gs);
+  if (bos < eos) {
+    fetch(0, t);
+    if (V == 2) fetch(1, t + step);
+  }
   int par = 0;
-  for (int t0 = bos; t0 < eos; t0 += kScanSpan * ranks, t += kScanSpan * ranks, par ^= 1) {
+  for (int t0 = bos; t0 < eos; t0 += step, t += step, par ^= 1) {
+    if (V == 2) {
+      copies_wait<1>();
+      __syncwarp();
+      gs.pad(par, eos - t, lane);
+      __syncwarp();
+    }
     // from a zero state: sum[j] the state after token j, keep[j] the product of
     // the alphas up to it
-    float keep[kScanTile][V], sum[kScanTile][V], logs[V];
+    Vec<V> keep[kScanTile], sum[kScanTile], log = all<V>(0.f);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      logs[i] = 0.f;
-      float k = 1.f, u = 0.f;
-#pragma unroll
-      for (int j = 0; j < kScanTile; ++j) {
-        const float g = kLogit ? gate_code(gs[j].get(i), ns[i], a.g_min) : at_most_zero(gs[j].get(i));
-        const float al = alpha_of(g), x = xs[j].get(i);
-        logs[i] += g;
-        k *= al;
-        u = fmaf(al, u, kComp ? one_minus(g, al) * x : x);
-        keep[j][i] = k;
-        sum[j][i] = u;
-      }
+    for (int j = 0; j < kScanTile; ++j) {
+      const Vec<V> l = gate.log(gs.at(par, j, lane)), al = gate.alpha(l);
+      Vec<V> u = xs.at(par, j, lane);
+      if (kComp) u = mul(u, gate.one_minus(l, al));
+      log = add(log, l);
+      keep[j] = j ? mul(keep[j - 1], al) : al;
+      sum[j] = j ? fma(al, sum[j - 1], u) : u;
     }
-    // the next round's loads run under the rest of this round
-    fetch(t + kScanSpan * ranks, xs, gs);
+    // later rounds' loads run under the rest of this round
+    __syncwarp();
+    if (V == 2) fetch(par, t + 2 * step);
+    else fetch(0, t + step);
     Span<V> mine;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      mine.c[i] = decay_code(logs[i]);
-      mine.add[i] = sum[kScanTile - 1][i];
+      mine.c[i] = decay_code(gate.unit * log.get(i));
+      mine.add[i] = sum[kScanTile - 1].get(i);
     }
     if (ranks == 1) join_one<V>(sh, par, warp, lane, mine, h);
-    else join_cluster<V>(sh, par, warp, lane, rank, ranks, mine, logs, state, h);
+    else join_cluster<V>(sh, par, warp, lane, rank, ranks, mine, state, h);
     const int left = live ? eos - t : 0;
+    const Vec<V> hv = lanes<V>([&](int i) { return h[i]; });
     if (a.states && left > 0) {
       const size_t slot = (size_t)(bos / kScanTile) + n + (t - bos) / kScanTile;
-      store<V>(a.states + slot * D + c, h);
+      store<V>(a.states + slot * D + c, hv);
     }
-    char *o = static_cast<char *>(a.o) + ((size_t)t * D + c) * sizeof(X);
-    const size_t row = (size_t)D * sizeof(X);
-    const int rows = a.o ? left : 0;
+    if (a.o) {
+      X *o = static_cast<X *>(a.o) + (size_t)t * D + c;
+      if (__all_sync(0xffffffffu, left >= kScanTile)) {
 #pragma unroll
-    for (int j = 0; j < kScanTile; ++j, o += row) {
-      float v[V];
+        for (int j = 0; j < kScanTile; ++j) store<V>(o + (unsigned)(j * D), fma(keep[j], hv, sum[j]));
+      } else {
 #pragma unroll
-      for (int i = 0; i < V; ++i) v[i] = fmaf(keep[j][i], h[i], sum[j][i]);
-      if (j < rows) store<V>(reinterpret_cast<X *>(o), v);
+        for (int j = 0; j < kScanTile; ++j)
+          if (j < left) store<V>(o + (unsigned)(j * D), fma(keep[j], hv, sum[j]));
+      }
     }
     if (ranks == 1) {
       mine.run(h);
@@ -110,6 +127,7 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_fwd_kernel(ScanArgs a, i
       for (int i = 0; i < V; ++i) h[i] = state[i];
     }
   }
+  if (V == 2) copies_wait<0>();
   if (a.sT && live && rank == 0 && warp == kScanWarps - 1)
 #pragma unroll
     for (int i = 0; i < V; ++i) a.sT[chain + i] = h[i];
@@ -117,14 +135,18 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_fwd_kernel(ScanArgs a, i
 
 constexpr int kStepThreads = 128;
 
+template <bool kLogit>
+__device__ __forceinline__ float step(const ScanArgs &a, int c, Vec<1> z, Vec<1> x, float h) {
+  const Gate<kLogit, 1> gate(a, c, true);
+  const Vec<1> l = gate.log(z);
+  return decay_apply(decay_code(gate.unit * l.v), h, a.complement ? gate.one_minus(l, gate.alpha(l)).v * x.v : x.v);
+}
+
 __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(ScanArgs a) {
   const size_t i = (size_t)blockIdx.x * kStepThreads + threadIdx.x;
   if (i >= (size_t)a.N * a.D) return;
-  float g = ld_elem(a.g, i, a.gdt());
-  if (a.A_log) g = gate_code(g, gate_scale(a.A_log[(i % a.D) / a.d]), a.g_min);
-  g = at_most_zero(g);
-  const float x = ld_elem(a.x, i, a.t);
-  const float h = decay_apply(decay_code(g), a.s0[i], a.complement ? one_minus(g, alpha_of(g)) * x : x);
+  const Vec<1> z{ld_elem(a.g, i, a.gdt())}, x{ld_elem(a.x, i, a.t)};
+  const float h = a.A_log ? step<true>(a, (int)(i % a.D), z, x, a.s0[i]) : step<false>(a, 0, z, x, a.s0[i]);
   a.sT[i] = h;
   st_elem(a.o, i, h, a.t);
 }
@@ -154,9 +176,14 @@ cudaError_t fwd_v(const ScanArgs &a, cudaStream_t s) {
   const int cblocks = (a.D + 32 * V - 1) / (32 * V), ranks = scan_cluster(a, 32 * V);
   const long long blocks = (long long)cblocks * a.N * ranks;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const auto kernel = scan_fwd_kernel<X, G, kLogit, kComp, V>;
+  constexpr int smem = FwdSmem<X, G, kLogit, V>::kBytes;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);
   cfg.blockDim = dim3(kScanThreads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -164,14 +191,14 @@ cudaError_t fwd_v(const ScanArgs &a, cudaStream_t s) {
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, scan_fwd_kernel<X, G, kLogit, kComp, V>, a, cblocks);
+  return cudaLaunchKernelEx(&cfg, kernel, a, cblocks);
 }
 
 template <typename X, typename G, bool kLogit>
 cudaError_t fwd_t(const ScanArgs &a, cudaStream_t s) {
-  const bool pairs = scan_pairs(a.D, {a.x, a.g, a.o, a.states});
-  if (a.complement) return pairs ? fwd_v<X, G, kLogit, true, 2>(a, s) : fwd_v<X, G, kLogit, true, 1>(a, s);
-  return pairs ? fwd_v<X, G, kLogit, false, 2>(a, s) : fwd_v<X, G, kLogit, false, 1>(a, s);
+  const bool v = scan_vectors(a.D, {{a.x, sizeof(X)}, {a.g, sizeof(G)}, {a.o, sizeof(X)}, {a.states, 4}});
+  if (a.complement) return v ? fwd_v<X, G, kLogit, true, 2>(a, s) : fwd_v<X, G, kLogit, true, 1>(a, s);
+  return v ? fwd_v<X, G, kLogit, false, 2>(a, s) : fwd_v<X, G, kLogit, false, 1>(a, s);
 }
 
 }  // namespace

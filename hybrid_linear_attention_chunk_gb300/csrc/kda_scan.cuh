@@ -24,13 +24,6 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ bool is_near(float c) { return __float_as_int(c) < 0; }
 
-// min(g, 0) that passes a NaN on (log_alpha above 0 counts as 0).
-__device__ __forceinline__ float at_most_zero(float g) {
-  float r;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(g), "f"(0.f));
-  return r;
-}
-
 // 2^x and 1 / x to 2 ulp, subnormal results flushed to 0.
 __device__ __forceinline__ float fast_exp2(float x) {
   float r;
@@ -46,14 +39,19 @@ __device__ __forceinline__ float fast_rcp(float x) {
 // expm1(g) on (-1/8, 0] as g + g^2 q(g), q the quadratic with the least maximum
 // relative error there (a reweighted least-squares fit to the series): 1.8e-8
 // of the value, a third of half a step.
+constexpr float kExpm1C0 = 0.4999971389770508f, kExpm1C1 = 0.16652730107307434f, kExpm1C2 = 0.03972300514578819f;
 __device__ __forceinline__ float expm1_near(float g) {
-  float q = fmaf(g, 0.03972300514578819f, 0.16652730107307434f);
-  q = fmaf(g, q, 0.4999971389770508f);
-  return fmaf(g * g, q, g);
+  return fmaf(g * g, fmaf(g, fmaf(g, kExpm1C2, kExpm1C1), kExpm1C0), g);
 }
 
 __device__ __forceinline__ float decay_code(float g) {
-  return g > kNearOne ? -fabsf(expm1_near(g)) : fast_exp2(g * kLog2e);
+  return g > kNearOne && g <= 0.f ? -fabsf(expm1_near(g)) : fast_exp2(g * kLog2e);
+}
+
+// The code of two spans in a row, c after d.
+__device__ __forceinline__ float decay_join(float c, float d) {
+  if (is_near(c) && is_near(d)) return -fabsf(fmaf(c, d, c + d));  // (0 keeps its sign bit)
+  return (is_near(c) ? 1.f + c : c) * (is_near(d) ? 1.f + d : d);
 }
 
 // alpha h + u
@@ -63,19 +61,8 @@ __device__ __forceinline__ float decay_apply(float c, float h, float u) {
   return r;
 }
 
-// alpha and w of one token from its g <= 0.
-__device__ __forceinline__ float alpha_of(float g) { return fast_exp2(g * kLog2e); }
-__device__ __forceinline__ float one_minus(float g, float alpha) {
-  return g > kNearOne ? -expm1_near(g) : 1.f - alpha;
-}
-
 // -exp(A) log2(e), never 0: the product with z = -inf, a masked token, stays inf.
 __device__ __forceinline__ float gate_scale(float A_log) { return fminf(-kLog2e * expf(A_log), -1e-37f); }
-
-// g = g_min Sigmoid(s z) from z and ns = -s log2(e); 2^x = inf gives g = -0.
-__device__ __forceinline__ float gate_code(float z, float ns, float g_min) {
-  return g_min * fast_rcp(1.f + fast_exp2(ns * z));
-}
 
 __device__ __forceinline__ void scan_range(const ScanArgs &a, int n, int &bos, int &eos) {
   if (a.cu) {  // clamped: cu_seqlens that break their precondition reach no other memory
@@ -87,70 +74,171 @@ __device__ __forceinline__ void scan_range(const ScanArgs &a, int n, int &bos, i
   }
 }
 
-// V consecutive elements as they lie in memory, and their fp32 values.
-template <typename T, int V> struct Pack;
-template <> struct Pack<float, 2> {
-  float2 v;
-  __device__ __forceinline__ void load(const void *p) { v = __ldcs(static_cast<const float2 *>(p)); }
-  __device__ __forceinline__ float get(int i) const { return i ? v.y : v.x; }
-  __device__ __forceinline__ void fill(float f) { v = make_float2(f, f); }
-};
-template <> struct Pack<float, 1> {
+// V fp32 values of one lane.  Two are one register pair, and one instruction
+// of the packed fp32 kind works on both: the scan is bound by instruction issue
+// before it is by anything else but HBM.
+template <int V> struct Vec;
+template <> struct Vec<1> {
   float v;
-  __device__ __forceinline__ void load(const void *p) { v = __ldcs(static_cast<const float *>(p)); }
   __device__ __forceinline__ float get(int) const { return v; }
-  __device__ __forceinline__ void fill(float f) { v = f; }
 };
-template <> struct Pack<__nv_bfloat16, 2> {
-  unsigned v;
-  __device__ __forceinline__ void load(const void *p) { v = __ldcs(static_cast<const unsigned *>(p)); }
-  __device__ __forceinline__ float get(int i) const { return __uint_as_float(i ? v & 0xffff0000u : v << 16); }
-  __device__ __forceinline__ void fill(float f) { v = __float_as_uint(f) | __float_as_uint(f) >> 16; }  // f exact in bf16
+template <> struct Vec<2> {
+  unsigned long long v;
+  __device__ __forceinline__ float get(int i) const { return __uint_as_float((unsigned)(i ? v >> 32 : v)); }
 };
-template <> struct Pack<__nv_bfloat16, 1> {
-  unsigned short v;
-  __device__ __forceinline__ void load(const void *p) { v = __ldcs(static_cast<const unsigned short *>(p)); }
-  __device__ __forceinline__ float get(int) const { return __uint_as_float((unsigned)v << 16); }
-  __device__ __forceinline__ void fill(float f) { v = (unsigned short)(__float_as_uint(f) >> 16); }
-};
+__device__ __forceinline__ Vec<2> pair(float x, float y) {
+  Vec<2> r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+  return r;
+}
+template <int V> __device__ __forceinline__ Vec<V> all(float x);
+template <> __device__ __forceinline__ Vec<1> all<1>(float x) { return Vec<1>{x}; }
+template <> __device__ __forceinline__ Vec<2> all<2>(float x) { return pair(x, x); }
+__device__ __forceinline__ Vec<1> fma(Vec<1> a, Vec<1> b, Vec<1> c) { return Vec<1>{fmaf(a.v, b.v, c.v)}; }
+__device__ __forceinline__ Vec<1> mul(Vec<1> a, Vec<1> b) { return Vec<1>{a.v * b.v}; }
+__device__ __forceinline__ Vec<1> add(Vec<1> a, Vec<1> b) { return Vec<1>{a.v + b.v}; }
+__device__ __forceinline__ Vec<2> fma(Vec<2> a, Vec<2> b, Vec<2> c) {
+  Vec<2> r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ Vec<2> mul(Vec<2> a, Vec<2> b) {
+  Vec<2> r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ Vec<2> add(Vec<2> a, Vec<2> b) {
+  Vec<2> r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+// f of every value's index
+template <int V, typename F> __device__ __forceinline__ Vec<V> lanes(F f) {
+  if constexpr (V == 2) return pair(f(0), f(1));
+  else return Vec<1>{f(0)};
+}
 
-// A warp's tile of one array: tokens t .. t + 15, `col` the lane's byte offset
-// in a row.  The row pointers are the same in a whole warp.  Tokens past `len`
-// get `pad`.
-template <typename T, int V>
-__device__ __forceinline__ void load_tile(Pack<T, V> (&v)[kScanTile], const void *base, int D, int t, unsigned col,
-                                          int len, bool full, float pad) {
-  const size_t row = (size_t)D * sizeof(T);
-  const char *p = static_cast<const char *>(base) + (size_t)t * row;
-  if (full) {
+// V consecutive elements as they lie in memory, as fp32.
+__device__ __forceinline__ Vec<1> values(float v) { return Vec<1>{v}; }
+__device__ __forceinline__ Vec<2> values(float2 v) { return pair(v.x, v.y); }
+__device__ __forceinline__ Vec<1> values(unsigned short v) { return Vec<1>{__uint_as_float((unsigned)v << 16)}; }
+__device__ __forceinline__ Vec<2> values(unsigned v) { return pair(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)); }
+template <typename T, int V> struct RawOf;
+template <> struct RawOf<float, 1> { using type = float; };
+template <> struct RawOf<float, 2> { using type = float2; };
+template <> struct RawOf<__nv_bfloat16, 1> { using type = unsigned short; };
+template <> struct RawOf<__nv_bfloat16, 2> { using type = unsigned; };
+template <typename T, int V> using Raw = typename RawOf<T, V>::type;
+
+template <int V> __device__ __forceinline__ void store(float *p, Vec<V> v) {
+  if constexpr (V == 2) *reinterpret_cast<float2 *>(p) = make_float2(v.get(0), v.get(1));
+  else *p = v.v;
+}
+template <int V> __device__ __forceinline__ void store(__nv_bfloat16 *p, Vec<V> v) {
+  if constexpr (V == 2) *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(v.get(0), v.get(1));
+  else *p = __float2bfloat16_rn(v.v);
+}
+
+// ------------------------------------------------------- a warp's input tiles
+// Rows of 16 tokens of one array, V channels per lane.  Two ways in:
+//  V = 2: 16-byte asynchronous copies into the warp's own shared memory, two
+//  tiles ahead, so that what is in flight costs no registers (needs 16-byte
+//  aligned arrays and rows);
+//  V = 1: elementwise loads into registers, for everything else.
+// Tokens past the end, and channels past D, read as 0 (kPad: -inf).
+template <typename T, int V, bool kPad> struct Tile;
+
+template <typename T, bool kPad> struct Tile<T, 2, kPad> {
+  static constexpr int kRow = 64;                           // elements
+  static constexpr int kChunk = 16 / (int)sizeof(T);        // elements of a copy
+  static constexpr int kPerRow = kRow / kChunk;
+  static constexpr int kBytes = kScanTile * kRow * (int)sizeof(T);
+  T *buf;                                                   // [2][16][64]
+  __device__ __forceinline__ void issue(int stage, const void *base, int D, int t, int c0, int len, int lane) {
+    T *dst = buf + stage * (kScanTile * kRow);
+    const int row = lane / kPerRow, col = (lane % kPerRow) * kChunk;
+    const bool in = c0 + col < D;
+    const T *src = static_cast<const T *>(base) + ((size_t)t * D + c0 + col);
 #pragma unroll
-    for (int j = 0; j < kScanTile; ++j, p += row) v[j].load(p + col);
-  } else {
-#pragma unroll
-    for (int j = 0; j < kScanTile; ++j, p += row) {
-      v[j].fill(pad);
-      if (j < len) v[j].load(p + col);
+    for (int k = 0; k < kScanTile * kPerRow / 32; ++k) {
+      const int r = row + k * (32 / kPerRow);
+      const bool ok = in && r < len;
+      const unsigned to = (unsigned)__cvta_generic_to_shared(dst + r * kRow + col);
+      const void *from = ok ? src + (unsigned)(r * D) : static_cast<const T *>(base);
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(ok ? 16 : 0) : "memory");
     }
   }
+  // after the copies have landed, before the first read
+  __device__ __forceinline__ void pad(int stage, int len, int lane) {
+    if (kPad && len < kScanTile) {
+      T *dst = buf + stage * (kScanTile * kRow);
+      for (int r = max(len, 0); r < kScanTile; ++r) {
+        dst[r * kRow + 2 * lane] = (T)-INFINITY;
+        dst[r * kRow + 2 * lane + 1] = (T)-INFINITY;
+      }
+    }
+  }
+  __device__ __forceinline__ Vec<2> at(int stage, int j, int lane) const {
+    return values(reinterpret_cast<const Raw<T, 2> *>(buf + stage * (kScanTile * kRow) + j * kRow)[lane]);
+  }
+};
+
+template <typename T, bool kPad> struct Tile<T, 1, kPad> {
+  static constexpr int kBytes = 0;
+  Raw<T, 1> v[kScanTile];
+  __device__ __forceinline__ void issue(int, const void *base, int D, int t, int c0, int len, int lane) {
+    const T *src = static_cast<const T *>(base) + ((size_t)t * D + c0 + lane);
+    if (c0 + lane >= D) len = 0;
+#pragma unroll
+    for (int j = 0; j < kScanTile; ++j) {
+      v[j] = sizeof(T) == 2 ? (kPad ? 0xff80 : 0) : (kPad ? -INFINITY : 0.f);
+      if (j < len) v[j] = __ldcs(reinterpret_cast<const Raw<T, 1> *>(src + (unsigned)(j * D)));
+    }
+  }
+  __device__ __forceinline__ void pad(int, int, int) {}
+  __device__ __forceinline__ Vec<1> at(int, int j, int) const { return values(v[j]); }
+};
+
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft> __device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
-template <int V> __device__ __forceinline__ void store(float *p, const float *v) {
-  if (V == 2) *reinterpret_cast<float2 *>(p) = make_float2(v[0], v[V - 1]);
-  else *p = v[0];
-}
-template <int V> __device__ __forceinline__ void store(__nv_bfloat16 *p, const float *v) {
-  if (V == 2) *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(v[0], v[V - 1]);
-  else *p = __float2bfloat16_rn(v[0]);
-}
-template <int V> __device__ __forceinline__ void load_f32(const float *p, float *v) {
-  if (V == 2) {
-    const float2 t = *reinterpret_cast<const float2 *>(p);
-    v[0] = t.x;
-    v[V - 1] = t.y;
-  } else {
-    v[0] = *p;
+// How a token's alpha and 1 - alpha come from its log-decay, or from its logit
+// through r = Sigmoid(s z), g = g_min r.  `log` is g or r; tile sums of it give
+// the tile's log-decay as log_unit() times the sum.
+template <bool kLogit, int V>
+struct Gate {
+  Vec<V> ns;                     // -s log2(e)
+  float unit, rate, edge;        // g = unit log; log2(alpha) = rate log; near 1 on log's near side of edge
+  float a0, a1, a2, a3;          // 1 - alpha near 1, a cubic times log
+  __device__ __forceinline__ Gate(const ScanArgs &a, int c, bool live) {
+    ns = lanes<V>([&](int i) { return kLogit && live ? gate_scale(a.A_log[(c + i) / a.d]) : -1.f; });
+    unit = kLogit ? a.g_min : 1.f;
+    rate = unit * kLog2e;
+    edge = kNearOne / unit;
+    a0 = -unit;
+    a1 = -unit * unit * kExpm1C0;
+    a2 = -unit * unit * unit * kExpm1C1;
+    a3 = -unit * unit * unit * unit * kExpm1C2;
   }
-}
+  __device__ __forceinline__ Vec<V> log(Vec<V> z) const {
+    if (!kLogit) return z;
+    const Vec<V> e = mul(ns, z);
+    const Vec<V> d = add(all<V>(1.f), lanes<V>([&](int i) { return fast_exp2(e.get(i)); }));
+    return lanes<V>([&](int i) { return fast_rcp(d.get(i)); });
+  }
+  __device__ __forceinline__ Vec<V> alpha(Vec<V> l) const {
+    const Vec<V> e = mul(all<V>(rate), l);
+    return lanes<V>([&](int i) { return fast_exp2(e.get(i)); });
+  }
+  __device__ __forceinline__ Vec<V> one_minus(Vec<V> l, Vec<V> al) const {
+    Vec<V> p = fma(l, all<V>(a3), all<V>(a2));
+    p = mul(l, fma(l, fma(l, p, all<V>(a1)), all<V>(a0)));
+    const Vec<V> f = fma(al, all<V>(-1.f), all<V>(1.f));
+    return lanes<V>([&](int i) { return (kLogit ? l.get(i) < edge : l.get(i) > edge) ? p.get(i) : f.get(i); });
+  }
+};
 
 // ------------------------------------------------------------------ clusters
 // A chain block (one sequence, 32 V channels) runs on one cluster; its CTAs take
@@ -209,7 +297,6 @@ template <int V>
 struct ScanJoin {
   Span<V> tile[2][kScanWarps][32];
   Span<V> cta[2][kScanMaxCluster][32];
-  float logs[2][kScanWarps][32 * V];
   float carry[2][32 * V];
 };
 
@@ -225,25 +312,17 @@ __device__ __forceinline__ void join_one(ScanJoin<V> &sh, int par, int warp, int
 
 template <int V>
 __device__ __forceinline__ void join_cluster(ScanJoin<V> &sh, int par, int warp, int lane, int rank, int ranks,
-                                             const Span<V> &mine, const float (&logs)[V], float (&state)[V],
-                                             float (&entry)[V]) {
+                                             const Span<V> &mine, float (&state)[V], float (&entry)[V]) {
   sh.tile[par][warp][lane] = mine;
-#pragma unroll
-  for (int i = 0; i < V; ++i) sh.logs[par][warp][lane * V + i] = logs[i];
   __syncthreads();
   if (warp == 0) {
-    float sum[V] = {}, add[V] = {};
+    Span<V> all = mine;
 #pragma unroll
-    for (int w = 0; w < kScanWarps; ++w) {
-      sh.tile[par][w][lane].run(add);
+    for (int w = 1; w < kScanWarps; ++w) {
+      const Span<V> t = sh.tile[par][w][lane];
+      t.run(all.add);
 #pragma unroll
-      for (int i = 0; i < V; ++i) sum[i] += sh.logs[par][w][lane * V + i];
-    }
-    Span<V> all;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      all.c[i] = decay_code(sum[i]);
-      all.add[i] = add[i];
+      for (int i = 0; i < V; ++i) all.c[i] = decay_join(t.c[i], all.c[i]);
     }
     for (int r = 0; r < ranks; ++r) store_remote(&sh.cta[par][rank][lane], r, all);
   }
@@ -255,11 +334,16 @@ __device__ __forceinline__ void join_cluster(ScanJoin<V> &sh, int par, int warp,
   for (int w = 0; w < warp; ++w) sh.tile[par][w][lane].run(entry);
 }
 
-// Whether every given pointer allows 2-element accesses on rows of D elements.
-inline bool scan_pairs(int D, std::initializer_list<const void *> ptrs) {
-  uintptr_t bits = (D & 1) ? 8 : 0;
-  for (const void *p : ptrs) bits |= reinterpret_cast<uintptr_t>(p);
-  return (bits & 15) == 0;
+// Whether rows of D elements of every given array can be copied 16 bytes at a
+// time: (address, element size) pairs.
+struct RowArray {
+  const void *p;
+  int size;
+};
+inline bool scan_vectors(int D, std::initializer_list<RowArray> arrays) {
+  for (const RowArray &r : arrays)
+    if (r.p && ((reinterpret_cast<uintptr_t>(r.p) & 15) || ((size_t)D * r.size) % 16)) return false;
+  return true;
 }
 
 // CTAs of a cluster: see the rule in kda_scan.cu.

@@ -8,6 +8,9 @@ namespace {
 
 constexpr int kThreads = 128;
 
+__device__ __forceinline__ float alpha_of(float g) { return fast_exp2(g * kLog2e); }
+__device__ __forceinline__ float one_minus(float g, float alpha) { return g > kNearOne ? -expm1_near(g) : 1.f - alpha; }
+
 __device__ __forceinline__ float gate_slope(float z, float s, float g_min, float *slope) {
   const float v = -s * z;
   const float e = expf(v > 80.f ? 80.f : v);

@@ -326,13 +326,13 @@ kda_status kda_chunk_bwd(const kda_chunk_desc *desc, const void *q, const void *
  *
  * Conventions shared by kda_scan_fwd, kda_scan_bwd and kda_scan_step
  *  - [tokens, H, d] tensors are token-major and dense, as kda_chunk_fwd's;
- *    H and d are any positive sizes with H * d < 2^31, and tokens is any size.
+ *    H and d are any positive sizes with H * d < 2^27; tokens is below 2^31 - 4096.
  *  - x, out and their gradients have dtype `dtype`.  `decay` is log_alpha in
  *    `gate_dtype` when A_log is NULL, and z in `dtype` otherwise (g_min is then
  *    in [-5, 0), KDA_ERR_RANGE otherwise).
  *  - Pointers need their element's alignment; tensors that are all 16-byte
- *    aligned with H * d a multiple of 4 run vectorised, others elementwise,
- *    with the same results up to rounding.
+ *    aligned, with rows of H * d elements that are multiples of 16 bytes, run
+ *    vectorised, others elementwise, with the same results up to rounding.
  *  - Arithmetic is fp32, states and state gradients are fp32; out, dx and
  *    d_decay are rounded once.  Results are deterministic.
  *  - log_alpha is any value <= 0; -inf is alpha = 0 and forgets the state.  z is
