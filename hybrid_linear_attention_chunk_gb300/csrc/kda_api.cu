@@ -344,7 +344,7 @@ kda_status scan_sizes(const kda_scan_desc *d, bool logits, bool varlen, ScanArgs
   if (varlen ? (d->B != 1 || d->num_seqs <= 0) : d->num_seqs != 0) return KDA_ERR_SHAPE;
   const long long D = (long long)d->H * d->d, tokens = (long long)d->B * d->T;
   const long long N = varlen ? d->num_seqs : d->B;
-  if (D >= (1LL << 27) || tokens >= (1LL << 31) - 4096 || N * D >= (1LL << 36) || tokens * D >= (1LL << 44))
+  if (D >= (1LL << 27) || tokens >= (1LL << 31) - 65536 || N * D >= (1LL << 36) || tokens * D >= (1LL << 44))
     return KDA_ERR_SHAPE;
   a->N = (int)N;
   a->T_total = (int)tokens;

@@ -21,59 +21,67 @@
 namespace kda {
 namespace {
 
-template <typename X, typename G, bool kLogit, int V>
+template <typename X, typename G, bool kLogit, typename L>
 struct FwdSmem {
-  static constexpr int kWarpBytes = 2 * (Tile<X, V, false>::kBytes + Tile<G, V, kLogit>::kBytes);
-  static constexpr int kBytes = (int)sizeof(ScanJoin<V>) + kScanWarps * kWarpBytes;
+  static constexpr int kWarpBytes = 2 * (Tile<X, L, false>::kBytes + Tile<G, L, kLogit>::kBytes);
+  static constexpr size_t bytes(int warps) { return ScanJoin<L>::bytes(warps) + (size_t)warps * kWarpBytes; }
+  static constexpr int kMaxWarps = bytes(16) <= 227 * 1024 ? 16 : 8;
 };
 
-template <typename X, typename G, bool kLogit, bool kComp, int V>
-__global__ void __launch_bounds__(kScanThreads, FwdSmem<X, G, kLogit, V>::kBytes <= 115712 ? 2 : 1)
-scan_fwd_kernel(ScanArgs a, int cblocks) {
+template <typename X, typename G, bool kLogit, bool kComp, typename L>
+__global__ void __launch_bounds__(32 * FwdSmem<X, G, kLogit, L>::kMaxWarps, 1) scan_fwd_kernel(ScanArgs a, int cblocks) {
+  constexpr int V = L::V;
   extern __shared__ __align__(128) char smem[];
-  ScanJoin<V> &sh = *reinterpret_cast<ScanJoin<V> *>(smem);
-  const int ranks = (int)cluster_size(), rank = (int)cluster_rank();
-  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const int block = blockIdx.x / ranks, n = block / cblocks, c0 = (block % cblocks) * 32 * V;
-  const int c = c0 + lane * V, D = a.D;
+  ScanJoin<L> sh;
+  sh.warps = blockDim.x / 32;
+  sh.warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+  sh.lane = threadIdx.x & 31;
+  sh.group = sh.lane / L::kLanes;
+  sh.ranks = (int)cluster_size();
+  sh.rank = (int)cluster_rank();
+  sh.place(smem);
+  const int lane = sh.lane, ranks = sh.ranks, D = a.D;
+  const int block = blockIdx.x / ranks, n = block / cblocks, c0 = (block % cblocks) * L::kWide;
+  const int wide = (lane % L::kLanes) * V, c = c0 + wide;
   const bool live = c < D;  // (with V = 2, D is a multiple of 4)
+  const bool last = sh.warp == sh.warps - 1 && sh.group == L::kGroups - 1;  // these lanes hold a round's last tokens
   int bos, eos;
   scan_range(a, n, bos, eos);
   const size_t chain = (size_t)n * D + c;
   const Gate<kLogit, V> gate(a, c, live);
   float h[V], state[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) h[i] = state[i] = live && a.s0 ? a.s0[chain + i] : 0.f;
-  if (ranks == 1 && warp == kScanWarps - 1)
-#pragma unroll
-    for (int i = 0; i < V; ++i) sh.carry[0][lane * V + i] = h[i];
+  for (int i = 0; i < V; ++i) {
+    h[i] = state[i] = live && a.s0 ? a.s0[chain + i] : 0.f;
+    if (ranks == 1 && last) sh.carry[wide + i] = h[i];
+  }
   if (ranks > 1) cluster_sync_all();  // every CTA has started before another stores in it
 
-  Tile<X, V, false> xs;
-  Tile<G, V, kLogit> gs;
+  Tile<X, L, false> xs;
+  Tile<G, L, kLogit> gs;
   if constexpr (V == 2) {
-    char *mine = smem + sizeof(ScanJoin<V>) + warp * FwdSmem<X, G, kLogit, V>::kWarpBytes;
+    char *mine = smem + ScanJoin<L>::bytes(sh.warps) + sh.warp * FwdSmem<X, G, kLogit, L>::kWarpBytes;
     xs.buf = reinterpret_cast<X *>(mine);
-    gs.buf = reinterpret_cast<G *>(mine + 2 * Tile<X, V, false>::kBytes);
+    gs.buf = reinterpret_cast<G *>(mine + 2 * Tile<X, L, false>::kBytes);
   }
-  const int step = kScanSpan * ranks;
-  int t = bos + rank * kScanSpan + warp * kScanTile;
+  const int span = sh.warps * L::kTokens, step = span * ranks;
+  int tw = bos + sh.rank * span + sh.warp * L::kTokens;  // the warp's first token
   // a token past the end has alpha = 1 (z = -inf) and adds nothing
-  auto fetch = [&](int stage, int at) {
-    gs.issue(stage, a.g, D, at, c0, eos - at, lane);
-    xs.issue(stage, a.x, D, at, c0, eos - at, lane);
+  auto fetch = [&](int stage, int t) {
+    gs.issue(stage, a.g, D, t, c0, eos - t, lane);
+    xs.issue(stage, a.x, D, t, c0, eos - t, lane);
     if (V == 2) copies_commit();
   };
   if (bos < eos) {
-    fetch(0, t);
-    if (V == 2) fetch(1, t + step);
+    fetch(0, tw);
+    if (V == 2) fetch(1, tw + step);
   }
   int par = 0;
-  for (int t0 = bos; t0 < eos; t0 += step, t += step, par ^= 1) {
+  for (int t0 = bos; t0 < eos; t0 += step, tw += step, par ^= 1) {
     if (V == 2) {
       copies_wait<1>();
       __syncwarp();
-      gs.pad(par, eos - t, lane);
+      gs.pad(par, eos - tw, lane);
       __syncwarp();
     }
     // from a zero state: sum[j] the state after token j, keep[j] the product of
@@ -90,17 +98,16 @@ scan_fwd_kernel(ScanArgs a, int cblocks) {
     }
     // later rounds' loads run under the rest of this round
     __syncwarp();
-    if (V == 2) fetch(par, t + 2 * step);
-    else fetch(0, t + step);
+    if (V == 2) fetch(par, tw + 2 * step);
+    else fetch(0, tw + step);
     Span<V> mine;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       mine.c[i] = decay_code(gate.unit * log.get(i));
       mine.add[i] = sum[kScanTile - 1].get(i);
     }
-    if (ranks == 1) join_one<V>(sh, par, warp, lane, mine, h);
-    else join_cluster<V>(sh, par, warp, lane, rank, ranks, mine, state, h);
-    const int left = live ? eos - t : 0;
+    sh.join(par, mine, state, h);
+    const int t = tw + sh.group * kScanTile, left = live ? eos - t : 0;
     const Vec<V> hv = lanes<V>([&](int i) { return h[i]; });
     if (a.states && left > 0) {
       const size_t slot = (size_t)(bos / kScanTile) + n + (t - bos) / kScanTile;
@@ -117,18 +124,15 @@ scan_fwd_kernel(ScanArgs a, int cblocks) {
           if (j < left) store<V>(o + (unsigned)(j * D), fma(keep[j], hv, sum[j]));
       }
     }
-    if (ranks == 1) {
-      mine.run(h);
-      if (warp == kScanWarps - 1)
+    mine.run(h);
 #pragma unroll
-        for (int i = 0; i < V; ++i) sh.carry[par ^ 1][lane * V + i] = h[i];
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; ++i) h[i] = state[i];
+    for (int i = 0; i < V; ++i) {
+      if (ranks > 1) h[i] = state[i];
+      else if (last) sh.carry[(par ^ 1) * L::kWide + wide + i] = h[i];
     }
   }
   if (V == 2) copies_wait<0>();
-  if (a.sT && live && rank == 0 && warp == kScanWarps - 1)
+  if (a.sT && live && sh.rank == 0 && last)
 #pragma unroll
     for (int i = 0; i < V; ++i) a.sT[chain + i] = h[i];
 }
@@ -171,18 +175,41 @@ __global__ void __launch_bounds__(256) validate_scan_kernel(ScanArgs a, int *fla
   if (bad) atomicOr(flag, bad);
 }
 
-template <typename X, typename G, bool kLogit, bool kComp, int V>
-cudaError_t fwd_v(const ScanArgs &a, cudaStream_t s) {
-  const int cblocks = (a.D + 32 * V - 1) / (32 * V), ranks = scan_cluster(a, 32 * V);
+// How chains and time are laid over the GPU.
+//   Blocks of 64 channels (2 CTAs of 8 warps on an SM) when there are enough of
+//   them for the 152 SMs; else blocks of 16 channels, whose warps span four
+//   times the tokens.  When even those are at most one for an SM, CTAs of 16
+//   warps, and clusters along the sequence while the grid has room for them and
+//   the sequences are longer than a round.
+struct Plan {
+  bool narrow;
+  int warps, ranks;
+};
+
+Plan plan_fwd(const ScanArgs &a, int max_warps) {
+  const long long tokens = a.T_total / a.N;
+  const auto blocks = [&](int wide) { return (long long)((a.D + wide - 1) / wide) * a.N; };
+  Plan p{blocks(64) < 152, 8, 1};
+  const long long b = blocks(p.narrow ? 16 : 64);
+  if (p.narrow) {
+    if (b <= 152 && tokens > 512) p.warps = max_warps;
+    while (p.ranks < kScanMaxCluster && b * p.ranks * 2 <= 152 && (long long)p.ranks * p.warps * 64 < tokens) p.ranks *= 2;
+  }
+  return p;
+}
+
+template <typename X, typename G, bool kLogit, bool kComp, typename L>
+cudaError_t fwd_l(const ScanArgs &a, int warps, int ranks, cudaStream_t s) {
+  const int cblocks = (a.D + L::kWide - 1) / L::kWide;
   const long long blocks = (long long)cblocks * a.N * ranks;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  const auto kernel = scan_fwd_kernel<X, G, kLogit, kComp, V>;
-  constexpr int smem = FwdSmem<X, G, kLogit, V>::kBytes;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const auto kernel = scan_fwd_kernel<X, G, kLogit, kComp, L>;
+  const size_t smem = FwdSmem<X, G, kLogit, L>::bytes(warps);
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);
-  cfg.blockDim = dim3(kScanThreads);
+  cfg.blockDim = dim3(32 * warps);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
@@ -194,24 +221,25 @@ cudaError_t fwd_v(const ScanArgs &a, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, kernel, a, cblocks);
 }
 
+template <typename X, typename G, bool kLogit, bool kComp>
+cudaError_t fwd_c(const ScanArgs &a, cudaStream_t s) {
+  if (!scan_vectors(a.D, {{a.x, sizeof(X)}, {a.g, sizeof(G)}, {a.o, sizeof(X)}, {a.states, 4}})) {
+    const long long blocks = (long long)((a.D + 31) / 32) * a.N, tokens = a.T_total / a.N;
+    int ranks = 1;
+    while (ranks < kScanMaxCluster && blocks * ranks < 152 && (long long)ranks * 128 < tokens) ranks *= 2;
+    return fwd_l<X, G, kLogit, kComp, Layout<32, 1>>(a, 8, ranks, s);
+  }
+  const Plan p = plan_fwd(a, FwdSmem<X, G, kLogit, Layout<16, 2>>::kMaxWarps);
+  return p.narrow ? fwd_l<X, G, kLogit, kComp, Layout<16, 2>>(a, p.warps, p.ranks, s)
+                  : fwd_l<X, G, kLogit, kComp, Layout<64, 2>>(a, p.warps, p.ranks, s);
+}
+
 template <typename X, typename G, bool kLogit>
 cudaError_t fwd_t(const ScanArgs &a, cudaStream_t s) {
-  const bool v = scan_vectors(a.D, {{a.x, sizeof(X)}, {a.g, sizeof(G)}, {a.o, sizeof(X)}, {a.states, 4}});
-  if (a.complement) return v ? fwd_v<X, G, kLogit, true, 2>(a, s) : fwd_v<X, G, kLogit, true, 1>(a, s);
-  return v ? fwd_v<X, G, kLogit, false, 2>(a, s) : fwd_v<X, G, kLogit, false, 1>(a, s);
+  return a.complement ? fwd_c<X, G, kLogit, true>(a, s) : fwd_c<X, G, kLogit, false>(a, s);
 }
 
 }  // namespace
-
-// A cluster grows until the grid fills the 152 SMs three times over or a round
-// covers the average sequence.
-int scan_cluster(const ScanArgs &a, int channels) {
-  const long long blocks = (long long)((a.D + channels - 1) / channels) * a.N;
-  const long long tokens = a.T_total / a.N;
-  int r = 1;
-  while (r < kScanMaxCluster && blocks * r < 3 * 152 && (long long)r * kScanSpan < tokens) r *= 2;
-  return r;
-}
 
 cudaError_t launch_scan_fwd(const ScanArgs &a, cudaStream_t s) {
   using B = __nv_bfloat16;

@@ -139,51 +139,67 @@ template <int V> __device__ __forceinline__ void store(__nv_bfloat16 *p, Vec<V> 
   else *p = __float2bfloat16_rn(v.v);
 }
 
-// ------------------------------------------------------- a warp's input tiles
-// Rows of 16 tokens of one array, V channels per lane.  Two ways in:
+// --------------------------------------------------------- layout of a warp
+// Each lane holds V channels of 16 consecutive tokens.  The lanes of a warp are
+// kGroups groups along the sequence, of kWide / V lanes that cover kWide
+// channels: 64 channels x 16 tokens where there are many chains, 16 x 64 where
+// there are few (32 x 16 in the elementwise form, V = 1).
+template <int kWide_, int V_>
+struct Layout {
+  static constexpr int kWide = kWide_, V = V_;
+  static constexpr int kLanes = kWide / V, kGroups = 32 / kLanes, kTokens = kScanTile * kGroups;
+};
+
+// The input tiles of a warp, of one array.  Two ways in:
 //  V = 2: 16-byte asynchronous copies into the warp's own shared memory, two
 //  tiles ahead, so that what is in flight costs no registers (needs 16-byte
-//  aligned arrays and rows);
+//  aligned arrays and rows).  Token j of group g lies in row 16 g + (j ^ g), so
+//  that the groups' rows of one j fall into different banks;
 //  V = 1: elementwise loads into registers, for everything else.
 // Tokens past the end, and channels past D, read as 0 (kPad: -inf).
-template <typename T, int V, bool kPad> struct Tile;
+template <typename T, typename L, bool kPad, int V = L::V> struct Tile;
 
-template <typename T, bool kPad> struct Tile<T, 2, kPad> {
-  static constexpr int kRow = 64;                           // elements
+template <typename T, typename L, bool kPad> struct Tile<T, L, kPad, 2> {
   static constexpr int kChunk = 16 / (int)sizeof(T);        // elements of a copy
-  static constexpr int kPerRow = kRow / kChunk;
-  static constexpr int kBytes = kScanTile * kRow * (int)sizeof(T);
-  T *buf;                                                   // [2][16][64]
+  static constexpr int kPerRow = L::kWide / kChunk;
+  static constexpr int kElems = L::kTokens * L::kWide;
+  static constexpr int kBytes = kElems * (int)sizeof(T);
+  T *buf;                                                   // [2][kTokens][kWide]
+  __device__ __forceinline__ static int place(int r) { return (r & ~(kScanTile - 1)) | ((r ^ r / kScanTile) & (kScanTile - 1)); }
   __device__ __forceinline__ void issue(int stage, const void *base, int D, int t, int c0, int len, int lane) {
-    T *dst = buf + stage * (kScanTile * kRow);
+    T *dst = buf + stage * kElems;
     const int row = lane / kPerRow, col = (lane % kPerRow) * kChunk;
     const bool in = c0 + col < D;
     const T *src = static_cast<const T *>(base) + ((size_t)t * D + c0 + col);
 #pragma unroll
-    for (int k = 0; k < kScanTile * kPerRow / 32; ++k) {
+    for (int k = 0; k < L::kTokens * kPerRow / 32; ++k) {
       const int r = row + k * (32 / kPerRow);
       const bool ok = in && r < len;
-      const unsigned to = (unsigned)__cvta_generic_to_shared(dst + r * kRow + col);
-      const void *from = ok ? src + (unsigned)(r * D) : static_cast<const T *>(base);
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(ok ? 16 : 0) : "memory");
+      const unsigned to = (unsigned)__cvta_generic_to_shared(dst + place(r) * L::kWide + col);
+      const void *from = ok ? src + (size_t)(unsigned)r * (unsigned)D : static_cast<const T *>(base);
+      if (L::kWide == 64)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(ok ? 16 : 0) : "memory");
+      else  // the neighbouring channels' blocks read the rest of the line at about the same time
+        asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(ok ? 16 : 0)
+                     : "memory");
     }
   }
   // after the copies have landed, before the first read
   __device__ __forceinline__ void pad(int stage, int len, int lane) {
-    if (kPad && len < kScanTile) {
-      T *dst = buf + stage * (kScanTile * kRow);
-      for (int r = max(len, 0); r < kScanTile; ++r) {
-        dst[r * kRow + 2 * lane] = (T)-INFINITY;
-        dst[r * kRow + 2 * lane + 1] = (T)-INFINITY;
-      }
+    if (kPad && len < L::kTokens) {
+      T *dst = buf + stage * kElems;
+      for (int i = max(len, 0) * L::kWide + lane; i < kElems; i += 32)
+        dst[place(i / L::kWide) * L::kWide + i % L::kWide] = (T)-INFINITY;
     }
   }
   __device__ __forceinline__ Vec<2> at(int stage, int j, int lane) const {
-    return values(reinterpret_cast<const Raw<T, 2> *>(buf + stage * (kScanTile * kRow) + j * kRow)[lane]);
+    const int g = lane / L::kLanes;
+    const T *p = buf + stage * kElems + (g * kScanTile + (j ^ g)) * L::kWide;
+    return values(reinterpret_cast<const Raw<T, 2> *>(p)[lane % L::kLanes]);
   }
 };
 
-template <typename T, bool kPad> struct Tile<T, 1, kPad> {
+template <typename T, typename L, bool kPad> struct Tile<T, L, kPad, 1> {
   static constexpr int kBytes = 0;
   Raw<T, 1> v[kScanTile];
   __device__ __forceinline__ void issue(int, const void *base, int D, int t, int c0, int len, int lane) {
@@ -270,9 +286,6 @@ __device__ __forceinline__ void store_remote(T *local, int rank, const T &v) {
                  : "memory");
 }
 
-constexpr int kScanWarps = 8;                               // warps of a CTA
-constexpr int kScanThreads = 32 * kScanWarps;
-constexpr int kScanSpan = kScanWarps * kScanTile;           // tokens of a CTA in one round
 constexpr int kScanMaxCluster = 8;
 
 // What a span of tokens does to the state, per channel of a lane: the decay
@@ -283,56 +296,89 @@ template <int V> struct __align__(8 * V) Span {
 #pragma unroll
     for (int i = 0; i < V; ++i) h[i] = decay_apply(c[i], h[i], add[i]);
   }
+  // this span after `first`
+  __device__ __forceinline__ void after(const Span &first) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      add[i] = decay_apply(c[i], first.add[i], add[i]);
+      c[i] = decay_join(c[i], first.c[i]);
+    }
+  }
+  __device__ __forceinline__ Span up(int lanes) const {
+    Span r;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      r.c[i] = __shfl_up_sync(0xffffffffu, c[i], lanes);
+      r.add[i] = __shfl_up_sync(0xffffffffu, add[i], lanes);
+    }
+    return r;
+  }
 };
 
 // Joins the tiles of one round, in the order the recurrence runs (warp 0 of
-// CTA 0 first).  Tile by tile each warp runs the state that entered the round
-// through the spans before its own.
+// CTA 0 first).  The groups of a warp join by shuffles; then each warp runs the
+// state that entered the round through the spans before its own.
 //   One CTA: the last warp leaves the state that enters the next round in
 //   `carry`, which the others read after the next round's barrier.
-//   A cluster: warp 0 joins its CTA's eight tiles into one span and stores it
-//   in every CTA; each thread keeps the round's state in registers.
-// Two buffers: a round's spans are read until the next round's barrier.
-template <int V>
+//   A cluster: warp 0 joins its CTA's warps into one span and stores it in
+//   every CTA; each thread keeps the round's state in registers.
+// Two buffers each: a round's spans are read until the next round's barrier.
+template <typename L>
 struct ScanJoin {
-  Span<V> tile[2][kScanWarps][32];
-  Span<V> cta[2][kScanMaxCluster][32];
-  float carry[2][32 * V];
-};
+  static constexpr int V = L::V;
+  Span<V> *tile, *cta;          // [2][warps][kLanes], [2][ranks][kLanes]
+  float *carry;                 // [2][kWide]
+  int warps, warp, lane, group, rank, ranks;
 
-template <int V>
-__device__ __forceinline__ void join_one(ScanJoin<V> &sh, int par, int warp, int lane, const Span<V> &mine,
-                                         float (&entry)[V]) {
-  sh.tile[par][warp][lane] = mine;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < V; ++i) entry[i] = sh.carry[par][lane * V + i];
-  for (int w = 0; w < warp; ++w) sh.tile[par][w][lane].run(entry);
-}
-
-template <int V>
-__device__ __forceinline__ void join_cluster(ScanJoin<V> &sh, int par, int warp, int lane, int rank, int ranks,
-                                             const Span<V> &mine, float (&state)[V], float (&entry)[V]) {
-  sh.tile[par][warp][lane] = mine;
-  __syncthreads();
-  if (warp == 0) {
-    Span<V> all = mine;
-#pragma unroll
-    for (int w = 1; w < kScanWarps; ++w) {
-      const Span<V> t = sh.tile[par][w][lane];
-      t.run(all.add);
-#pragma unroll
-      for (int i = 0; i < V; ++i) all.c[i] = decay_join(t.c[i], all.c[i]);
-    }
-    for (int r = 0; r < ranks; ++r) store_remote(&sh.cta[par][rank][lane], r, all);
+  static constexpr size_t bytes(int warps) {
+    return (2 * warps + 2 * kScanMaxCluster) * L::kLanes * sizeof(Span<V>) + 2 * L::kWide * sizeof(float);
   }
-  cluster_sync_all();
-  for (int r = 0; r < rank; ++r) sh.cta[par][r][lane].run(state);
+  __device__ __forceinline__ void place(char *smem) {
+    tile = reinterpret_cast<Span<V> *>(smem);
+    cta = tile + 2 * warps * L::kLanes;
+    carry = reinterpret_cast<float *>(cta + 2 * kScanMaxCluster * L::kLanes);
+  }
+
+  // `mine`: this lane's tile.  state: in, the state that enters the round (in a
+  // cluster), out, the one that leaves it; entry: the one that enters the tile.
+  __device__ __forceinline__ void join(int par, const Span<V> &mine, float (&state)[V], float (&entry)[V]) {
+    const int l = lane % L::kLanes;
+    Span<V> upto = mine, before;
+    if (L::kGroups > 1) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) entry[i] = state[i];
-  for (int r = rank; r < ranks; ++r) sh.cta[par][r][lane].run(state);
-  for (int w = 0; w < warp; ++w) sh.tile[par][w][lane].run(entry);
-}
+      for (int d = 1; d < L::kGroups; d *= 2) {
+        const Span<V> o = upto.up(d * L::kLanes);
+        if (group >= d) upto.after(o);
+      }
+      before = upto.up(L::kLanes);
+    }
+    Span<V> *tiles = tile + par * warps * L::kLanes + l;
+    if (group == L::kGroups - 1) tiles[warp * L::kLanes] = upto;
+    __syncthreads();
+    if (ranks == 1) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) entry[i] = carry[par * L::kWide + l * V + i];
+    } else {
+      Span<V> *spans = cta + par * kScanMaxCluster * L::kLanes + l;
+      if (warp == 0) {
+        Span<V> all = tiles[0];
+        for (int w = 1; w < warps; ++w) {
+          Span<V> t = tiles[w * L::kLanes];
+          t.after(all);
+          all = t;
+        }
+        for (int r = group; r < ranks; r += L::kGroups) store_remote(spans + rank * L::kLanes, r, all);
+      }
+      cluster_sync_all();
+      for (int r = 0; r < rank; ++r) spans[r * L::kLanes].run(state);
+#pragma unroll
+      for (int i = 0; i < V; ++i) entry[i] = state[i];
+      for (int r = rank; r < ranks; ++r) spans[r * L::kLanes].run(state);
+    }
+    for (int w = 0; w < warp; ++w) tiles[w * L::kLanes].run(entry);
+    if (group > 0) before.run(entry);
+  }
+};
 
 // Whether rows of D elements of every given array can be copied 16 bytes at a
 // time: (address, element size) pairs.
@@ -345,8 +391,5 @@ inline bool scan_vectors(int D, std::initializer_list<RowArray> arrays) {
     if (r.p && ((reinterpret_cast<uintptr_t>(r.p) & 15) || ((size_t)D * r.size) % 16)) return false;
   return true;
 }
-
-// CTAs of a cluster: see the rule in kda_scan.cu.
-int scan_cluster(const ScanArgs &a, int channels);
 
 }  // namespace kda

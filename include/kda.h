@@ -326,7 +326,7 @@ kda_status kda_chunk_bwd(const kda_chunk_desc *desc, const void *q, const void *
  *
  * Conventions shared by kda_scan_fwd, kda_scan_bwd and kda_scan_step
  *  - [tokens, H, d] tensors are token-major and dense, as kda_chunk_fwd's;
- *    H and d are any positive sizes with H * d < 2^27; tokens is below 2^31 - 4096.
+ *    H and d are any positive sizes with H * d < 2^27; tokens are below 2^31 - 65536.
  *  - x, out and their gradients have dtype `dtype`.  `decay` is log_alpha in
  *    `gate_dtype` when A_log is NULL, and z in `dtype` otherwise (g_min is then
  *    in [-5, 0), KDA_ERR_RANGE otherwise).
