@@ -24,48 +24,37 @@ namespace {
 template <typename X, typename G, bool kLogit, typename L>
 struct FwdSmem {
   static constexpr int kWarpBytes = 2 * (Tile<X, L, false>::kBytes + Tile<G, L, kLogit>::kBytes);
-  static constexpr size_t bytes(int warps) { return ScanJoin<L>::bytes(warps) + (size_t)warps * kWarpBytes; }
-  static constexpr int kMaxWarps = bytes(16) <= 227 * 1024 ? 16 : 8;
+  static constexpr size_t bytes(int warps, int ranks) { return ScanJoin<L>::bytes(warps, ranks) + (size_t)warps * kWarpBytes; }
+  static constexpr int kMaxWarps = bytes(16, kScanMaxCluster) <= 227 * 1024 ? 16 : 8;
 };
 
 template <typename X, typename G, bool kLogit, bool kComp, typename L>
 __global__ void __launch_bounds__(32 * FwdSmem<X, G, kLogit, L>::kMaxWarps, 1) scan_fwd_kernel(ScanArgs a, int cblocks) {
   constexpr int V = L::V;
   extern __shared__ __align__(128) char smem[];
-  ScanJoin<L> sh;
-  sh.warps = blockDim.x / 32;
-  sh.warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
-  sh.lane = threadIdx.x & 31;
-  sh.group = sh.lane / L::kLanes;
-  sh.ranks = (int)cluster_size();
-  sh.rank = (int)cluster_rank();
-  sh.place(smem);
+  ScanJoin<L> sh(smem);
   const int lane = sh.lane, ranks = sh.ranks, D = a.D;
   const int block = blockIdx.x / ranks, n = block / cblocks, c0 = (block % cblocks) * L::kWide;
   const int wide = (lane % L::kLanes) * V, c = c0 + wide;
   const bool live = c < D;  // (with V = 2, D is a multiple of 4)
-  const bool last = sh.warp == sh.warps - 1 && sh.group == L::kGroups - 1;  // these lanes hold a round's last tokens
   int bos, eos;
   scan_range(a, n, bos, eos);
   const size_t chain = (size_t)n * D + c;
   const Gate<kLogit, V> gate(a, c, live);
   float h[V], state[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    h[i] = state[i] = live && a.s0 ? a.s0[chain + i] : 0.f;
-    if (ranks == 1 && last) sh.carry[wide + i] = h[i];
-  }
+  for (int i = 0; i < V; ++i) h[i] = state[i] = live && a.s0 ? a.s0[chain + i] : 0.f;
   if (ranks > 1) cluster_sync_all();  // every CTA has started before another stores in it
 
   Tile<X, L, false> xs;
   Tile<G, L, kLogit> gs;
   if constexpr (V == 2) {
-    char *mine = smem + ScanJoin<L>::bytes(sh.warps) + sh.warp * FwdSmem<X, G, kLogit, L>::kWarpBytes;
+    char *mine = smem + ScanJoin<L>::bytes(sh.warps, ranks) + sh.warp * FwdSmem<X, G, kLogit, L>::kWarpBytes;
     xs.buf = reinterpret_cast<X *>(mine);
     gs.buf = reinterpret_cast<G *>(mine + 2 * Tile<X, L, false>::kBytes);
   }
-  const int span = sh.warps * L::kTokens, step = span * ranks;
-  int tw = bos + sh.rank * span + sh.warp * L::kTokens;  // the warp's first token
+  const int step = sh.warps * L::kTokens * ranks;
+  int tw = bos + (sh.rank * sh.warps + sh.warp) * L::kTokens;  // the warp's first token
   // a token past the end has alpha = 1 (z = -inf) and adds nothing
   auto fetch = [&](int stage, int t) {
     gs.issue(stage, a.g, D, t, c0, eos - t, lane);
@@ -77,7 +66,8 @@ __global__ void __launch_bounds__(32 * FwdSmem<X, G, kLogit, L>::kMaxWarps, 1) s
     if (V == 2) fetch(1, tw + step);
   }
   int par = 0;
-  for (int t0 = bos; t0 < eos; t0 += step, tw += step, par ^= 1) {
+  // alone, a warp stops at the sequence's end; the CTAs of a cluster run the same rounds
+  for (int t0 = ranks > 1 ? bos : tw; t0 < eos; t0 += step, tw += step, par ^= 1) {
     if (V == 2) {
       copies_wait<1>();
       __syncwarp();
@@ -106,7 +96,9 @@ __global__ void __launch_bounds__(32 * FwdSmem<X, G, kLogit, L>::kMaxWarps, 1) s
       mine.c[i] = decay_code(gate.unit * log.get(i));
       mine.add[i] = sum[kScanTile - 1].get(i);
     }
-    sh.join(par, mine, state, h);
+    const bool ends = eos - tw <= L::kTokens;  // the sequence's last tile
+    if (ranks == 1) sh.ring(par, mine, tw == bos, !ends, h);
+    else sh.cluster(par, mine, state, h);
     const int t = tw + sh.group * kScanTile, left = live ? eos - t : 0;
     const Vec<V> hv = lanes<V>([&](int i) { return h[i]; });
     if (a.states && left > 0) {
@@ -124,17 +116,16 @@ __global__ void __launch_bounds__(32 * FwdSmem<X, G, kLogit, L>::kMaxWarps, 1) s
           if (j < left) store<V>(o + (unsigned)(j * D), fma(keep[j], hv, sum[j]));
       }
     }
-    mine.run(h);
+    if (ranks == 1 && ends && a.sT && live && sh.group == L::kGroups - 1) {
+      mine.run(h);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      if (ranks > 1) h[i] = state[i];
-      else if (last) sh.carry[(par ^ 1) * L::kWide + wide + i] = h[i];
+      for (int i = 0; i < V; ++i) a.sT[chain + i] = h[i];
     }
   }
   if (V == 2) copies_wait<0>();
-  if (a.sT && live && sh.rank == 0 && last)
+  if ((ranks > 1 || bos == eos) && a.sT && live && sh.rank == 0 && sh.warp == 0 && sh.group == 0)
 #pragma unroll
-    for (int i = 0; i < V; ++i) a.sT[chain + i] = h[i];
+    for (int i = 0; i < V; ++i) a.sT[chain + i] = state[i];
 }
 
 constexpr int kStepThreads = 128;
@@ -204,7 +195,7 @@ cudaError_t fwd_l(const ScanArgs &a, int warps, int ranks, cudaStream_t s) {
   const long long blocks = (long long)cblocks * a.N * ranks;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   const auto kernel = scan_fwd_kernel<X, G, kLogit, kComp, L>;
-  const size_t smem = FwdSmem<X, G, kLogit, L>::bytes(warps);
+  const size_t smem = FwdSmem<X, G, kLogit, L>::bytes(warps, ranks);
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};

@@ -50,8 +50,9 @@ __device__ __forceinline__ float decay_code(float g) {
 
 // The code of two spans in a row, c after d.
 __device__ __forceinline__ float decay_join(float c, float d) {
-  if (is_near(c) && is_near(d)) return -fabsf(fmaf(c, d, c + d));  // (0 keeps its sign bit)
-  return (is_near(c) ? 1.f + c : c) * (is_near(d) ? 1.f + d : d);
+  const float near_both = -fabsf(fmaf(c, d, c + d));  // (0 keeps its sign bit)
+  const float alpha = (is_near(c) ? 1.f + c : c) * (is_near(d) ? 1.f + d : d);
+  return is_near(c) && is_near(d) ? near_both : alpha;
 }
 
 // alpha h + u
@@ -315,35 +316,50 @@ template <int V> struct __align__(8 * V) Span {
   }
 };
 
-// Joins the tiles of one round, in the order the recurrence runs (warp 0 of
-// CTA 0 first).  The groups of a warp join by shuffles; then each warp runs the
-// state that entered the round through the spans before its own.
-//   One CTA: the last warp leaves the state that enters the next round in
-//   `carry`, which the others read after the next round's barrier.
-//   A cluster: warp 0 joins its CTA's warps into one span and stores it in
-//   every CTA; each thread keeps the round's state in registers.
-// Two buffers each: a round's spans are read until the next round's barrier.
+__device__ __forceinline__ void barrier_sync(int id, int threads) {
+  asm volatile("barrier.cta.sync.aligned %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ void barrier_arrive(int id, int threads) {
+  asm volatile("barrier.cta.arrive.aligned %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// Brings every tile the state that enters it, in the order the recurrence runs.
+//   One CTA for a chain block: the warps take the tiles of a sequence in turn
+//   and hand the state on in a ring, each as soon as it has its own: the tile's
+//   effect is known by then, so a state waits for a few instructions per tile,
+//   and no warp waits for more than its predecessor.  Warp w waits at named
+//   barrier w, where its predecessor's arrival is the one it needs.  A
+//   predecessor never arrives a round ahead, as its own next state comes through
+//   the waiter.
+//   A cluster: its CTAs take consecutive spans of a round.  Warp 0 joins its
+//   CTA's warps into one span and stores it in every CTA; each thread keeps the
+//   round's state in registers.
+// Two buffers each: what one round reads, the round after next overwrites.
 template <typename L>
 struct ScanJoin {
   static constexpr int V = L::V;
-  Span<V> *tile, *cta;          // [2][warps][kLanes], [2][ranks][kLanes]
-  float *carry;                 // [2][kWide]
+  float *carry;                 // [2][warps][kWide]
+  Span<V> *tile, *cta;          // a cluster's: [2][warps][kLanes], [2][ranks][kLanes]
   int warps, warp, lane, group, rank, ranks;
 
-  static constexpr size_t bytes(int warps) {
-    return (2 * warps + 2 * kScanMaxCluster) * L::kLanes * sizeof(Span<V>) + 2 * L::kWide * sizeof(float);
+  static constexpr size_t bytes(int warps, int ranks) {
+    return ranks > 1 ? (2 * warps + 2 * ranks) * L::kLanes * sizeof(Span<V>) : 2 * warps * L::kWide * sizeof(float);
   }
-  __device__ __forceinline__ void place(char *smem) {
+  __device__ __forceinline__ explicit ScanJoin(char *smem) {
+    warps = blockDim.x / 32;
+    warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+    lane = threadIdx.x & 31;
+    group = lane / L::kLanes;
+    ranks = (int)cluster_size();
+    rank = (int)cluster_rank();
+    carry = reinterpret_cast<float *>(smem);
     tile = reinterpret_cast<Span<V> *>(smem);
     cta = tile + 2 * warps * L::kLanes;
-    carry = reinterpret_cast<float *>(cta + 2 * kScanMaxCluster * L::kLanes);
   }
 
-  // `mine`: this lane's tile.  state: in, the state that enters the round (in a
-  // cluster), out, the one that leaves it; entry: the one that enters the tile.
-  __device__ __forceinline__ void join(int par, const Span<V> &mine, float (&state)[V], float (&entry)[V]) {
-    const int l = lane % L::kLanes;
-    Span<V> upto = mine, before;
+  // A lane's tile -> `upto`, with the tiles before it in its warp; `before`, those alone.
+  __device__ __forceinline__ void groups(const Span<V> &mine, Span<V> &upto, Span<V> &before) const {
+    upto = mine;
     if (L::kGroups > 1) {
 #pragma unroll
       for (int d = 1; d < L::kGroups; d *= 2) {
@@ -352,31 +368,62 @@ struct ScanJoin {
       }
       before = upto.up(L::kLanes);
     }
-    Span<V> *tiles = tile + par * warps * L::kLanes + l;
+  }
+
+  // h: in, the sequence's first state (read with `first`); out, the state that
+  // enters the tile.  `more`: a tile of another warp follows.
+  __device__ __forceinline__ void ring(int par, const Span<V> &mine, bool first, bool more, float (&h)[V]) {
+    const int wide = (lane % L::kLanes) * V;
+    Span<V> upto, before;
+    groups(mine, upto, before);
+    if (!first) {
+      barrier_sync(warp, 64);
+      const float *in = carry + (par * warps + warp) * L::kWide + wide;
+#pragma unroll
+      for (int i = 0; i < V; ++i) h[i] = in[i];
+    }
+    if (more) {
+      const int next = warp + 1 < warps ? warp + 1 : 0, npar = next ? par : par ^ 1;
+      if (group == L::kGroups - 1) {
+        float out[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) out[i] = h[i];
+        upto.run(out);
+        float *to = carry + (npar * warps + next) * L::kWide + wide;
+#pragma unroll
+        for (int i = 0; i < V; ++i) to[i] = out[i];
+      }
+      __syncwarp();
+      barrier_arrive(next, 64);
+    }
+    if (group > 0) before.run(h);
+  }
+
+  // state: in, the state that enters the cluster's round, out, the one that
+  // leaves it; h: the one that enters the tile.
+  __device__ __forceinline__ void cluster(int par, const Span<V> &mine, float (&state)[V], float (&h)[V]) {
+    const int l = lane % L::kLanes;
+    Span<V> upto, before;
+    groups(mine, upto, before);
+    Span<V> *tiles = tile + par * warps * L::kLanes + l, *spans = cta + par * ranks * L::kLanes + l;
     if (group == L::kGroups - 1) tiles[warp * L::kLanes] = upto;
     __syncthreads();
-    if (ranks == 1) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) entry[i] = carry[par * L::kWide + l * V + i];
-    } else {
-      Span<V> *spans = cta + par * kScanMaxCluster * L::kLanes + l;
-      if (warp == 0) {
-        Span<V> all = tiles[0];
-        for (int w = 1; w < warps; ++w) {
-          Span<V> t = tiles[w * L::kLanes];
-          t.after(all);
-          all = t;
-        }
-        for (int r = group; r < ranks; r += L::kGroups) store_remote(spans + rank * L::kLanes, r, all);
+    if (warp == 0) {
+      Span<V> all = tiles[0];
+      for (int w = 1; w < warps; ++w) {
+        Span<V> t = tiles[w * L::kLanes];
+        t.after(all);
+        all = t;
       }
-      cluster_sync_all();
-      for (int r = 0; r < rank; ++r) spans[r * L::kLanes].run(state);
-#pragma unroll
-      for (int i = 0; i < V; ++i) entry[i] = state[i];
-      for (int r = rank; r < ranks; ++r) spans[r * L::kLanes].run(state);
+      for (int r = group; r < ranks; r += L::kGroups) store_remote(spans + rank * L::kLanes, r, all);
     }
-    for (int w = 0; w < warp; ++w) tiles[w * L::kLanes].run(entry);
-    if (group > 0) before.run(entry);
+    cluster_sync_all();
+    for (int r = 0; r < rank; ++r) spans[r * L::kLanes].run(state);
+#pragma unroll
+    for (int i = 0; i < V; ++i) h[i] = state[i];
+    for (int r = rank; r < ranks; ++r) spans[r * L::kLanes].run(state);
+    for (int w = 0; w < warp; ++w) tiles[w * L::kLanes].run(h);
+    if (group > 0) before.run(h);
   }
 };
 
