@@ -79,8 +79,8 @@ __global__ void __launch_bounds__(32 * FwdSmem<X, G, kLogit, L>::kMaxWarps, 1) s
     Vec<V> keep[kScanTile], sum[kScanTile], log = all<V>(0.f);
 #pragma unroll
     for (int j = 0; j < kScanTile; ++j) {
-      const Vec<V> l = gate.log(gs.at(par, j, lane)), al = gate.alpha(l);
-      Vec<V> u = xs.at(par, j, lane);
+      const Vec<V> l = gate.log(gs.at(par, j, sh.group, lane)), al = gate.alpha(l);
+      Vec<V> u = xs.at(par, j, sh.group, lane);
       if (kComp) u = mul(u, gate.one_minus(l, al));
       log = add(log, l);
       keep[j] = j ? mul(keep[j - 1], al) : al;
@@ -166,61 +166,17 @@ __global__ void __launch_bounds__(256) validate_scan_kernel(ScanArgs a, int *fla
   if (bad) atomicOr(flag, bad);
 }
 
-// How chains and time are laid over the GPU.
-//   Blocks of 64 channels (2 CTAs of 8 warps on an SM) when there are enough of
-//   them for the 152 SMs; else blocks of 16 channels, whose warps span four
-//   times the tokens.  When even those are at most one for an SM, CTAs of 16
-//   warps, and clusters along the sequence while the grid has room for them and
-//   the sequences are longer than a round.
-struct Plan {
-  bool narrow;
-  int warps, ranks;
-};
-
-Plan plan_fwd(const ScanArgs &a, int max_warps) {
-  const long long tokens = a.T_total / a.N;
-  const auto blocks = [&](int wide) { return (long long)((a.D + wide - 1) / wide) * a.N; };
-  Plan p{blocks(64) < 152, 8, 1};
-  const long long b = blocks(p.narrow ? 16 : 64);
-  if (p.narrow) {
-    if (b <= 152 && tokens > 512) p.warps = max_warps;
-    while (p.ranks < kScanMaxCluster && b * p.ranks * 2 <= 152 && (long long)p.ranks * p.warps * 64 < tokens) p.ranks *= 2;
-  }
-  return p;
-}
-
 template <typename X, typename G, bool kLogit, bool kComp, typename L>
 cudaError_t fwd_l(const ScanArgs &a, int warps, int ranks, cudaStream_t s) {
-  const int cblocks = (a.D + L::kWide - 1) / L::kWide;
-  const long long blocks = (long long)cblocks * a.N * ranks;
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  const auto kernel = scan_fwd_kernel<X, G, kLogit, kComp, L>;
-  const size_t smem = FwdSmem<X, G, kLogit, L>::bytes(warps, ranks);
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)blocks);
-  cfg.blockDim = dim3(32 * warps);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = ranks;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a, cblocks);
+  return launch_chains<L>(scan_fwd_kernel<X, G, kLogit, kComp, L>, a, warps, ranks,
+                          FwdSmem<X, G, kLogit, L>::bytes(warps, ranks), s, a, (a.D + L::kWide - 1) / L::kWide);
 }
 
 template <typename X, typename G, bool kLogit, bool kComp>
 cudaError_t fwd_c(const ScanArgs &a, cudaStream_t s) {
-  if (!scan_vectors(a.D, {{a.x, sizeof(X)}, {a.g, sizeof(G)}, {a.o, sizeof(X)}, {a.states, 4}})) {
-    const long long blocks = (long long)((a.D + 31) / 32) * a.N, tokens = a.T_total / a.N;
-    int ranks = 1;
-    while (ranks < kScanMaxCluster && blocks * ranks < 152 && (long long)ranks * 128 < tokens) ranks *= 2;
-    return fwd_l<X, G, kLogit, kComp, Layout<32, 1>>(a, 8, ranks, s);
-  }
-  const Plan p = plan_fwd(a, FwdSmem<X, G, kLogit, Layout<16, 2>>::kMaxWarps);
+  if (!scan_vectors(a.D, {{a.x, sizeof(X)}, {a.g, sizeof(G)}, {a.o, sizeof(X)}, {a.states, 4}}))
+    return fwd_l<X, G, kLogit, kComp, Layout<32, 1>>(a, 8, scan_ranks_elementwise(a), s);
+  const ScanPlan p = scan_plan(a, FwdSmem<X, G, kLogit, Layout<16, 2>>::kMaxWarps);
   return p.narrow ? fwd_l<X, G, kLogit, kComp, Layout<16, 2>>(a, p.warps, p.ranks, s)
                   : fwd_l<X, G, kLogit, kComp, Layout<64, 2>>(a, p.warps, p.ranks, s);
 }

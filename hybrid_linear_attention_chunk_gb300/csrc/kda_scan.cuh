@@ -193,8 +193,8 @@ template <typename T, typename L, bool kPad> struct Tile<T, L, kPad, 2> {
         dst[place(i / L::kWide) * L::kWide + i % L::kWide] = (T)-INFINITY;
     }
   }
-  __device__ __forceinline__ Vec<2> at(int stage, int j, int lane) const {
-    const int g = lane / L::kLanes;
+  // token j of group g, for a lane
+  __device__ __forceinline__ Vec<2> at(int stage, int j, int g, int lane) const {
     const T *p = buf + stage * kElems + (g * kScanTile + (j ^ g)) * L::kWide;
     return values(reinterpret_cast<const Raw<T, 2> *>(p)[lane % L::kLanes]);
   }
@@ -213,7 +213,7 @@ template <typename T, typename L, bool kPad> struct Tile<T, L, kPad, 1> {
     }
   }
   __device__ __forceinline__ void pad(int, int, int) {}
-  __device__ __forceinline__ Vec<1> at(int, int j, int) const { return values(v[j]); }
+  __device__ __forceinline__ Vec<1> at(int, int j, int, int) const { return values(v[j]); }
 };
 
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -244,6 +244,16 @@ struct Gate {
     const Vec<V> e = mul(ns, z);
     const Vec<V> d = add(all<V>(1.f), lanes<V>([&](int i) { return fast_exp2(e.get(i)); }));
     return lanes<V>([&](int i) { return fast_rcp(d.get(i)); });
+  }
+  // dg/dz: g (1 - Sigmoid) s.  1 - r below a half, 2^(ns z) r above it (where r
+  // is near 1, and the power is finite).
+  __device__ __forceinline__ Vec<V> slope(Vec<V> z, Vec<V> l) const {
+    const Vec<V> e = mul(ns, z);
+    const Vec<V> rest = lanes<V>([&](int i) {
+      const float r = l.get(i);
+      return r <= 0.5f ? 1.f - r : fast_exp2(e.get(i)) * r;
+    });
+    return mul(mul(mul(ns, all<V>(-unit / kLog2e)), l), rest);
   }
   __device__ __forceinline__ Vec<V> alpha(Vec<V> l) const {
     const Vec<V> e = mul(all<V>(rate), l);
@@ -426,6 +436,59 @@ struct ScanJoin {
     if (group > 0) before.run(h);
   }
 };
+
+// How chains and time are laid over the GPU.
+//   Blocks of 64 channels (two CTAs of 8 warps on an SM, as far as shared memory
+//   goes) when there are enough of them for the 152 SMs; else blocks of 16
+//   channels, whose warps span four times the tokens: 32768 x 4096 of one
+//   sequence took 200 us against 240 in blocks of 64 with clusters, 262144 x 128
+//   0.2 ms against 0.7.  When even those are at most one for an SM, CTAs of
+//   `most` warps, and clusters along the sequence while the grid has room for
+//   them and the sequences are longer than a round.
+struct ScanPlan {
+  bool narrow;
+  int warps, ranks;
+};
+inline ScanPlan scan_plan(const ScanArgs &a, int most) {
+  const long long tokens = a.T_total / a.N;
+  const auto blocks = [&](int wide) { return (long long)((a.D + wide - 1) / wide) * a.N; };
+  ScanPlan p{blocks(64) < 152, 8, 1};
+  if (p.narrow) {
+    const long long b = blocks(16);
+    if (b <= 152 && tokens > 512) p.warps = most;
+    while (p.ranks < kScanMaxCluster && b * p.ranks * 2 <= 152 && (long long)p.ranks * p.warps * 64 < tokens) p.ranks *= 2;
+  }
+  return p;
+}
+// The elementwise form: blocks of 32 channels, a warp's tile 16 tokens.
+inline int scan_ranks_elementwise(const ScanArgs &a) {
+  const long long blocks = (long long)((a.D + 31) / 32) * a.N, tokens = a.T_total / a.N;
+  int ranks = 1;
+  while (ranks < kScanMaxCluster && blocks * ranks < 152 && (long long)ranks * 128 < tokens) ranks *= 2;
+  return ranks;
+}
+
+// Launches one cluster of `ranks` CTAs for each chain block.
+template <typename L, typename... P>
+cudaError_t launch_chains(void (*kernel)(P...), const ScanArgs &a, int warps, int ranks, size_t smem, cudaStream_t s,
+                          P... args) {
+  const long long blocks = (long long)((a.D + L::kWide - 1) / L::kWide) * a.N * ranks;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(32 * warps);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = ranks;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
 
 // Whether rows of D elements of every given array can be copied 16 bytes at a
 // time: (address, element size) pairs.
