@@ -5,106 +5,105 @@
 // a group of kThreads threads (half a warp to 512 threads, by the width) holds
 // kChunks pieces of V elements per thread.  Sums run in fp32, per thread, then
 // by shuffles, then over the warps in order.
+#include <type_traits>
+
 #include "kda_internal.cuh"
+#include "kda_packed.cuh"
 
 namespace kda {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
-
-__device__ __forceinline__ float fast_exp2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
+// Sigmoid(g), with the power e = exp(-g) it came from.
+template <int P> __device__ __forceinline__ Vec<P> sigmoid_of(Vec<P> g, Vec<P> &e) {
+  const Vec<P> x = mul(g, all<P>(-kLog2e));
+  e = lanes<P>([&](int i) { return fast_exp2(x.get(i)); });
+  const Vec<P> d = add(e, all<P>(1.f));
+  return lanes<P>([&](int i) { return fast_rcp(d.get(i)); });
 }
-__device__ __forceinline__ float fast_rcp(float x) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
+// 1 - Sigmoid: the difference below a half, e r above it, where e is finite.
+template <int P> __device__ __forceinline__ Vec<P> sigmoid_rest(Vec<P> r, Vec<P> e) {
+  return lanes<P>([&](int i) { return r.get(i) <= 0.5f ? 1.f - r.get(i) : e.get(i) * r.get(i); });
 }
 
-// Sigmoid(g), and 1 - Sigmoid(g): the difference below a half, e r above it,
-// where the power e is finite.
-__device__ __forceinline__ float sigmoid_fast(float g, float &e) {
-  e = fast_exp2(-kLog2e * g);
-  return fast_rcp(1.f + e);
-}
-__device__ __forceinline__ float sigmoid_rest(float r, float e) { return r <= 0.5f ? 1.f - r : e * r; }
-
-// V elements as they lie in memory.
+// V elements as they lie in memory, read as V / P vectors of P.
 template <typename T, int V> struct Piece;
 template <> struct Piece<__nv_bfloat16, 8> {
   uint4 v;
-  __device__ __forceinline__ void load(const __nv_bfloat16 *p) { v = *reinterpret_cast<const uint4 *>(p); }
-  __device__ __forceinline__ float get(int i) const {
-    const unsigned w = i < 2 ? v.x : i < 4 ? v.y : i < 6 ? v.z : v.w;
-    return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
+  static constexpr int kParts = 1;                           // 16-byte parts
+  __device__ __forceinline__ void load(const void *p) { v = *static_cast<const uint4 *>(p); }
+  __device__ __forceinline__ void part(int, uint4 x) { v = x; }
+  __device__ __forceinline__ Vec<2> get(int i) const {
+    const unsigned w = i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+    return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
   }
   __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
 };
 template <> struct Piece<float, 8> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const float *p) {
-    a = *reinterpret_cast<const float4 *>(p);
-    b = *reinterpret_cast<const float4 *>(p + 4);
+  uint4 a, b;
+  static constexpr int kParts = 2;
+  __device__ __forceinline__ void load(const void *p) {
+    a = static_cast<const uint4 *>(p)[0];
+    b = static_cast<const uint4 *>(p)[1];
   }
-  __device__ __forceinline__ float get(int i) const {
-    const float4 &q = i < 4 ? a : b;
-    return (i & 3) == 0 ? q.x : (i & 3) == 1 ? q.y : (i & 3) == 2 ? q.z : q.w;
+  __device__ __forceinline__ void part(int k, uint4 x) {
+    if (k) b = x;
+    else a = x;
   }
-  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ Vec<2> get(int i) const {
+    const uint4 &q = i < 2 ? a : b;
+    return i & 1 ? pair(__uint_as_float(q.z), __uint_as_float(q.w)) : pair(__uint_as_float(q.x), __uint_as_float(q.y));
+  }
+  __device__ __forceinline__ void zero() { a = b = make_uint4(0, 0, 0, 0); }
 };
 template <> struct Piece<__nv_bfloat16, 1> {
   __nv_bfloat16 v;
-  __device__ __forceinline__ void load(const __nv_bfloat16 *p) { v = *p; }
-  __device__ __forceinline__ float get(int) const { return __bfloat162float(v); }
+  __device__ __forceinline__ void load(const void *p) { v = *static_cast<const __nv_bfloat16 *>(p); }
+  __device__ __forceinline__ Vec<1> get(int) const { return Vec<1>{__bfloat162float(v)}; }
   __device__ __forceinline__ void zero() { v = __float2bfloat16_rn(0.f); }
 };
 template <> struct Piece<float, 1> {
   float v;
-  __device__ __forceinline__ void load(const float *p) { v = *p; }
-  __device__ __forceinline__ float get(int) const { return v; }
+  __device__ __forceinline__ void load(const void *p) { v = *static_cast<const float *>(p); }
+  __device__ __forceinline__ Vec<1> get(int) const { return Vec<1>{v}; }
   __device__ __forceinline__ void zero() { v = 0.f; }
 };
 
-template <int V> __device__ __forceinline__ void put(float *p, const float (&f)[V]) {
-  if constexpr (V == 8) {
-    reinterpret_cast<float4 *>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-    reinterpret_cast<float4 *>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
-  } else {
-    *p = f[0];
-  }
+__device__ __forceinline__ void put(float *p, const Vec<1> (&f)[1]) { *p = f[0].v; }
+__device__ __forceinline__ void put(__nv_bfloat16 *p, const Vec<1> (&f)[1]) { *p = __float2bfloat16_rn(f[0].v); }
+__device__ __forceinline__ void put(float *p, const Vec<2> (&f)[4]) {
+  reinterpret_cast<float4 *>(p)[0] = make_float4(f[0].get(0), f[0].get(1), f[1].get(0), f[1].get(1));
+  reinterpret_cast<float4 *>(p)[1] = make_float4(f[2].get(0), f[2].get(1), f[3].get(0), f[3].get(1));
 }
-template <int V> __device__ __forceinline__ void put(__nv_bfloat16 *p, const float (&f)[V]) {
-  if constexpr (V == 8) {
-    __nv_bfloat162 h[4];
+__device__ __forceinline__ void put(__nv_bfloat16 *p, const Vec<2> (&f)[4]) {
+  __nv_bfloat162 h[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-    *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<uint4 *>(h);
-  } else {
-    *p = __float2bfloat16_rn(f[0]);
-  }
+  for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(f[i].get(0), f[i].get(1));
+  *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<uint4 *>(h);
 }
 // A weight row's piece; ones when it is absent.
-template <int V> __device__ __forceinline__ void weight(const float *w, int j, float (&f)[V]) {
+__device__ __forceinline__ void weight(const float *w, int j, Vec<1> (&f)[1]) { f[0].v = w ? __ldg(w + j) : 1.f; }
+__device__ __forceinline__ void weight(const float *w, int j, Vec<2> (&f)[4]) {
   if (!w) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) f[i] = 1.f;
-  } else if constexpr (V == 8) {
-    const float4 a = __ldg(reinterpret_cast<const float4 *>(w + j)), b = __ldg(reinterpret_cast<const float4 *>(w + j) + 1);
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    for (int i = 0; i < 4; ++i) f[i] = all<2>(1.f);
   } else {
-    f[0] = __ldg(w + j);
+    const float4 a = __ldg(reinterpret_cast<const float4 *>(w + j)), b = __ldg(reinterpret_cast<const float4 *>(w + j) + 1);
+    f[0] = pair(a.x, a.y);
+    f[1] = pair(a.z, a.w);
+    f[2] = pair(b.x, b.y);
+    f[3] = pair(b.z, b.w);
   }
 }
+__device__ __forceinline__ float total(Vec<1> v) { return v.v; }
+__device__ __forceinline__ float total(Vec<2> v) { return v.get(0) + v.get(1); }
 
 template <typename T_, typename R_, int V_, int kChunks_, int kThreads_>
 struct Shape {
   using T = T_;                                              // y, gate, normed
   using R = R_;                                              // residual, out
   static constexpr int V = V_, kChunks = kChunks_, kThreads = kThreads_;
-  static constexpr int kBlock = kThreads > 32 ? kThreads : 256, kGroups = kBlock / kThreads;
+  static constexpr int P = V == 8 ? 2 : 1, kVecs = V / P;    // values of one instruction
+  static constexpr int kBlock = kThreads > 256 ? kThreads : 256, kGroups = kBlock / kThreads;
   static constexpr int kMaxWidth = V * kChunks * kThreads;
 };
 
@@ -121,11 +120,12 @@ __device__ __forceinline__ void row_sum(float (&v)[kN], float (*sh)[16]) {
 #pragma unroll
       for (int k = 0; k < kN; ++k) sh[k][threadIdx.x >> 5] = v[k];
     __syncthreads();
+    const int first = threadIdx.x / kThreads * (kThreads / 32);
 #pragma unroll
     for (int k = 0; k < kN; ++k) {
       v[k] = 0.f;
 #pragma unroll
-      for (int i = 0; i < kThreads / 32; ++i) v[k] += sh[k][i];
+      for (int i = 0; i < kThreads / 32; ++i) v[k] += sh[k][first + i];
     }
   }
 }
@@ -134,7 +134,7 @@ template <typename S>
 __global__ void __launch_bounds__(S::kBlock) norm_fwd_kernel(NormArgs a) {
   using T = typename S::T;
   using R = typename S::R;
-  constexpr int V = S::V, C = S::kChunks;
+  constexpr int V = S::V, C = S::kChunks, P = S::P;
   __shared__ float sh[2][1][16];
   const long long row = (long long)blockIdx.x * S::kGroups + threadIdx.x / S::kThreads;
   const bool valid = row < a.rows;  // (a whole warp stays for the shuffles)
@@ -154,55 +154,50 @@ __global__ void __launch_bounds__(S::kBlock) norm_fwd_kernel(NormArgs a) {
   const float inv = 1.f / (float)a.width;
   float r1 = 1.f;
   if (a.post) {
-    float ss[1] = {0.f};
+    Vec<P> s = all<P>(0.f);
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
-      for (int i = 0; i < V; ++i) ss[0] = fmaf(y[c].get(i), y[c].get(i), ss[0]);
+      for (int i = 0; i < S::kVecs; ++i) s = fma(y[c].get(i), y[c].get(i), s);
+    float ss[1] = {total(s)};
     row_sum<S::kThreads, 1>(ss, sh[0]);
     r1 = rsqrtf(ss[0] * inv + a.e1);
   }
-  float o[C][V], so[1] = {0.f};
+  Vec<P> o[C][S::kVecs], sum = all<P>(0.f);
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int j = (c * S::kThreads + t) * V;
-    const bool in = j < a.width;
-    float w[V], s[V];
-    if (in) {
-      weight<V>(a.w1, j, w);
-      weight<V>(a.sc, j, s);
-    }
+    if (j >= a.width) continue;
+    Vec<P> w[S::kVecs], sc[S::kVecs];
+    weight(a.w1, j, w);
+    weight(a.sc, j, sc);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      float b = 0.f;
-      if (in) {
-        b = y[c].get(i) * r1 * w[i];
-        float e;
-        if (a.gate) b *= sigmoid_fast(g[c].get(i), e);
-        b = a.res ? fmaf(b, s[i], r[c].get(i)) : b * s[i];
-      }
-      o[c][i] = b;
-      so[0] = fmaf(b, b, so[0]);
+    for (int i = 0; i < S::kVecs; ++i) {
+      Vec<P> b = mul(mul(y[c].get(i), all<P>(r1)), w[i]), e;
+      if (a.gate) b = mul(b, sigmoid_of(g[c].get(i), e));
+      o[c][i] = a.res ? fma(b, sc[i], r[c].get(i)) : mul(b, sc[i]);
+      sum = fma(o[c][i], o[c][i], sum);
     }
-    if (in && valid && a.out) put<V>(static_cast<R *>(a.out) + base + j, o[c]);
+    if (valid && a.out) put(static_cast<R *>(a.out) + base + j, o[c]);
   }
   if (!a.normed) return;
+  float so[1] = {total(sum)};
   row_sum<S::kThreads, 1>(so, sh[1]);
   const float r2 = rsqrtf(so[0] * inv + a.e2);
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int j = (c * S::kThreads + t) * V;
     if (j < a.width && valid) {
-      float w[V];
-      weight<V>(a.w2, j, w);
+      Vec<P> w[S::kVecs];
+      weight(a.w2, j, w);
 #pragma unroll
-      for (int i = 0; i < V; ++i) w[i] *= o[c][i] * r2;
-      put<V>(static_cast<T *>(a.normed) + base + j, w);
+      for (int i = 0; i < S::kVecs; ++i) w[i] = mul(mul(o[c][i], all<P>(r2)), w[i]);
+      put(static_cast<T *>(a.normed) + base + j, w);
     }
   }
 }
 
-constexpr int kBwdBlocks = 304;  // at most; a block leaves one set of weight-gradient partials
+constexpr int kBwdBlocks = 304;  // at most (two to an SM); a block leaves one set of weight-gradient partials
 
 // Backward.  With tr = scale o b the branch's part of out, everything that the
 // row's gradients need of the row as a whole are sums that are known as soon as
@@ -211,140 +206,216 @@ constexpr int kBwdBlocks = 304;  // at most; a block leaves one set of weight-gr
 // since sum dy yh = sum D tr = sum (d_out + r2 q - back out) tr.  So a row takes
 // two sums over its threads, not three.  Blocks walk over rows; a thread owns
 // fixed channels, so its sums of the weight gradients stay in registers.
-template <typename S>
-__global__ void __launch_bounds__(S::kBlock) norm_bwd_kernel(NormArgs a, NormBwdIo io, float *part) {
+//
+// In pieces of 8 elements the rows come in by asynchronous copies, up to two
+// rows ahead as far as shared memory goes, each thread into places of its own that no other thread reads.
+template <typename S> struct RowStages {
   using T = typename S::T;
   using R = typename S::R;
-  constexpr int V = S::V, C = S::kChunks;
+  static constexpr int parts() {
+    if constexpr (S::V == 8) return 3 * Piece<T, 8>::kParts + 2 * Piece<R, 8>::kParts;
+    else return 0;
+  }
+  static constexpr int kStage = parts() * S::kChunks * S::kBlock * 16;  // bytes
+  static constexpr int kLimit = S::kBlock > 256 ? 227 * 1024 : 113 * 1024;
+  static constexpr int kStages = 3 * kStage <= kLimit ? 3 : 2 * kStage <= kLimit ? 2 : 1;
+  static constexpr int kSums = S::kGroups > 1 ? (int)sizeof(float) * S::kGroups * S::kMaxWidth : 0;
+  static constexpr int kBytes = kStages * kStage > kSums ? kStages * kStage : kSums;
+};
+
+template <typename S>
+__global__ void __launch_bounds__(S::kBlock, S::kBlock > 256 ? 1 : 2) norm_bwd_kernel(NormArgs a, NormBwdIo io, float *part) {
+  using T = typename S::T;
+  using R = typename S::R;
+  using St = RowStages<S>;
+  constexpr int V = S::V, C = S::kChunks, P = S::P, N = S::kVecs;
+  extern __shared__ __align__(16) uint4 stage_mem[];
   __shared__ float sh1[2][1][16], sh2[2][5][16];
   const int t = threadIdx.x % S::kThreads, group = threadIdx.x / S::kThreads;
   const float inv = 1.f / (float)a.width;
-  float p1[C][V], ps[C][V], p2[C][V];
+  Vec<P> p1[C][N], ps[C][N], p2[C][N];
 #pragma unroll
   for (int c = 0; c < C; ++c)
 #pragma unroll
-    for (int i = 0; i < V; ++i) p1[c][i] = ps[c][i] = p2[c][i] = 0.f;
-  int par = 0;
-  for (long long r0 = (long long)blockIdx.x * S::kGroups; r0 < a.rows; r0 += (long long)gridDim.x * S::kGroups, par ^= 1) {
-    const bool valid = r0 + group < a.rows;
-    const size_t base = (size_t)(valid ? r0 + group : 0) * a.width;
-    Piece<T, V> y[C], g[C], dn[C];
-    Piece<R, V> res[C], dout[C];
+    for (int i = 0; i < N; ++i) p1[c][i] = ps[c][i] = p2[c][i] = all<P>(0.f);
+  const long long step = (long long)gridDim.x * S::kGroups;
+  const long long first = (long long)blockIdx.x * S::kGroups + group;
+
+  Piece<T, V> y[C], g[C], dn[C];
+  Piece<R, V> res[C], dout[C];
+  const void *const src[5] = {a.y, a.gate, io.dn, a.res, io.dout};
+  // `row` into stage `k`, as zeros past the last row and for absent tensors
+  auto fetch = [&](long long row, int k) {
+    if constexpr (V == 8) {
+      uint4 *to = stage_mem + (size_t)k * (St::kStage / 16) + threadIdx.x;
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int j = (c * S::kThreads + t) * V;
-      const bool in = j < a.width && valid;
-      y[c].zero();
-      g[c].zero();
-      dn[c].zero();
-      res[c].zero();
-      dout[c].zero();
-      if (in) {
-        y[c].load(static_cast<const T *>(a.y) + base + j);
-        if (a.gate) g[c].load(static_cast<const T *>(a.gate) + base + j);
-        if (a.res) res[c].load(static_cast<const R *>(a.res) + base + j);
-        if (io.dout) dout[c].load(static_cast<const R *>(io.dout) + base + j);
-        if (io.dn) dn[c].load(static_cast<const T *>(io.dn) + base + j);
+      for (int c = 0; c < C; ++c) {
+        const int j = (c * S::kThreads + t) * V;
+        const bool in = j < a.width && row < a.rows;
+#pragma unroll
+        for (int m = 0; m < 5; ++m) {
+          constexpr int kT = (int)sizeof(T), kR = (int)sizeof(R);
+          const int size = m < 3 ? kT : kR;
+          const bool ok = in && src[m];
+          const char *from = ok ? static_cast<const char *>(src[m]) + ((size_t)row * a.width + j) * size
+                                : static_cast<const char *>(a.y);
+#pragma unroll
+          for (int h = 0; h < (m < 3 ? kT : kR) / 2; ++h, to += S::kBlock)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((unsigned)__cvta_generic_to_shared(to)),
+                         "l"(from + 16 * h), "r"(ok ? 16 : 0)
+                         : "memory");
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+  };
+  auto take = [&](long long row, int k) {
+    if constexpr (V == 8) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(St::kStages - 1) : "memory");
+      const uint4 *from = stage_mem + (size_t)k * (St::kStage / 16) + threadIdx.x;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        auto read = [&](auto &piece) {
+#pragma unroll
+          for (int h = 0; h < std::remove_reference_t<decltype(piece)>::kParts; ++h, from += S::kBlock) piece.part(h, *from);
+        };
+        read(y[c]);
+        read(g[c]);
+        read(dn[c]);
+        read(res[c]);
+        read(dout[c]);
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const int j = c * S::kThreads + t;
+        const size_t at = (size_t)row * a.width + j;
+        const bool in = j < a.width && row < a.rows;
+        y[c].zero();
+        g[c].zero();
+        dn[c].zero();
+        res[c].zero();
+        dout[c].zero();
+        if (in) {
+          y[c].load(static_cast<const T *>(a.y) + at);
+          if (a.gate) g[c].load(static_cast<const T *>(a.gate) + at);
+          if (io.dn) dn[c].load(static_cast<const T *>(io.dn) + at);
+          if (a.res) res[c].load(static_cast<const R *>(a.res) + at);
+          if (io.dout) dout[c].load(static_cast<const R *>(io.dout) + at);
+        }
       }
     }
+  };
+#pragma unroll
+  for (int k = 0; k < St::kStages - 1; ++k) fetch(first + k * step, k);
+  int par = 0, stage = 0;
+  // the groups of a block run the same number of rows
+  for (long long r0 = (long long)blockIdx.x * S::kGroups; r0 < a.rows; r0 += step, par ^= 1) {
+    const long long row = r0 + group;
+    const bool valid = row < a.rows;
+    {
+      int k = stage + St::kStages - 1;
+      fetch(row + (St::kStages - 1) * step, k >= St::kStages ? k - St::kStages : k);
+    }
+    take(row, stage);
+    stage = stage + 1 < St::kStages ? stage + 1 : 0;
     float r1 = 1.f;
     if (a.post) {
-      float ss[1] = {0.f};
+      Vec<P> s = all<P>(0.f);
 #pragma unroll
       for (int c = 0; c < C; ++c)
 #pragma unroll
-        for (int i = 0; i < V; ++i) ss[0] = fmaf(y[c].get(i), y[c].get(i), ss[0]);
+        for (int i = 0; i < N; ++i) s = fma(y[c].get(i), y[c].get(i), s);
+      float ss[1] = {total(s)};
       row_sum<S::kThreads, 1>(ss, sh1[par]);
       r1 = rsqrtf(ss[0] * inv + a.e1);
     }
-    float sums[5] = {0.f, 0.f, 0.f, 0.f, 0.f};
+    Vec<P> v[5];
+#pragma unroll
+    for (int k = 0; k < 5; ++k) v[k] = all<P>(0.f);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int j = (c * S::kThreads + t) * V;
       if (j >= a.width) continue;
-      float w1[V], sc[V], w2[V];
-      weight<V>(a.w1, j, w1);
-      weight<V>(a.sc, j, sc);
-      weight<V>(a.w2, j, w2);
+      Vec<P> w1[N], sc[N], w2[N];
+      weight(a.w1, j, w1);
+      weight(a.sc, j, sc);
+      weight(a.w2, j, w2);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        float tr = y[c].get(i) * r1 * w1[i], e;
-        if (a.gate) tr *= sigmoid_fast(g[c].get(i), e);
-        tr *= sc[i];
-        const float o = a.res ? tr + res[c].get(i) : tr;
-        const float q = dn[c].get(i) * w2[i];
-        sums[0] = fmaf(o, o, sums[0]);
-        sums[1] = fmaf(q, o, sums[1]);
-        sums[2] = fmaf(dout[c].get(i), tr, sums[2]);
-        sums[3] = fmaf(q, tr, sums[3]);
-        sums[4] = fmaf(o, tr, sums[4]);
+      for (int i = 0; i < N; ++i) {
+        Vec<P> tr = mul(mul(y[c].get(i), all<P>(r1)), mul(w1[i], sc[i])), e;
+        if (a.gate) tr = mul(tr, sigmoid_of(g[c].get(i), e));
+        const Vec<P> o = add(tr, res[c].get(i)), q = mul(dn[c].get(i), w2[i]);
+        v[0] = fma(o, o, v[0]);
+        v[1] = fma(q, o, v[1]);
+        v[2] = fma(dout[c].get(i), tr, v[2]);
+        v[3] = fma(q, tr, v[3]);
+        v[4] = fma(o, tr, v[4]);
       }
     }
+    float sums[5];
+#pragma unroll
+    for (int k = 0; k < 5; ++k) sums[k] = total(v[k]);
     row_sum<S::kThreads, 5>(sums, sh2[par]);
     const float r2 = io.dn ? rsqrtf(sums[0] * inv + a.e2) : 0.f;
     const float back = r2 * r2 * r2 * sums[1] * inv;
-    const float m = (sums[2] + r2 * sums[3] - back * sums[4]) * inv;
+    const float m = a.post ? (sums[2] + r2 * sums[3] - back * sums[4]) * inv : 0.f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int j = (c * S::kThreads + t) * V;
       if (j >= a.width || !valid) continue;
-      float w1[V], sc[V], w2[V], dres[V], dgate[V], dy[V];
-      weight<V>(a.w1, j, w1);
-      weight<V>(a.sc, j, sc);
-      weight<V>(a.w2, j, w2);
+      Vec<P> w1[N], sc[N], w2[N], dres[N], dgate[N], dy[N];
+      weight(a.w1, j, w1);
+      weight(a.sc, j, sc);
+      weight(a.w2, j, w2);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float yh = y[c].get(i) * r1;
-        float sg = 1.f, rest = 0.f;
+      for (int i = 0; i < N; ++i) {
+        const Vec<P> yh = mul(y[c].get(i), all<P>(r1));
+        Vec<P> sg = all<P>(1.f), rest = all<P>(0.f);
         if (a.gate) {
-          float e;
-          sg = sigmoid_fast(g[c].get(i), e);
+          Vec<P> e;
+          sg = sigmoid_of(g[c].get(i), e);
           rest = sigmoid_rest(sg, e);
         }
-        const float b = yh * w1[i] * sg;
-        const float o = a.res ? fmaf(b, sc[i], res[c].get(i)) : b * sc[i];
-        const float n = dn[c].get(i);
-        const float D = fmaf(r2 * w2[i], n, fmaf(-back, o, dout[c].get(i)));
-        p2[c][i] = fmaf(n * r2, o, p2[c][i]);
-        ps[c][i] = fmaf(D, b, ps[c][i]);
-        const float db = D * sc[i], du = db * sg;
-        p1[c][i] = fmaf(du, yh, p1[c][i]);
+        const Vec<P> b = mul(mul(yh, w1[i]), sg), o = fma(b, sc[i], res[c].get(i));
+        const Vec<P> n = mul(dn[c].get(i), all<P>(r2));
+        const Vec<P> D = fma(n, w2[i], fma(o, all<P>(-back), dout[c].get(i)));
+        p2[c][i] = fma(n, o, p2[c][i]);
+        ps[c][i] = fma(D, b, ps[c][i]);
+        const Vec<P> db = mul(D, sc[i]), du = mul(db, sg);
+        p1[c][i] = fma(du, yh, p1[c][i]);
         dres[i] = D;
-        dgate[i] = db * b * rest;
-        dy[i] = a.post ? r1 * fmaf(du, w1[i], -yh * m) : du;
+        dgate[i] = mul(mul(db, b), rest);
+        dy[i] = a.post ? mul(fma(du, w1[i], mul(yh, all<P>(-m))), all<P>(r1)) : du;
       }
-      put<V>(static_cast<T *>(io.dy) + base + j, dy);
-      if (io.dgate) put<V>(static_cast<T *>(io.dgate) + base + j, dgate);
-      if (io.dres) put<V>(static_cast<R *>(io.dres) + base + j, dres);
+      const size_t at = (size_t)row * a.width + j;
+      put(static_cast<T *>(io.dy) + at, dy);
+      if (io.dgate) put(static_cast<T *>(io.dgate) + at, dgate);
+      if (io.dres) put(static_cast<R *>(io.dres) + at, dres);
     }
   }
+  if constexpr (V == 8) asm volatile("cp.async.wait_group 0;" ::: "memory");
   if (!part) return;
   // the groups of a block in order, then one row of partials
-  extern __shared__ float sums[];  // [kGroups][kMaxWidth]
+  float *sums = reinterpret_cast<float *>(stage_mem);  // [kGroups][kMaxWidth]
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
     float *to = part + ((size_t)k * gridDim.x + blockIdx.x) * a.width;
+    if constexpr (S::kGroups > 1) __syncthreads();
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int j = (c * S::kThreads + t) * V;
+      const Vec<P>(&p)[N] = k == 0 ? p1[c] : k == 1 ? ps[c] : p2[c];
+      if constexpr (S::kGroups > 1) put(sums + group * S::kMaxWidth + j, p);
+      else if (j < a.width) put(to + j, p);
+    }
     if constexpr (S::kGroups > 1) {
-      __syncthreads();
-#pragma unroll
-      for (int c = 0; c < C; ++c)
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          sums[group * S::kMaxWidth + (c * S::kThreads + t) * V + i] = k == 0 ? p1[c][i] : k == 1 ? ps[c][i] : p2[c][i];
       __syncthreads();
       for (int j = threadIdx.x; j < a.width; j += S::kBlock) {
         float s = 0.f;
 #pragma unroll
         for (int q = 0; q < S::kGroups; ++q) s += sums[q * S::kMaxWidth + j];
         to[j] = s;
-      }
-    } else {
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const int j = (c * S::kThreads + t) * V;
-        if (j < a.width)
-#pragma unroll
-          for (int i = 0; i < V; ++i) to[j + i] = k == 0 ? p1[c][i] : k == 1 ? ps[c][i] : p2[c][i];
       }
     }
   }
@@ -377,27 +448,30 @@ template <typename S> cudaError_t fwd(const NormArgs &a, cudaStream_t s) {
 
 template <typename S> cudaError_t bwd(const NormArgs &a, const NormBwdIo &io, float *ws, cudaStream_t s) {
   const bool weights = io.dw1 || io.dsc || io.dw2;
-  const long long groups = (a.rows + S::kGroups - 1) / S::kGroups;
-  const int blocks = (int)(groups < 1 ? 1 : groups < kBwdBlocks ? groups : kBwdBlocks);
-  const size_t smem = S::kGroups > 1 ? sizeof(float) * S::kGroups * S::kMaxWidth : 0;
+  const long long groups = (a.rows + S::kGroups - 1) / S::kGroups, most = S::kBlock > 256 ? kBwdBlocks / 2 : kBwdBlocks;
+  const int blocks = (int)(groups < 1 ? 1 : groups < most ? groups : most);
+  constexpr int smem = RowStages<S>::kBytes;
+  cudaError_t e = cudaFuncSetAttribute(norm_bwd_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
   norm_bwd_kernel<S><<<blocks, S::kBlock, smem, s>>>(a, io, weights ? ws : nullptr);
-  cudaError_t e = cudaGetLastError();
+  e = cudaGetLastError();
   if (e != cudaSuccess || !weights) return e;
   norm_weights_kernel<<<dim3((a.width + 31) / 32, 3), 512, 0, s>>>(ws, blocks, a.width, io);
   return cudaGetLastError();
 }
 
 // Calls f with the row shape for this width: pieces of 8 elements when every
-// row of every tensor starts on 16 bytes, else single elements.
-template <typename T, typename R, typename F>
+// row of every tensor starts on 16 bytes, else single elements.  kBwd: one piece
+// per thread as far as threads go, for the registers of the three weight sums.
+template <typename T, typename R, bool kBwd, typename F>
 cudaError_t with_shape(int width, bool vectors, F f) {
   if (vectors) {
     if (width <= 128) return f(Shape<T, R, 8, 1, 16>());
     if (width <= 256) return f(Shape<T, R, 8, 1, 32>());
-    if (width <= 512) return f(Shape<T, R, 8, 2, 32>());
+    if (width <= 512) return f(Shape<T, R, 8, kBwd ? 1 : 2, kBwd ? 64 : 32>());
     if (width <= 1024) return f(Shape<T, R, 8, 1, 128>());
     if (width <= 2048) return f(Shape<T, R, 8, 1, 256>());
-    if (width <= 4096) return f(Shape<T, R, 8, 2, 256>());
+    if (width <= 4096) return f(Shape<T, R, 8, kBwd ? 1 : 2, kBwd ? 512 : 256>());
     return f(Shape<T, R, 8, 2, 512>());
   }
   if (width <= 128) return f(Shape<T, R, 1, 4, 32>());
@@ -405,11 +479,11 @@ cudaError_t with_shape(int width, bool vectors, F f) {
   return f(Shape<T, R, 1, 16, 512>());
 }
 
-template <typename F> cudaError_t with_types(const NormArgs &a, bool vectors, F f) {
+template <bool kBwd, typename F> cudaError_t with_types(const NormArgs &a, bool vectors, F f) {
   using B = __nv_bfloat16;
   if (a.t == KDA_BF16)
-    return a.rt == KDA_BF16 ? with_shape<B, B>(a.width, vectors, f) : with_shape<B, float>(a.width, vectors, f);
-  return a.rt == KDA_BF16 ? with_shape<float, B>(a.width, vectors, f) : with_shape<float, float>(a.width, vectors, f);
+    return a.rt == KDA_BF16 ? with_shape<B, B, kBwd>(a.width, vectors, f) : with_shape<B, float, kBwd>(a.width, vectors, f);
+  return a.rt == KDA_BF16 ? with_shape<float, B, kBwd>(a.width, vectors, f) : with_shape<float, float, kBwd>(a.width, vectors, f);
 }
 
 template <int kN> bool on_16_bytes(const NormArgs &a, const void *const (&p)[kN]) {
@@ -425,13 +499,13 @@ size_t norm_bwd_workspace_bytes(int width) { return (size_t)3 * kBwdBlocks * wid
 cudaError_t launch_norm_fwd(const NormArgs &a, cudaStream_t s) {
   if (a.rows == 0) return cudaSuccess;
   const void *const p[] = {a.y, a.res, a.gate, a.w1, a.sc, a.w2, a.out, a.normed};
-  return with_types(a, on_16_bytes(a, p), [&](auto shape) { return fwd<decltype(shape)>(a, s); });
+  return with_types<false>(a, on_16_bytes(a, p), [&](auto shape) { return fwd<decltype(shape)>(a, s); });
 }
 
 cudaError_t launch_norm_bwd(const NormArgs &a, const NormBwdIo &io, void *ws, cudaStream_t s) {
   const void *const p[] = {a.y, a.res, a.gate, a.w1, a.sc, a.w2, io.dout, io.dn, io.dy, io.dres, io.dgate};
-  return with_types(a, on_16_bytes(a, p),
-                    [&](auto shape) { return bwd<decltype(shape)>(a, io, static_cast<float *>(ws), s); });
+  return with_types<true>(a, on_16_bytes(a, p),
+                          [&](auto shape) { return bwd<decltype(shape)>(a, io, static_cast<float *>(ws), s); });
 }
 
 }  // namespace kda
