@@ -97,103 +97,138 @@ __device__ __forceinline__ void weight(const float *w, int j, Vec<2> (&f)[4]) {
 __device__ __forceinline__ float total(Vec<1> v) { return v.v; }
 __device__ __forceinline__ float total(Vec<2> v) { return v.get(0) + v.get(1); }
 
-template <typename T_, typename R_, int V_, int kChunks_, int kThreads_>
+template <typename T_, typename R_, int V_, int kChunks_, int kThreads_, int kRows_ = 1>
 struct Shape {
   using T = T_;                                              // y, gate, normed
   using R = R_;                                              // residual, out
-  static constexpr int V = V_, kChunks = kChunks_, kThreads = kThreads_;
+  static constexpr int V = V_, kChunks = kChunks_, kThreads = kThreads_, kRows = kRows_;
   static constexpr int P = V == 8 ? 2 : 1, kVecs = V / P;    // values of one instruction
   static constexpr int kBlock = kThreads > 256 ? kThreads : 256, kGroups = kBlock / kThreads;
   static constexpr int kMaxWidth = V * kChunks * kThreads;
 };
 
-// Sums of kN values over the threads of a row, the same in each of them.
-// `sh`: kN x 16 floats, not in use by an earlier sum of the same place.
+// Sums of kN (at most 8) values over the threads of a row, the same in each of
+// them.  `sh`: a row of 8 for each warp of the block, not in use by an earlier sum.
+// Behind the warps' own sums each warp adds up the row's warps again: lane l takes
+// value l % 8 of every fourth warp from l / 8, two steps join these, and the
+// lanes 0 .. kN - 1 hand the values out (an eighth of the instructions of every
+// thread reading every warp's values).
 template <int kThreads, int kN>
-__device__ __forceinline__ void row_sum(float (&v)[kN], float (*sh)[16]) {
+__device__ __forceinline__ void row_sum(float (&v)[kN], float (*sh)[8]) {
 #pragma unroll
   for (int k = 0; k < kN; ++k)
 #pragma unroll
     for (int off = (kThreads < 32 ? kThreads : 32) / 2; off > 0; off >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], off);
   if constexpr (kThreads > 32) {
-    if ((threadIdx.x & 31) == 0)
+    constexpr int kWarps = kThreads / 32;
+    const int lane = threadIdx.x & 31;
+    if (lane == 0)
 #pragma unroll
-      for (int k = 0; k < kN; ++k) sh[k][threadIdx.x >> 5] = v[k];
+      for (int k = 0; k < kN; ++k) sh[threadIdx.x >> 5][k] = v[k];
     __syncthreads();
-    const int first = threadIdx.x / kThreads * (kThreads / 32);
+    const int first = threadIdx.x / kThreads * kWarps;
+    float s = 0.f;
 #pragma unroll
-    for (int k = 0; k < kN; ++k) {
-      v[k] = 0.f;
+    for (int i = 0; i < kWarps; i += 4)
+      if (i + lane / 8 < kWarps && lane % 8 < kN) s += sh[first + i + lane / 8][lane % 8];
+    s += __shfl_xor_sync(0xffffffffu, s, 8);
+    s += __shfl_xor_sync(0xffffffffu, s, 16);
 #pragma unroll
-      for (int i = 0; i < kThreads / 32; ++i) v[k] += sh[k][first + i];
-    }
+    for (int k = 0; k < kN; ++k) v[k] = __shfl_sync(0xffffffffu, s, k);
   }
 }
 
+// Forward.  A group takes kRows rows at once where a row is only a piece or two
+// per thread, so that weights and addresses are spread over several rows.
 template <typename S>
 __global__ void __launch_bounds__(S::kBlock) norm_fwd_kernel(NormArgs a) {
   using T = typename S::T;
   using R = typename S::R;
-  constexpr int V = S::V, C = S::kChunks, P = S::P;
-  __shared__ float sh[2][1][16];
-  const long long row = (long long)blockIdx.x * S::kGroups + threadIdx.x / S::kThreads;
-  const bool valid = row < a.rows;  // (a whole warp stays for the shuffles)
+  constexpr int V = S::V, C = S::kChunks, P = S::P, N = S::kVecs, K = S::kRows;
+  __shared__ float sh[2][16][8];
   const int t = threadIdx.x % S::kThreads;
-  const size_t base = (size_t)(valid ? row : 0) * a.width;
-  Piece<T, V> y[C], g[C];
-  Piece<R, V> r[C];
+  const long long row = ((long long)blockIdx.x * S::kGroups + threadIdx.x / S::kThreads) * K;
+  const size_t base = (size_t)row * a.width;
+  const int rows = (int)max(min((long long)K, a.rows - row), 0LL);  // (a whole warp stays for the shuffles)
+  Piece<T, V> y[K][C], g[K][C];
+  Piece<R, V> r[K][C];
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const int j = (c * S::kThreads + t) * V;
-    const bool in = j < a.width;
-    y[c].zero();
-    if (in) y[c].load(static_cast<const T *>(a.y) + base + j);
-    if (in && a.gate) g[c].load(static_cast<const T *>(a.gate) + base + j);
-    if (in && a.res) r[c].load(static_cast<const R *>(a.res) + base + j);
-  }
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int j = (c * S::kThreads + t) * V;
+      const bool in = j < a.width && k < rows;
+      const size_t at = base + (size_t)k * a.width + j;
+      y[k][c].zero();
+      g[k][c].zero();
+      r[k][c].zero();
+      if (in) {
+        y[k][c].load(static_cast<const T *>(a.y) + at);
+        if (a.gate) g[k][c].load(static_cast<const T *>(a.gate) + at);
+        if (a.res) r[k][c].load(static_cast<const R *>(a.res) + at);
+      }
+    }
   const float inv = 1.f / (float)a.width;
-  float r1 = 1.f;
+  float r1[K], r2[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) r1[k] = 1.f;
   if (a.post) {
-    Vec<P> s = all<P>(0.f);
 #pragma unroll
-    for (int c = 0; c < C; ++c)
+    for (int k = 0; k < K; ++k) {
+      Vec<P> s = all<P>(0.f);
 #pragma unroll
-      for (int i = 0; i < S::kVecs; ++i) s = fma(y[c].get(i), y[c].get(i), s);
-    float ss[1] = {total(s)};
-    row_sum<S::kThreads, 1>(ss, sh[0]);
-    r1 = rsqrtf(ss[0] * inv + a.e1);
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int i = 0; i < N; ++i) s = fma(y[k][c].get(i), y[k][c].get(i), s);
+      r1[k] = total(s);
+    }
+    row_sum<S::kThreads, K>(r1, sh[0]);
+#pragma unroll
+    for (int k = 0; k < K; ++k) r1[k] = rsqrtf(r1[k] * inv + a.e1);
   }
-  Vec<P> o[C][S::kVecs], sum = all<P>(0.f);
+  Vec<P> o[K][C][N], sum[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) sum[k] = all<P>(0.f);
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int j = (c * S::kThreads + t) * V;
     if (j >= a.width) continue;
-    Vec<P> w[S::kVecs], sc[S::kVecs];
+    Vec<P> w[N], sc[N];
     weight(a.w1, j, w);
     weight(a.sc, j, sc);
 #pragma unroll
-    for (int i = 0; i < S::kVecs; ++i) {
-      Vec<P> b = mul(mul(y[c].get(i), all<P>(r1)), w[i]), e;
-      if (a.gate) b = mul(b, sigmoid_of(g[c].get(i), e));
-      o[c][i] = a.res ? fma(b, sc[i], r[c].get(i)) : mul(b, sc[i]);
-      sum = fma(o[c][i], o[c][i], sum);
+    for (int i = 0; i < N; ++i) w[i] = mul(w[i], sc[i]);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        Vec<P> b = mul(mul(y[k][c].get(i), all<P>(r1[k])), w[i]), e;
+        if (a.gate) b = mul(b, sigmoid_of(g[k][c].get(i), e));
+        o[k][c][i] = add(b, r[k][c].get(i));
+        sum[k] = fma(o[k][c][i], o[k][c][i], sum[k]);
+      }
+      if (k < rows && a.out) put(static_cast<R *>(a.out) + base + (size_t)k * a.width + j, o[k][c]);
     }
-    if (valid && a.out) put(static_cast<R *>(a.out) + base + j, o[c]);
   }
   if (!a.normed) return;
-  float so[1] = {total(sum)};
-  row_sum<S::kThreads, 1>(so, sh[1]);
-  const float r2 = rsqrtf(so[0] * inv + a.e2);
+#pragma unroll
+  for (int k = 0; k < K; ++k) r2[k] = total(sum[k]);
+  row_sum<S::kThreads, K>(r2, sh[1]);
+#pragma unroll
+  for (int k = 0; k < K; ++k) r2[k] = rsqrtf(r2[k] * inv + a.e2);
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int j = (c * S::kThreads + t) * V;
-    if (j < a.width && valid) {
-      Vec<P> w[S::kVecs];
-      weight(a.w2, j, w);
+    if (j >= a.width) continue;
+    Vec<P> w[N], v[N];
+    weight(a.w2, j, w);
 #pragma unroll
-      for (int i = 0; i < S::kVecs; ++i) w[i] = mul(mul(o[c][i], all<P>(r2)), w[i]);
-      put(static_cast<T *>(a.normed) + base + j, w);
-    }
+    for (int k = 0; k < K; ++k)
+      if (k < rows) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = mul(mul(o[k][c][i], all<P>(r2[k])), w[i]);
+        put(static_cast<T *>(a.normed) + base + (size_t)k * a.width + j, v);
+      }
   }
 }
 
@@ -230,7 +265,7 @@ __global__ void __launch_bounds__(S::kBlock, S::kBlock > 256 ? 1 : 2) norm_bwd_k
   using St = RowStages<S>;
   constexpr int V = S::V, C = S::kChunks, P = S::P, N = S::kVecs;
   extern __shared__ __align__(16) uint4 stage_mem[];
-  __shared__ float sh1[2][1][16], sh2[2][5][16];
+  __shared__ float sh1[2][16][8], sh2[2][16][8];
   const int t = threadIdx.x % S::kThreads, group = threadIdx.x / S::kThreads;
   const float inv = 1.f / (float)a.width;
   Vec<P> p1[C][N], ps[C][N], p2[C][N];
@@ -442,7 +477,8 @@ __global__ void __launch_bounds__(512) norm_weights_kernel(const float *part, in
 }
 
 template <typename S> cudaError_t fwd(const NormArgs &a, cudaStream_t s) {
-  norm_fwd_kernel<S><<<(unsigned)((a.rows + S::kGroups - 1) / S::kGroups), S::kBlock, 0, s>>>(a);
+  const long long rows = (long long)S::kGroups * S::kRows;
+  norm_fwd_kernel<S><<<(unsigned)((a.rows + rows - 1) / rows), S::kBlock, 0, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -461,11 +497,16 @@ template <typename S> cudaError_t bwd(const NormArgs &a, const NormBwdIo &io, fl
 }
 
 // Calls f with the row shape for this width: pieces of 8 elements when every
-// row of every tensor starts on 16 bytes, else single elements.  kBwd: one piece
-// per thread as far as threads go, for the registers of the three weight sums.
+// row of every tensor starts on 16 bytes, else single elements.  Backward: one
+// piece per thread as far as threads go, for the registers of the three weight
+// sums.  Forward: 4 narrow rows at once when there are many.
 template <typename T, typename R, bool kBwd, typename F>
-cudaError_t with_shape(int width, bool vectors, F f) {
+cudaError_t with_shape(int width, bool vectors, bool many, F f) {
   if (vectors) {
+    if constexpr (!kBwd) {
+      if (many && width <= 128) return f(Shape<T, R, 8, 1, 16, 4>());
+      if (many && width <= 256) return f(Shape<T, R, 8, 1, 32, 4>());
+    }
     if (width <= 128) return f(Shape<T, R, 8, 1, 16>());
     if (width <= 256) return f(Shape<T, R, 8, 1, 32>());
     if (width <= 512) return f(Shape<T, R, 8, kBwd ? 1 : 2, kBwd ? 64 : 32>());
@@ -481,9 +522,10 @@ cudaError_t with_shape(int width, bool vectors, F f) {
 
 template <bool kBwd, typename F> cudaError_t with_types(const NormArgs &a, bool vectors, F f) {
   using B = __nv_bfloat16;
+  const bool many = a.rows >= 16384;
   if (a.t == KDA_BF16)
-    return a.rt == KDA_BF16 ? with_shape<B, B, kBwd>(a.width, vectors, f) : with_shape<B, float, kBwd>(a.width, vectors, f);
-  return a.rt == KDA_BF16 ? with_shape<float, B, kBwd>(a.width, vectors, f) : with_shape<float, float, kBwd>(a.width, vectors, f);
+    return a.rt == KDA_BF16 ? with_shape<B, B, kBwd>(a.width, vectors, many, f) : with_shape<B, float, kBwd>(a.width, vectors, many, f);
+  return a.rt == KDA_BF16 ? with_shape<float, B, kBwd>(a.width, vectors, many, f) : with_shape<float, float, kBwd>(a.width, vectors, many, f);
 }
 
 template <int kN> bool on_16_bytes(const NormArgs &a, const void *const (&p)[kN]) {
