@@ -7,6 +7,7 @@ libkda.so is missing or cannot load, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from typing import Optional
@@ -440,107 +441,121 @@ def kda_affine_compose(pairs, initial_state=None, entry_states=None, *, stream=N
 
 
 # ------------------------------------------------ gated linear recurrence, norms
+# These calls are short enough that marshalling shows, so each tensor is checked
+# and turned into its address in one step, and descriptors are kept by their
+# sizes and types.
 
 WRITES = {"one": 0, "complement": 1}
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _addr(t: Optional[torch.Tensor]):
-    """A tensor's address for the C call.  One without elements may have none;
-    the library reads nothing through it but refuses NULL, so it gets a
-    non-null stand-in."""
+def _arg(name, t, shape, dtype, index):
+    """Address of an optional tensor, checked.  One without elements may have no
+    address; the library reads nothing through it but refuses NULL, so it gets
+    a non-null stand-in."""
     if t is None:
         return None
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on CUDA device {index}, not {t.device}")
     if not t.is_contiguous():
-        raise ValueError("tensors must be contiguous")
+        raise ValueError(f"{name} must be contiguous")
     return t.data_ptr() or 256
 
 
-def _expect(name, t, shape, dtype, dev):
-    if t is None:
-        return
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}, not {t.device}")
+def _elsewhere(index, stream):
+    """Whether a call has to be made on another device or stream than the current ones."""
+    if index < 0:
+        raise ValueError("tensors must be on a CUDA device")
+    return stream is not None or index != _current_device()
 
 
-class _Launch:
-    """The device and stream of one call.  On a stream other than the current
-    one, new tensors come from that stream's memory, and every tensor of the
-    call is kept from reuse until both streams are done with it."""
-
-    def __init__(self, dev, stream, tensors):
-        if dev.type != "cuda":
-            raise ValueError(f"tensors must be on a CUDA device, not {dev}")
-        current = torch.cuda.current_stream(dev)
-        self.stream = current if stream is None else stream
-        self.side = self.stream != current
-        self.current, self.tensors, self.guard = current, tensors, None
-        if self.side:
-            if self.stream.device != dev:
-                raise ValueError(f"the stream must be on {dev}, not {self.stream.device}")
-            self.guard = torch.cuda.stream(self.stream)
-        elif dev.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(dev)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self.stream.cuda_stream
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-    def keep(self, *new):
-        if self.side:
-            for t in self.tensors:
-                if t is not None:
-                    t.record_stream(self.stream)
-            for t in new:
-                if t is not None:
-                    t.record_stream(self.current)
+def _there(call, index, stream, tensors):
+    """call() with `stream` (or device `index`) current, so that what it allocates
+    belongs there.  On a side stream, every tensor of the call is kept from reuse
+    until both streams are done with it."""
+    if stream is None:
+        with torch.cuda.device(index):
+            return call()
+    if stream.device.index != index:
+        raise ValueError(f"the stream must be on CUDA device {index}, not {stream.device}")
+    before = torch.cuda.current_stream(index)
+    with torch.cuda.stream(stream):
+        result = call()
+    if stream != before:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+        for t in result.values() if isinstance(result, dict) else result:
+            if t is not None:
+                t.record_stream(before)
+    return result
 
 
-def _scan_desc(x, decay, A_log, initial_state, cu_seqlens, write, B, validate):
-    """Checked descriptor, (sequences, tokens) and the [N, H, d] state shape."""
-    if x.dim() not in (3, 4):
+class _Sized:
+    """A descriptor, the pointer to it that calls take, and sizes that follow from it."""
+
+    def __init__(self, desc):
+        self.desc, self.ref, self.sizes = desc, ctypes.byref(desc), {}
+
+    def size(self, fn, *args) -> int:
+        key = (fn, *args)
+        if key not in self.sizes:
+            n = ctypes.c_size_t(0)
+            _check(getattr(load(), fn)(self.ref, *args, ctypes.byref(n)), fn)
+            self.sizes[key] = n.value
+        return self.sizes[key]
+
+
+@functools.lru_cache(maxsize=512)
+def _scan_sized(*fields) -> _Sized:
+    return _Sized(KdaScanDesc(*fields))
+
+
+@functools.lru_cache(maxsize=512)
+def _norm_sized(*fields) -> _Sized:
+    return _Sized(KdaNormDesc(*fields))
+
+
+def _scan_call(x, decay, A_log, initial_state, cu_seqlens, write, B, validate):
+    """The sized descriptor, the [N, H, d] state shape and the addresses of the
+    inputs that every scan call has."""
+    shape = x.shape
+    if len(shape) == 3:
+        tokens, H, d = shape
+        batch = 1 if B is None else B
+    elif len(shape) == 4:
+        batch, T, H, d = shape
+        tokens = batch * T
+    else:
         raise ValueError("x must be [tokens, H, d] or [B, T, H, d]")
-    if write not in WRITES:
-        raise ValueError(f"write must be one of {sorted(WRITES)}")
-    dev = x.device
-    H, dd = x.shape[-2:]
-    tokens = x.shape[0] if x.dim() == 3 else x.shape[0] * x.shape[1]
-    batch = x.shape[0] if x.dim() == 4 else (1 if B is None else B)
     if B is not None and (B != batch or B <= 0 or tokens % B):
         raise ValueError(f"{tokens} tokens are no batch of {B} sequences")
-    if A_log is None:
-        _expect("decay", decay, x.shape, decay.dtype, dev)
-    else:
-        _expect("decay", decay, x.shape, x.dtype, dev)
-        _expect("A_log", A_log, (H,), torch.float32, dev)
-    d = KdaScanDesc()
+    if write not in WRITES:
+        raise ValueError(f"write must be one of {sorted(WRITES)}")
+    index, seqs, dt = x.get_device(), 0, x.dtype
     if cu_seqlens is not None:
         if batch != 1:
             raise ValueError("cu_seqlens needs B = 1")
         if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
             raise ValueError("cu_seqlens must be [N + 1] with N >= 1")
-        _expect("cu_seqlens", cu_seqlens, cu_seqlens.shape, torch.int32, dev)
-        d.num_seqs = cu_seqlens.numel() - 1
-    d.B, d.T, d.H, d.d = batch, (tokens // batch if batch else 0), H, dd
-    d.dtype, d.gate_dtype = _dt(x), _dt(decay)
-    d.write, d.validate = WRITES[write], int(bool(validate))
-    state = (d.num_seqs or batch, H, dd)
-    _expect("initial_state", initial_state, state, torch.float32, dev)
-    return d, state
+        seqs = cu_seqlens.numel() - 1
+    sized = _scan_sized(batch, tokens // batch if batch else 0, H, d, seqs, _dt(x), _dt(decay), WRITES[write],
+                        1 if validate else 0)
+    state = (seqs or batch, H, d)
+    return sized, state, (_arg("x", x, shape, dt, index),
+                          _arg("decay", decay, shape, decay.dtype if A_log is None else dt, index),
+                          _arg("A_log", A_log, (H,), torch.float32, index)), \
+        _arg("initial_state", initial_state, state, torch.float32, index), \
+        None if cu_seqlens is None else _arg("cu_seqlens", cu_seqlens, cu_seqlens.shape, torch.int32, index)
 
 
 def kda_scan_states_size(desc: KdaScanDesc) -> int:
-    n = ctypes.c_size_t(0)
-    _check(load().kda_scan_states_size(ctypes.byref(desc), ctypes.byref(n)), "kda_scan_states_size")
-    return n.value
+    return _Sized(desc).size("kda_scan_states_size")
 
 
 def kda_scan_fwd(x, decay, A_log=None, g_min=-5.0, initial_state=None, cu_seqlens=None, out=None, final_state=None,
@@ -553,26 +568,29 @@ def kda_scan_fwd(x, decay, A_log=None, g_min=-5.0, initial_state=None, cu_seqlen
     initial_state: [N, H, d] fp32 or None; write: "one" (w = 1) or
     "complement" (w = 1 - alpha).  Returns (out, final_state), and with
     want_states (or a `states` buffer) a third, the states for kda_scan_bwd."""
-    lib = load()
-    dev = x.device
-    d, state = _scan_desc(x, decay, A_log, initial_state, cu_seqlens, write, B, validate)
-    _expect("out", out, x.shape, x.dtype, dev)
-    _expect("final_state", final_state, state, torch.float32, dev)
-    launch = _Launch(dev, stream, (x, decay, A_log, initial_state, cu_seqlens, out, final_state, states))
-    with launch as handle:
-        if want_states or states is not None:
-            n = kda_scan_states_size(d) // 4
-            if states is None:
-                states = torch.empty(n, dtype=torch.float32, device=dev)
-            _expect("states", states, (n,), torch.float32, dev)
-        if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        if final_state is None and want_final_state:
-            final_state = torch.empty(state, dtype=torch.float32, device=dev)
-        st = lib.kda_scan_fwd(ctypes.byref(d), _addr(x), _addr(decay), _addr(A_log), g_min, _addr(initial_state),
-                              _addr(cu_seqlens), _addr(out), _addr(final_state), _addr(states), handle)
-    _check(st, "kda_scan_fwd")
-    launch.keep(out, final_state, states)
+    lib = _lib or load()
+    sized, state, ins, s0, cu = _scan_call(x, decay, A_log, initial_state, cu_seqlens, write, B, validate)
+    index = x.get_device()
+    if _elsewhere(index, stream):
+        return _there(lambda: kda_scan_fwd(x, decay, A_log, g_min, initial_state, cu_seqlens, out, final_state, states,
+                                           write=write, validate=validate, want_final_state=want_final_state,
+                                           want_states=want_states, B=B),
+                      index, stream, (x, decay, A_log, initial_state, cu_seqlens, out, final_state, states))
+    if out is None:
+        out = torch.empty_like(x)
+    if final_state is None and want_final_state:
+        final_state = torch.empty(state, dtype=torch.float32, device=x.device)
+    if want_states or states is not None:
+        n = sized.size("kda_scan_states_size") // 4
+        if states is None:
+            states = torch.empty(n, dtype=torch.float32, device=x.device)
+        kept = _arg("states", states, (n,), torch.float32, index)
+    else:
+        kept = None
+    st = lib.kda_scan_fwd(sized.ref, *ins, g_min, s0, cu, _arg("out", out, x.shape, x.dtype, index),
+                          _arg("final_state", final_state, state, torch.float32, index), kept, _current_stream(index))
+    if st:
+        _check(st, "kda_scan_fwd")
     return (out, final_state) if states is None else (out, final_state, states)
 
 
@@ -587,42 +605,44 @@ def kda_scan_bwd(x, decay, d_out, A_log=None, g_min=-5.0, initial_state=None, d_
     d_decay (decay's dtype), dA_log ([H] fp32; None without A_log) and
     d_initial_state (fp32; None unless wanted).  Rows behind the last sequence
     of cu_seqlens are not written.  `grads` may pass that dict preallocated."""
-    lib = load()
-    dev = x.device
-    d, state = _scan_desc(x, decay, A_log, initial_state, cu_seqlens, write, B, validate)
-    _expect("d_out", d_out, x.shape, x.dtype, dev)
-    _expect("d_final_state", d_final_state, state, torch.float32, dev)
+    lib = _lib or load()
+    sized, state, ins, s0, cu = _scan_call(x, decay, A_log, initial_state, cu_seqlens, write, B, validate)
+    index, shape, f32 = x.get_device(), x.shape, torch.float32
+    do = _arg("d_out", d_out, shape, x.dtype, index)
+    dst = _arg("d_final_state", d_final_state, state, f32, index)
+    if _elsewhere(index, stream):
+        return _there(lambda: kda_scan_bwd(x, decay, d_out, A_log, g_min, initial_state, d_final_state, cu_seqlens,
+                                           states, write=write, validate=validate,
+                                           want_d_initial_state=want_d_initial_state, B=B, workspace=workspace,
+                                           grads=grads),
+                      index, stream, (x, decay, d_out, A_log, initial_state, d_final_state, cu_seqlens, states,
+                                      workspace))
+    kept = None
     if states is not None:
-        _expect("states", states, (kda_scan_states_size(d) // 4,), torch.float32, dev)
-    given = tuple((grads or {}).values())
-    launch = _Launch(dev, stream, (x, decay, A_log, initial_state, d_out, d_final_state, cu_seqlens, states,
-                                   workspace) + given)
-    with launch as handle:
-        if grads is None:
-            grads = dict(dx=torch.empty(x.shape, dtype=x.dtype, device=dev),
-                         d_decay=torch.empty(x.shape, dtype=decay.dtype, device=dev),
-                         dA_log=None if A_log is None else torch.empty(A_log.shape, dtype=torch.float32, device=dev),
-                         d_initial_state=(torch.empty(state, dtype=torch.float32, device=dev)
-                                          if want_d_initial_state else None))
-        else:
-            _expect("dx", grads["dx"], x.shape, x.dtype, dev)
-            _expect("d_decay", grads["d_decay"], x.shape, decay.dtype, dev)
-            _expect("dA_log", grads.get("dA_log"), (d.H,), torch.float32, dev)
-            _expect("d_initial_state", grads.get("d_initial_state"), state, torch.float32, dev)
-        if workspace is None:
-            n = ctypes.c_size_t(0)
-            _check(lib.kda_scan_bwd_workspace_size(ctypes.byref(d), int(A_log is not None), int(states is not None),
-                                                   ctypes.byref(n)), "kda_scan_bwd_workspace_size")
-            if n.value:
-                workspace = torch.empty(n.value, dtype=torch.uint8, device=dev)
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        st = lib.kda_scan_bwd(ctypes.byref(d), _addr(x), _addr(decay), _addr(A_log), g_min, _addr(initial_state),
-                              _addr(cu_seqlens), _addr(states), _addr(d_out), _addr(d_final_state),
-                              _addr(grads["dx"]), _addr(grads["d_decay"]), _addr(grads.get("dA_log")),
-                              _addr(grads.get("d_initial_state")), _addr(workspace), ws_bytes, handle)
-    _check(st, "kda_scan_bwd")
-    launch.keep(*grads.values())
+        kept = _arg("states", states, (sized.size("kda_scan_states_size") // 4,), f32, index)
+    if grads is None:
+        grads = {"dx": torch.empty_like(x), "d_decay": torch.empty_like(decay),
+                 "dA_log": None if A_log is None else torch.empty_like(A_log),
+                 "d_initial_state": (torch.empty(state, dtype=f32, device=x.device) if want_d_initial_state else None)}
+    if workspace is None:
+        n = sized.size("kda_scan_bwd_workspace_size", int(A_log is not None), int(states is not None))
+        if n:
+            workspace = torch.empty(n, dtype=torch.uint8, device=x.device)
+    ws, ws_bytes = _workspace(workspace, index)
+    st = lib.kda_scan_bwd(sized.ref, *ins, g_min, s0, cu, kept, do, dst, _arg("dx", grads["dx"], shape, x.dtype, index),
+                          _arg("d_decay", grads["d_decay"], shape, decay.dtype, index),
+                          _arg("dA_log", grads.get("dA_log"), state[1:2], f32, index),
+                          _arg("d_initial_state", grads.get("d_initial_state"), state, f32, index), ws, ws_bytes,
+                          _current_stream(index))
+    if st:
+        _check(st, "kda_scan_bwd")
     return grads
+
+
+def _workspace(t, index):
+    if t is None:
+        return None, 0
+    return _arg("workspace", t, t.shape, t.dtype, index), t.numel() * t.element_size()
 
 
 def kda_scan_step(x, decay, state_in, A_log=None, g_min=-5.0, state_out=None, out=None, *, write="one",
@@ -630,40 +650,41 @@ def kda_scan_step(x, decay, state_in, A_log=None, g_min=-5.0, state_out=None, ou
     """One token of kda_scan_fwd for N sequences: x, decay [N, H, d], state_in
     [N, H, d] fp32.  The new state goes to state_out (None: in place of
     state_in).  Returns (out, state_out)."""
-    lib = load()
-    dev = x.device
+    lib = _lib or load()
     if x.dim() != 3 or x.shape[0] == 0:
         raise ValueError("x must be [N, H, d] with N >= 1")
-    d, state = _scan_desc(x, decay, A_log, state_in, None, write, x.shape[0], validate)
+    sized, state, ins, s0, _ = _scan_call(x, decay, A_log, state_in, None, write, x.shape[0], validate)
+    index = x.get_device()
+    if _elsewhere(index, stream):
+        return _there(lambda: kda_scan_step(x, decay, state_in, A_log, g_min, state_out, out, write=write,
+                                            validate=validate),
+                      index, stream, (x, decay, state_in, A_log, state_out, out))
     if state_out is None:
         state_out = state_in
-    _expect("state_out", state_out, state, torch.float32, dev)
-    _expect("out", out, x.shape, x.dtype, dev)
-    launch = _Launch(dev, stream, (x, decay, A_log, state_in, state_out, out))
-    with launch as handle:
-        if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        st = lib.kda_scan_step(ctypes.byref(d), _addr(x), _addr(decay), _addr(A_log), g_min, _addr(state_in),
-                               _addr(state_out), _addr(out), handle)
-    _check(st, "kda_scan_step")
-    launch.keep(out)
+    if out is None:
+        out = torch.empty_like(x)
+    st = lib.kda_scan_step(sized.ref, *ins, g_min, s0, _arg("state_out", state_out, state, torch.float32, index),
+                           _arg("out", out, x.shape, x.dtype, index), _current_stream(index))
+    if st:
+        _check(st, "kda_scan_step")
     return out, state_out
 
 
-def _norm_desc(y, residual, gate, post_norm, post_weight, scale, pre_weight, post_eps, pre_eps):
-    if y.dim() < 1 or y.shape[-1] < 1:
+def _norm_call(y, residual, gate, post_norm, post_weight, scale, pre_weight, post_eps, pre_eps):
+    """The sized descriptor, out's dtype and the inputs' addresses."""
+    shape = y.shape
+    if not shape or shape[-1] < 1:
         raise ValueError("y must be [..., width] with width >= 1")
-    dev, width = y.device, y.shape[-1]
-    _expect("residual", residual, y.shape, y.dtype if residual is None else residual.dtype, dev)
-    _expect("gate", gate, y.shape, y.dtype, dev)
-    for name, t in (("post_weight", post_weight), ("scale", scale), ("pre_weight", pre_weight)):
-        _expect(name, t, (width,), torch.float32, dev)
-    d = KdaNormDesc()
-    d.rows, d.width = y.numel() // width, width
-    d.dtype = _dt(y)
-    d.res_dtype = d.dtype if residual is None else _dt(residual)
-    d.post_norm, d.post_eps, d.pre_eps = int(bool(post_norm)), post_eps, pre_eps
-    return d
+    index, width, dt = y.get_device(), shape[-1], y.dtype
+    rdt = dt if residual is None else residual.dtype
+    code = _dt(y)
+    sized = _norm_sized(y.numel() // width, width, code, code if residual is None else _dt(residual),
+                        1 if post_norm else 0, post_eps, pre_eps)
+    row = shape[-1:]
+    return sized, rdt, (_arg("y", y, shape, dt, index), _arg("residual", residual, shape, rdt, index),
+                        _arg("gate", gate, shape, dt, index), _arg("post_weight", post_weight, row, torch.float32, index),
+                        _arg("scale", scale, row, torch.float32, index),
+                        _arg("pre_weight", pre_weight, row, torch.float32, index))
 
 
 def kda_block_norm_fwd(y, residual=None, gate=None, *, post_norm=True, post_weight=None, scale=None, pre_weight=None,
@@ -678,22 +699,23 @@ def kda_block_norm_fwd(y, residual=None, gate=None, *, post_norm=True, post_weig
     and scale are ones, no gate is 1, no residual is 0.  gate has y's dtype;
     residual (fp32 or bf16) sets out's.  Returns (out, normed), None for the
     one not wanted; out may be `residual` itself (update in place)."""
-    lib = load()
-    dev = y.device
-    d = _norm_desc(y, residual, gate, post_norm, post_weight, scale, pre_weight, post_eps, pre_eps)
-    odt = y.dtype if residual is None else residual.dtype
-    _expect("out", out, y.shape, odt, dev)
-    _expect("normed", normed, y.shape, y.dtype, dev)
-    launch = _Launch(dev, stream, (y, residual, gate, post_weight, scale, pre_weight, out, normed))
-    with launch as handle:
-        if out is None and want_out:
-            out = torch.empty(y.shape, dtype=odt, device=dev)
-        if normed is None and want_normed:
-            normed = torch.empty(y.shape, dtype=y.dtype, device=dev)
-        st = lib.kda_block_norm_fwd(ctypes.byref(d), _addr(y), _addr(residual), _addr(gate), _addr(post_weight),
-                                    _addr(scale), _addr(pre_weight), _addr(out), _addr(normed), handle)
-    _check(st, "kda_block_norm_fwd")
-    launch.keep(out, normed)
+    lib = _lib or load()
+    sized, rdt, ins = _norm_call(y, residual, gate, post_norm, post_weight, scale, pre_weight, post_eps, pre_eps)
+    index, shape = y.get_device(), y.shape
+    if _elsewhere(index, stream):
+        return _there(lambda: kda_block_norm_fwd(y, residual, gate, post_norm=post_norm, post_weight=post_weight,
+                                                 scale=scale, pre_weight=pre_weight, post_eps=post_eps,
+                                                 pre_eps=pre_eps, want_out=want_out, want_normed=want_normed,
+                                                 out=out, normed=normed),
+                      index, stream, (y, residual, gate, post_weight, scale, pre_weight, out, normed))
+    if out is None and want_out:
+        out = torch.empty_like(y if residual is None else residual)
+    if normed is None and want_normed:
+        normed = torch.empty_like(y)
+    st = lib.kda_block_norm_fwd(sized.ref, *ins, _arg("out", out, shape, rdt, index),
+                                _arg("normed", normed, shape, y.dtype, index), _current_stream(index))
+    if st:
+        _check(st, "kda_block_norm_fwd")
     return out, normed
 
 
@@ -706,37 +728,30 @@ def kda_block_norm_bwd(y, d_out, d_normed=None, residual=None, gate=None, *, pos
     d_scale, d_pre_weight in fp32; None for each input that was not given.
     `grads` may pass that dict preallocated: then the entries it holds (d_y
     and, with a gate, d_gate are required) are written."""
-    lib = load()
-    dev = y.device
-    d = _norm_desc(y, residual, gate, post_norm, post_weight, scale, pre_weight, post_eps, pre_eps)
-    rdt, width = (y.dtype if residual is None else residual.dtype), y.shape[-1]
-    _expect("d_out", d_out, y.shape, rdt, dev)
-    _expect("d_normed", d_normed, y.shape, y.dtype, dev)
-    given = tuple((grads or {}).values())
-    launch = _Launch(dev, stream, (y, residual, gate, post_weight, scale, pre_weight, d_out, d_normed, workspace)
-                     + given)
-    with launch as handle:
-        if grads is None:
-            new = lambda like: None if like is None else torch.empty(like.shape, dtype=like.dtype, device=dev)  # noqa: E731
-            grads = dict(d_y=new(y), d_residual=new(residual), d_gate=new(gate), d_post_weight=new(post_weight),
-                         d_scale=new(scale), d_pre_weight=None if d_normed is None else new(pre_weight))
-        else:
-            for name, dt in (("d_y", y.dtype), ("d_residual", rdt), ("d_gate", y.dtype)):
-                _expect(name, grads.get(name), y.shape, dt, dev)
-            for name in ("d_post_weight", "d_scale", "d_pre_weight"):
-                _expect(name, grads.get(name), (width,), torch.float32, dev)
-        if workspace is None:
-            n = ctypes.c_size_t(0)
-            _check(lib.kda_block_norm_bwd_workspace_size(ctypes.byref(d), ctypes.byref(n)),
-                   "kda_block_norm_bwd_workspace_size")
-            if n.value:
-                workspace = torch.empty(n.value, dtype=torch.uint8, device=dev)
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        g = {k: _addr(grads.get(k)) for k in ("d_y", "d_residual", "d_gate", "d_post_weight", "d_scale", "d_pre_weight")}
-        st = lib.kda_block_norm_bwd(ctypes.byref(d), _addr(y), _addr(residual), _addr(gate), _addr(post_weight),
-                                    _addr(scale), _addr(pre_weight), _addr(d_out), _addr(d_normed), g["d_y"],
-                                    g["d_residual"], g["d_gate"], g["d_post_weight"], g["d_scale"],
-                                    g["d_pre_weight"], _addr(workspace), ws_bytes, handle)
-    _check(st, "kda_block_norm_bwd")
-    launch.keep(*grads.values())
+    lib = _lib or load()
+    sized, rdt, ins = _norm_call(y, residual, gate, post_norm, post_weight, scale, pre_weight, post_eps, pre_eps)
+    index, shape, dt = y.get_device(), y.shape, y.dtype
+    do = _arg("d_out", d_out, shape, rdt, index)
+    dn = _arg("d_normed", d_normed, shape, dt, index)
+    if _elsewhere(index, stream):
+        return _there(lambda: kda_block_norm_bwd(y, d_out, d_normed, residual, gate, post_norm=post_norm,
+                                                 post_weight=post_weight, scale=scale, pre_weight=pre_weight,
+                                                 post_eps=post_eps, pre_eps=pre_eps, workspace=workspace, grads=grads),
+                      index, stream, (y, d_out, d_normed, residual, gate, post_weight, scale, pre_weight, workspace))
+    if grads is None:
+        new = lambda like: None if like is None else torch.empty_like(like)  # noqa: E731
+        grads = {"d_y": torch.empty_like(y), "d_residual": new(residual), "d_gate": new(gate),
+                 "d_post_weight": new(post_weight), "d_scale": new(scale),
+                 "d_pre_weight": None if d_normed is None else new(pre_weight)}
+    get, row, f32 = grads.get, shape[-1:], torch.float32
+    weights = [_arg(n, get(n), row, f32, index) for n in ("d_post_weight", "d_scale", "d_pre_weight")]
+    if workspace is None and any(weights):
+        workspace = torch.empty(sized.size("kda_block_norm_bwd_workspace_size"), dtype=torch.uint8, device=y.device)
+    ws, ws_bytes = _workspace(workspace, index)
+    st = lib.kda_block_norm_bwd(sized.ref, *ins, do, dn, _arg("d_y", get("d_y"), shape, dt, index),
+                                _arg("d_residual", get("d_residual"), shape, rdt, index),
+                                _arg("d_gate", get("d_gate"), shape, dt, index), *weights, ws, ws_bytes,
+                                _current_stream(index))
+    if st:
+        _check(st, "kda_block_norm_bwd")
     return grads

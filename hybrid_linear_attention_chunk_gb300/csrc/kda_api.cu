@@ -850,7 +850,10 @@ kda_status kda_block_norm_bwd(const kda_norm_desc *desc, const void *y, const vo
   if (aliased(in, 8, outs, 7, 7, 6)) return KDA_ERR_ALIAS;
   const NormBwdIo io{d_out, d_normed, d_y, d_residual, d_gate, d_post_weight, d_scale, d_pre_weight};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return with_workspace(workspace, workspace_bytes, norm_bwd_workspace_bytes(a.width), s,
+  const size_t full = norm_bwd_workspace_bytes(a.width);
+  if (workspace && workspace_bytes < full) return KDA_ERR_SHAPE;
+  const bool weights = d_post_weight || d_scale || d_pre_weight;
+  return with_workspace(workspace, workspace_bytes, weights ? full : 0, s,
                         [&](void *ws) { return launch_norm_bwd(a, io, ws, s); });
 }
 

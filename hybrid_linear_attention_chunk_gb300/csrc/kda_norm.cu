@@ -101,10 +101,11 @@ template <typename T_, typename R_, int V_, int kChunks_, int kThreads_, int kRo
 struct Shape {
   using T = T_;                                              // y, gate, normed
   using R = R_;                                              // residual, out
-  static constexpr int V = V_, kChunks = kChunks_, kThreads = kThreads_, kRows = kRows_;
+  static constexpr int V = V_, kChunks = kChunks_, kThreads = kThreads_;
+  static constexpr int rows() { return kRows_; }              // at once, in the forward
   static constexpr int P = V == 8 ? 2 : 1, kVecs = V / P;    // values of one instruction
   static constexpr int kBlock = kThreads > 256 ? kThreads : 256, kGroups = kBlock / kThreads;
-  static constexpr int kMaxWidth = V * kChunks * kThreads;
+  static constexpr int max_width() { return V * kChunks * kThreads; }
 };
 
 // Sums of kN (at most 8) values over the threads of a row, the same in each of
@@ -144,7 +145,7 @@ template <typename S>
 __global__ void __launch_bounds__(S::kBlock) norm_fwd_kernel(NormArgs a) {
   using T = typename S::T;
   using R = typename S::R;
-  constexpr int V = S::V, C = S::kChunks, P = S::P, N = S::kVecs, K = S::kRows;
+  constexpr int V = S::V, C = S::kChunks, P = S::P, N = S::kVecs, K = S::rows();
   __shared__ float sh[2][16][8];
   const int t = threadIdx.x % S::kThreads;
   const long long row = ((long long)blockIdx.x * S::kGroups + threadIdx.x / S::kThreads) * K;
@@ -254,7 +255,7 @@ template <typename S> struct RowStages {
   static constexpr int kStage = parts() * S::kChunks * S::kBlock * 16;  // bytes
   static constexpr int kLimit = S::kBlock > 256 ? 227 * 1024 : 113 * 1024;
   static constexpr int kStages = 3 * kStage <= kLimit ? 3 : 2 * kStage <= kLimit ? 2 : 1;
-  static constexpr int kSums = S::kGroups > 1 ? (int)sizeof(float) * S::kGroups * S::kMaxWidth : 0;
+  static constexpr int kSums = S::kGroups > 1 ? (int)sizeof(float) * S::kGroups * S::max_width() : 0;
   static constexpr int kBytes = kStages * kStage > kSums ? kStages * kStage : kSums;
 };
 
@@ -432,7 +433,7 @@ __global__ void __launch_bounds__(S::kBlock, S::kBlock > 256 ? 1 : 2) norm_bwd_k
   if constexpr (V == 8) asm volatile("cp.async.wait_group 0;" ::: "memory");
   if (!part) return;
   // the groups of a block in order, then one row of partials
-  float *sums = reinterpret_cast<float *>(stage_mem);  // [kGroups][kMaxWidth]
+  float *sums = reinterpret_cast<float *>(stage_mem);  // [kGroups][max_width]
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
     float *to = part + ((size_t)k * gridDim.x + blockIdx.x) * a.width;
@@ -441,7 +442,7 @@ __global__ void __launch_bounds__(S::kBlock, S::kBlock > 256 ? 1 : 2) norm_bwd_k
     for (int c = 0; c < C; ++c) {
       const int j = (c * S::kThreads + t) * V;
       const Vec<P>(&p)[N] = k == 0 ? p1[c] : k == 1 ? ps[c] : p2[c];
-      if constexpr (S::kGroups > 1) put(sums + group * S::kMaxWidth + j, p);
+      if constexpr (S::kGroups > 1) put(sums + group * S::max_width() + j, p);
       else if (j < a.width) put(to + j, p);
     }
     if constexpr (S::kGroups > 1) {
@@ -449,7 +450,7 @@ __global__ void __launch_bounds__(S::kBlock, S::kBlock > 256 ? 1 : 2) norm_bwd_k
       for (int j = threadIdx.x; j < a.width; j += S::kBlock) {
         float s = 0.f;
 #pragma unroll
-        for (int q = 0; q < S::kGroups; ++q) s += sums[q * S::kMaxWidth + j];
+        for (int q = 0; q < S::kGroups; ++q) s += sums[q * S::max_width() + j];
         to[j] = s;
       }
     }
@@ -477,7 +478,7 @@ __global__ void __launch_bounds__(512) norm_weights_kernel(const float *part, in
 }
 
 template <typename S> cudaError_t fwd(const NormArgs &a, cudaStream_t s) {
-  const long long rows = (long long)S::kGroups * S::kRows;
+  const long long rows = (long long)S::kGroups * S::rows();
   norm_fwd_kernel<S><<<(unsigned)((a.rows + rows - 1) / rows), S::kBlock, 0, s>>>(a);
   return cudaGetLastError();
 }

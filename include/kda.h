@@ -480,8 +480,9 @@ kda_status kda_block_norm_fwd(const kda_norm_desc *desc, const void *y, const vo
  *               the rows (zeros when rows = 0).  d_post_weight needs post_norm,
  *               d_pre_weight needs d_normed (KDA_ERR_NULL otherwise); the
  *               gradient of an absent (all ones) weight or scale may be asked for
- *   workspace   kda_block_norm_bwd_workspace_size bytes, 16-byte aligned, or
- *               NULL: then a call that needs some allocates it stream-ordered
+ *   workspace   kda_block_norm_bwd_workspace_size bytes, 16-byte aligned (used
+ *               for the weights' gradients only), or NULL: then a call that needs
+ *               some allocates it stream-ordered
  */
 kda_status kda_block_norm_bwd_workspace_size(const kda_norm_desc *desc, size_t *bytes);
 kda_status kda_block_norm_bwd(const kda_norm_desc *desc, const void *y, const void *residual, const void *gate,
