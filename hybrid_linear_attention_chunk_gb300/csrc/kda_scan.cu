@@ -97,7 +97,8 @@ __global__ void __launch_bounds__(32 * FwdSmem<X, G, kLogit, L>::kMaxWarps, 1) s
       mine.add[i] = sum[kScanTile - 1].get(i);
     }
     const bool ends = eos - tw <= L::kTokens;  // the sequence's last tile
-    if (ranks == 1) sh.ring(par, mine, tw == bos, !ends, h);
+    float leave[V];
+    if (ranks == 1) sh.ring(par, mine, tw == bos, !ends, h, leave);
     else sh.cluster(par, mine, state, h);
     const int t = tw + sh.group * kScanTile, left = live ? eos - t : 0;
     const Vec<V> hv = lanes<V>([&](int i) { return h[i]; });
@@ -116,11 +117,9 @@ __global__ void __launch_bounds__(32 * FwdSmem<X, G, kLogit, L>::kMaxWarps, 1) s
           if (j < left) store<V>(o + (unsigned)(j * D), fma(keep[j], hv, sum[j]));
       }
     }
-    if (ranks == 1 && ends && a.sT && live && sh.group == L::kGroups - 1) {
-      mine.run(h);
+    if (ranks == 1 && ends && a.sT && live && sh.group == L::kGroups - 1)
 #pragma unroll
-      for (int i = 0; i < V; ++i) a.sT[chain + i] = h[i];
-    }
+      for (int i = 0; i < V; ++i) a.sT[chain + i] = leave[i];
   }
   if (V == 2) copies_wait<0>();
   if ((ranks > 1 || bos == eos) && a.sT && live && sh.rank == 0 && sh.warp == 0 && sh.group == 0)
@@ -130,20 +129,20 @@ __global__ void __launch_bounds__(32 * FwdSmem<X, G, kLogit, L>::kMaxWarps, 1) s
 
 constexpr int kStepThreads = 128;
 
-template <bool kLogit>
-__device__ __forceinline__ float step(const ScanArgs &a, int c, Vec<1> z, Vec<1> x, float h) {
-  const Gate<kLogit, 1> gate(a, c, true);
-  const Vec<1> l = gate.log(z);
-  return decay_apply(decay_code(gate.unit * l.v), h, a.complement ? gate.one_minus(l, gate.alpha(l)).v * x.v : x.v);
-}
-
+// One token of every chain, V channels of one sequence per thread.
+template <typename X, typename G, bool kLogit, bool kComp, int V>
 __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(ScanArgs a) {
-  const size_t i = (size_t)blockIdx.x * kStepThreads + threadIdx.x;
+  const size_t i = ((size_t)blockIdx.x * kStepThreads + threadIdx.x) * V;
   if (i >= (size_t)a.N * a.D) return;
-  const Vec<1> z{ld_elem(a.g, i, a.gdt())}, x{ld_elem(a.x, i, a.t)};
-  const float h = a.A_log ? step<true>(a, (int)(i % a.D), z, x, a.s0[i]) : step<false>(a, 0, z, x, a.s0[i]);
-  a.sT[i] = h;
-  st_elem(a.o, i, h, a.t);
+  const Vec<V> z = values(*reinterpret_cast<const Raw<G, V> *>(static_cast<const G *>(a.g) + i));
+  const Vec<V> x = values(*reinterpret_cast<const Raw<X, V> *>(static_cast<const X *>(a.x) + i));
+  const Vec<V> s = values(*reinterpret_cast<const Raw<float, V> *>(a.s0 + i));
+  const Gate<kLogit, V> gate(a, (int)(i % a.D), true);
+  const Vec<V> l = gate.log(z);
+  const Vec<V> u = kComp ? mul(x, gate.one_minus(l, gate.alpha(l))) : x;
+  const Vec<V> h = lanes<V>([&](int k) { return decay_apply(decay_code(gate.unit * l.get(k)), s.get(k), u.get(k)); });
+  store<V>(a.sT + i, h);
+  store<V>(static_cast<X *>(a.o) + i, h);
 }
 
 __global__ void __launch_bounds__(256) validate_scan_kernel(ScanArgs a, int *flag) {
@@ -186,6 +185,21 @@ cudaError_t fwd_t(const ScanArgs &a, cudaStream_t s) {
   return a.complement ? fwd_c<X, G, kLogit, true>(a, s) : fwd_c<X, G, kLogit, false>(a, s);
 }
 
+template <typename X, typename G, bool kLogit, bool kComp, int V>
+cudaError_t step_v(const ScanArgs &a, cudaStream_t s) {
+  const size_t threads = ((size_t)a.N * a.D + V - 1) / V;
+  scan_step_kernel<X, G, kLogit, kComp, V>
+      <<<(unsigned)((threads + kStepThreads - 1) / kStepThreads), kStepThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename X, typename G, bool kLogit>
+cudaError_t step_t(const ScanArgs &a, cudaStream_t s) {
+  const bool v = scan_vectors(a.D, {{a.x, sizeof(X)}, {a.g, sizeof(G)}, {a.o, sizeof(X)}, {a.s0, 4}, {a.sT, 4}});
+  if (a.complement) return v ? step_v<X, G, kLogit, true, 2>(a, s) : step_v<X, G, kLogit, true, 1>(a, s);
+  return v ? step_v<X, G, kLogit, false, 2>(a, s) : step_v<X, G, kLogit, false, 1>(a, s);
+}
+
 }  // namespace
 
 cudaError_t launch_scan_fwd(const ScanArgs &a, cudaStream_t s) {
@@ -203,9 +217,10 @@ cudaError_t launch_scan_states(const ScanArgs &a, cudaStream_t s) {
 }
 
 cudaError_t launch_scan_step(const ScanArgs &a, cudaStream_t s) {
-  const size_t n = (size_t)a.N * a.D;
-  scan_step_kernel<<<(unsigned)((n + kStepThreads - 1) / kStepThreads), kStepThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  using B = __nv_bfloat16;
+  if (a.A_log) return a.t == KDA_BF16 ? step_t<B, B, true>(a, s) : step_t<float, float, true>(a, s);
+  if (a.t == KDA_BF16) return a.gate == KDA_BF16 ? step_t<B, B, false>(a, s) : step_t<B, float, false>(a, s);
+  return a.gate == KDA_BF16 ? step_t<float, B, false>(a, s) : step_t<float, float, false>(a, s);
 }
 
 cudaError_t launch_validate_scan(const ScanArgs &a, int *d_flag, cudaStream_t s) {

@@ -114,20 +114,22 @@ template <typename T, typename L, bool kPad> struct Tile<T, L, kPad, 2> {
   __device__ __forceinline__ void issue(int stage, const void *base, int D, int t, int c0, int len, int lane) {
     T *dst = buf + stage * kElems;
     const int row = lane / kPerRow, col = (lane % kPerRow) * kChunk;
-    const bool in = c0 + col < D;
     const T *src = static_cast<const T *>(base) + ((size_t)t * D + c0 + col);
+    const unsigned to = (unsigned)__cvta_generic_to_shared(dst + col);
+    const bool in = c0 + col < D;
 #pragma unroll
     for (int k = 0; k < L::kTokens * kPerRow / 32; ++k) {
       const int r = row + k * (32 / kPerRow);
       const bool ok = in && r < len;
-      const unsigned to = (unsigned)__cvta_generic_to_shared(dst + place(r) * L::kWide + col);
-      const void *from = ok ? src + (size_t)(unsigned)r * (unsigned)D : static_cast<const T *>(base);
-      if (L::kWide == 64)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(ok ? 16 : 0) : "memory");
-      else  // the neighbouring channels' blocks read the rest of the line at about the same time
-        asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(ok ? 16 : 0)
-                     : "memory");
+      copy(to + place(r) * L::kWide * (int)sizeof(T), ok ? src + (size_t)(unsigned)r * (unsigned)D : static_cast<const T *>(base),
+           ok ? 16 : 0);
     }
+  }
+  static __device__ __forceinline__ void copy(unsigned to, const void *from, int size) {
+    if (L::kWide == 64)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(size) : "memory");
+    else  // the neighbouring channels' blocks read the rest of the line at about the same time
+      asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(size) : "memory");
   }
   // after the copies have landed, before the first read
   __device__ __forceinline__ void pad(int stage, int len, int lane) {
@@ -189,15 +191,15 @@ struct Gate {
     const Vec<V> d = add(all<V>(1.f), lanes<V>([&](int i) { return fast_exp2(e.get(i)); }));
     return lanes<V>([&](int i) { return fast_rcp(d.get(i)); });
   }
-  // dg/dz: g (1 - Sigmoid) s.  1 - r below a half, 2^(ns z) r above it (where r
-  // is near 1, and the power is finite).
-  __device__ __forceinline__ Vec<V> slope(Vec<V> z, Vec<V> l) const {
-    const Vec<V> e = mul(ns, z);
-    const Vec<V> rest = lanes<V>([&](int i) {
-      const float r = l.get(i);
-      return r <= 0.5f ? 1.f - r : fast_exp2(e.get(i)) * r;
-    });
-    return mul(mul(mul(ns, all<V>(-unit / kLog2e)), l), rest);
+  // The same, with dg/dz: g (1 - Sigmoid) s.  1 - r below a half, 2^(ns z) r
+  // above it (where r is near 1, and the power is finite).
+  __device__ __forceinline__ Vec<V> log(Vec<V> z, Vec<V> &slope) const {
+    const Vec<V> x = mul(ns, z), e = lanes<V>([&](int i) { return fast_exp2(x.get(i)); });
+    const Vec<V> d = add(all<V>(1.f), e), r = lanes<V>([&](int i) { return fast_rcp(d.get(i)); });
+    const Vec<V> er = mul(e, r), below = fma(r, all<V>(-1.f), all<V>(1.f));
+    const Vec<V> rest = lanes<V>([&](int i) { return r.get(i) <= 0.5f ? below.get(i) : er.get(i); });
+    slope = mul(mul(mul(ns, all<V>(-unit / kLog2e)), r), rest);
+    return r;
   }
   __device__ __forceinline__ Vec<V> alpha(Vec<V> l) const {
     const Vec<V> e = mul(all<V>(rate), l);
@@ -279,12 +281,13 @@ __device__ __forceinline__ void barrier_arrive(int id, int threads) {
 
 // Brings every tile the state that enters it, in the order the recurrence runs.
 //   One CTA for a chain block: the warps take the tiles of a sequence in turn
-//   and hand the state on in a ring, each as soon as it has its own: the tile's
-//   effect is known by then, so a state waits for a few instructions per tile,
-//   and no warp waits for more than its predecessor.  Warp w waits at named
-//   barrier w, where its predecessor's arrival is the one it needs.  A
-//   predecessor never arrives a round ahead, as its own next state comes through
-//   the waiter.
+//   and hand the state on in a ring.  A warp knows beforehand what its tile does,
+//   so a state waits for a load, a step and a store per tile, and one warp's
+//   arithmetic runs under another's waiting.  Warp w waits at named barrier w for
+//   its predecessor's arrival, which is never a round ahead, as the predecessor's
+//   own next state comes through the waiter.  (Rings of teams of 2, 4 and 8 warps
+//   that join their tiles first were slower: 262144 x 2048 in 0.68 to 0.99 ms
+//   against 0.65 to 0.75.)
 //   A cluster: its CTAs take consecutive spans of a round.  Warp 0 joins its
 //   CTA's warps into one span and stores it in every CTA; each thread keeps the
 //   round's state in registers.
@@ -292,7 +295,7 @@ __device__ __forceinline__ void barrier_arrive(int id, int threads) {
 template <typename L>
 struct ScanJoin {
   static constexpr int V = L::V;
-  float *carry;                 // [2][warps][kWide]
+  float *carry;                 // one CTA's: [2][warps][kWide]
   Span<V> *tile, *cta;          // a cluster's: [2][warps][kLanes], [2][ranks][kLanes]
   int warps, warp, lane, group, rank, ranks;
 
@@ -325,31 +328,29 @@ struct ScanJoin {
   }
 
   // h: in, the sequence's first state (read with `first`); out, the state that
-  // enters the tile.  `more`: a tile of another warp follows.
-  __device__ __forceinline__ void ring(int par, const Span<V> &mine, bool first, bool more, float (&h)[V]) {
-    const int wide = (lane % L::kLanes) * V;
+  // enters the tile.  out: the state that leaves the warp's tiles, in the last
+  // group.  `more`: a tile of another warp follows.
+  __device__ __forceinline__ void ring(int par, const Span<V> &mine, bool first, bool more, float (&h)[V],
+                                       float (&out)[V]) {
+    const int wide = (lane % L::kLanes) * V, next = warp + 1 < warps ? warp + 1 : 0, npar = next ? par : par ^ 1;
+    using F = Raw<float, V>;
+    const F *in = reinterpret_cast<const F *>(carry + (par * warps + warp) * L::kWide + wide);
+    F *to = reinterpret_cast<F *>(carry + (npar * warps + next) * L::kWide + wide);
+    const bool gives = more && group == L::kGroups - 1;
     Span<V> upto, before;
     groups(mine, upto, before);
     if (!first) {
       barrier_sync(warp, 64);
-      const float *in = carry + (par * warps + warp) * L::kWide + wide;
+      const F v = *in;
+      const float *f = reinterpret_cast<const float *>(&v);
 #pragma unroll
-      for (int i = 0; i < V; ++i) h[i] = in[i];
+      for (int i = 0; i < V; ++i) h[i] = f[i];
     }
-    if (more) {
-      const int next = warp + 1 < warps ? warp + 1 : 0, npar = next ? par : par ^ 1;
-      if (group == L::kGroups - 1) {
-        float out[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) out[i] = h[i];
-        upto.run(out);
-        float *to = carry + (npar * warps + next) * L::kWide + wide;
-#pragma unroll
-        for (int i = 0; i < V; ++i) to[i] = out[i];
-      }
-      __syncwarp();
-      barrier_arrive(next, 64);
-    }
+    for (int i = 0; i < V; ++i) out[i] = h[i];
+    upto.run(out);
+    if (gives) *to = *reinterpret_cast<const F *>(out);
+    if (more) barrier_arrive(next, 64);
     if (group > 0) before.run(h);
   }
 

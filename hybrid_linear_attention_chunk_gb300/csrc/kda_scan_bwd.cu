@@ -122,7 +122,8 @@ scan_bwd_kernel(ScanArgs a, ScanBwdIo io, float *dA_part, int cblocks) {
       mine.add[i] = c1.get(i);
     }
     const bool ends = q == tiles - 1;  // (one CTA) the sequence's first tile
-    if (ranks == 1) sh.ring(par, mine, q == 0, !ends, h);
+    float leave[V];
+    if (ranks == 1) sh.ring(par, mine, q == 0, !ends, h, leave);
     else sh.cluster(par, mine, state, h);
     Vec<V> cv = lanes<V>([&](int i) { return h[i]; });
     const int rows = live ? len - tg * kScanTile : 0;
@@ -132,11 +133,13 @@ scan_bwd_kernel(ScanArgs a, ScanBwdIo io, float *dA_part, int cblocks) {
 #pragma unroll
     for (int j = kScanTile - 1; j >= 0; --j) {
       const Vec<V> grad = add(ds.at(par, j, tg, lane), cv);
-      const Vec<V> z = gs.at(par, j, tg, lane), l = kLogit ? gate.log(z) : z;
+      const Vec<V> z = gs.at(par, j, tg, lane);
+      Vec<V> slope, l = z;
+      if (kLogit) l = gate.log(z, slope);
       cv = mul(al[j], grad);
       Vec<V> out = mul(cv, meet[j]);
       if (kLogit) {
-        out = mul(out, gate.slope(z, l));
+        out = mul(out, slope);
         dA = fma(out, lanes<V>([&](int i) { return isinf(z.get(i)) ? 0.f : z.get(i); }), dA);  // (out is 0 at z = +-inf)
       }
       if (j < rows) {
@@ -144,11 +147,9 @@ scan_bwd_kernel(ScanArgs a, ScanBwdIo io, float *dA_part, int cblocks) {
         store<V>(dg + (unsigned)(j * D), out);
       }
     }
-    if (ranks == 1 && ends && io.ds0 && live && tg == 0) {
-      mine.run(h);
+    if (ranks == 1 && ends && io.ds0 && live && sh.group == L::kGroups - 1)
 #pragma unroll
-      for (int i = 0; i < V; ++i) io.ds0[chain + i] = h[i];
-    }
+      for (int i = 0; i < V; ++i) io.ds0[chain + i] = leave[i];
     __syncwarp();
     fetch(V == 2 ? par : 0, V == 2 ? q + 2 * step : q + step);
   }
