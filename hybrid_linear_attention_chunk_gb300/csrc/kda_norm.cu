@@ -109,33 +109,38 @@ struct Shape {
 };
 
 // Sums of kN (at most 8) values over the threads of a row, the same in each of
-// them.  `sh`: a row of 8 for each warp of the block, not in use by an earlier sum.
-// Behind the warps' own sums each warp adds up the row's warps again: lane l takes
-// value l % 8 of every fourth warp from l / 8, two steps join these, and the
-// lanes 0 .. kN - 1 hand the values out (an eighth of the instructions of every
-// thread reading every warp's values).
+// them.  `sh`: 16 warps' values of each, not in use by an earlier sum.
+// Behind the warps' own sums, one value is read from every warp of the row by
+// every thread.  With more of them that would be most of a row's instructions, so
+// lane l takes value l % 8 of every fourth warp from l / 8, two steps join these,
+// and the lanes 0 .. kN - 1 hand the values out.
 template <int kThreads, int kN>
-__device__ __forceinline__ void row_sum(float (&v)[kN], float (*sh)[8]) {
+__device__ __forceinline__ void row_sum(float (&v)[kN], float (*sh)[16]) {
 #pragma unroll
   for (int k = 0; k < kN; ++k)
 #pragma unroll
     for (int off = (kThreads < 32 ? kThreads : 32) / 2; off > 0; off >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], off);
   if constexpr (kThreads > 32) {
     constexpr int kWarps = kThreads / 32;
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, first = threadIdx.x / kThreads * kWarps;
     if (lane == 0)
 #pragma unroll
-      for (int k = 0; k < kN; ++k) sh[threadIdx.x >> 5][k] = v[k];
+      for (int k = 0; k < kN; ++k) sh[k][threadIdx.x >> 5] = v[k];
     __syncthreads();
-    const int first = threadIdx.x / kThreads * kWarps;
-    float s = 0.f;
+    if constexpr (kN == 1) {
+      v[0] = 0.f;
 #pragma unroll
-    for (int i = 0; i < kWarps; i += 4)
-      if (i + lane / 8 < kWarps && lane % 8 < kN) s += sh[first + i + lane / 8][lane % 8];
-    s += __shfl_xor_sync(0xffffffffu, s, 8);
-    s += __shfl_xor_sync(0xffffffffu, s, 16);
+      for (int i = 0; i < kWarps; ++i) v[0] += sh[0][first + i];
+    } else {
+      float s = 0.f;
 #pragma unroll
-    for (int k = 0; k < kN; ++k) v[k] = __shfl_sync(0xffffffffu, s, k);
+      for (int i = 0; i < kWarps; i += 4)
+        if (i + lane / 8 < kWarps && lane % 8 < kN) s += sh[lane % 8][first + i + lane / 8];
+      s += __shfl_xor_sync(0xffffffffu, s, 8);
+      s += __shfl_xor_sync(0xffffffffu, s, 16);
+#pragma unroll
+      for (int k = 0; k < kN; ++k) v[k] = __shfl_sync(0xffffffffu, s, k);
+    }
   }
 }
 
@@ -146,7 +151,7 @@ __global__ void __launch_bounds__(S::kBlock) norm_fwd_kernel(NormArgs a) {
   using T = typename S::T;
   using R = typename S::R;
   constexpr int V = S::V, C = S::kChunks, P = S::P, N = S::kVecs, K = S::rows();
-  __shared__ float sh[2][16][8];
+  __shared__ float sh[2][K][16];
   const int t = threadIdx.x % S::kThreads;
   const long long row = ((long long)blockIdx.x * S::kGroups + threadIdx.x / S::kThreads) * K;
   const size_t base = (size_t)row * a.width;
@@ -266,7 +271,7 @@ __global__ void __launch_bounds__(S::kBlock, S::kBlock > 256 ? 1 : 2) norm_bwd_k
   using St = RowStages<S>;
   constexpr int V = S::V, C = S::kChunks, P = S::P, N = S::kVecs;
   extern __shared__ __align__(16) uint4 stage_mem[];
-  __shared__ float sh1[2][16][8], sh2[2][16][8];
+  __shared__ float sh1[2][1][16], sh2[2][5][16];
   const int t = threadIdx.x % S::kThreads, group = threadIdx.x / S::kThreads;
   const float inv = 1.f / (float)a.width;
   Vec<P> p1[C][N], ps[C][N], p2[C][N];
@@ -279,26 +284,26 @@ __global__ void __launch_bounds__(S::kBlock, S::kBlock > 256 ? 1 : 2) norm_bwd_k
 
   Piece<T, V> y[C], g[C], dn[C];
   Piece<R, V> res[C], dout[C];
-  const void *const src[5] = {a.y, a.gate, io.dn, a.res, io.dout};
+  // absent tensors: no bytes of y
+  const void *const src[5] = {a.y, a.gate ? a.gate : a.y, io.dn ? io.dn : a.y, a.res ? a.res : a.y, io.dout ? io.dout : a.y};
+  const bool here[5] = {true, a.gate != nullptr, io.dn != nullptr, a.res != nullptr, io.dout != nullptr};
   // `row` into stage `k`, as zeros past the last row and for absent tensors
   auto fetch = [&](long long row, int k) {
     if constexpr (V == 8) {
-      uint4 *to = stage_mem + (size_t)k * (St::kStage / 16) + threadIdx.x;
+      unsigned to = (unsigned)__cvta_generic_to_shared(stage_mem + (size_t)k * (St::kStage / 16) + threadIdx.x);
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         const int j = (c * S::kThreads + t) * V;
         const bool in = j < a.width && row < a.rows;
+        const size_t at = in ? (size_t)row * a.width + j : 0;
 #pragma unroll
         for (int m = 0; m < 5; ++m) {
           constexpr int kT = (int)sizeof(T), kR = (int)sizeof(R);
-          const int size = m < 3 ? kT : kR;
-          const bool ok = in && src[m];
-          const char *from = ok ? static_cast<const char *>(src[m]) + ((size_t)row * a.width + j) * size
-                                : static_cast<const char *>(a.y);
+          const char *from = static_cast<const char *>(src[m]) + (here[m] ? at * (m < 3 ? kT : kR) : 0);
+          const int size = in && here[m] ? 16 : 0;
 #pragma unroll
-          for (int h = 0; h < (m < 3 ? kT : kR) / 2; ++h, to += S::kBlock)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((unsigned)__cvta_generic_to_shared(to)),
-                         "l"(from + 16 * h), "r"(ok ? 16 : 0)
+          for (int h = 0; h < (m < 3 ? kT : kR) / 2; ++h, to += 16 * S::kBlock)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from + (here[m] ? 16 * h : 0)), "r"(size)
                          : "memory");
         }
       }
