@@ -147,7 +147,8 @@ __device__ __forceinline__ void row_sum(float (&v)[kN], float (*sh)[16]) {
 // Forward.  A group takes kRows rows at once where a row is only a piece or two
 // per thread, so that weights and addresses are spread over several rows.
 template <typename S>
-__global__ void __launch_bounds__(S::kBlock) norm_fwd_kernel(NormArgs a) {
+__global__ void __launch_bounds__(S::kBlock, (sizeof(typename S::T) + sizeof(typename S::R) <= 6 ? 1024 : 768) / S::kBlock)
+norm_fwd_kernel(NormArgs a) {
   using T = typename S::T;
   using R = typename S::R;
   constexpr int V = S::V, C = S::kChunks, P = S::P, N = S::kVecs, K = S::rows();
@@ -246,7 +247,9 @@ constexpr int kBwdBlocks = 304;  // at most (two to an SM); a block leaves one s
 //     sum q out,  sum d_out tr,  sum q tr,  sum out tr
 // since sum dy yh = sum D tr = sum (d_out + r2 q - back out) tr.  So a row takes
 // two sums over its threads, not three.  Blocks walk over rows; a thread owns
-// fixed channels, so its sums of the weight gradients stay in registers.
+// fixed channels, so its sums of the weight gradients stay in registers: with
+// b = yh w1 s (s the gate) and du yh = D scale s yh, both d_scale = w1 Q and
+// d_post_weight = scale Q come from Q = sum over rows of D s yh.
 //
 // In pieces of 8 elements the rows come in by asynchronous copies, up to two
 // rows ahead as far as shared memory goes, each thread into places of its own that no other thread reads.
@@ -274,11 +277,11 @@ __global__ void __launch_bounds__(S::kBlock, S::kBlock > 256 ? 1 : 2) norm_bwd_k
   __shared__ float sh1[2][1][16], sh2[2][5][16];
   const int t = threadIdx.x % S::kThreads, group = threadIdx.x / S::kThreads;
   const float inv = 1.f / (float)a.width;
-  Vec<P> p1[C][N], ps[C][N], p2[C][N];
+  Vec<P> p1[C][N], p2[C][N];  // Q, and d_pre_weight
 #pragma unroll
   for (int c = 0; c < C; ++c)
 #pragma unroll
-    for (int i = 0; i < N; ++i) p1[c][i] = ps[c][i] = p2[c][i] = all<P>(0.f);
+    for (int i = 0; i < N; ++i) p1[c][i] = p2[c][i] = all<P>(0.f);
   const long long step = (long long)gridDim.x * S::kGroups;
   const long long first = (long long)blockIdx.x * S::kGroups + group;
 
@@ -418,13 +421,12 @@ __global__ void __launch_bounds__(S::kBlock, S::kBlock > 256 ? 1 : 2) norm_bwd_k
           sg = sigmoid_of(g[c].get(i), e);
           rest = sigmoid_rest(sg, e);
         }
-        const Vec<P> b = mul(mul(yh, w1[i]), sg), o = fma(b, sc[i], res[c].get(i));
+        const Vec<P> ys = mul(yh, sg), b = mul(ys, w1[i]), o = fma(b, sc[i], res[c].get(i));
         const Vec<P> n = mul(dn[c].get(i), all<P>(r2));
         const Vec<P> D = fma(n, w2[i], fma(o, all<P>(-back), dout[c].get(i)));
         p2[c][i] = fma(n, o, p2[c][i]);
-        ps[c][i] = fma(D, b, ps[c][i]);
+        p1[c][i] = fma(D, ys, p1[c][i]);
         const Vec<P> db = mul(D, sc[i]), du = mul(db, sg);
-        p1[c][i] = fma(du, yh, p1[c][i]);
         dres[i] = D;
         dgate[i] = mul(mul(db, b), rest);
         dy[i] = a.post ? mul(fma(du, w1[i], mul(yh, all<P>(-m))), all<P>(r1)) : du;
@@ -440,13 +442,13 @@ __global__ void __launch_bounds__(S::kBlock, S::kBlock > 256 ? 1 : 2) norm_bwd_k
   // the groups of a block in order, then one row of partials
   float *sums = reinterpret_cast<float *>(stage_mem);  // [kGroups][max_width]
 #pragma unroll
-  for (int k = 0; k < 3; ++k) {
+  for (int k = 0; k < 2; ++k) {
     float *to = part + ((size_t)k * gridDim.x + blockIdx.x) * a.width;
     if constexpr (S::kGroups > 1) __syncthreads();
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int j = (c * S::kThreads + t) * V;
-      const Vec<P>(&p)[N] = k == 0 ? p1[c] : k == 1 ? ps[c] : p2[c];
+      const Vec<P>(&p)[N] = k == 0 ? p1[c] : p2[c];
       if constexpr (S::kGroups > 1) put(sums + group * S::max_width() + j, p);
       else if (j < a.width) put(to + j, p);
     }
@@ -464,21 +466,25 @@ __global__ void __launch_bounds__(S::kBlock, S::kBlock > 256 ? 1 : 2) norm_bwd_k
 
 // Weight gradients: the blocks' partials summed, 32 columns and 16 strides of
 // blocks to a CTA.
-__global__ void __launch_bounds__(512) norm_weights_kernel(const float *part, int blocks, int width, NormBwdIo io) {
+__global__ void __launch_bounds__(512) norm_weights_kernel(NormArgs a, const float *part, int blocks, NormBwdIo io) {
   const int lane = threadIdx.x & 31, stride = threadIdx.x >> 5, j = blockIdx.x * 32 + lane, k = blockIdx.y;
-  float *out = k == 0 ? io.dw1 : k == 1 ? io.dsc : io.dw2;
-  if (!out) return;
+  if (k == 0 ? !io.dw1 && !io.dsc : !io.dw2) return;
   __shared__ float sh[16][32];
   float s = 0.f;
-  if (j < width)
-    for (int b = stride; b < blocks; b += 16) s += part[((size_t)k * blocks + b) * width + j];
+  if (j < a.width)
+    for (int b = stride; b < blocks; b += 16) s += part[((size_t)k * blocks + b) * a.width + j];
   sh[stride][lane] = s;
   __syncthreads();
-  if (stride == 0 && j < width) {
+  if (stride == 0 && j < a.width) {
     s = 0.f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) s += sh[i][lane];
-    out[j] = s;
+    if (k == 1) {
+      io.dw2[j] = s;
+    } else {
+      if (io.dw1) io.dw1[j] = a.sc ? s * a.sc[j] : s;
+      if (io.dsc) io.dsc[j] = a.w1 ? s * a.w1[j] : s;
+    }
   }
 }
 
@@ -498,14 +504,16 @@ template <typename S> cudaError_t bwd(const NormArgs &a, const NormBwdIo &io, fl
   norm_bwd_kernel<S><<<blocks, S::kBlock, smem, s>>>(a, io, weights ? ws : nullptr);
   e = cudaGetLastError();
   if (e != cudaSuccess || !weights) return e;
-  norm_weights_kernel<<<dim3((a.width + 31) / 32, 3), 512, 0, s>>>(ws, blocks, a.width, io);
+  norm_weights_kernel<<<dim3((a.width + 31) / 32, 2), 512, 0, s>>>(a, ws, blocks, io);
   return cudaGetLastError();
 }
 
 // Calls f with the row shape for this width: pieces of 8 elements when every
 // row of every tensor starts on 16 bytes, else single elements.  Backward: one
-// piece per thread as far as threads go, for the registers of the three weight
-// sums.  Forward: 2 narrow rows at once when there are many
+// piece per thread mostly, for the registers of the weights' sums; two in blocks
+// of 256 for rows up to 4096, two blocks to an SM (16384 x 4096 forward and
+// backward: 362 us against 399 in blocks of 512), but for all-fp32 rows, whose
+// copies leave room for one block only (905 against 950).  Forward: 2 narrow rows at once when there are many
 // (262144 rows of 128: 36.9 us against 43.4 of one and 41.0 of four at once).
 template <typename T, typename R, bool kBwd, typename F>
 cudaError_t with_shape(int width, bool vectors, bool many, F f) {
@@ -519,7 +527,10 @@ cudaError_t with_shape(int width, bool vectors, bool many, F f) {
     if (width <= 512) return f(Shape<T, R, 8, kBwd ? 1 : 2, kBwd ? 64 : 32>());
     if (width <= 1024) return f(Shape<T, R, 8, 1, 128>());
     if (width <= 2048) return f(Shape<T, R, 8, 1, 256>());
-    if (width <= 4096) return f(Shape<T, R, 8, kBwd ? 1 : 2, kBwd ? 512 : 256>());
+    if (width <= 4096) {
+      if constexpr (kBwd && sizeof(T) + sizeof(R) > 6) return f(Shape<T, R, 8, 1, 512>());
+      else return f(Shape<T, R, 8, 2, 256>());
+    }
     return f(Shape<T, R, 8, 2, 512>());
   }
   if (width <= 128) return f(Shape<T, R, 1, 4, 32>());
@@ -543,7 +554,7 @@ template <int kN> bool on_16_bytes(const NormArgs &a, const void *const (&p)[kN]
 
 }  // namespace
 
-size_t norm_bwd_workspace_bytes(int width) { return (size_t)3 * kBwdBlocks * width * sizeof(float); }
+size_t norm_bwd_workspace_bytes(int width) { return (size_t)2 * kBwdBlocks * width * sizeof(float); }
 
 cudaError_t launch_norm_fwd(const NormArgs &a, cudaStream_t s) {
   if (a.rows == 0) return cudaSuccess;
