@@ -456,15 +456,15 @@ def _arg(name, t, shape, dtype, index):
     a non-null stand-in."""
     if t is None:
         return None
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+        return t.data_ptr() or 256
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     if t.get_device() != index:
         raise ValueError(f"{name} must be on CUDA device {index}, not {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr() or 256
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _elsewhere(index, stream):

@@ -167,6 +167,11 @@ template <int kLeft> __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
+__device__ __forceinline__ float clamp_126(float x) {
+  asm("min.NaN.f32 %0, %0, %1;\n\tmax.NaN.f32 %0, %0, %2;" : "+f"(x) : "f"(126.f), "f"(-126.f));
+  return x;
+}
+
 // How a token's alpha and 1 - alpha come from its log-decay, or from its logit
 // through r = Sigmoid(s z), g = g_min r.  `log` is g or r; tile sums of it give
 // the tile's log-decay as log_unit() times the sum.
@@ -191,14 +196,16 @@ struct Gate {
     const Vec<V> d = add(all<V>(1.f), lanes<V>([&](int i) { return fast_exp2(e.get(i)); }));
     return lanes<V>([&](int i) { return fast_rcp(d.get(i)); });
   }
-  // The same, with dg/dz: g (1 - Sigmoid) s.  1 - r below a half, 2^(ns z) r
-  // above it (where r is near 1, and the power is finite).
-  __device__ __forceinline__ Vec<V> log(Vec<V> z, Vec<V> &slope) const {
-    const Vec<V> x = mul(ns, z), e = lanes<V>([&](int i) { return fast_exp2(x.get(i)); });
+  // The same, with dg/dz = g (1 - Sigmoid) s and `x` = -s log2(e) z.  With e = 2^x,
+  // Sigmoid = r = 1 / (1 + e) and 1 - Sigmoid = e r.  x is held in +-126 (a NaN
+  // passes), where e is finite and nothing but the last 1e-38 of r is lost: so
+  // z = +-inf has slope 0, and x times a gradient is finite there.
+  __device__ __forceinline__ Vec<V> log(Vec<V> z, Vec<V> &slope, Vec<V> &x) const {
+    const Vec<V> v = mul(ns, z);
+    x = lanes<V>([&](int i) { return clamp_126(v.get(i)); });
+    const Vec<V> e = lanes<V>([&](int i) { return fast_exp2(x.get(i)); });
     const Vec<V> d = add(all<V>(1.f), e), r = lanes<V>([&](int i) { return fast_rcp(d.get(i)); });
-    const Vec<V> er = mul(e, r), below = fma(r, all<V>(-1.f), all<V>(1.f));
-    const Vec<V> rest = lanes<V>([&](int i) { return r.get(i) <= 0.5f ? below.get(i) : er.get(i); });
-    slope = mul(mul(mul(ns, all<V>(-unit / kLog2e)), r), rest);
+    slope = mul(mul(mul(ns, all<V>(-unit / kLog2e)), r), mul(e, r));
     return r;
   }
   __device__ __forceinline__ Vec<V> alpha(Vec<V> l) const {

@@ -134,13 +134,13 @@ scan_bwd_kernel(ScanArgs a, ScanBwdIo io, float *dA_part, int cblocks) {
     for (int j = kScanTile - 1; j >= 0; --j) {
       const Vec<V> grad = add(ds.at(par, j, tg, lane), cv);
       const Vec<V> z = gs.at(par, j, tg, lane);
-      Vec<V> slope, l = z;
-      if (kLogit) l = gate.log(z, slope);
+      Vec<V> slope, scaled, l = z;
+      if (kLogit) l = gate.log(z, slope, scaled);
       cv = mul(al[j], grad);
       Vec<V> out = mul(cv, meet[j]);
       if (kLogit) {
         out = mul(out, slope);
-        dA = fma(out, lanes<V>([&](int i) { return isinf(z.get(i)) ? 0.f : z.get(i); }), dA);  // (out is 0 at z = +-inf)
+        dA = fma(out, scaled, dA);
       }
       if (j < rows) {
         store<V>(dx + (unsigned)(j * D), kComp ? mul(grad, gate.one_minus(l, al[j])) : grad);
@@ -161,7 +161,8 @@ scan_bwd_kernel(ScanArgs a, ScanBwdIo io, float *dA_part, int cblocks) {
     cluster_sync_all();  // (not barrier 0, at which the ring's warp 0 may still wait)
     float *sums = reinterpret_cast<float *>(smem);
 #pragma unroll
-    for (int i = 0; i < V; ++i) sums[(sh.warp * L::kGroups + sh.group) * L::kWide + wide + i] = dA.get(i);
+    for (int i = 0; i < V; ++i)
+      sums[(sh.warp * L::kGroups + sh.group) * L::kWide + wide + i] = dA.get(i) / gate.ns.get(i);  // dz z = dz scaled / ns
     __syncthreads();
     for (int i = threadIdx.x; i < L::kWide && c0 + i < D; i += blockDim.x) {
       float s = 0.f;
