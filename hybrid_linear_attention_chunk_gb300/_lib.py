@@ -493,6 +493,7 @@ def _there(call, index, stream, tensors):
         for t in result.values() if isinstance(result, dict) else result:
             if t is not None:
                 t.record_stream(before)
+                t.record_stream(stream)
     return result
 
 
@@ -513,12 +514,16 @@ class _Sized:
 
 @functools.lru_cache(maxsize=512)
 def _scan_sized(*fields) -> _Sized:
+    if max(fields) >= 1 << 31:  # (ctypes would cut it off)
+        raise ValueError("a size passes 32 bits")
     return _Sized(KdaScanDesc(*fields))
 
 
 @functools.lru_cache(maxsize=512)
-def _norm_sized(*fields) -> _Sized:
-    return _Sized(KdaNormDesc(*fields))
+def _norm_sized(rows, width, *rest) -> _Sized:
+    if max(rows, width) >= 1 << 31:
+        raise ValueError("a size passes 32 bits")
+    return _Sized(KdaNormDesc(rows, width, *rest))
 
 
 def _scan_call(x, decay, A_log, initial_state, cu_seqlens, write, B, validate):

@@ -5,6 +5,7 @@
 // a group of kThreads threads (half a warp to 512 threads, by the width) holds
 // kChunks pieces of V elements per thread.  Sums run in fp32, per thread, then
 // by shuffles, then over the warps in order.
+#include <initializer_list>
 #include <type_traits>
 
 #include "kda_internal.cuh"
@@ -497,7 +498,7 @@ template <typename S> cudaError_t fwd(const NormArgs &a, cudaStream_t s) {
 template <typename S> cudaError_t bwd(const NormArgs &a, const NormBwdIo &io, float *ws, cudaStream_t s) {
   const bool weights = io.dw1 || io.dsc || io.dw2;
   const long long groups = (a.rows + S::kGroups - 1) / S::kGroups, most = S::kBlock > 256 ? kBwdBlocks / 2 : kBwdBlocks;
-  const int blocks = (int)(groups < 1 ? 1 : groups < most ? groups : most);
+  const int blocks = (int)(groups < most ? groups : most);
   constexpr int smem = RowStages<S>::kBytes;
   cudaError_t e = cudaFuncSetAttribute(norm_bwd_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -563,6 +564,12 @@ cudaError_t launch_norm_fwd(const NormArgs &a, cudaStream_t s) {
 }
 
 cudaError_t launch_norm_bwd(const NormArgs &a, const NormBwdIo &io, void *ws, cudaStream_t s) {
+  if (a.rows == 0) {
+    cudaError_t e = cudaSuccess;
+    for (float *w : {io.dw1, io.dsc, io.dw2})
+      if (w && e == cudaSuccess) e = cudaMemsetAsync(w, 0, sizeof(float) * a.width, s);
+    return e;
+  }
   const void *const p[] = {a.y, a.res, a.gate, a.w1, a.sc, a.w2, io.dout, io.dn, io.dy, io.dres, io.dgate};
   return with_types<true>(a, on_16_bytes(a, p),
                           [&](auto shape) { return bwd<decltype(shape)>(a, io, static_cast<float *>(ws), s); });

@@ -146,7 +146,8 @@ __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(ScanArgs a) {
 }
 
 __global__ void __launch_bounds__(256) validate_scan_kernel(ScanArgs a, int *flag) {
-  const size_t n = (size_t)a.T_total * a.D, stride = (size_t)gridDim.x * blockDim.x;
+  const int tokens = a.cu ? min(max(a.cu[a.N], 0), a.T_total) : a.T_total;  // rows behind the last sequence are not read
+  const size_t n = (size_t)tokens * a.D, stride = (size_t)gridDim.x * blockDim.x;
   int bad = 0;
   for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += stride) {
     const float g = ld_elem(a.g, i, a.gdt());

@@ -158,6 +158,14 @@ def test_norm_bwd_refusals(lib):
     assert nbwd(lib, d(), dsc=9 * FAKE, dw1=9 * FAKE) == -8 and nbwd(lib, d(), dy=4 * FAKE) == -8
 
 
+def test_sizes_past_32_bits_are_refused():
+    from hybrid_linear_attention_chunk_gb300 import _lib
+    with pytest.raises(ValueError):
+        _lib._scan_sized(1, (1 << 31) + 5, 1, 1, 0, 1, 0, 0, 0)
+    with pytest.raises(ValueError):
+        _lib._norm_sized(1 << 31, 8, 1, 1, 1, 1e-6, 1e-6)
+
+
 def test_binding_refusals():
     import hybrid_linear_attention_chunk_gb300 as kda
     x = torch.randn(8, 2, 4)

@@ -92,6 +92,40 @@ def test_forward_and_gradients(kda, shape, dtype, gate, write):
         assert (gr["dx"][rows:] == mark).all() and (gr["d_decay"][rows:] == mark).all()
 
 
+LAYOUTS = {
+    # few chains, long: a cluster of CTAs along the sequence; and the same elementwise
+    "cluster": ([5000, 90], 1, 1, 32),
+    "cluster_elementwise": ([1500, 90], 1, 1, 33),
+    # up to one block of 16 channels for an SM: rings of 16 (8 in fp32) warps, several rounds
+    "ring16": ([1500], 2, 25, 64),
+    # more of them: rings of 8 warps
+    "ring8": ([700, 40], 3, 24, 64),
+    # enough blocks of 64 channels
+    "wide": ([300, 129, 128, 15], 5, 48, 64),
+}
+
+
+@pytest.mark.parametrize("dtype,gate", KINDS)
+@pytest.mark.parametrize("shape", list(LAYOUTS))
+def test_every_layout(kda, shape, dtype, gate):
+    """Shapes on both sides of each rule that lays chains over the GPU."""
+    write = "complement" if gate != "fp32" else "one"
+    a = make(LAYOUTS[shape], dtype, gate, seed=40)
+    rows = live_rows(a)
+    want = definition(a, write, bwd=True)
+    o, fs, states = kda.kda_scan_fwd(a["x"], a["decay"], a["A_log"], G_MIN, a["initial_state"], a["cu_seqlens"],
+                                     write=write, want_states=True)
+    check(o, want["out"], a["x"].dtype, rows, "out")
+    check(fs, want["final_state"], torch.float32, None, "final_state")
+    gr = kda.kda_scan_bwd(a["x"], a["decay"], a["d_out"], a["A_log"], G_MIN, a["initial_state"], a["dST"],
+                          a["cu_seqlens"], states, write=write)
+    check(gr["dx"], want["dx"], a["x"].dtype, rows, "dx")
+    check(gr["d_decay"], want["d_decay"], a["decay"].dtype, rows, "d_decay")
+    check(gr["d_initial_state"], want["d_initial_state"], torch.float32, None, "d_initial_state")
+    if a["A_log"] is not None:
+        check(gr["dA_log"], want["dA_log"], torch.float32, None, "dA_log")
+
+
 @pytest.mark.parametrize("dtype,gate", KINDS)
 def test_without_states(kda, dtype, gate):
     """No initial state, no final state wanted, no final-state gradient."""
@@ -356,6 +390,62 @@ def test_malformed_cu_seqlens(kda):
     kda.kda_scan_fwd(x, g, cu_seqlens=cu, out=buf[64:128])
     torch.cuda.synchronize()
     assert (buf[:64] == 5).all() and (buf[128:] == 5).all()
+
+
+def test_rows_behind_the_last_sequence_are_not_read(kda):
+    """NaN there passes validate mode and reaches nothing."""
+    a = make(([40, 23], 9, 2, 24), "fp32", "logit", seed=41)
+    clean = kda.kda_scan_bwd(a["x"], a["decay"], a["d_out"], a["A_log"], G_MIN, a["initial_state"], a["dST"], a["cu_seqlens"])
+    o0, fs0 = kda.kda_scan_fwd(a["x"], a["decay"], a["A_log"], G_MIN, a["initial_state"], a["cu_seqlens"])
+    for n in ("x", "decay", "d_out"):
+        a[n][63:] = float("nan")
+    o, fs = kda.kda_scan_fwd(a["x"], a["decay"], a["A_log"], G_MIN, a["initial_state"], a["cu_seqlens"], validate=True)
+    gr = kda.kda_scan_bwd(a["x"], a["decay"], a["d_out"], a["A_log"], G_MIN, a["initial_state"], a["dST"], a["cu_seqlens"],
+                          validate=True)
+    assert torch.equal(o[:63], o0[:63]) and torch.equal(fs, fs0)
+    assert torch.equal(gr["dA_log"], clean["dA_log"]) and torch.equal(gr["d_initial_state"], clean["d_initial_state"])
+    assert torch.equal(gr["dx"][:63], clean["dx"][:63])
+
+
+def test_lowest_values_as_masks(kda):
+    """The type's lowest value in place of -inf: as a log-decay it forgets, as a logit it keeps."""
+    for dt in (torch.float32, torch.bfloat16):
+        low = torch.finfo(dt).min
+        x = torch.randn(50, 1, 16, device=DEV).to(dt)
+        g = torch.full_like(x, -0.01)
+        g[20:23] = low
+        g2 = g.clone()
+        g2[20:23] = -float("inf")
+        s0 = torch.full((1, 1, 16), 1e20, device=DEV)
+        for write in ("one", "complement"):
+            p, q = (kda.kda_scan_fwd(x, v, initial_state=s0, write=write) for v in (g, g2))
+            assert torch.equal(p[0], q[0]) and torch.equal(p[1], q[1])
+            assert torch.equal(p[0][20:23], x[20:23])
+            A = torch.zeros(1, device=DEV)
+            r = kda.kda_scan_bwd(x, g, x, A, d_final_state=s0, write=write)
+            r2 = kda.kda_scan_bwd(x, g2, x, A, d_final_state=s0, write=write)
+            for n in r:
+                assert r[n].isfinite().all() and torch.equal(r[n], r2[n]), n
+
+
+@pytest.mark.skipif(torch.cuda.is_available() and torch.cuda.mem_get_info()[1] < 80 << 30, reason="needs 80 GB")
+def test_offsets_past_32_bits(kda):
+    """2.3e9 elements: the tail behind a token that forgets, against a call on the tail alone."""
+    T, H, d, cut = 70010, 256, 128, 69950
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(42)
+    x = torch.randn(T, H, d, generator=gen, device=DEV, dtype=torch.bfloat16)
+    g = torch.full_like(x, -0.125)
+    g[cut] = -float("inf")
+    o, fs, st = kda.kda_scan_fwd(x, g, want_states=True)
+    o2, fs2 = kda.kda_scan_fwd(x[cut:], g[cut:])
+    # the two calls cut the tail into tiles at other tokens: fp32 roundings, then one of bf16
+    assert float((o[cut:].float() - o2.float()).norm() / o2.float().norm()) <= 2.0 ** -8
+    assert float((fs - fs2).norm() / fs2.norm()) <= 1e-5
+    gr = kda.kda_scan_bwd(x, g, x, states=st)
+    g2 = kda.kda_scan_bwd(x[cut:], g[cut:], x[cut:])
+    for n in ("dx", "d_decay"):
+        assert float((gr[n][cut:].float() - g2[n].float()).norm() / g2[n].float().norm()) <= 2.0 ** -8, n
 
 
 def test_value_checks(kda):
