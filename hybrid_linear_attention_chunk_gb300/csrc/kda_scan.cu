@@ -57,8 +57,8 @@ __global__ void __launch_bounds__(32 * FwdSmem<X, G, kLogit, L>::kMaxWarps, 1) s
   int tw = bos + (sh.rank * sh.warps + sh.warp) * L::kTokens;  // the warp's first token
   // a token past the end has alpha = 1 (z = -inf) and adds nothing
   auto fetch = [&](int stage, int t) {
-    gs.issue(stage, a.g, D, t, c0, eos - t, lane);
-    xs.issue(stage, a.x, D, t, c0, eos - t, lane);
+    gs.issue(stage, a.g, D, t, c0, eos - t, sh.group, lane);
+    xs.issue(stage, a.x, D, t, c0, eos - t, sh.group, lane);
     if (V == 2) copies_commit();
   };
   if (bos < eos) {
@@ -172,18 +172,22 @@ cudaError_t fwd_l(const ScanArgs &a, int warps, int ranks, cudaStream_t s) {
                           FwdSmem<X, G, kLogit, L>::bytes(warps, ranks), s, a, (a.D + L::kWide - 1) / L::kWide);
 }
 
-template <typename X, typename G, bool kLogit, bool kComp>
+template <typename X, typename G, bool kLogit, bool kComp, typename Wide, typename Narrow>
 cudaError_t fwd_c(const ScanArgs &a, cudaStream_t s) {
-  if (!scan_vectors(a.D, {{a.x, sizeof(X)}, {a.g, sizeof(G)}, {a.o, sizeof(X)}, {a.states, 4}}))
-    return fwd_l<X, G, kLogit, kComp, Layout<32, 1>>(a, 8, scan_ranks_elementwise(a), s);
-  const ScanPlan p = scan_plan(a, FwdSmem<X, G, kLogit, Layout<16, 2>>::kMaxWarps);
-  return p.narrow ? fwd_l<X, G, kLogit, kComp, Layout<16, 2>>(a, p.warps, p.ranks, s)
-                  : fwd_l<X, G, kLogit, kComp, Layout<64, 2>>(a, p.warps, p.ranks, s);
+  const ScanPlan p = scan_plan(a, Wide::V == 2, FwdSmem<X, G, kLogit, Narrow>::kMaxWarps);
+  return p.narrow ? fwd_l<X, G, kLogit, kComp, Narrow>(a, p.warps, p.ranks, s)
+                  : fwd_l<X, G, kLogit, kComp, Wide>(a, p.warps, p.ranks, s);
 }
 
 template <typename X, typename G, bool kLogit>
 cudaError_t fwd_t(const ScanArgs &a, cudaStream_t s) {
-  return a.complement ? fwd_c<X, G, kLogit, true>(a, s) : fwd_c<X, G, kLogit, false>(a, s);
+  using W = Layout<64, 2>;
+  using N = Layout<16, 2>;
+  using EW = Layout<32, 1>;
+  using EN = Layout<8, 1>;
+  if (!scan_vectors(a.D, {{a.x, sizeof(X)}, {a.g, sizeof(G)}, {a.o, sizeof(X)}, {a.states, 4}}))
+    return a.complement ? fwd_c<X, G, kLogit, true, EW, EN>(a, s) : fwd_c<X, G, kLogit, false, EW, EN>(a, s);
+  return a.complement ? fwd_c<X, G, kLogit, true, W, N>(a, s) : fwd_c<X, G, kLogit, false, W, N>(a, s);
 }
 
 template <typename X, typename G, bool kLogit, bool kComp, int V>

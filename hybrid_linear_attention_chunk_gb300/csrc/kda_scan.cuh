@@ -111,7 +111,7 @@ template <typename T, typename L, bool kPad> struct Tile<T, L, kPad, 2> {
   static constexpr int kBytes = kElems * (int)sizeof(T);
   T *buf;                                                   // [2][kTokens][kWide]
   __device__ __forceinline__ static int place(int r) { return (r & ~(kScanTile - 1)) | ((r ^ r / kScanTile) & (kScanTile - 1)); }
-  __device__ __forceinline__ void issue(int stage, const void *base, int D, int t, int c0, int len, int lane) {
+  __device__ __forceinline__ void issue(int stage, const void *base, int D, int t, int c0, int len, int, int lane) {
     T *dst = buf + stage * kElems;
     const int row = lane / kPerRow, col = (lane % kPerRow) * kChunk;
     const T *src = static_cast<const T *>(base) + ((size_t)t * D + c0 + col);
@@ -149,9 +149,11 @@ template <typename T, typename L, bool kPad> struct Tile<T, L, kPad, 2> {
 template <typename T, typename L, bool kPad> struct Tile<T, L, kPad, 1> {
   static constexpr int kBytes = 0;
   Raw<T, 1> v[kScanTile];
-  __device__ __forceinline__ void issue(int, const void *base, int D, int t, int c0, int len, int lane) {
-    const T *src = static_cast<const T *>(base) + ((size_t)t * D + c0 + lane);
-    if (c0 + lane >= D) len = 0;
+  // (a lane loads what it will use: group g's tokens)
+  __device__ __forceinline__ void issue(int, const void *base, int D, int t, int c0, int len, int g, int lane) {
+    const int c = c0 + lane % L::kLanes;
+    const T *src = static_cast<const T *>(base) + ((size_t)(t + g * kScanTile) * D + c);
+    len = c < D ? len - g * kScanTile : 0;
 #pragma unroll
     for (int j = 0; j < kScanTile; ++j) {
       v[j] = sizeof(T) == 2 ? (kPad ? 0xff80 : 0) : (kPad ? -INFINITY : 0.f);
@@ -397,27 +399,25 @@ struct ScanJoin {
 //   0.2 ms against 0.7.  When even those are at most one for an SM, CTAs of
 //   `most` warps, and clusters along the sequence while the grid has room for
 //   them and the sequences are longer than a round.
+//   The elementwise form has blocks of 32 and 8 channels, the narrow ones only
+//   when clusters alone would leave most SMs without work.
 struct ScanPlan {
   bool narrow;
   int warps, ranks;
 };
-inline ScanPlan scan_plan(const ScanArgs &a, int most) {
+inline ScanPlan scan_plan(const ScanArgs &a, bool vectors, int most) {
+  const int wide = vectors ? 64 : 32, narrow = wide / 4;
   const long long tokens = a.T_total / a.N;
-  const auto blocks = [&](int wide) { return (long long)((a.D + wide - 1) / wide) * a.N; };
-  ScanPlan p{blocks(64) < 152, 8, 1};
-  if (p.narrow) {
-    const long long b = blocks(16);
-    if (b <= 152 && tokens > 512) p.warps = most;
-    while (p.ranks < kScanMaxCluster && b * p.ranks * 2 <= 152 && (long long)p.ranks * p.warps * 64 < tokens) p.ranks *= 2;
-  }
+  const auto blocks = [&](int w) { return (long long)((a.D + w - 1) / w) * a.N; };
+  ScanPlan p{blocks(wide) < (vectors ? 152 : 40), 8, 1};
+  const long long b = blocks(p.narrow ? narrow : wide);
+  const int span = p.narrow ? 64 : 16;  // tokens of a warp
+  if (p.narrow && b <= 152 && tokens > 512) p.warps = most;
+  if (p.narrow || !vectors)
+    while (p.ranks < kScanMaxCluster && b * p.ranks * 2 <= (p.narrow ? 152 : 304) &&
+           (long long)p.ranks * p.warps * span < tokens)
+      p.ranks *= 2;
   return p;
-}
-// The elementwise form: blocks of 32 channels, a warp's tile 16 tokens.
-inline int scan_ranks_elementwise(const ScanArgs &a) {
-  const long long blocks = (long long)((a.D + 31) / 32) * a.N, tokens = a.T_total / a.N;
-  int ranks = 1;
-  while (ranks < kScanMaxCluster && blocks * ranks < 152 && (long long)ranks * 128 < tokens) ranks *= 2;
-  return ranks;
 }
 
 // Launches one cluster of `ranks` CTAs for each chain block.

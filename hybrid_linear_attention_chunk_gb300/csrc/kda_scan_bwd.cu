@@ -70,9 +70,9 @@ scan_bwd_kernel(ScanArgs a, ScanBwdIo io, float *dA_part, int cblocks) {
   auto length = [&](int q) { return q < tiles ? eos - first(q) : 0; };
   auto fetch = [&](int stage, int q) {
     const int t = first(q), len = length(q);
-    gs.issue(stage, a.g, D, t, c0, len, lane);
-    xs.issue(stage, a.x, D, t, c0, len, lane);
-    ds.issue(stage, io.dO, D, t, c0, len, lane);
+    gs.issue(stage, a.g, D, t, c0, len, tg, lane);
+    xs.issue(stage, a.x, D, t, c0, len, tg, lane);
+    ds.issue(stage, io.dO, D, t, c0, len, tg, lane);
     // the state before the lane's tile
     const bool ok = live && tg * kScanTile < len;
     const size_t slot = (size_t)(bos / kScanTile) + n + (t - bos) / kScanTile + tg;
@@ -204,22 +204,26 @@ cudaError_t bwd_l(const ScanArgs &a, const ScanBwdIo &io, float *part, int warps
                           BwdSmem<X, G, kLogit, L>::bytes(warps, ranks), s, a, io, part, (a.D + L::kWide - 1) / L::kWide);
 }
 
-template <typename X, typename G, bool kLogit, bool kComp>
+template <typename X, typename G, bool kLogit, bool kComp, typename Wide, typename Narrow>
 cudaError_t bwd_c(const ScanArgs &a, const ScanBwdIo &io, float *part, int *ranks, cudaStream_t s) {
-  if (!scan_vectors(a.D, {{a.x, sizeof(X)}, {a.g, sizeof(G)}, {io.dO, sizeof(X)}, {io.dx, sizeof(X)}, {io.dg, sizeof(G)},
-                          {a.states, 4}})) {
-    *ranks = scan_ranks_elementwise(a);
-    return bwd_l<X, G, kLogit, kComp, Layout<32, 1>>(a, io, part, 8, *ranks, s);
-  }
-  const ScanPlan p = scan_plan(a, BwdSmem<X, G, kLogit, Layout<16, 2>>::kMaxWarps);
+  const ScanPlan p = scan_plan(a, Wide::V == 2, BwdSmem<X, G, kLogit, Narrow>::kMaxWarps);
   *ranks = p.ranks;
-  return p.narrow ? bwd_l<X, G, kLogit, kComp, Layout<16, 2>>(a, io, part, p.warps, p.ranks, s)
-                  : bwd_l<X, G, kLogit, kComp, Layout<64, 2>>(a, io, part, p.warps, p.ranks, s);
+  return p.narrow ? bwd_l<X, G, kLogit, kComp, Narrow>(a, io, part, p.warps, p.ranks, s)
+                  : bwd_l<X, G, kLogit, kComp, Wide>(a, io, part, p.warps, p.ranks, s);
 }
 
 template <typename X, typename G, bool kLogit>
 cudaError_t bwd_t(const ScanArgs &a, const ScanBwdIo &io, float *part, int *ranks, cudaStream_t s) {
-  return a.complement ? bwd_c<X, G, kLogit, true>(a, io, part, ranks, s) : bwd_c<X, G, kLogit, false>(a, io, part, ranks, s);
+  using W = Layout<64, 2>;
+  using N = Layout<16, 2>;
+  using EW = Layout<32, 1>;
+  using EN = Layout<8, 1>;
+  if (!scan_vectors(a.D, {{a.x, sizeof(X)}, {a.g, sizeof(G)}, {io.dO, sizeof(X)}, {io.dx, sizeof(X)}, {io.dg, sizeof(G)},
+                          {a.states, 4}}))
+    return a.complement ? bwd_c<X, G, kLogit, true, EW, EN>(a, io, part, ranks, s)
+                        : bwd_c<X, G, kLogit, false, EW, EN>(a, io, part, ranks, s);
+  return a.complement ? bwd_c<X, G, kLogit, true, W, N>(a, io, part, ranks, s)
+                      : bwd_c<X, G, kLogit, false, W, N>(a, io, part, ranks, s);
 }
 
 cudaError_t bwd(const ScanArgs &a, const ScanBwdIo &io, float *part, int *ranks, cudaStream_t s) {
@@ -237,7 +241,7 @@ size_t slice_bytes(const ScanArgs &a) { return (size_t)a.H * kSlices * sizeof(do
 // Slices first (8-byte aligned), then one row of channel sums per sequence and
 // CTA of its cluster.  Alignment decides the cluster size, so the larger counts.
 size_t scan_dA_bytes(const ScanArgs &a) {
-  const int ranks = max(scan_plan(a, 8).ranks, scan_ranks_elementwise(a));
+  const int ranks = max(scan_plan(a, true, 8).ranks, scan_plan(a, false, 8).ranks);
   return slice_bytes(a) + (size_t)a.N * ranks * a.D * sizeof(float);
 }
 
