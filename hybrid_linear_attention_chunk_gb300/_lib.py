@@ -467,6 +467,11 @@ def _arg(name, t, shape, dtype, index):
     raise ValueError(f"{name} must be contiguous")
 
 
+def _new(t):
+    """Address of a tensor that this call has just made."""
+    return None if t is None else t.data_ptr() or 256
+
+
 def _elsewhere(index, stream):
     """Whether a call has to be made on another device or stream than the current ones."""
     if index < 0:
@@ -581,19 +586,22 @@ def kda_scan_fwd(x, decay, A_log=None, g_min=-5.0, initial_state=None, cu_seqlen
                                            write=write, validate=validate, want_final_state=want_final_state,
                                            want_states=want_states, B=B),
                       index, stream, (x, decay, A_log, initial_state, cu_seqlens, out, final_state, states))
+    given_out, given_final, kept = (_arg("out", out, x.shape, x.dtype, index),
+                                    _arg("final_state", final_state, state, torch.float32, index), None)
     if out is None:
         out = torch.empty_like(x)
+        given_out = _new(out)
     if final_state is None and want_final_state:
         final_state = torch.empty(state, dtype=torch.float32, device=x.device)
+        given_final = _new(final_state)
     if want_states or states is not None:
         n = sized.size("kda_scan_states_size") // 4
         if states is None:
             states = torch.empty(n, dtype=torch.float32, device=x.device)
-        kept = _arg("states", states, (n,), torch.float32, index)
-    else:
-        kept = None
-    st = lib.kda_scan_fwd(sized.ref, *ins, g_min, s0, cu, _arg("out", out, x.shape, x.dtype, index),
-                          _arg("final_state", final_state, state, torch.float32, index), kept, _current_stream(index))
+            kept = _new(states)
+        else:
+            kept = _arg("states", states, (n,), torch.float32, index)
+    st = lib.kda_scan_fwd(sized.ref, *ins, g_min, s0, cu, given_out, given_final, kept, _current_stream(index))
     if st:
         _check(st, "kda_scan_fwd")
     return (out, final_state) if states is None else (out, final_state, states)
@@ -629,16 +637,18 @@ def kda_scan_bwd(x, decay, d_out, A_log=None, g_min=-5.0, initial_state=None, d_
         grads = {"dx": torch.empty_like(x), "d_decay": torch.empty_like(decay),
                  "dA_log": None if A_log is None else torch.empty_like(A_log),
                  "d_initial_state": (torch.empty(state, dtype=f32, device=x.device) if want_d_initial_state else None)}
+        outs = [_new(t) for t in grads.values()]
+    else:
+        outs = (_arg("dx", grads["dx"], shape, x.dtype, index),
+                _arg("d_decay", grads["d_decay"], shape, decay.dtype, index),
+                _arg("dA_log", grads.get("dA_log"), state[1:2], f32, index),
+                _arg("d_initial_state", grads.get("d_initial_state"), state, f32, index))
     if workspace is None:
         n = sized.size("kda_scan_bwd_workspace_size", int(A_log is not None), int(states is not None))
         if n:
             workspace = torch.empty(n, dtype=torch.uint8, device=x.device)
     ws, ws_bytes = _workspace(workspace, index)
-    st = lib.kda_scan_bwd(sized.ref, *ins, g_min, s0, cu, kept, do, dst, _arg("dx", grads["dx"], shape, x.dtype, index),
-                          _arg("d_decay", grads["d_decay"], shape, decay.dtype, index),
-                          _arg("dA_log", grads.get("dA_log"), state[1:2], f32, index),
-                          _arg("d_initial_state", grads.get("d_initial_state"), state, f32, index), ws, ws_bytes,
-                          _current_stream(index))
+    st = lib.kda_scan_bwd(sized.ref, *ins, g_min, s0, cu, kept, do, dst, *outs, ws, ws_bytes, _current_stream(index))
     if st:
         _check(st, "kda_scan_bwd")
     return grads
@@ -665,11 +675,15 @@ def kda_scan_step(x, decay, state_in, A_log=None, g_min=-5.0, state_out=None, ou
                                             validate=validate),
                       index, stream, (x, decay, state_in, A_log, state_out, out))
     if state_out is None:
-        state_out = state_in
+        state_out, to = state_in, s0
+    else:
+        to = _arg("state_out", state_out, state, torch.float32, index)
     if out is None:
         out = torch.empty_like(x)
-    st = lib.kda_scan_step(sized.ref, *ins, g_min, s0, _arg("state_out", state_out, state, torch.float32, index),
-                           _arg("out", out, x.shape, x.dtype, index), _current_stream(index))
+        given = _new(out)
+    else:
+        given = _arg("out", out, x.shape, x.dtype, index)
+    st = lib.kda_scan_step(sized.ref, *ins, g_min, s0, to, given, _current_stream(index))
     if st:
         _check(st, "kda_scan_step")
     return out, state_out
@@ -713,12 +727,14 @@ def kda_block_norm_fwd(y, residual=None, gate=None, *, post_norm=True, post_weig
                                                  pre_eps=pre_eps, want_out=want_out, want_normed=want_normed,
                                                  out=out, normed=normed),
                       index, stream, (y, residual, gate, post_weight, scale, pre_weight, out, normed))
+    given_out, given_normed = _arg("out", out, shape, rdt, index), _arg("normed", normed, shape, y.dtype, index)
     if out is None and want_out:
         out = torch.empty_like(y if residual is None else residual)
+        given_out = _new(out)
     if normed is None and want_normed:
         normed = torch.empty_like(y)
-    st = lib.kda_block_norm_fwd(sized.ref, *ins, _arg("out", out, shape, rdt, index),
-                                _arg("normed", normed, shape, y.dtype, index), _current_stream(index))
+        given_normed = _new(normed)
+    st = lib.kda_block_norm_fwd(sized.ref, *ins, given_out, given_normed, _current_stream(index))
     if st:
         _check(st, "kda_block_norm_fwd")
     return out, normed
@@ -748,15 +764,16 @@ def kda_block_norm_bwd(y, d_out, d_normed=None, residual=None, gate=None, *, pos
         grads = {"d_y": torch.empty_like(y), "d_residual": new(residual), "d_gate": new(gate),
                  "d_post_weight": new(post_weight), "d_scale": new(scale),
                  "d_pre_weight": None if d_normed is None else new(pre_weight)}
-    get, row, f32 = grads.get, shape[-1:], torch.float32
-    weights = [_arg(n, get(n), row, f32, index) for n in ("d_post_weight", "d_scale", "d_pre_weight")]
-    if workspace is None and any(weights):
+        outs = [_new(t) for t in grads.values()]
+    else:
+        get, row, f32 = grads.get, shape[-1:], torch.float32
+        outs = [_arg("d_y", get("d_y"), shape, dt, index), _arg("d_residual", get("d_residual"), shape, rdt, index),
+                _arg("d_gate", get("d_gate"), shape, dt, index)]
+        outs += [_arg(n, get(n), row, f32, index) for n in ("d_post_weight", "d_scale", "d_pre_weight")]
+    if workspace is None and any(outs[3:]):
         workspace = torch.empty(sized.size("kda_block_norm_bwd_workspace_size"), dtype=torch.uint8, device=y.device)
     ws, ws_bytes = _workspace(workspace, index)
-    st = lib.kda_block_norm_bwd(sized.ref, *ins, do, dn, _arg("d_y", get("d_y"), shape, dt, index),
-                                _arg("d_residual", get("d_residual"), shape, rdt, index),
-                                _arg("d_gate", get("d_gate"), shape, dt, index), *weights, ws, ws_bytes,
-                                _current_stream(index))
+    st = lib.kda_block_norm_bwd(sized.ref, *ins, do, dn, *outs, ws, ws_bytes, _current_stream(index))
     if st:
         _check(st, "kda_block_norm_bwd")
     return grads

@@ -26,7 +26,8 @@ template <int P> __device__ __forceinline__ Vec<P> sigmoid_rest(Vec<P> r, Vec<P>
   return lanes<P>([&](int i) { return r.get(i) <= 0.5f ? 1.f - r.get(i) : e.get(i) * r.get(i); });
 }
 
-// V elements as they lie in memory, read as V / P vectors of P.
+// V elements as they lie in memory, read as V / P vectors of P.  open(): a gate
+// of 128, whose Sigmoid is 1 and whose 1 - Sigmoid is 0.
 template <typename T, int V> struct Piece;
 template <> struct Piece<__nv_bfloat16, 8> {
   uint4 v;
@@ -38,6 +39,7 @@ template <> struct Piece<__nv_bfloat16, 8> {
     return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
   }
   __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void open() { v = make_uint4(0x43004300, 0x43004300, 0x43004300, 0x43004300); }  // 128
 };
 template <> struct Piece<float, 8> {
   uint4 a, b;
@@ -55,18 +57,21 @@ template <> struct Piece<float, 8> {
     return i & 1 ? pair(__uint_as_float(q.z), __uint_as_float(q.w)) : pair(__uint_as_float(q.x), __uint_as_float(q.y));
   }
   __device__ __forceinline__ void zero() { a = b = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void open() { a = b = make_uint4(0x43000000, 0x43000000, 0x43000000, 0x43000000); }  // 128
 };
 template <> struct Piece<__nv_bfloat16, 1> {
   __nv_bfloat16 v;
   __device__ __forceinline__ void load(const void *p) { v = *static_cast<const __nv_bfloat16 *>(p); }
   __device__ __forceinline__ Vec<1> get(int) const { return Vec<1>{__bfloat162float(v)}; }
   __device__ __forceinline__ void zero() { v = __float2bfloat16_rn(0.f); }
+  __device__ __forceinline__ void open() { v = __float2bfloat16_rn(128.f); }
 };
 template <> struct Piece<float, 1> {
   float v;
   __device__ __forceinline__ void load(const void *p) { v = *static_cast<const float *>(p); }
   __device__ __forceinline__ Vec<1> get(int) const { return Vec<1>{v}; }
   __device__ __forceinline__ void zero() { v = 0.f; }
+  __device__ __forceinline__ void open() { v = 128.f; }
 };
 
 __device__ __forceinline__ void put(float *p, const Vec<1> (&f)[1]) { *p = f[0].v; }
@@ -330,6 +335,9 @@ __global__ void __launch_bounds__(S::kBlock, S::kBlock > 256 ? 1 : 2) norm_bwd_k
         read(res[c]);
         read(dout[c]);
       }
+      if (!a.gate)
+#pragma unroll
+        for (int c = 0; c < C; ++c) g[c].open();
     } else {
 #pragma unroll
       for (int c = 0; c < C; ++c) {
@@ -337,7 +345,7 @@ __global__ void __launch_bounds__(S::kBlock, S::kBlock > 256 ? 1 : 2) norm_bwd_k
         const size_t at = (size_t)row * a.width + j;
         const bool in = j < a.width && row < a.rows;
         y[c].zero();
-        g[c].zero();
+        g[c].open();
         dn[c].zero();
         res[c].zero();
         dout[c].zero();
@@ -389,7 +397,7 @@ __global__ void __launch_bounds__(S::kBlock, S::kBlock > 256 ? 1 : 2) norm_bwd_k
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         Vec<P> tr = mul(mul(y[c].get(i), all<P>(r1)), mul(w1[i], sc[i])), e;
-        if (a.gate) tr = mul(tr, sigmoid_of(g[c].get(i), e));
+        tr = mul(tr, sigmoid_of(g[c].get(i), e));
         const Vec<P> o = add(tr, res[c].get(i)), q = mul(dn[c].get(i), w2[i]);
         v[0] = fma(o, o, v[0]);
         v[1] = fma(q, o, v[1]);
@@ -416,12 +424,8 @@ __global__ void __launch_bounds__(S::kBlock, S::kBlock > 256 ? 1 : 2) norm_bwd_k
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const Vec<P> yh = mul(y[c].get(i), all<P>(r1));
-        Vec<P> sg = all<P>(1.f), rest = all<P>(0.f);
-        if (a.gate) {
-          Vec<P> e;
-          sg = sigmoid_of(g[c].get(i), e);
-          rest = sigmoid_rest(sg, e);
-        }
+        Vec<P> e;
+        const Vec<P> sg = sigmoid_of(g[c].get(i), e), rest = sigmoid_rest(sg, e);
         const Vec<P> ys = mul(yh, sg), b = mul(ys, w1[i]), o = fma(b, sc[i], res[c].get(i));
         const Vec<P> n = mul(dn[c].get(i), all<P>(r2));
         const Vec<P> D = fma(n, w2[i], fma(o, all<P>(-back), dout[c].get(i)));
