@@ -110,7 +110,7 @@ struct Shape {
   static constexpr int V = V_, kChunks = kChunks_, kThreads = kThreads_;
   static constexpr int rows() { return kRows_; }              // at once, in the forward
   static constexpr int P = V == 8 ? 2 : 1, kVecs = V / P;    // values of one instruction
-  static constexpr int kBlock = kThreads > 256 ? kThreads : 256, kGroups = kBlock / kThreads;
+  static constexpr int kBlock = kThreads >= 128 ? kThreads : 256, kGroups = kBlock / kThreads;
   static constexpr int max_width() { return V * kChunks * kThreads; }
 };
 
@@ -245,7 +245,7 @@ norm_fwd_kernel(NormArgs a) {
   }
 }
 
-constexpr int kBwdBlocks = 304;  // at most (two to an SM); a block leaves one set of weight-gradient partials
+constexpr int kBwdThreads = 152 * 512;  // at most, in blocks that each leave one set of weight-gradient partials
 
 // Backward.  With tr = scale o b the branch's part of out, everything that the
 // row's gradients need of the row as a whole are sums that are known as soon as
@@ -267,14 +267,14 @@ template <typename S> struct RowStages {
     else return 0;
   }
   static constexpr int kStage = parts() * S::kChunks * S::kBlock * 16;  // bytes
-  static constexpr int kLimit = S::kBlock > 256 ? 227 * 1024 : 113 * 1024;
+  static constexpr int kLimit = S::kBlock > 256 ? 227 * 1024 : 225 * 1024 / (512 / S::kBlock);
   static constexpr int kStages = 3 * kStage <= kLimit ? 3 : 2 * kStage <= kLimit ? 2 : 1;
   static constexpr int kSums = S::kGroups > 1 ? (int)sizeof(float) * S::kGroups * S::max_width() : 0;
   static constexpr int kBytes = kStages * kStage > kSums ? kStages * kStage : kSums;
 };
 
 template <typename S>
-__global__ void __launch_bounds__(S::kBlock, S::kBlock > 256 ? 1 : 2) norm_bwd_kernel(NormArgs a, NormBwdIo io, float *part) {
+__global__ void __launch_bounds__(S::kBlock, 512 / S::kBlock) norm_bwd_kernel(NormArgs a, NormBwdIo io, float *part) {
   using T = typename S::T;
   using R = typename S::R;
   using St = RowStages<S>;
@@ -501,7 +501,7 @@ template <typename S> cudaError_t fwd(const NormArgs &a, cudaStream_t s) {
 
 template <typename S> cudaError_t bwd(const NormArgs &a, const NormBwdIo &io, float *ws, cudaStream_t s) {
   const bool weights = io.dw1 || io.dsc || io.dw2;
-  const long long groups = (a.rows + S::kGroups - 1) / S::kGroups, most = S::kBlock > 256 ? kBwdBlocks / 2 : kBwdBlocks;
+  const long long groups = (a.rows + S::kGroups - 1) / S::kGroups, most = kBwdThreads / S::kBlock;
   const int blocks = (int)(groups < most ? groups : most);
   constexpr int smem = RowStages<S>::kBytes;
   cudaError_t e = cudaFuncSetAttribute(norm_bwd_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -514,15 +514,16 @@ template <typename S> cudaError_t bwd(const NormArgs &a, const NormBwdIo &io, fl
 }
 
 // Calls f with the row shape for this width: pieces of 8 elements when every
-// row of every tensor starts on 16 bytes, else single elements.  Backward: one
-// piece per thread mostly, for the registers of the weights' sums; two in blocks
-// of 256 for rows up to 4096, two blocks to an SM (16384 x 4096 forward and
-// backward: 362 us against 399 in blocks of 512), but for all-fp32 rows, whose
-// copies leave room for one block only (905 against 950).  Forward: 2 narrow rows at once when there are many
-// (262144 rows of 128: 36.9 us against 43.4 of one and 41.0 of four at once).
+// row of every tensor starts on 16 bytes, else single elements.  Two pieces per
+// thread where rows are wide enough (65536 x 2048 forward: 310 us against 350 of
+// one; 32768 x 2048 forward and backward in bf16: 359 against 430), one in the
+// backward of all-fp32 rows, whose sums and copies take the registers and the
+// shared memory (815 against 926).  Forward: two narrow rows at once when there
+// are many (262144 rows of 128: 36.9 us against 43.4 of one and 41.0 of four).
 template <typename T, typename R, bool kBwd, typename F>
 cudaError_t with_shape(int width, bool vectors, bool many, F f) {
   if (vectors) {
+    constexpr bool one = kBwd && sizeof(T) + sizeof(R) > 6;
     if constexpr (!kBwd) {
       if (many && width <= 128) return f(Shape<T, R, 8, 1, 16, 2>());
       if (many && width <= 256) return f(Shape<T, R, 8, 1, 32, 2>());
@@ -530,12 +531,9 @@ cudaError_t with_shape(int width, bool vectors, bool many, F f) {
     if (width <= 128) return f(Shape<T, R, 8, 1, 16>());
     if (width <= 256) return f(Shape<T, R, 8, 1, 32>());
     if (width <= 512) return f(Shape<T, R, 8, kBwd ? 1 : 2, kBwd ? 64 : 32>());
-    if (width <= 1024) return f(Shape<T, R, 8, 1, 128>());
-    if (width <= 2048) return f(Shape<T, R, 8, 1, 256>());
-    if (width <= 4096) {
-      if constexpr (kBwd && sizeof(T) + sizeof(R) > 6) return f(Shape<T, R, 8, 1, 512>());
-      else return f(Shape<T, R, 8, 2, 256>());
-    }
+    if (width <= 1024) return f(Shape<T, R, 8, one ? 1 : 2, one ? 128 : 64>());
+    if (width <= 2048) return f(Shape<T, R, 8, one ? 1 : 2, one ? 256 : 128>());
+    if (width <= 4096) return f(Shape<T, R, 8, one ? 1 : 2, one ? 512 : 256>());
     return f(Shape<T, R, 8, 2, 512>());
   }
   if (width <= 128) return f(Shape<T, R, 1, 4, 32>());
@@ -559,7 +557,8 @@ template <int kN> bool on_16_bytes(const NormArgs &a, const void *const (&p)[kN]
 
 }  // namespace
 
-size_t norm_bwd_workspace_bytes(int width) { return (size_t)2 * kBwdBlocks * width * sizeof(float); }
+// (blocks of at least 128 threads)
+size_t norm_bwd_workspace_bytes(int width) { return (size_t)2 * (kBwdThreads / 128) * width * sizeof(float); }
 
 cudaError_t launch_norm_fwd(const NormArgs &a, cudaStream_t s) {
   if (a.rows == 0) return cudaSuccess;
