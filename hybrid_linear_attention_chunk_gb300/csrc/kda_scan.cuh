@@ -74,6 +74,8 @@ template <> struct RawOf<float, 2> { using type = float2; };
 template <> struct RawOf<__nv_bfloat16, 1> { using type = unsigned short; };
 template <> struct RawOf<__nv_bfloat16, 2> { using type = unsigned; };
 template <typename T, int V> using Raw = typename RawOf<T, V>::type;
+__device__ __forceinline__ float raw_of(const float (&f)[1]) { return f[0]; }
+__device__ __forceinline__ float2 raw_of(const float (&f)[2]) { return make_float2(f[0], f[1]); }
 
 template <int V> __device__ __forceinline__ void store(float *p, Vec<V> v) {
   if constexpr (V == 2) *reinterpret_cast<float2 *>(p) = make_float2(v.get(0), v.get(1));
@@ -88,7 +90,7 @@ template <int V> __device__ __forceinline__ void store(__nv_bfloat16 *p, Vec<V> 
 // Each lane holds V channels of 16 consecutive tokens.  The lanes of a warp are
 // kGroups groups along the sequence, of kWide / V lanes that cover kWide
 // channels: 64 channels x 16 tokens where there are many chains, 16 x 64 where
-// there are few (32 x 16 in the elementwise form, V = 1).
+// there are few (32 x 16 and 8 x 64 in the elementwise form, V = 1).
 template <int kWide_, int V_>
 struct Layout {
   static constexpr int kWide = kWide_, V = V_;
@@ -176,7 +178,7 @@ __device__ __forceinline__ float clamp_126(float x) {
 
 // How a token's alpha and 1 - alpha come from its log-decay, or from its logit
 // through r = Sigmoid(s z), g = g_min r.  `log` is g or r; tile sums of it give
-// the tile's log-decay as log_unit() times the sum.
+// the tile's log-decay as `unit` times the sum.
 template <bool kLogit, int V>
 struct Gate {
   Vec<V> ns;                     // -s log2(e)
@@ -223,7 +225,7 @@ struct Gate {
 };
 
 // ------------------------------------------------------------------ clusters
-// A chain block (one sequence, 32 V channels) runs on one cluster; its CTAs take
+// A chain block (one sequence, kWide channels) runs on one cluster; its CTAs take
 // consecutive spans of tokens of a round.  The hardware schedules a cluster's
 // CTAs together, so its barrier needs no spinning on memory.
 __device__ __forceinline__ unsigned cluster_rank() {
@@ -350,15 +352,14 @@ struct ScanJoin {
     groups(mine, upto, before);
     if (!first) {
       barrier_sync(warp, 64);
-      const F v = *in;
-      const float *f = reinterpret_cast<const float *>(&v);
+      const Vec<V> v = values(*in);
 #pragma unroll
-      for (int i = 0; i < V; ++i) h[i] = f[i];
+      for (int i = 0; i < V; ++i) h[i] = v.get(i);
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) out[i] = h[i];
     upto.run(out);
-    if (gives) *to = *reinterpret_cast<const F *>(out);
+    if (gives) *to = raw_of(out);
     if (more) barrier_arrive(next, 64);
     if (group > 0) before.run(h);
   }
