@@ -592,7 +592,8 @@ def kda_scan_fwd(x, decay, A_log=None, g_min=-5.0, initial_state=None, cu_seqlen
         out = torch.empty_like(x)
         given_out = _new(out)
     if final_state is None and want_final_state:
-        final_state = torch.empty(state, dtype=torch.float32, device=x.device)
+        final_state = (torch.empty(state, dtype=torch.float32, device=x.device) if initial_state is None
+                       else torch.empty_like(initial_state))
         given_final = _new(final_state)
     if want_states or states is not None:
         n = sized.size("kda_scan_states_size") // 4
@@ -636,7 +637,8 @@ def kda_scan_bwd(x, decay, d_out, A_log=None, g_min=-5.0, initial_state=None, d_
     if grads is None:
         grads = {"dx": torch.empty_like(x), "d_decay": torch.empty_like(decay),
                  "dA_log": None if A_log is None else torch.empty_like(A_log),
-                 "d_initial_state": (torch.empty(state, dtype=f32, device=x.device) if want_d_initial_state else None)}
+                 "d_initial_state": (None if not want_d_initial_state else torch.empty_like(d_final_state)
+                                     if d_final_state is not None else torch.empty(state, dtype=f32, device=x.device))}
         outs = [_new(t) for t in grads.values()]
     else:
         outs = (_arg("dx", grads["dx"], shape, x.dtype, index),
