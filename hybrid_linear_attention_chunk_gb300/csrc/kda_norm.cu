@@ -512,7 +512,8 @@ template <typename S> cudaError_t bwd(const NormArgs &a, const NormBwdIo &io, fl
   const long long groups = (a.rows + S::kGroups - 1) / S::kGroups, most = kBwdThreads / S::kBlock;
   const int blocks = (int)(groups < most ? groups : most);
   constexpr int smem = RowStages<S>::kBytes;
-  cudaError_t e = cudaFuncSetAttribute(norm_bwd_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = cudaSuccess;
+  if (smem > 48 * 1024) e = cudaFuncSetAttribute(norm_bwd_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   norm_bwd_kernel<S><<<blocks, S::kBlock, smem, s>>>(a, io, weights ? ws : nullptr);
   e = cudaGetLastError();

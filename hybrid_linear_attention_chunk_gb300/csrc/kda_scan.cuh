@@ -427,8 +427,10 @@ cudaError_t launch_chains(void (*kernel)(P...), const ScanArgs &a, int warps, in
                           P... args) {
   const long long blocks = (long long)((a.D + L::kWide - 1) / L::kWide) * a.N * ranks;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);
   cfg.blockDim = dim3(32 * warps);
@@ -439,7 +441,7 @@ cudaError_t launch_chains(void (*kernel)(P...), const ScanArgs &a, int warps, in
   at[0].val.clusterDim.x = ranks;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 1;  // (of one CTA too: the cluster barrier is then a barrier of that CTA)
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 

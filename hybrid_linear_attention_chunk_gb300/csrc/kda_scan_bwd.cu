@@ -165,12 +165,14 @@ scan_bwd_kernel(ScanArgs a, ScanBwdIo io, float *dA_part, int cblocks) {
 #pragma unroll
     for (int i = 0; i < V; ++i) io.ds0[chain + i] = state[i];
   if (kLogit) {  // the block's sums over time, per channel: warps and groups in order
-    cluster_sync_all();  // (not barrier 0, at which the ring's warp 0 may still wait)
+    // The cluster's barrier, also where the cluster is one CTA: the ring's warps may
+    // still wait at the CTA's barriers, barrier 0 (that of __syncthreads) among them.
+    cluster_sync_all();
     float *sums = reinterpret_cast<float *>(smem);
 #pragma unroll
     for (int i = 0; i < V; ++i)
       sums[(sh.warp * L::kGroups + sh.group) * L::kWide + wide + i] = dA.get(i) / gate.ns.get(i);  // dz z = dz scaled / ns
-    __syncthreads();
+    cluster_sync_all();
     for (int i = threadIdx.x; i < L::kWide && c0 + i < D; i += blockDim.x) {
       float s = 0.f;
       for (int w = 0; w < sh.warps * L::kGroups; ++w) s += sums[w * L::kWide + i];

@@ -176,3 +176,40 @@ def test_generation_after_a_prefill(kda, dtype):
         for a, b in ((out, want[r]), (normed, want_n[r])):
             assert float((a.double() - b.double()).norm() / b.double().norm()) <= tol
     assert float((state - s_all).norm() / s_all.norm()) <= 1e-5
+
+
+def test_calls_from_two_threads(kda):
+    """Two threads, a stream each, the same calls over and over on data of their own."""
+    import threading
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    sets = []
+    for T in (400, 130):
+        x, z, do = (torch.randn(T, 3, 40, generator=gen, device=DEV) for _ in range(3))
+        sets.append((x, z, do, torch.randn(3, generator=gen, device=DEV) * 0.2))
+
+    def calls(x, z, do, A):
+        h, fs, st = kda.kda_scan_fwd(x, z, A, G_MIN, want_states=True)
+        g = kda.kda_scan_bwd(x, z, do, A, G_MIN, states=st)
+        w = torch.ones(40, device=DEV)
+        n = kda.kda_block_norm_bwd(h, do, do, post_weight=w, scale=w, pre_weight=w)
+        return [h, fs, *(v for v in g.values() if v is not None), *(v for v in n.values() if v is not None)]
+
+    want = [calls(*s) for s in sets]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(60):
+                got = calls(*sets[i])
+                stream.synchronize()
+                if not all(torch.equal(a, b) for a, b in zip(got, want[i])):
+                    bad.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
