@@ -418,9 +418,10 @@ __global__ void __launch_bounds__(S::kBlock, 512 / S::kBlock) norm_bwd_kernel(No
 #pragma unroll
     for (int k = 0; k < 5; ++k) sums[k] = total(v[k]);
     row_sum<S::kThreads, 5>(sums, sh2[par]);
+    // without d_normed nothing depends on out, however large or infinite it is
     const float r2 = io.dn ? rsqrtf(sums[0] * inv + a.e2) : 0.f;
-    const float back = r2 * r2 * r2 * sums[1] * inv;
-    const float m = a.post ? (sums[2] + r2 * sums[3] - back * sums[4]) * inv : 0.f;
+    const float back = io.dn ? r2 * r2 * r2 * sums[1] * inv : 0.f;
+    const float m = !a.post ? 0.f : io.dn ? (sums[2] + r2 * sums[3] - back * sums[4]) * inv : sums[2] * inv;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int j = (c * S::kThreads + t) * V;
@@ -434,7 +435,8 @@ __global__ void __launch_bounds__(S::kBlock, 512 / S::kBlock) norm_bwd_kernel(No
         const Vec<P> yh = mul(y[c].get(i), all<P>(r1));
         Vec<P> e;
         const Vec<P> sg = sigmoid_of(g[c].get(i), e), rest = sigmoid_rest(sg, e);
-        const Vec<P> ys = mul(yh, sg), b = mul(ys, w1[i]), o = fma(b, sc[i], res[c].get(i));
+        const Vec<P> ys = mul(yh, sg), b = mul(ys, w1[i]);
+        const Vec<P> o = io.dn ? fma(b, sc[i], res[c].get(i)) : all<P>(0.f);
         const Vec<P> n = mul(dn[c].get(i), all<P>(r2));
         const Vec<P> D = fma(n, w2[i], fma(o, all<P>(-back), dout[c].get(i)));
         p2[c][i] = fma(n, o, p2[c][i]);

@@ -436,7 +436,8 @@ kda_status kda_scan_step(const kda_scan_desc *desc, const void *x, const void *d
  *    multiple of 8 run vectorised.
  *  - Arithmetic is fp32 (mean squares too: a row's squares must not overflow)
  *    and each output is rounded once; normed is formed from the unrounded out.
- *    A row of zeros gives zeros when eps > 0.  Results are deterministic.
+ *    A row of zeros gives zeros when eps > 0.  Non-finite values reach their own
+ *    row and the weights' gradients alone.  Results are deterministic.
  */
 #define KDA_NORM_MAX_WIDTH 8192
 

@@ -154,6 +154,21 @@ def test_bad_rows_stay_alone(kda):
     assert n1[7].isnan().all() and o1[20, 263].isnan()
 
 
+@pytest.mark.parametrize("width", [264, 33])
+def test_infinite_residual_without_normed(kda, width):
+    """Without d_normed no gradient depends on the residual's values, infinite or NaN as they may be."""
+    a = make(9, width, BF, BF, seed=18)
+    p = {**parts(a), "pre_weight": None}
+    want = kda.kda_block_norm_bwd(a["y"], a["d_out"], None, **p)
+    res = a["residual"].clone()
+    res[2, 5], res[4, 0], res[7] = float("inf"), -float("inf"), float("nan")
+    got = kda.kda_block_norm_bwd(a["y"], a["d_out"], None, **{**p, "residual": res})
+    assert torch.equal(got["d_residual"], a["d_out"])
+    for n in want:
+        if want[n] is not None:
+            assert torch.equal(got[n], want[n]), n
+
+
 def test_extreme_gates(kda):
     """Closed and open gates: sigmoid and its slope at +-200 and +-inf."""
     a = make(4, 48, F32, F32, seed=6)
