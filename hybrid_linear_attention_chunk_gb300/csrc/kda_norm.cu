@@ -2,13 +2,13 @@
 // their backward (formulas in include/kda.h).
 //
 // A row is read once, held in registers across its sums, and written once:
-// a group of kThreads threads (half a warp to 512 threads, by the width) holds
+// a group of kThreads threads (2 lanes to 512 threads, by the width) holds
 // kChunks pieces of V elements per thread.  Sums run in fp32, per thread, then
 // by shuffles, then over the warps in order.
 //
 // Measured (6.78 TB/s is a measured copy on the same GPU): the forward is bound by
 // HBM, 32768 x 4096 with gate and fp32 residual 272 us, 6.9 TB/s; rows of 128
-// (262144, gate) 36.9 us, 5.4 TB/s (0.80), where latency of the short rows shows.
+// (262144, gate) 35.1 us, 5.7 TB/s (0.85), where latency of the short rows shows.
 // Forward and backward of 16384 x 4096 in bf16 take 344 us, of them the backward
 // 225 us: 16 bytes an element at 4.8 TB/s (0.70), bound by instruction issue (75 an
 // element; 128 registers leave two blocks of 256 on an SM) and by its two sums
@@ -529,15 +529,24 @@ template <typename S> cudaError_t bwd(const NormArgs &a, const NormBwdIo &io, fl
 // thread where rows are wide enough (65536 x 2048 forward: 310 us against 350 of
 // one; 32768 x 2048 forward and backward in bf16: 359 against 430), one in the
 // backward of all-fp32 rows, whose sums and copies take the registers and the
-// shared memory (815 against 926).  Forward: two narrow rows at once when there
-// are many (262144 rows of 128: 36.9 us against 43.4 of one and 41.0 of four).
+// shared memory (815 against 926).  Narrow rows take as few lanes as hold them,
+// and in the forward two rows at once when there are many (262144 rows of 128: 35.1
+// us against 38.3 of one row, 36.9 on 16 lanes of one piece; 4194304 rows of 32:
+// 157 us against 440 on 16 lanes).
 template <typename T, typename R, bool kBwd, typename F>
 cudaError_t with_shape(int width, bool vectors, bool many, F f) {
   if (vectors) {
     constexpr bool one = kBwd && sizeof(T) + sizeof(R) > 6;
     if constexpr (!kBwd) {
-      if (many && width <= 128) return f(Shape<T, R, 8, 1, 16, 2>());
-      if (many && width <= 256) return f(Shape<T, R, 8, 1, 32, 2>());
+      if (many && width <= 16) return f(Shape<T, R, 8, 1, 2, 2>());
+      if (many && width <= 32) return f(Shape<T, R, 8, 1, 4, 2>());
+      if (many && width <= 64) return f(Shape<T, R, 8, 1, 8, 2>());
+      if (many && width <= 128) return f(Shape<T, R, 8, 2, 8, 2>());
+      if (many && width <= 256) return f(Shape<T, R, 8, 2, 16, 2>());
+    } else {
+      if (width <= 16) return f(Shape<T, R, 8, 1, 2>());
+      if (width <= 32) return f(Shape<T, R, 8, 1, 4>());
+      if (width <= 64) return f(Shape<T, R, 8, 1, 8>());
     }
     if (width <= 128) return f(Shape<T, R, 8, 1, 16>());
     if (width <= 256) return f(Shape<T, R, 8, 1, 32>());

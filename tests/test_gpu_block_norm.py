@@ -121,6 +121,13 @@ def test_is_the_output_equation_of_the_recurrence(kda):
     assert_within(y.reshape(200, 128), *want, BF, "y")
 
 
+@pytest.mark.parametrize("width", [8, 16, 24, 32, 64, 128, 200, 256])
+@pytest.mark.parametrize("dtype,res", [(BF, BF), (F32, None)])
+def test_many_narrow_rows(kda, width, dtype, res):
+    """Row counts past the rule that takes two at once, odd ones, and every narrow shape."""
+    check_all(kda, make(16385, width, dtype, res, seed=19))
+
+
 def test_zero_rows_and_rows_of_zeros(kda):
     y = torch.zeros(3, 64, device=DEV)
     w = torch.ones(64, device=DEV)
