@@ -253,7 +253,7 @@ norm_fwd_kernel(NormArgs a) {
   }
 }
 
-constexpr int kBwdThreads = 152 * 512;  // at most, in blocks that each leave one set of weight-gradient partials
+constexpr int kSms = 152;  // the backward's grid fills these once; each block leaves one set of weight-gradient partials
 
 // Backward.  With tr = scale o b the branch's part of out, everything that the
 // row's gradients need of the row as a whole are sums that are known as soon as
@@ -279,10 +279,12 @@ template <typename S> struct RowStages {
   static constexpr int kStages = 3 * kStage <= kLimit ? 3 : 2 * kStage <= kLimit ? 2 : 1;
   static constexpr int kSums = S::kGroups > 1 ? (int)sizeof(float) * S::kGroups * S::max_width() : 0;
   static constexpr int kBytes = kStages * kStage > kSums ? kStages * kStage : kSums;
+  // an SM's: single elements have no copies in flight ahead of them, and need few registers
+  static constexpr int kBlocks = (S::V == 1 && S::kChunks <= 4 ? 1024 : 512) / S::kBlock;
 };
 
 template <typename S>
-__global__ void __launch_bounds__(S::kBlock, 512 / S::kBlock) norm_bwd_kernel(NormArgs a, NormBwdIo io, float *part) {
+__global__ void __launch_bounds__(S::kBlock, RowStages<S>::kBlocks) norm_bwd_kernel(NormArgs a, NormBwdIo io, float *part) {
   using T = typename S::T;
   using R = typename S::R;
   using St = RowStages<S>;
@@ -511,7 +513,7 @@ template <typename S> cudaError_t fwd(const NormArgs &a, cudaStream_t s) {
 
 template <typename S> cudaError_t bwd(const NormArgs &a, const NormBwdIo &io, float *ws, cudaStream_t s) {
   const bool weights = io.dw1 || io.dsc || io.dw2;
-  const long long groups = (a.rows + S::kGroups - 1) / S::kGroups, most = kBwdThreads / S::kBlock;
+  const long long groups = (a.rows + S::kGroups - 1) / S::kGroups, most = kSms * RowStages<S>::kBlocks;
   const int blocks = (int)(groups < most ? groups : most);
   constexpr int smem = RowStages<S>::kBytes;
   cudaError_t e = cudaSuccess;
@@ -533,6 +535,10 @@ template <typename S> cudaError_t bwd(const NormArgs &a, const NormBwdIo &io, fl
 // and in the forward two rows at once when there are many (262144 rows of 128: 35.1
 // us against 38.3 of one row, 36.9 on 16 lanes of one piece; 4194304 rows of 32:
 // 157 us against 440 on 16 lanes).
+// Rows of single elements have a step of threads for each doubling of the width, as
+// a piece past the row costs as much as one in it: bf16 with every part, 258111 x 130
+// on 64 threads 139 us forward and 363 backward, on 256 threads 416 and 1215;
+// 31359 x 1070 on 4 pieces of 512 threads 172 and 340, on 16 pieces 321 and 851.
 template <typename T, typename R, bool kBwd, typename F>
 cudaError_t with_shape(int width, bool vectors, bool many, F f) {
   if (vectors) {
@@ -556,8 +562,14 @@ cudaError_t with_shape(int width, bool vectors, bool many, F f) {
     if (width <= 4096) return f(Shape<T, R, 8, one ? 1 : 2, one ? 512 : 256>());
     return f(Shape<T, R, 8, 2, 512>());
   }
+  if (width <= 32) return f(Shape<T, R, 1, 1, 32>());
+  if (width <= 64) return f(Shape<T, R, 1, 2, 32>());
   if (width <= 128) return f(Shape<T, R, 1, 4, 32>());
+  if (width <= 256) return f(Shape<T, R, 1, 4, 64>());
+  if (width <= 512) return f(Shape<T, R, 1, 4, 128>());
   if (width <= 1024) return f(Shape<T, R, 1, 4, 256>());
+  if (width <= 2048) return f(Shape<T, R, 1, 4, 512>());
+  if (width <= 4096) return f(Shape<T, R, 1, 8, 512>());
   return f(Shape<T, R, 1, 16, 512>());
 }
 
@@ -577,8 +589,8 @@ template <int kN> bool on_16_bytes(const NormArgs &a, const void *const (&p)[kN]
 
 }  // namespace
 
-// (blocks of at least 128 threads)
-size_t norm_bwd_workspace_bytes(int width) { return (size_t)2 * (kBwdThreads / 128) * width * sizeof(float); }
+// (an SM holds up to 8 blocks, of 128 threads, where rows have at most 512 elements, and 4 above)
+size_t norm_bwd_workspace_bytes(int width) { return (size_t)2 * kSms * (width <= 512 ? 8 : 4) * width * sizeof(float); }
 
 cudaError_t launch_norm_fwd(const NormArgs &a, cudaStream_t s) {
   if (a.rows == 0) return cudaSuccess;

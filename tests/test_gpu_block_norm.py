@@ -161,6 +161,14 @@ def test_bad_rows_stay_alone(kda):
     assert n1[7].isnan().all() and o1[20, 263].isnan()
 
 
+@pytest.mark.parametrize("rows,width", [(5001, 1), (5001, 30), (5001, 33), (5001, 63), (5001, 130), (2500, 257), (1300, 511),
+                                        (650, 1001), (330, 1070), (7, 2047), (160, 3001), (3, 4095), (160, 8001)])
+@pytest.mark.parametrize("dtype,res", [(BF, BF), (BF, F32), (F32, F32)])
+def test_rows_off_16_bytes(kda, rows, width, dtype, res):
+    """Widths that no 16-byte piece divides, with more rows than the grid takes at once."""
+    check_all(kda, make(rows, width, dtype, res, seed=20))
+
+
 @pytest.mark.parametrize("width", [264, 33])
 def test_infinite_residual_without_normed(kda, width):
     """Without d_normed no gradient depends on the residual's values, infinite or NaN as they may be."""
