@@ -36,11 +36,13 @@ __device__ __forceinline__ float decay_code(float g) {
   return g > kNearOne && g <= 0.f ? -fabsf(expm1_near(g)) : fast_exp2(g * kLog2e);
 }
 
-// The code of two spans in a row, c after d.
+// The code of two spans in a row, c after d.  Near 1 both, e = c + d + c d; past
+// -1/8 it becomes the product of the alphas, as 1 + e would lose what e has
+// rounded to: e's error is relative to e, and alpha may be far smaller.
 __device__ __forceinline__ float decay_join(float c, float d) {
-  const float near_both = -fabsf(fmaf(c, d, c + d));  // (0 keeps its sign bit)
+  const float e = fmaf(c, d, c + d);
   const float alpha = (is_near(c) ? 1.f + c : c) * (is_near(d) ? 1.f + d : d);
-  return is_near(c) && is_near(d) ? near_both : alpha;
+  return is_near(c) && is_near(d) && e > kNearOne ? -fabsf(e) : alpha;  // (0 keeps its sign bit)
 }
 
 // alpha h + u
