@@ -598,7 +598,9 @@ cudaError_t launch_norm_fwd(const NormArgs &a, cudaStream_t s) {
   return with_types<false>(a, on_16_bytes(a, p), [&](auto shape) { return fwd<decltype(shape)>(a, s); });
 }
 
-cudaError_t launch_norm_bwd(const NormArgs &a, const NormBwdIo &io, void *ws, cudaStream_t s) {
+cudaError_t launch_norm_bwd(const NormArgs &args, const NormBwdIo &io, void *ws, cudaStream_t s) {
+  NormArgs a = args;
+  if (!io.dn) a.w2 = nullptr;  // not read, whatever it holds
   if (a.rows == 0) {
     cudaError_t e = cudaSuccess;
     for (float *w : {io.dw1, io.dsc, io.dw2})
