@@ -52,8 +52,12 @@ __device__ __forceinline__ float decay_apply(float c, float h, float u) {
   return r;
 }
 
-// -exp(A) log2(e), never 0: the product with z = -inf, a masked token, stays inf.
-__device__ __forceinline__ float gate_scale(float A_log) { return fminf(-kLog2e * expf(A_log), -1e-37f); }
+// -exp(A) log2(e), never 0: the product with z = -inf, a masked token, stays inf.  A NaN stays one.
+__device__ __forceinline__ float gate_scale(float A_log) {
+  float s = -kLog2e * expf(A_log);
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(s) : "f"(-1e-37f));
+  return s;
+}
 
 __device__ __forceinline__ void scan_range(const ScanArgs &a, int n, int &bos, int &eos) {
   if (a.cu) {  // clamped: cu_seqlens that break their precondition reach no other memory
