@@ -177,8 +177,8 @@ template <int kLeft> __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
-__device__ __forceinline__ float clamp_126(float x) {
-  asm("min.NaN.f32 %0, %0, %1;\n\tmax.NaN.f32 %0, %0, %2;" : "+f"(x) : "f"(126.f), "f"(-126.f));
+__device__ __forceinline__ float clamp_127(float x) {
+  asm("min.NaN.f32 %0, %0, %1;\n\tmax.NaN.f32 %0, %0, %2;" : "+f"(x) : "f"(127.f), "f"(-127.f));
   return x;
 }
 
@@ -207,12 +207,12 @@ struct Gate {
     return lanes<V>([&](int i) { return fast_rcp(d.get(i)); });
   }
   // The same, with dg/dz = g (1 - Sigmoid) s and `x` = -s log2(e) z.  With e = 2^x,
-  // Sigmoid = r = 1 / (1 + e) and 1 - Sigmoid = e r.  x is held in +-126 (a NaN
-  // passes), where e is finite and nothing but the last 1e-38 of r is lost: so
-  // z = +-inf has slope 0, and x times a gradient is finite there.
+  // Sigmoid = r = 1 / (1 + e) and 1 - Sigmoid = e r.  x is held in +-127 (a NaN
+  // passes): there e is finite, and at the ends r, or e, is flushed to 0, so that
+  // z = +-inf has slope 0 exactly, and x times a gradient is finite there.
   __device__ __forceinline__ Vec<V> log(Vec<V> z, Vec<V> &slope, Vec<V> &x) const {
     const Vec<V> v = mul(ns, z);
-    x = lanes<V>([&](int i) { return clamp_126(v.get(i)); });
+    x = lanes<V>([&](int i) { return clamp_127(v.get(i)); });
     const Vec<V> e = lanes<V>([&](int i) { return fast_exp2(x.get(i)); });
     const Vec<V> d = add(all<V>(1.f), e), r = lanes<V>([&](int i) { return fast_rcp(d.get(i)); });
     slope = mul(mul(mul(ns, all<V>(-unit / kLog2e)), r), mul(e, r));

@@ -33,3 +33,18 @@ def test_nan_scale_reaches_its_own_head(kda, write, dtype, d):
         others = torch.tensor([0, 2], device=DEV)
         assert torch.equal(p.index_select(dim, others), q.index_select(dim, others)), name
         assert q.select(dim, 1).isnan().all(), name
+
+
+@pytest.mark.parametrize("d", [16, 33])
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("write", ["one", "complement"])
+def test_infinite_logits_have_no_gradient(kda, write, dtype, d):
+    """Exactly none, however large the gradient of the outputs is."""
+    x, z, do, A, s0 = inputs(70, 2, d, DT[dtype], 1)
+    low, high = torch.finfo(DT[dtype]).min, torch.finfo(DT[dtype]).max
+    z[5:9], z[30], z[31], z[50:52] = -float("inf"), float("inf"), high, low
+    gr = kda.kda_scan_bwd(x, z, (1e30 * do.float()).to(DT[dtype]), A, initial_state=s0, write=write)
+    at = [5, 6, 7, 8, 30, 31, 50, 51]
+    assert torch.equal(gr["d_decay"][at], torch.zeros_like(gr["d_decay"][at]))
+    rest = [t for t in range(70) if t not in at]
+    assert (gr["d_decay"][rest] != 0).all() and gr["dA_log"].isfinite().all()
