@@ -101,6 +101,7 @@ template <int kWide_, int V_>
 struct Layout {
   static constexpr int kWide = kWide_, V = V_;
   static constexpr int kLanes = kWide / V, kGroups = 32 / kLanes, kTokens = kScanTile * kGroups;
+  static constexpr bool kClusters = kWide < 64;  // as scan_plan() has it
 };
 
 // The input tiles of a warp, of one array.  Two ways in:
@@ -324,8 +325,8 @@ struct ScanJoin {
     warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
     lane = threadIdx.x & 31;
     group = lane / L::kLanes;
-    ranks = (int)cluster_size();
-    rank = (int)cluster_rank();
+    ranks = L::kClusters ? (int)cluster_size() : 1;
+    rank = L::kClusters ? (int)cluster_rank() : 0;
     carry = reinterpret_cast<float *>(smem);
     tile = reinterpret_cast<Span<V> *>(smem);
     cta = tile + 2 * warps * L::kLanes;
