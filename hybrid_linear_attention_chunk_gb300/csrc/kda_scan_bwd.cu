@@ -35,6 +35,13 @@ struct BwdSmem {
   static constexpr int kMaxWarps = bytes(16, kScanMaxCluster) <= 227 * 1024 ? 16 : 8;
 };
 
+// sum += low, and low what that addition's rounding left out, to be added the next time.
+template <int V> __device__ __forceinline__ void settle(Vec<V> &sum, Vec<V> &low) {
+  const Vec<V> s = add(sum, low), part = fma(sum, all<V>(-1.f), s);
+  low = fma(part, all<V>(-1.f), low);
+  sum = s;
+}
+
 template <typename X, typename G, bool kLogit, bool kComp, typename L>
 __global__ void __launch_bounds__(32 * BwdSmem<X, G, kLogit, L>::kMaxWarps,
                                   BwdSmem<X, G, kLogit, L>::kMaxWarps == 8 &&
@@ -96,7 +103,10 @@ scan_bwd_kernel(ScanArgs a, ScanBwdIo io, float *dA_part, int cblocks) {
     fetch(0, q);
     if (V == 2) fetch(1, q + step);
   }
-  Vec<V> dA = all<V>(0.f);
+  // Over the lane's tiles, of which there may be thousands: a running sum, and the tile's own on top of what the
+  // roundings of the running one left out.  (Where tokens are alike, so are these: of 131072 equal ones a plain sum
+  // was off by 3856 half steps.)
+  Vec<V> dA = all<V>(0.f), dA_tile = all<V>(0.f);
   int par = 0;
   for (int q0 = ranks > 1 ? 0 : q; q0 < tiles; q0 += step, q += step, par ^= 1) {
     const int len = length(q);
@@ -147,13 +157,14 @@ scan_bwd_kernel(ScanArgs a, ScanBwdIo io, float *dA_part, int cblocks) {
       Vec<V> out = mul(cv, meet[j]);
       if (kLogit) {
         out = mul(out, slope);
-        dA = fma(out, scaled, dA);
+        dA_tile = fma(out, scaled, dA_tile);
       }
       if (j < rows) {
         store<V>(dx + (unsigned)(j * D), kComp ? mul(grad, gate.one_minus(l, al[j])) : grad);
         store<V>(dg + (unsigned)(j * D), out);
       }
     }
+    if (kLogit) settle(dA, dA_tile);
     if (ranks == 1 && ends && io.ds0 && live && sh.group == L::kGroups - 1)
 #pragma unroll
       for (int i = 0; i < V; ++i) io.ds0[chain + i] = leave[i];
@@ -174,9 +185,9 @@ scan_bwd_kernel(ScanArgs a, ScanBwdIo io, float *dA_part, int cblocks) {
       sums[(sh.warp * L::kGroups + sh.group) * L::kWide + wide + i] = dA.get(i) / gate.ns.get(i);  // dz z = dz scaled / ns
     cluster_sync_all();
     for (int i = threadIdx.x; i < L::kWide && c0 + i < D; i += blockDim.x) {
-      float s = 0.f;
+      double s = 0.0;
       for (int w = 0; w < sh.warps * L::kGroups; ++w) s += sums[w * L::kWide + i];
-      dA_part[((size_t)n * ranks + sh.rank) * D + c0 + i] = s;
+      dA_part[((size_t)n * ranks + sh.rank) * D + c0 + i] = (float)s;
     }
   }
 }
