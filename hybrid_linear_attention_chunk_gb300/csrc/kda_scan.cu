@@ -33,6 +33,8 @@ struct FwdSmem {
   static constexpr int kWarpBytes = 2 * (Tile<X, L, false>::kBytes + Tile<G, L, kLogit>::kBytes);
   static constexpr size_t bytes(int warps, int ranks) { return ScanJoin<L>::bytes(warps, ranks) + (size_t)warps * kWarpBytes; }
   static constexpr int kMaxWarps = bytes(16, kScanMaxCluster) <= 227 * 1024 ? 16 : 8;
+  static constexpr size_t kMost = bytes(kMaxWarps, kScanMaxCluster);
+  static_assert(kMost <= 227 * 1024);
 };
 
 template <typename X, typename G, bool kLogit, bool kComp, typename L>
@@ -176,7 +178,8 @@ __global__ void __launch_bounds__(256) validate_scan_kernel(ScanArgs a, int *fla
 template <typename X, typename G, bool kLogit, bool kComp, typename L>
 cudaError_t fwd_l(const ScanArgs &a, int warps, int ranks, cudaStream_t s) {
   return launch_chains<L>(scan_fwd_kernel<X, G, kLogit, kComp, L>, a, warps, ranks,
-                          FwdSmem<X, G, kLogit, L>::bytes(warps, ranks), s, a, (a.D + L::kWide - 1) / L::kWide);
+                          FwdSmem<X, G, kLogit, L>::bytes(warps, ranks),
+                          FwdSmem<X, G, kLogit, L>::kMost, s, a, (a.D + L::kWide - 1) / L::kWide);
 }
 
 template <typename X, typename G, bool kLogit, bool kComp, typename Wide, typename Narrow>

@@ -428,14 +428,17 @@ inline ScanPlan scan_plan(const ScanArgs &a, bool vectors, int most) {
   return p;
 }
 
-// Launches one cluster of `ranks` CTAs for each chain block.
+// Launches one cluster of `ranks` CTAs for each chain block.  `most`: the most
+// shared memory that any layout of this kernel takes.  The limit belongs to the
+// kernel, which other threads may be about to launch on another layout, so every
+// call sets the same.
 template <typename L, typename... P>
-cudaError_t launch_chains(void (*kernel)(P...), const ScanArgs &a, int warps, int ranks, size_t smem, cudaStream_t s,
-                          P... args) {
+cudaError_t launch_chains(void (*kernel)(P...), const ScanArgs &a, int warps, int ranks, size_t smem, size_t most,
+                          cudaStream_t s, P... args) {
   const long long blocks = (long long)((a.D + L::kWide - 1) / L::kWide) * a.N * ranks;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};

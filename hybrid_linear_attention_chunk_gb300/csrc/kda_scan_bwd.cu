@@ -33,6 +33,8 @@ struct BwdSmem {
   }
   static constexpr size_t bytes(int warps, int ranks) { return join(warps, ranks) + (size_t)warps * kWarpBytes; }
   static constexpr int kMaxWarps = bytes(16, kScanMaxCluster) <= 227 * 1024 ? 16 : 8;
+  static constexpr size_t kMost = bytes(kMaxWarps, kScanMaxCluster);
+  static_assert(kMost <= 227 * 1024);
 };
 
 // sum += low, and low what that addition's rounding left out, to be added the next time.
@@ -224,7 +226,8 @@ __global__ void __launch_bounds__(256) scan_dA_final_kernel(const double *sums, 
 template <typename X, typename G, bool kLogit, bool kComp, typename L>
 cudaError_t bwd_l(const ScanArgs &a, const ScanBwdIo &io, float *part, int warps, int ranks, cudaStream_t s) {
   return launch_chains<L>(scan_bwd_kernel<X, G, kLogit, kComp, L>, a, warps, ranks,
-                          BwdSmem<X, G, kLogit, L>::bytes(warps, ranks), s, a, io, part, (a.D + L::kWide - 1) / L::kWide);
+                          BwdSmem<X, G, kLogit, L>::bytes(warps, ranks),
+                          BwdSmem<X, G, kLogit, L>::kMost, s, a, io, part, (a.D + L::kWide - 1) / L::kWide);
 }
 
 template <typename X, typename G, bool kLogit, bool kComp, typename Wide, typename Narrow>
