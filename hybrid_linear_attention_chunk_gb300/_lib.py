@@ -446,8 +446,15 @@ def kda_affine_compose(pairs, initial_state=None, entry_states=None, *, stream=N
 # sizes and types.
 
 WRITES = {"one": 0, "complement": 1}
-_current_device = torch._C._cuda_getDevice
-_current_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _stream_of(index):
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# Without the Python layers around them (0.4 us a call), where this build of torch has them: one without CUDA does not.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream_of)
 
 
 def _arg(name, t, shape, dtype, index):
