@@ -515,9 +515,9 @@ template <typename S> cudaError_t bwd(const NormArgs &a, const NormBwdIo &io, fl
   const bool weights = io.dw1 || io.dsc || io.dw2;
   const long long groups = (a.rows + S::kGroups - 1) / S::kGroups, most = kSms * RowStages<S>::kBlocks;
   const int blocks = (int)(groups < most ? groups : most);
-  constexpr int smem = RowStages<S>::kBytes;
+  constexpr int smem = RowStages<S>::kBytes;  // with the kernel's own sums, below 2 KB, past 48 KB only after leave
   cudaError_t e = cudaSuccess;
-  if (smem > 48 * 1024) e = cudaFuncSetAttribute(norm_bwd_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (smem > 46 * 1024) e = cudaFuncSetAttribute(norm_bwd_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   norm_bwd_kernel<S><<<blocks, S::kBlock, smem, s>>>(a, io, weights ? ws : nullptr);
   e = cudaGetLastError();
@@ -529,12 +529,19 @@ template <typename S> cudaError_t bwd(const NormArgs &a, const NormBwdIo &io, fl
 // Calls f with the row shape for this width: pieces of 8 elements when every
 // row of every tensor starts on 16 bytes, else single elements.  Two pieces per
 // thread where rows are wide enough (65536 x 2048 forward: 310 us against 350 of
-// one; 32768 x 2048 forward and backward in bf16: 359 against 430), one in the
-// backward of all-fp32 rows, whose sums and copies take the registers and the
-// shared memory (815 against 926).  Narrow rows take as few lanes as hold them,
-// and in the forward two rows at once when there are many (262144 rows of 128: 35.1
-// us against 38.3 of one row, 36.9 on 16 lanes of one piece; 4194304 rows of 32:
-// 157 us against 440 on 16 lanes).
+// one; 32768 x 2048 forward and backward in bf16: 359 against 430), in the
+// backward from 1025 on (32768 x 1024 in bf16: 131 us against 142 of two).  Wider
+// types fill its registers and shared memory with fewer: all-fp32 rows take one
+// piece (16384 x 2048: 299 us against 367); rows of one fp32 and one bf16 type take
+// one up to 2048 (bf16 y with fp32 residual 204 us against 289, fp32 y with bf16
+// residual 240 against 285) and two above, where one would leave a single block on
+// an SM (16384 x 4096: 406 against 496, and 564 against 583).
+// Narrow rows take as few lanes as hold them, and in the forward two rows at once when
+// there are many: in bf16 of two pieces a lane from 65 to 256 (262144 rows of 128: 35.1
+// us against 38.3 of one row, 36.9 on 16 lanes of one piece; 4194304 rows of 32: 157 us
+// against 440 on 16 lanes), where a tensor is fp32 of one, as two do not fit the
+// registers (262144 x 128, bf16 y with fp32 residual: 74 us against 98, 80 of one row;
+// fp32 y with bf16 residual 84, 123, 86; all fp32 102, 143, 102).
 // Rows of single elements have a step of threads for each doubling of the width, as
 // a piece past the row costs as much as one in it: bf16 with every part, 258111 x 130
 // on 64 threads 139 us forward and 363 backward, on 256 threads 416 and 1215;
@@ -542,13 +549,15 @@ template <typename S> cudaError_t bwd(const NormArgs &a, const NormBwdIo &io, fl
 template <typename T, typename R, bool kBwd, typename F>
 cudaError_t with_shape(int width, bool vectors, bool many, F f) {
   if (vectors) {
-    constexpr bool one = kBwd && sizeof(T) + sizeof(R) > 6;
+    constexpr int bytes = sizeof(T) + sizeof(R);
+    constexpr bool one2048 = kBwd && bytes > 4, one4096 = kBwd && bytes > 6;
     if constexpr (!kBwd) {
+      constexpr int c = bytes > 4 ? 1 : 2;
       if (many && width <= 16) return f(Shape<T, R, 8, 1, 2, 2>());
       if (many && width <= 32) return f(Shape<T, R, 8, 1, 4, 2>());
       if (many && width <= 64) return f(Shape<T, R, 8, 1, 8, 2>());
-      if (many && width <= 128) return f(Shape<T, R, 8, 2, 8, 2>());
-      if (many && width <= 256) return f(Shape<T, R, 8, 2, 16, 2>());
+      if (many && width <= 128) return f(Shape<T, R, 8, c, 16 / c, 2>());
+      if (many && width <= 256) return f(Shape<T, R, 8, c, 32 / c, 2>());
     } else {
       if (width <= 16) return f(Shape<T, R, 8, 1, 2>());
       if (width <= 32) return f(Shape<T, R, 8, 1, 4>());
@@ -557,9 +566,9 @@ cudaError_t with_shape(int width, bool vectors, bool many, F f) {
     if (width <= 128) return f(Shape<T, R, 8, 1, 16>());
     if (width <= 256) return f(Shape<T, R, 8, 1, 32>());
     if (width <= 512) return f(Shape<T, R, 8, kBwd ? 1 : 2, kBwd ? 64 : 32>());
-    if (width <= 1024) return f(Shape<T, R, 8, one ? 1 : 2, one ? 128 : 64>());
-    if (width <= 2048) return f(Shape<T, R, 8, one ? 1 : 2, one ? 256 : 128>());
-    if (width <= 4096) return f(Shape<T, R, 8, one ? 1 : 2, one ? 512 : 256>());
+    if (width <= 1024) return f(Shape<T, R, 8, kBwd ? 1 : 2, kBwd ? 128 : 64>());
+    if (width <= 2048) return f(Shape<T, R, 8, one2048 ? 1 : 2, one2048 ? 256 : 128>());
+    if (width <= 4096) return f(Shape<T, R, 8, one4096 ? 1 : 2, one4096 ? 512 : 256>());
     return f(Shape<T, R, 8, 2, 512>());
   }
   if (width <= 32) return f(Shape<T, R, 1, 1, 32>());
