@@ -21,7 +21,7 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 bool aligned_to(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 
-bool dim_ok(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
+bool dim_ok(int d) { return d == kMinDim || d == 32 || d == 64 || d == kMaxDim; }
 
 bool dtype_ok(kda_dtype t) { return t == KDA_F32 || t == KDA_BF16; }
 

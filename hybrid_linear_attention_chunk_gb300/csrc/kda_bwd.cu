@@ -913,19 +913,23 @@ cudaError_t launch_chunk_bwd(const PrefillArgs &p, const BwdIo &io, void *ws, cu
   a.Sent = w; w += sl * (size_t)p.dk * p.dv;
   a.dSx = w;
   if (a.N * a.H == 0) return cudaSuccess;
+  // The limits belong to the kernels, which other threads may be about to launch with other head sizes, so every call
+  // sets those of the largest (the scan's: the most partial sums, of the fewest columns, too).
   cudaError_t e;
   if (a.nslots > 0) {
     const size_t sp = prep_smem_bytes(p.dk);
-    e = cudaFuncSetAttribute(bwd_prep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sp);
+    e = cudaFuncSetAttribute(bwd_prep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)prep_smem_bytes(kMaxDim));
     if (e != cudaSuccess) return e;
     bwd_prep_kernel<<<dim3(a.nslots, p.H), kBThreads, sp, s>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   const size_t ssf = scan_smem_bytes(false, p.dk, p.dv), ssr = scan_smem_bytes(true, p.dk, p.dv);
   const dim3 sgrid(p.N * p.H, (p.dv + kScanDvt - 1) / kScanDvt);
-  e = cudaFuncSetAttribute(bwd_scan_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ssf);
+  e = cudaFuncSetAttribute(bwd_scan_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)scan_smem_bytes(false, kMaxDim, kMinDim));
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(bwd_scan_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ssr);
+    e = cudaFuncSetAttribute(bwd_scan_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)scan_smem_bytes(true, kMaxDim, kMinDim));
   if (e != cudaSuccess) return e;
   bwd_scan_kernel<false><<<sgrid, kBThreads, ssf, s>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
@@ -933,7 +937,7 @@ cudaError_t launch_chunk_bwd(const PrefillArgs &p, const BwdIo &io, void *ws, cu
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (a.nslots > 0) {
     const size_t sg = grads_smem_bytes(p.dk);
-    e = cudaFuncSetAttribute(bwd_grads_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sg);
+    e = cudaFuncSetAttribute(bwd_grads_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)grads_smem_bytes(kMaxDim));
     if (e != cudaSuccess) return e;
     bwd_grads_kernel<<<dim3(a.nslots, p.H), kBThreads, sg, s>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;

@@ -247,8 +247,9 @@ chunk_simt_kernel(PrefillArgs a, int dvt) {
 cudaError_t launch_chunk_simt(const PrefillArgs &a, cudaStream_t s) {
   const int dvt = a.dv >= 64 ? 64 : a.dv;
   const size_t smem = simt_smem_bytes(a.chunk, a.dk, dvt);
+  // the largest call's: the limit belongs to the kernel, which another thread may be about to launch on other sizes
   cudaError_t e = cudaFuncSetAttribute(chunk_simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem);
+                                       (int)simt_smem_bytes(64, kMaxDim, 64));
   if (e != cudaSuccess) return e;
   dim3 grid(a.N * a.H, a.dv / dvt);
   if (grid.x == 0) return cudaSuccess;

@@ -21,6 +21,8 @@ constexpr float kLogDecayFloor = -5.0f;
 // factored per 16-token tile ([K3-notes §2.2, Fig. 3]).
 constexpr float kSingleRefBound = -80.0f;
 
+constexpr int kMinDim = 16, kMaxDim = 128;  // of dk and dv: 16, 32, 64 or 128
+
 struct PrefillArgs {
   int N;        // sequences
   int T_total;  // tokens in the packed buffer

@@ -13,20 +13,17 @@ DEV = "cuda:0"
 HERE = os.path.dirname(os.path.abspath(__file__))
 
 
-@pytest.fixture(scope="module")
-def hammer(tmp_path_factory):
-    so = str(tmp_path_factory.mktemp("hammer") / "hammer.so")
+def compiled_loops(folder):
+    so = str(folder / "hammer.so")
     subprocess.run(["gcc", "-O2", "-shared", "-fPIC", "-I", os.path.join(os.path.dirname(HERE), "include"),
                     os.path.join(HERE, "_hammer.c"), "-o", so], check=True)
-    fn = ctypes.CDLL(so).hammer
-    fn.restype = ctypes.c_int
-    return fn
+    return ctypes.CDLL(so)
 
 
 @pytest.mark.parametrize("d", [64, 33])
-def test_two_layouts_of_one_kernel_from_two_threads(kda, hammer, d):
+def test_two_layouts_of_one_kernel_from_two_threads(kda, tmp_path, d):
     """bf16 logits: 300 tokens run on 8 warps, 5000 on a cluster of CTAs of 16."""
-    lib = kda.load()
+    lib, hammer = kda.load(), compiled_loops(tmp_path).hammer
     gen = torch.Generator(device=DEV)
     gen.manual_seed(1)
     P, A, results, sets = ctypes.c_void_p, torch.zeros(1, device=DEV), {}, []
