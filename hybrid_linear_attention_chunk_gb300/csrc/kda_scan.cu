@@ -7,14 +7,14 @@
 // product of alphas; once the state that enters the tile is known, a token's
 // output is sum + product * state: one read of the inputs, one write of the
 // output.  The state passes from tile to tile in the recurrence's order (ScanJoin
-// in kda_scan.cuh), so it keeps the error of a token-by-token run and is the same
-// from run to run.  Inputs come in two tiles ahead, so loads are in flight under
+// in kda_scan.cuh) by the tiles' own log-sums, so its error grows no faster than in a
+// token-by-token run, and it is the same from run to run.  Inputs come in two tiles ahead, so loads are in flight under
 // everything else.
 //
 // Bounds and measurements (6.78 TB/s is a measured copy on the same GPU):
 //   bound by HBM where chains are many: 24 packed sequences, 49152 x 4096, bf16
-//   with fp32 log-decay, 240 us, 6.7 TB/s (0.99 of the copy); 16 instructions an
-//   element, issue slots 42 % used;
+//   with fp32 log-decay, 240 us, 6.7 TB/s (0.99 of the copy); 15 instructions an
+//   element, issue slots 41 % used;
 //   few chains (262144 x 2048 of one sequence, decay logits): 661 us, 4.9 TB/s
 //   (0.72): rows of 16 channels are 32-byte requests, and the logits' two
 //   exponentials, reciprocal and expm1 make 28 instructions an element (67 % of

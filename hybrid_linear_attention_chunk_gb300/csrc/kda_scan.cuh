@@ -1,15 +1,23 @@
 // Device pieces that the kernels of the gated linear recurrence share
 // (kda_scan.cu, kda_scan_bwd.cu).
 //
-// Numerics.  With alpha near 1 (a memory of thousands of tokens) rounding
-// alpha to fp32 costs up to 3e-8 / (1 - alpha) of the state, the same way at
-// every token of a constant decay.  So the decay of a whole 16-token tile, by
-// which a state is carried on, comes from the sum of its logs: h' = h + (e h + B)
-// with e = expm1(sum g) when sum g > -1/8, whose rounding error is relative to
-// 1 - alpha, and alpha itself below that, so that a strong decay (alpha = 0 at
-// the least) leaves nothing of h behind.  Inside a tile the products of up to 16
-// rounded alphas are off by at most 16 roundings, of the tile's own sums alone.
-// w = 1 - alpha comes from expm1(g) too.  Everything is fp32.
+// Numerics, in half steps of fp32 (2^-24 relative).  With alpha near 1 (a memory of
+// thousands of tokens) rounding alpha to fp32 costs up to 3e-8 / (1 - alpha) of the
+// state, the same way at every token of a constant decay.  So the decay of a whole
+// 16-token tile, by which a state is carried on, comes from the sum of its logs:
+// h' = h + (e h + B) with e = expm1(sum g) when sum g > -1/8, whose rounding error is
+// relative to 1 - alpha, and alpha itself below that, so that a strong decay (alpha
+// = 0 at the least) leaves nothing of h behind.  What is left of a state after a tile
+// of log-sum G is off by at most 9 + 18 |G| more: 16 |G| from the sum, 4 + 2 |G| from the
+// power (less from expm1), 3 where spans join, 2 where they act.  (With logits g itself
+// is off by (10 + |s z|) |g|.)
+//   Inside a tile, products of up to 16 alphas multiply the state (or gradient) that
+// enters it.  Each alpha is a power off by up to 4 half steps and by |g| from its
+// argument, and each product rounds: 16 (5 + |g|) at the tile's last token.  They
+// reach the tile's outputs (in the backward its gradients, and the states that it
+// rebuilds), and nothing that is carried on: out of a sequence's last token and its
+// final state may differ by as much.
+//   w = 1 - alpha comes from expm1(g) too.  Everything is fp32; alphas below 2^-126 are 0.
 //
 // The decay of a tile or span is one float c: the sign bit set means c = e
 // (e <= 0; -0 for a sum of 0), clear means c = alpha.
@@ -25,7 +33,7 @@ constexpr float kNearOne = -0.125f;
 __device__ __forceinline__ bool is_near(float c) { return __float_as_int(c) < 0; }
 
 // expm1(g) on (-1/8, 0] as g + g^2 q(g), q the quadratic with the least maximum
-// relative error there (a reweighted least-squares fit to the series): 1.8e-8
+// relative error there (a reweighted least-squares fit to the series): 1.96e-8
 // of the value, a third of half a step.
 constexpr float kExpm1C0 = 0.4999971389770508f, kExpm1C1 = 0.16652730107307434f, kExpm1C2 = 0.03972300514578819f;
 __device__ __forceinline__ float expm1_near(float g) {
@@ -303,9 +311,11 @@ __device__ __forceinline__ void barrier_arrive(int id, int threads) {
 //   so a state waits for a load, a step and a store per tile, and one warp's
 //   arithmetic runs under another's waiting.  Warp w waits at named barrier w for
 //   its predecessor's arrival, which is never a round ahead, as the predecessor's
-//   own next state comes through the waiter.  (Rings of teams of 2, 4 and 8 warps
-//   that join their tiles first were slower: 262144 x 2048 in 0.68 to 0.99 ms
-//   against 0.65 to 0.75.)
+//   own next state comes through the waiter.  So the ring has every barrier of the
+//   CTA, that of __syncthreads (0) among them, and uses with different thread counts
+//   must not meet: a kernel on this path has the cluster's barrier for anything else.
+//   (Rings of teams of 2, 4 and 8 warps that join their tiles first were slower:
+//   262144 x 2048 in 0.68 to 0.99 ms against 0.65 to 0.75.)
 //   A cluster: its CTAs take consecutive spans of a round.  Warp 0 joins its
 //   CTA's warps into one span and stores it in every CTA; each thread keeps the
 //   round's state in registers.

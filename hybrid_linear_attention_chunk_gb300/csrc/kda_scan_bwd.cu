@@ -9,12 +9,12 @@
 // of a channel); with it the tile's 16 states are rebuilt in registers.  Each
 // input is read once, each gradient written once.
 //
-// Measured on 32768 x 4096 (4 sequences, bf16, decay logits, w = 1 - alpha): 283 us
-// of the 437 us that forward and backward take, 10.25 bytes an element at 4.9 TB/s
-// (0.72 of a measured copy).  It is bound by instruction issue (53 an element,
-// 69 % of the slots of two CTAs of 8 warps that 128 registers leave on an SM):
-// the gate and 1 - alpha are formed twice, since keeping them across the hand-on
-// of the gradient would take 64 registers more.
+// Measured on 32768 x 4096 (4 sequences, bf16, decay logits, w = 1 - alpha): 284 us
+// of the 436 us that forward and backward take, 10.25 bytes an element at 4.8 TB/s
+// (0.71 of a measured copy).  It issues 53 instructions an element into 68 % of the
+// slots; the two CTAs of 8 warps that 128 registers leave on an SM do not cover the
+// rest of the latency.  The gate and 1 - alpha are formed twice, since keeping them
+// across the hand-on of the gradient would take 64 registers more.
 #include <initializer_list>
 
 #include "kda_scan.cuh"
