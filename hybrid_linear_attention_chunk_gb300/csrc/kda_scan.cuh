@@ -10,7 +10,7 @@
 // = 0 at the least) leaves nothing of h behind.  What is left of a state after a tile
 // of log-sum G is off by at most 9 + 18 |G| more: 16 |G| from the sum, 4 + 2 |G| from the
 // power (less from expm1), 3 where spans join, 2 where they act.  (With logits g itself
-// is off by (10 + |s z|) |g|.)
+// is off by (10 + 7 |s z|) |g|, 6 of the 7 from s.)
 //   Inside a tile, products of up to 16 alphas multiply the state (or gradient) that
 // enters it.  Each alpha is a power off by up to 4 half steps and by |g| from its
 // argument, and each product rounds: 16 (5 + |g|) at the tile's last token.  They
