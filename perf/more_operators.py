@@ -83,7 +83,7 @@ def draw(rng):
     Hk = _log_int(rng, 1, 16)
     Hq = Hk * rng.choice([1, 1, 2, 3, 4, 5, 7, 8])
     if kind.startswith("rope"):
-        rot = rng.choice([0, d // 2, d, d, 2 * rng.randint(0, d // 2)])
+        rot = rng.choice([0, d // 2, d, d, 8 * rng.randint(0, d // 8)])
         T = _log_int(rng, 1, min(1 << 16, (1 << 27) // (Hq + Hk) // d))
         return dict(kind=kind, T=T, Hq=Hq, Hk=Hk, d=d, rot=rot, layout=rng.choice(["half", "interleaved"]),
                     norm=rng.random() < 0.7 or rot == 0, dtype=dtype, far=rng.choice([0, 0, 1 << 20]),
