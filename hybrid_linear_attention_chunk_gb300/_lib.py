@@ -57,6 +57,25 @@ class KdaNormDesc(ctypes.Structure):
                 ("pre_eps", ctypes.c_float)]
 
 
+class KdaRopeDesc(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int), ("Hq", ctypes.c_int), ("Hk", ctypes.c_int), ("d", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("rot", ctypes.c_int), ("layout", ctypes.c_int),
+                ("rot_scale", ctypes.c_float), ("norm", ctypes.c_int), ("eps", ctypes.c_float),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("q_out_stride", ctypes.c_int64),
+                ("k_out_stride", ctypes.c_int64), ("dq_stride", ctypes.c_int64), ("dk_stride", ctypes.c_int64)]
+
+
+class KdaPagedDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("Hq", ctypes.c_int), ("Hk", ctypes.c_int),
+                ("d", ctypes.c_int), ("num_seqs", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("num_pages", ctypes.c_int), ("max_pages", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                ("out_stride", ctypes.c_int64), ("cache_stride", ctypes.c_int64), ("rot", ctypes.c_int),
+                ("layout", ctypes.c_int), ("rot_scale", ctypes.c_float), ("norm", ctypes.c_int),
+                ("eps", ctypes.c_float), ("causal", ctypes.c_int), ("scale", ctypes.c_float),
+                ("validate", ctypes.c_int)]
+
+
 class KdaError(RuntimeError):
     def __init__(self, status: int, fn: str, detail: str = ""):
         self.status = status
@@ -126,6 +145,16 @@ def load() -> ctypes.CDLL:
         for fn in (lib.kda_scan_states_size, lib.kda_scan_fwd, lib.kda_scan_bwd_workspace_size, lib.kda_scan_bwd,
                    lib.kda_scan_step, lib.kda_block_norm_fwd, lib.kda_block_norm_bwd_workspace_size,
                    lib.kda_block_norm_bwd):
+            fn.restype = ctypes.c_int
+        RP, PP = ctypes.POINTER(KdaRopeDesc), ctypes.POINTER(KdaPagedDesc)
+        lib.kda_qk_rope_fwd.argtypes = [RP, P, P, P, P, P, P, P, P, P]
+        lib.kda_qk_rope_bwd_workspace_size.argtypes = [RP, Z]
+        lib.kda_qk_rope_bwd.argtypes = [RP, P, P, P, P, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
+        lib.kda_kv_append.argtypes = [PP, P, P, P, P, P, P, P, P, P, P, P, P, P]
+        lib.kda_paged_attn_workspace_size.argtypes = [PP, Z]
+        lib.kda_paged_attn.argtypes = [PP, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
+        for fn in (lib.kda_qk_rope_fwd, lib.kda_qk_rope_bwd_workspace_size, lib.kda_qk_rope_bwd, lib.kda_kv_append,
+                   lib.kda_paged_attn_workspace_size, lib.kda_paged_attn):
             fn.restype = ctypes.c_int
         lib.kda_status_string.argtypes = [ctypes.c_int]
         lib.kda_status_string.restype = ctypes.c_char_p
@@ -786,3 +815,266 @@ def kda_block_norm_bwd(y, d_out, d_normed=None, residual=None, gate=None, *, pos
     if st:
         _check(st, "kda_block_norm_bwd")
     return grads
+
+
+# --------------------------------- norm and rotation, append and attention over a paged cache
+
+LAYOUTS = {"half": 0, "interleaved": 1}
+
+
+def _fits(*sizes):
+    if max(sizes) >= 1 << 31:  # (ctypes would cut it off)
+        raise ValueError("a size passes 32 bits")
+
+
+@functools.lru_cache(maxsize=512)
+def _rope_sized(*fields) -> _Sized:
+    _fits(*fields[:4])
+    return _Sized(KdaRopeDesc(*fields))
+
+
+@functools.lru_cache(maxsize=512)
+def _paged_sized(*fields) -> _Sized:
+    _fits(*fields[:9])
+    return _Sized(KdaPagedDesc(*fields))
+
+
+def _rows_arg(name, t, lead, heads, d, dtype, index):
+    """Address and token stride of an optional [..., heads, d] tensor with dense
+    heads, whose tokens lie a fixed distance apart (as the parts of one
+    projection's output do)."""
+    if t is None:
+        return None, 0
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.shape != lead + (heads, d):
+        raise ValueError(f"{name} must have shape {tuple(lead) + (heads, d)}, not {tuple(t.shape)}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on CUDA device {index}, not {t.device}")
+    if t.is_contiguous():
+        return t.data_ptr() or 256, 0
+    st = t.stride()
+    if (st[-1] != 1 and d > 1) or (st[-2] != d and heads > 1):
+        raise ValueError(f"{name} must have dense heads")
+    if len(lead) == 2 and lead[0] > 1 and lead[1] > 1 and st[0] != lead[1] * st[1]:
+        raise ValueError(f"{name} must have its tokens a fixed distance apart")
+    if len(lead) == 2 and lead[1] == 1:
+        return t.data_ptr() or 256, st[0] if lead[0] > 1 else 0
+    return t.data_ptr() or 256, st[len(lead) - 1] if lead[-1] > 1 else 0
+
+
+def _layout(name):
+    if name not in LAYOUTS:
+        raise ValueError(f"layout must be one of {sorted(LAYOUTS)}")
+    return LAYOUTS[name]
+
+
+def _turn_args(inv_freq, q_weight, k_weight, d, index):
+    """rot, and the addresses of the frequencies and weights."""
+    if inv_freq is not None and inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be [rot / 2]")
+    n = 0 if inv_freq is None else inv_freq.shape[0]
+    return 2 * n, (None if n == 0 else _arg("inv_freq", inv_freq, (n,), torch.float32, index),
+                   _arg("q_weight", q_weight, (d,), torch.float32, index),
+                   _arg("k_weight", k_weight, (d,), torch.float32, index))
+
+
+def _rope_call(q, k, positions, inv_freq, q_weight, k_weight, layout, rot_scale, norm, eps, outs):
+    """The sized descriptor and the addresses of inputs, weights and `outs`: pairs
+    (name, tensor) of one more q-like and k-like tensor in turn."""
+    if q.dim() not in (3, 4):
+        raise ValueError("q must be [tokens, Hq, d] or [B, T, Hq, d]")
+    lead, (Hq, d), index, dt = q.shape[:-2], q.shape[-2:], q.get_device(), q.dtype
+    tokens = lead.numel()
+    Hk = 0 if k is None else k.shape[-2] if k.dim() > 1 else -1
+    pq, sq = _rows_arg("q", q, lead, Hq, d, dt, index)
+    pk, sk = _rows_arg("k", k, lead, Hk, d, dt, index)
+    rot, turn = _turn_args(inv_freq, q_weight, k_weight, d, index)
+    pos = None if rot == 0 else _arg("positions", positions, lead, torch.int32, index)
+    if rot and positions is None:
+        raise ValueError("a rotation needs positions")
+    there, strides = [], [sq, sk]
+    for i, (name, t) in enumerate(outs):
+        p, s = _rows_arg(name, t, lead, Hk if i % 2 else Hq, d, dt, index)
+        there.append(p)
+        strides.append(s)
+    strides += [0] * (6 - len(strides))
+    sized = _rope_sized(tokens, Hq, Hk, d, _dt(q), rot, _layout(layout), rot_scale, 1 if norm else 0, eps, *strides)
+    return sized, (pq, pk, pos, *turn), there
+
+
+def kda_qk_rope_fwd(q, k=None, positions=None, inv_freq=None, q_weight=None, k_weight=None, *, layout="half",
+                    rot_scale=1.0, norm=True, eps=1e-6, q_out=None, k_out=None, stream=None):
+    """Norm and position rotation of queries and keys through the C ABI.
+
+    q [tokens, Hq, d] (or [B, T, Hq, d]) and k [.., Hk, d] or None, possibly
+    parts of one projection's output; positions: int32 [tokens]; inv_freq: fp32
+    [rot / 2], None for no rotation; weights: fp32 [d] or None for ones;
+    layout: pairs (i, i + rot / 2), "half", or (2i, 2i + 1), "interleaved";
+    norm=False leaves the RMS norm out.  Returns (q_out, k_out); an output may
+    be its input (in place)."""
+    lib = _lib or load()
+    index = q.get_device()
+    if _elsewhere(index, stream):
+        return _there(lambda: kda_qk_rope_fwd(q, k, positions, inv_freq, q_weight, k_weight, layout=layout,
+                                              rot_scale=rot_scale, norm=norm, eps=eps, q_out=q_out, k_out=k_out),
+                      index, stream, (q, k, positions, inv_freq, q_weight, k_weight, q_out, k_out))
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if k_out is None and k is not None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    sized, ins, outs = _rope_call(q, k, positions, inv_freq, q_weight, k_weight, layout, rot_scale, norm, eps,
+                                  (("q_out", q_out), ("k_out", k_out)))
+    st = lib.kda_qk_rope_fwd(sized.ref, *ins, *outs, _current_stream(index))
+    if st:
+        _check(st, "kda_qk_rope_fwd")
+    return q_out, k_out
+
+
+def kda_qk_rope_bwd(d_q_out, d_k_out, q, k=None, positions=None, inv_freq=None, q_weight=None, k_weight=None, *,
+                    layout="half", rot_scale=1.0, norm=True, eps=1e-6, stream=None, workspace=None, grads=None):
+    """Gradients of kda_qk_rope_fwd through the C ABI for
+    L = <d_q_out, q_out> + <d_k_out, k_out>.  Returns a dict: d_q and d_k in q's
+    dtype, d_q_weight and d_k_weight in fp32; None for an input that was not
+    given.  `grads` may pass that dict preallocated (parts of one projection's
+    gradient, say): then the weights' gradients that it holds are written."""
+    lib = _lib or load()
+    index, f32 = q.get_device(), torch.float32
+    if _elsewhere(index, stream):
+        return _there(lambda: kda_qk_rope_bwd(d_q_out, d_k_out, q, k, positions, inv_freq, q_weight, k_weight,
+                                              layout=layout, rot_scale=rot_scale, norm=norm, eps=eps,
+                                              workspace=workspace, grads=grads),
+                      index, stream, (d_q_out, d_k_out, q, k, positions, inv_freq, q_weight, k_weight, workspace))
+    if grads is None:
+        new = lambda like: None if like is None else torch.empty(like.shape, dtype=like.dtype, device=q.device)  # noqa: E731
+        grads = {"d_q": new(q), "d_k": new(k), "d_q_weight": new(q_weight), "d_k_weight": new(k_weight)}
+    get, d = grads.get, q.shape[-1:]
+    weights = (_arg("d_q_weight", get("d_q_weight"), d, f32, index), _arg("d_k_weight", get("d_k_weight"), d, f32, index))
+    sized, ins, outs = _rope_call(q, k, positions, inv_freq, q_weight, k_weight, layout, rot_scale, norm, eps,
+                                  (("d_q_out", d_q_out), ("d_k_out", d_k_out), ("d_q", get("d_q")), ("d_k", get("d_k"))))
+    if workspace is None and any(weights):
+        workspace = torch.empty(sized.size("kda_qk_rope_bwd_workspace_size"), dtype=torch.uint8, device=q.device)
+    ws, ws_bytes = _workspace(workspace, index)
+    st = lib.kda_qk_rope_bwd(sized.ref, *ins, *outs, *weights, ws, ws_bytes, _current_stream(index))
+    if st:
+        _check(st, "kda_qk_rope_bwd")
+    return grads
+
+
+def _paged_call(lead, heads, dtype, k_cache, v_cache, page_table, lens, cu_seqlens, index):
+    """Sizes and the addresses of what the append and the attention share: the
+    descriptor's fields up to dtype, the cache's stride, (lens, cu_seqlens, table), caches."""
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must be [num_pages, Hk, page_size, d]")
+    pages, Hk, page, d = k_cache.shape
+    if page_table.dim() != 2 or lens.dim() != 1:
+        raise ValueError("page_table must be [N, max_pages] and lens [N]")
+    N, max_pages = page_table.shape
+    tokens = lead.numel()
+    if cu_seqlens is None:
+        if N == 0 or tokens % N or (len(lead) == 2 and lead[0] != N):
+            raise ValueError(f"{tuple(lead)} tokens are no batch of {N} sequences")
+        B, T, seqs = N, tokens // N, 0
+    else:
+        if len(lead) == 2 and lead[0] != 1:
+            raise ValueError("cu_seqlens needs B = 1")
+        B, T, seqs = 1, tokens, N
+    caches, strides = [], []
+    for name, c in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if c.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, not {c.dtype}")
+        if c.shape != k_cache.shape:
+            raise ValueError(f"{name} must have shape {tuple(k_cache.shape)}, not {tuple(c.shape)}")
+        if c.get_device() != index:
+            raise ValueError(f"{name} must be on CUDA device {index}, not {c.device}")
+        st = c.stride()
+        if not c.is_contiguous() and ((st[3] != 1 and d > 1) or (st[2] != d and page > 1) or (st[1] != page * d and Hk > 1)):
+            raise ValueError(f"{name} must have dense pages")
+        caches.append(c.data_ptr() or 256)
+        strides.append(st[0] if pages > 1 else Hk * page * d)
+    if strides[0] != strides[1]:
+        raise ValueError("k_cache and v_cache must have the same distance from page to page")
+    where = (_arg("lens", lens, (N,), torch.int32, index),
+             None if cu_seqlens is None else _arg("cu_seqlens", cu_seqlens, (N + 1,), torch.int32, index),
+             _arg("page_table", page_table, (N, max_pages), torch.int32, index))
+    return (B, T, heads, Hk, d, seqs, page, pages, max_pages, _dt(k_cache)), strides[0], where, caches
+
+
+def kda_kv_append(k, v, k_cache, v_cache, page_table, lens, cu_seqlens=None, *, q=None, inv_freq=None, q_weight=None,
+                  k_weight=None, layout="half", rot_scale=1.0, norm=False, eps=1e-6, q_out=None, validate=False,
+                  stream=None):
+    """Stores new tokens' keys and values in a paged cache through the C ABI, the
+    keys (and the queries q, where given) normed and rotated on the way.
+
+    k, v: [tokens, Hk, d] (or [B, T, Hk, d]), q [.., Hq, d]; k_cache, v_cache:
+    [num_pages, Hk, page_size, d]; page_table: int32 [N, max_pages]; lens: int32
+    [N], the sequences' lengths with the new tokens; cu_seqlens: int32 [N + 1]
+    for packed sequences, None for the same number of tokens each.  The rotation
+    is kda_qk_rope_fwd's, at the tokens' positions.  Returns q_out (None without q)."""
+    lib = _lib or load()
+    index = k.get_device()
+    if _elsewhere(index, stream):
+        return _there(lambda: (kda_kv_append(k, v, k_cache, v_cache, page_table, lens, cu_seqlens, q=q,
+                                             inv_freq=inv_freq, q_weight=q_weight, k_weight=k_weight, layout=layout,
+                                             rot_scale=rot_scale, norm=norm, eps=eps, q_out=q_out, validate=validate),),
+                      index, stream, (k, v, k_cache, v_cache, page_table, lens, cu_seqlens, q, inv_freq, q_weight,
+                                      k_weight, q_out))[0]
+    if k.dim() not in (3, 4):
+        raise ValueError("k must be [tokens, Hk, d] or [B, T, Hk, d]")
+    lead, (Hk, d), dt = k.shape[:-2], k.shape[-2:], k.dtype
+    Hq = Hk if q is None else q.shape[-2] if q.dim() > 1 else -1
+    sizes, cs, where, caches = _paged_call(lead, Hq, dt, k_cache, v_cache, page_table, lens, cu_seqlens, index)
+    if sizes[3:5] != (Hk, d):
+        raise ValueError(f"k has {Hk} heads of {d}, the cache {sizes[3]} of {sizes[4]}")
+    if q is None and q_out is not None:
+        raise ValueError("q_out needs q")
+    if q is not None and q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    (pq, sq), (pk, sk), (pv, sv), (po, so) = (
+        _rows_arg("q", q, lead, Hq, d, dt, index), _rows_arg("k", k, lead, Hk, d, dt, index),
+        _rows_arg("v", v, lead, Hk, d, dt, index), _rows_arg("q_out", q_out, lead, Hq, d, dt, index))
+    rot, turn = _turn_args(inv_freq, q_weight, k_weight, d, index)
+    sized = _paged_sized(*sizes, sq, sk, sv, so, cs, rot, _layout(layout), rot_scale, 1 if norm else 0, eps, 1, 1.0,
+                         1 if validate else 0)
+    st = lib.kda_kv_append(sized.ref, pq, pk, pv, *where, *turn, po, *caches, _current_stream(index))
+    if st:
+        _check(st, "kda_kv_append")
+    return q_out
+
+
+def kda_paged_attn(q, k_cache, v_cache, page_table, lens, cu_seqlens=None, out=None, lse=None, *, causal=True,
+                   scale=None, want_lse=False, validate=False, stream=None, workspace=None):
+    """Softmax attention of new tokens over a paged cache through the C ABI, for
+    prefills, single tokens and packed mixtures of both.
+
+    q: [tokens, Hq, d] (or [B, T, Hq, d]); the cache, page_table, lens and
+    cu_seqlens as kda_kv_append's; scale: on the scores (None: d^-1/2); causal:
+    keys up to the query's own position, else all.  Returns (out, lse): out as
+    q, lse [.., Hq] fp32 with want_lse (or an `lse` buffer), else None."""
+    lib = _lib or load()
+    index = q.get_device()
+    if _elsewhere(index, stream):
+        return _there(lambda: kda_paged_attn(q, k_cache, v_cache, page_table, lens, cu_seqlens, out, lse, causal=causal,
+                                             scale=scale, want_lse=want_lse, validate=validate, workspace=workspace),
+                      index, stream, (q, k_cache, v_cache, page_table, lens, cu_seqlens, out, lse, workspace))
+    if q.dim() not in (3, 4):
+        raise ValueError("q must be [tokens, Hq, d] or [B, T, Hq, d]")
+    lead, (Hq, d), dt = q.shape[:-2], q.shape[-2:], q.dtype
+    sizes, cs, where, caches = _paged_call(lead, Hq, dt, k_cache, v_cache, page_table, lens, cu_seqlens, index)
+    if sizes[4] != d:
+        raise ValueError(f"q has heads of {d}, the cache of {sizes[4]}")
+    if out is None:
+        out = torch.empty(q.shape, dtype=dt, device=q.device)
+    if lse is None and want_lse:
+        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+    (pq, sq), (po, so) = _rows_arg("q", q, lead, Hq, d, dt, index), _rows_arg("out", out, lead, Hq, d, dt, index)
+    pl = _arg("lse", lse, q.shape[:-1], torch.float32, index)
+    sized = _paged_sized(*sizes, sq, 0, 0, so, cs, 0, 0, 1.0, 0, 0.0, 1 if causal else 0,
+                         d ** -0.5 if scale is None else scale, 1 if validate else 0)
+    if workspace is None:
+        workspace = torch.empty(sized.size("kda_paged_attn_workspace_size"), dtype=torch.uint8, device=q.device)
+    ws, ws_bytes = _workspace(workspace, index)
+    st = lib.kda_paged_attn(sized.ref, pq, *caches, *where, po, pl, ws, ws_bytes, _current_stream(index))
+    if st:
+        _check(st, "kda_paged_attn")
+    return out, lse

@@ -4,12 +4,14 @@
 #include <stdio.h>
 #include <string.h>
 
-#include "kda_internal.cuh"
+#include "kda_check.cuh"
 
 namespace kda {
 namespace {
 
 thread_local char g_last_cuda_error[256] = "";
+
+}  // namespace
 
 kda_status cuda_fail(cudaError_t e) {
   snprintf(g_last_cuda_error, sizeof(g_last_cuda_error), "%s: %s", cudaGetErrorName(e),
@@ -17,26 +19,7 @@ kda_status cuda_fail(cudaError_t e) {
   return KDA_ERR_CUDA;
 }
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-bool aligned_to(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
-
-bool dim_ok(int d) { return d == kMinDim || d == 32 || d == 64 || d == kMaxDim; }
-
-bool dtype_ok(kda_dtype t) { return t == KDA_F32 || t == KDA_BF16; }
-
-size_t esize(kda_dtype t) { return t == KDA_BF16 ? 2 : 4; }
-
-struct Range {
-  uintptr_t lo, hi;
-};
-
-Range span(const void *p, size_t bytes) {
-  uintptr_t a = reinterpret_cast<uintptr_t>(p);
-  return Range{a, a + bytes};
-}
-
-bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi && a.hi > a.lo && b.hi > b.lo; }
+namespace {
 
 // --------------------------------------------------------------- validation
 
@@ -96,23 +79,6 @@ __global__ void validate_decode_kernel(DecodeArgs a, int *flag) {
     if (!(b >= 0.f && b <= 1.f)) bad |= 2;
   }
   if (bad) atomicOr(flag, bad);
-}
-
-// Runs a check kernel, waits for it and reports KDA_ERR_RANGE on a bad value.
-template <class Launch>
-kda_status run_validation(cudaStream_t s, Launch launch) {
-  int *d_flag = nullptr;
-  cudaError_t e = cudaMallocAsync(reinterpret_cast<void **>(&d_flag), sizeof(int), s);
-  if (e != cudaSuccess) return cuda_fail(e);
-  int h_flag = 0;
-  e = cudaMemsetAsync(d_flag, 0, sizeof(int), s);
-  if (e == cudaSuccess) e = launch(d_flag);
-  if (e == cudaSuccess) e = cudaMemcpyAsync(&h_flag, d_flag, sizeof(int), cudaMemcpyDeviceToHost, s);
-  cudaError_t ef = cudaFreeAsync(d_flag, s);
-  if (e == cudaSuccess) e = ef;
-  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  if (e != cudaSuccess) return cuda_fail(e);
-  return h_flag ? KDA_ERR_RANGE : KDA_OK;
 }
 
 // Host checks of the layer gates shared by the prefill and decode entries.
@@ -322,20 +288,6 @@ kda_status run_decode(const kda_decode_desc *d, const kda_layer_gates *lg, const
 
 // --------------------------------------------- gated linear recurrence, norms
 
-// No output may overlap an input or another output, but for the listed pairs
-// (in, out) that may be the same buffer.
-bool aliased(const Range *in, int n_in, const Range *out, int n_out, int same_in = -1, int same_out = -1) {
-  for (int o = 0; o < n_out; ++o) {
-    for (int i = 0; i < n_in; ++i) {
-      if (i == same_in && o == same_out && in[i].lo == out[o].lo && in[i].hi == out[o].hi) continue;
-      if (overlap(in[i], out[o])) return true;
-    }
-    for (int p = 0; p < o; ++p)
-      if (overlap(out[p], out[o])) return true;
-  }
-  return false;
-}
-
 // Sizes and types of a scan descriptor.
 kda_status scan_sizes(const kda_scan_desc *d, bool logits, bool varlen, ScanArgs *a) {
   if (!dtype_ok(d->dtype) || (!logits && !dtype_ok(d->gate_dtype))) return KDA_ERR_DTYPE;
@@ -429,30 +381,6 @@ Range rows_span(const NormArgs &a, const void *p, kda_dtype t) {
 }
 
 Range width_span(const NormArgs &a, const float *p) { return span(p, p ? (size_t)a.width * 4 : 0); }
-
-// A workspace of `need` bytes: the caller's, or one allocated on s around `run`.
-template <class Run>
-kda_status with_workspace(void *ws, size_t ws_bytes, size_t need, cudaStream_t s, Run run) {
-  if (ws) {
-    if (ws_bytes < need) return KDA_ERR_SHAPE;
-    if (!aligned16(ws)) return KDA_ERR_ALIGN;
-  }
-  cudaError_t e;
-  if (ws || need == 0) {
-    e = run(ws);
-  } else {
-    void *tmp = nullptr;
-    e = cudaMallocAsync(&tmp, need, s);
-    if (e == cudaSuccess) {
-      e = run(tmp);
-      const cudaError_t ef = cudaFreeAsync(tmp, s);
-      if (e == cudaSuccess) e = ef;
-    }
-  }
-  return e == cudaSuccess ? KDA_OK : cuda_fail(e);
-}
-
-size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 }  // namespace
 

@@ -1,0 +1,181 @@
+// Attention over a paged cache: the division of the work, shared by its kernels.
+//
+// The query rows of a sequence and a head of the cache are its new tokens times
+// the G query heads that share the head, token by token: row i is token i / G,
+// head h G + i % G.  An item is R of these rows; it runs over the keys that they
+// may see in tiles of KT.  All items' tiles, in the order (sequence, head, rows),
+// are cut into one stretch of equal length for each block of the grid: blocks
+// then finish together whatever the lengths are, which only the device knows.  An
+// item that a stretch does not hold whole leaves, for each block that has a part of it, the
+// maxima, sums and unnormalised outputs of that part in the workspace, and a second
+// kernel joins them in order.  A block has two such parts at most: one that goes on
+// with an item (slot 0) and one that begins one (slot 1).
+#pragma once
+
+#include "kda_internal.cuh"
+#include "kda_packed.cuh"
+
+namespace kda {
+
+constexpr int kSms = 152;
+
+// The joining record of a block: the item that it begins and does not end.
+struct AttnRec {
+  int n, h, r, parts;  // parts: blocks that hold some of it; 0: there is none
+};
+
+__host__ __device__ inline size_t attn_rec_floats(int grid) { return (size_t)grid * 4; }
+// floats of the workspace: records, then [grid][2][R] rows of d + 2
+__host__ __device__ inline size_t attn_part_floats(int grid, int R, int d) {
+  return attn_rec_floats(grid) + (size_t)grid * 2 * R * (d + 2);
+}
+__device__ __forceinline__ float *attn_part_out(const AttnArgs &a, int grid, int block, int slot, int R, int row) {
+  return a.part + attn_rec_floats(grid) + ((size_t)(block * 2 + slot) * R + row) * a.d;
+}
+__device__ __forceinline__ float2 *attn_part_ml(const AttnArgs &a, int grid, int block, int slot, int R, int row) {
+  return reinterpret_cast<float2 *>(a.part + attn_rec_floats(grid) + (size_t)grid * 2 * R * a.d) +
+         ((size_t)(block * 2 + slot) * R + row);
+}
+
+// Keys that rows up to `row` of a sequence may see: the first `end` ones.
+__device__ __forceinline__ int attn_end(const AttnArgs &a, const PagedSeq &s, int row) {
+  if (!a.causal) return s.kv;
+  return min(max(s.kv - s.len + row / a.G + 1, 0), s.kv);
+}
+
+// Items of a (sequence, head), and tiles of one: at least one, so that rows
+// without keys are written too.
+template <int R> __device__ __forceinline__ int attn_items(const AttnArgs &a, const PagedSeq &s) {
+  return (s.len * a.G + R - 1) / R;
+}
+template <int R, int KT> __device__ __forceinline__ int attn_tiles(const AttnArgs &a, const PagedSeq &s, int r) {
+  return max(1, (attn_end(a, s, min((r + 1) * R, s.len * a.G) - 1) + KT - 1) / KT);
+}
+template <int R, int KT> __device__ __forceinline__ long long attn_head_tiles(const AttnArgs &a, const PagedSeq &s) {
+  const int items = attn_items<R>(a, s);
+  if (items == 0) return 0;
+  if (!a.causal) return (long long)items * attn_tiles<R, KT>(a, s, 0);
+  long long sum = 0;
+  for (int r = 0; r < items; ++r) sum += attn_tiles<R, KT>(a, s, r);
+  return sum;
+}
+
+// Where a block's stretch begins and what is left of it.
+struct AttnWalk {
+  int n, h, r, t;   // sequence, head, rows, tile
+  int block, blocks;  // this block, and those that have a stretch
+  long long left, at, total;  // tiles left; index of the next tile among `total`
+};
+
+// The stretch of block c of `grid`, by all NT threads of the block.
+template <int R, int KT, int NT>
+__device__ __forceinline__ AttnWalk attn_walk(const AttnArgs &a, int c, int grid) {
+  __shared__ long long warp_sums[NT / 32];
+  __shared__ AttnWalk walk;
+  const int tid = threadIdx.x, per = (a.N + NT - 1) / NT;
+  const int lo = min(tid * per, a.N), hi = min(lo + per, a.N);
+  long long sum = 0;
+  for (int n = lo; n < hi; ++n) sum += attn_head_tiles<R, KT>(a, paged_seq(a, n)) * a.Hk;
+  long long upto = sum;  // sum of this thread and those below, first within the warp
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(~0u, upto, o);
+    if ((tid & 31) >= o) upto += x;
+  }
+  if ((tid & 31) == 31) warp_sums[tid >> 5] = upto;
+  if (tid == 0) walk.left = walk.total = 0;
+  __syncthreads();
+  long long total = 0;
+  for (int w = 0; w < NT / 32; ++w) {
+    if (w < (tid >> 5)) upto += warp_sums[w];
+    total += warp_sums[w];
+  }
+  // no stretch is empty, so that the parts of an item lie in consecutive blocks
+  const int blocks = (int)min(total, (long long)grid);
+  const long long begin = c < blocks ? total * c / blocks : 0, end = c < blocks ? total * (c + 1) / blocks : 0;
+  if (begin < end && begin >= upto - sum && begin < upto) {
+    long long rest = begin - (upto - sum);
+    AttnWalk w{};
+    for (w.n = lo; w.n < hi; ++w.n) {
+      const PagedSeq s = paged_seq(a, w.n);
+      const long long head = attn_head_tiles<R, KT>(a, s);
+      if (rest < head * a.Hk) {
+        w.h = (int)(rest / head);
+        rest -= w.h * head;
+        for (;; ++w.r) {
+          const int nt = attn_tiles<R, KT>(a, s, w.r);
+          if (rest < nt) break;
+          rest -= nt;
+        }
+        w.t = (int)rest;
+        break;
+      }
+      rest -= head * a.Hk;
+    }
+    w.block = c;
+    w.blocks = blocks;
+    w.left = end - begin;
+    w.at = begin;
+    w.total = total;
+    walk = w;
+  }
+  __syncthreads();
+  return walk;
+}
+
+// One part of a stretch: tiles [t0, t1) of an item.
+struct AttnPart {
+  PagedSeq s;
+  int n, h, r, t0, t1;
+  bool whole;
+  int slot;     // of the workspace, unless whole
+  int parts;    // when it begins an item that it does not end: blocks that hold some of it
+};
+template <int R, int KT>
+__device__ __forceinline__ bool attn_next(const AttnArgs &a, AttnWalk &w, AttnPart &p) {
+  if (w.left <= 0) return false;
+  p.s = paged_seq(a, w.n);
+  int items = attn_items<R>(a, p.s);
+  while (w.r >= items) {  // past the last item of a head
+    w.r = 0;
+    if (items == 0 || ++w.h >= a.Hk) {
+      w.h = 0;
+      p.s = paged_seq(a, ++w.n);  // (some sequence follows as long as tiles are left)
+      items = attn_items<R>(a, p.s);
+    }
+  }
+  const int nt = attn_tiles<R, KT>(a, p.s, w.r);
+  p.n = w.n;
+  p.h = w.h;
+  p.r = w.r;
+  p.t0 = w.t;
+  p.t1 = (int)min((long long)nt, w.t + w.left);
+  p.whole = p.t0 == 0 && p.t1 == nt;
+  p.slot = p.t0 == 0 ? 1 : 0;
+  p.parts = 0;
+  if (p.t0 == 0 && !p.whole) {
+    // up to the block whose stretch holds its last tile; stretch c begins at floor(total c / blocks)
+    p.parts = (int)(((w.at + nt) * w.blocks - 1) / w.total) - w.block + 1;
+  }
+  w.at += p.t1 - p.t0;
+  w.left -= p.t1 - p.t0;
+  w.t = 0;
+  ++w.r;
+  return true;
+}
+
+// Element offset of (page of key j, slot, head h) in the cache.
+__device__ __forceinline__ long long key_offset(const AttnArgs &a, int page_id, int slot, int h) {
+  return min(max(page_id, 0), a.pages - 1) * a.cs + ((long long)h * a.page + slot) * a.d;
+}
+
+// Joins the parts of the items that blocks of `grid` began and did not end.
+cudaError_t launch_attn_join(const AttnArgs &a, int grid, int R, cudaStream_t s);
+
+// kda_attn_f32.cu, kda_attn_mma.cu
+size_t attn_f32_floats(const AttnArgs &a);
+cudaError_t launch_attn_f32(const AttnArgs &a, cudaStream_t s);
+size_t attn_mma_floats(const AttnArgs &a);
+cudaError_t launch_attn_mma(const AttnArgs &a, cudaStream_t s);
+
+}  // namespace kda

@@ -1,0 +1,187 @@
+// Attention over a paged cache in fp32, on CUDA cores: there is no fp32 tensor
+// product, and what tf32 drops would show in the 24 bits of the result.
+//
+// An item of R = 64 or 16 rows runs over the keys in tiles of 64, by 256 threads as
+// 16 x 16.  Scores: a thread has R / 16 rows and 4 keys, both from shared memory as
+// float4.  Outputs: the same rows and d / 16 channels, probabilities through shared memory.
+#include "kda_attn.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kKeys = 64, kThreads = 256;
+
+template <int D, int R> struct F32Smem {
+  static constexpr int kRow = D + 4, kProw = kKeys + 4;  // padded: rows of a quarter warp in distinct banks
+  static constexpr size_t kBytes = ((size_t)(R + 2 * kKeys) * kRow + (size_t)R * kProw) * 4;
+};
+
+// acc += p v of the tile.  With kMask keys that the row may not see are left out,
+// whatever their values are (0 times a non-finite value is not 0).
+template <int D, int RT, int V, bool kMask>
+__device__ __forceinline__ void add_values(float (&o)[RT][V], const float *P, const float *Vs, int tx, const int *lim,
+                                           int key0) {
+  constexpr int kRow = D + 4, kProw = kKeys + 4;
+#pragma unroll 4
+  for (int k = 0; k < kKeys; ++k) {
+    float p[RT], v[V];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) p[i] = P[i * kProw + k];
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[j] = Vs[k * kRow + (V >= 4 ? tx * 4 + (j / 4) * 64 + j % 4 : tx * V + j)];
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+      if (!kMask || key0 + k < lim[i])
+#pragma unroll
+        for (int j = 0; j < V; ++j) o[i][j] = fmaf(p[i], v[j], o[i][j]);
+  }
+}
+
+template <int D, int R>
+__global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnArgs a) {
+  constexpr int kRow = F32Smem<D, R>::kRow, kProw = F32Smem<D, R>::kProw, RT = R / 16, V = D / 16;
+  extern __shared__ float4 smem4[];
+  float *Qs = reinterpret_cast<float *>(smem4), *Ks = Qs + R * kRow, *Vs = Ks + kKeys * kRow, *Ps = Vs + kKeys * kRow;
+  const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16, grid = gridDim.x;
+  AttnWalk walk = attn_walk<R, kKeys, kThreads>(a, blockIdx.x, grid);
+  AttnRec rec{0, 0, 0, 0};
+  AttnPart p;
+  while (attn_next<R, kKeys>(a, walk, p)) {
+    if (p.parts) rec = AttnRec{p.n, p.h, p.r, p.parts};
+    const float *q = static_cast<const float *>(a.q), *kc = static_cast<const float *>(a.kc),
+                *vc = static_cast<const float *>(a.vc);
+    const int rows = p.s.len * a.G, row0 = p.r * R;
+    __syncthreads();  // the part before is done with shared memory
+    for (int i = tid; i < R * (D / 4); i += kThreads) {
+      const int r = i / (D / 4), c = i % (D / 4) * 4, at = row0 + r;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (at < rows)
+        x = *reinterpret_cast<const float4 *>(q + (p.s.bos + at / a.G) * a.qs + (p.h * a.G + at % a.G) * D + c);
+      *reinterpret_cast<float4 *>(Qs + r * kRow + c) = x;
+    }
+    int lim[RT];  // keys that each of the thread's rows may see
+    float m[RT], l[RT], o[RT][V];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      const int at = row0 + ty * RT + i;
+      lim[i] = at < rows ? attn_end(a, p.s, at) : 0;
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+#pragma unroll
+      for (int j = 0; j < V; ++j) o[i][j] = 0.f;
+    }
+    const int all = attn_end(a, p.s, row0);            // keys that every row sees
+    const int most = attn_end(a, p.s, min(row0 + R, rows) - 1);
+    for (int t = p.t0; t < p.t1; ++t) {
+      const int key0 = t * kKeys;
+      __syncthreads();  // Ks, Vs, Ps are free (and Qs is there, after the next barrier)
+      for (int i = tid; i < kKeys * (D / 4); i += kThreads) {
+        const int k = i / (D / 4), c = i % (D / 4) * 4, j = key0 + k;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+        if (j < most) {
+          const int id = a.table[(long long)p.n * a.max_pages + j / a.page];
+          const long long off = key_offset(a, id, j % a.page, p.h) + c;
+          x = *reinterpret_cast<const float4 *>(kc + off);
+          y = *reinterpret_cast<const float4 *>(vc + off);
+        }
+        *reinterpret_cast<float4 *>(Ks + k * kRow + c) = x;
+        *reinterpret_cast<float4 *>(Vs + k * kRow + c) = y;
+      }
+      __syncthreads();
+      float s[RT][4] = {};
+#pragma unroll 2
+      for (int c = 0; c < D; c += 4) {
+        float4 x[RT], y[4];
+#pragma unroll
+        for (int i = 0; i < RT; ++i) x[i] = *reinterpret_cast<const float4 *>(Qs + (ty * RT + i) * kRow + c);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const float4 *>(Ks + (tx + 16 * j) * kRow + c);
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            s[i][j] = fmaf(x[i].x, y[j].x, fmaf(x[i].y, y[j].y, fmaf(x[i].z, y[j].z, fmaf(x[i].w, y[j].w, s[i][j]))));
+      }
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        float top = m[i];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          s[i][j] = key0 + tx + 16 * j < lim[i] ? s[i][j] * a.scale2 : -INFINITY;
+          top = fmaxf(top, s[i][j]);
+        }
+#pragma unroll
+        for (int x = 8; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, x));
+        const float ref = top == -INFINITY ? 0.f : top, f = exp2f(m[i] - ref);
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float e = exp2f(s[i][j] - ref);
+          Ps[(ty * RT + i) * kProw + tx + 16 * j] = e;
+          sum += e;
+        }
+#pragma unroll
+        for (int x = 8; x > 0; x >>= 1) sum += __shfl_xor_sync(~0u, sum, x);
+        l[i] = l[i] * f + sum;
+        m[i] = top;
+#pragma unroll
+        for (int j = 0; j < V; ++j) o[i][j] *= f;
+      }
+      __syncthreads();
+      if (key0 + kKeys <= all) add_values<D, RT, V, false>(o, Ps + ty * RT * kProw, Vs, tx, lim, key0);
+      else add_values<D, RT, V, true>(o, Ps + ty * RT * kProw, Vs, tx, lim, key0);
+    }
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      const int r = ty * RT + i, at = row0 + r;
+      if (at >= rows) continue;
+      const size_t tok = p.s.bos + at / a.G;
+      const int head = p.h * a.G + at % a.G;
+      const bool none = lim[i] == 0;
+      float *out = p.whole ? static_cast<float *>(a.o) + tok * a.os + head * D
+                           : attn_part_out(a, grid, blockIdx.x, p.slot, R, r);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int c = V >= 4 ? tx * 4 + (j / 4) * 64 + j % 4 : tx * V + j;
+        out[c] = p.whole ? (none ? 0.f : o[i][j] / l[i]) : o[i][j];
+      }
+      if (tx != 0) continue;
+      if (!p.whole) *attn_part_ml(a, grid, blockIdx.x, p.slot, R, r) = make_float2(m[i], l[i]);
+      else if (a.lse) a.lse[tok * a.Hq + head] = none ? -INFINITY : (m[i] + log2f(l[i])) * 0.6931471805599453f;
+    }
+  }
+  if (tid == 0) reinterpret_cast<AttnRec *>(a.part)[blockIdx.x] = rec;
+}
+
+// Few rows of a (sequence, head) on average run in items of 16, whose products are
+// not four times too many; the kernel is right for any.
+bool few_rows(const AttnArgs &a) { return (long long)a.T_total * a.G <= 24LL * a.N; }
+template <int D, int R> int f32_grid() { return kSms * (F32Smem<D, R>::kBytes > 110 * 1024 ? 1 : 2); }
+
+template <int D, int R> cudaError_t launch_f32(const AttnArgs &a, cudaStream_t s) {
+  const size_t bytes = F32Smem<D, R>::kBytes;
+  cudaError_t e = cudaFuncSetAttribute(attn_f32_kernel<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e != cudaSuccess) return e;
+  attn_f32_kernel<D, R><<<f32_grid<D, R>(), kThreads, bytes, s>>>(a);
+  e = cudaGetLastError();
+  return e == cudaSuccess ? launch_attn_join(a, f32_grid<D, R>(), R, s) : e;
+}
+
+}  // namespace
+
+size_t attn_f32_floats(const AttnArgs &a) {
+  const int R = few_rows(a) ? 16 : 64;
+  return attn_part_floats(2 * kSms, R, a.d);
+}
+
+cudaError_t launch_attn_f32(const AttnArgs &a, cudaStream_t s) {
+  const bool few = few_rows(a);
+  switch (a.d) {
+    case 16: return few ? launch_f32<16, 16>(a, s) : launch_f32<16, 64>(a, s);
+    case 32: return few ? launch_f32<32, 16>(a, s) : launch_f32<32, 64>(a, s);
+    case 64: return few ? launch_f32<64, 16>(a, s) : launch_f32<64, 64>(a, s);
+    default: return few ? launch_f32<128, 16>(a, s) : launch_f32<128, 64>(a, s);
+  }
+}
+
+}  // namespace kda

@@ -202,6 +202,74 @@ size_t norm_bwd_workspace_bytes(int width);
 cudaError_t launch_norm_fwd(const NormArgs &a, cudaStream_t s);
 cudaError_t launch_norm_bwd(const NormArgs &a, const NormBwdIo &io, void *ws, cudaStream_t s);
 
+// Norm and rotation of query and key rows (kda_rope.cu).
+struct RopeArgs {
+  int tokens, Hq, Hk, d, rot;
+  kda_dtype t;
+  bool inter, norm;          // interleaved pairs; RMSNorm
+  float rot_scale, eps;
+  const void *q, *k;         // nullable
+  const int32_t *positions;
+  const float *freq, *qw, *kw;  // weights nullable: ones
+  void *qo, *ko;
+  long long qs, ks, qos, kos;  // strides in elements
+};
+struct RopeBwdIo {
+  const void *dqo, *dko;
+  void *dq, *dk;
+  long long dqs, dks;
+  float *dqw, *dkw;
+};
+size_t rope_bwd_workspace_bytes(int d);
+cudaError_t launch_rope_fwd(const RopeArgs &a, cudaStream_t s);
+cudaError_t launch_rope_bwd(const RopeArgs &a, const RopeBwdIo &io, float *ws, cudaStream_t s);
+
+// Sequences over a paged cache (kda_kv_append, kda_paged_attn).
+struct PagedArgs {
+  int N, T_total, T_seq;     // sequences; new tokens of all, and of each when cu == nullptr
+  int Hq, Hk, d;
+  int page, pages, max_pages;
+  kda_dtype t;
+  long long cs;              // elements from page to page
+  const int32_t *lens, *cu, *table;
+};
+struct PagedSeq {
+  int bos, len, kv;          // first new token, new tokens, length of the cache with them
+};
+// Sequence n, clamped so that nothing it implies lies outside the tensors.
+__device__ __forceinline__ PagedSeq paged_seq(const PagedArgs &a, int n) {
+  PagedSeq s;
+  if (a.cu) {
+    s.bos = min(max(a.cu[n], 0), a.T_total);
+    s.len = min(max(a.cu[n + 1], s.bos), a.T_total) - s.bos;
+  } else {
+    s.bos = n * a.T_seq;
+    s.len = a.T_seq;
+  }
+  s.kv = min(max(a.lens[n], 0), a.max_pages * a.page);
+  return s;
+}
+
+// Append to a paged cache: r's token tensors, with k going to the cache and v
+// (stride vs) beside it; r.positions is not read.
+cudaError_t launch_kv_append(const RopeArgs &r, const PagedArgs &p, const void *v, long long vs, void *kc, void *vc,
+                             cudaStream_t s);
+
+// Attention over a paged cache (kda_attn*.cu).
+struct AttnArgs : PagedArgs {
+  int G;                     // query heads that share a head of the cache
+  const void *q, *kc, *vc;
+  void *o;
+  float *lse;                // nullable
+  long long qs, os;
+  float scale2;              // scale / ln 2: scores are powers of two
+  bool causal;
+  float *part;               // workspace
+};
+size_t attn_workspace_bytes(const AttnArgs &a);
+cudaError_t launch_attn(const AttnArgs &a, cudaStream_t s);
+cudaError_t launch_validate_paged(const PagedArgs &a, int *d_flag, cudaStream_t s);
+
 // ---------------------------------------------------------------- device helpers
 
 __device__ __forceinline__ float ld_elem(const void *p, size_t i, kda_dtype t) {

@@ -1,7 +1,8 @@
 /*
  * kda.h - C ABI of libkda.so: Kimi Delta Attention (KDA) chunked prefill and
- * decode step on one GB300 (sm_103a), the gated linear recurrence, and the
- * norms around a block.
+ * decode step on one GB300 (sm_103a), the gated linear recurrence, the norms
+ * around a block, and the softmax attention over a paged cache of the layers
+ * that stand between recurrent ones.
  *
  * Cited page: "Kimi K3：从 3T 稀疏预训练到百万 Token Agent 的端到端扩展"
  * (liuzhao09.github.io/papers/kimi-k3), [K3-notes] below.
@@ -496,6 +497,172 @@ kda_status kda_block_norm_bwd(const kda_norm_desc *desc, const void *y, const vo
                               const void *d_out, const void *d_normed, void *d_y, void *d_residual, void *d_gate,
                               float *d_post_weight, float *d_scale, float *d_pre_weight, void *workspace,
                               size_t workspace_bytes, kda_stream_t stream);
+
+/*
+ * Norm and position rotation of queries and keys.  Per token and head, a row x
+ * of d channels becomes
+ *     u   = x o w / sqrt(mean x^2 + eps)              (norm; else u = x)
+ *     y_a = rot_scale (u_a cos f - u_b sin f)
+ *     y_b = rot_scale (u_b cos f + u_a sin f),  f = position * inv_freq[i]
+ * for the rot / 2 pairs (a, b) of its first rot channels: (i, i + rot / 2) with
+ * KDA_ROPE_HALF, (2i, 2i + 1) with KDA_ROPE_INTERLEAVED; the others stay, y = u.
+ * Frequencies scaled for long contexts are the caller's: inv_freq holds them as
+ * they are, and rot_scale is the factor on the rotated channels that goes with
+ * some scalings (1 otherwise).  With rot = 0, norm and a weight of d^-1/2
+ * everywhere a row is divided by its L2 norm, as the delta rule wants its q and k.
+ *
+ * Conventions
+ *  - d is 16, 32, 64 or 128; rot a multiple of 8 from 0 to d.
+ *  - q and k (outputs and gradients likewise) are [tokens, heads, d] of `dtype`
+ *    with dense heads; a token's row starts `stride` elements after the one
+ *    before (0: dense), so they may be parts of one projection's output.
+ *    Pointers and strides are multiples of 16 bytes; a stride is at least
+ *    heads * d.  Hk may be 0, without any k then.
+ *  - positions are any int32 (negative ones turn backwards), inv_freq is fp32
+ *    and below 2^16 in magnitude.  position * inv_freq is reduced to a part of a
+ *    turn in 64-bit fixed point, to 2^-30 of a turn at any position, and its sine
+ *    and cosine are those of fp32.  Arithmetic is fp32 and each output is rounded
+ *    once.
+ *  - A non-finite value reaches its own row and, in the backward, the weight's
+ *    gradient.  Results are deterministic.
+ */
+typedef enum { KDA_ROPE_HALF = 0, KDA_ROPE_INTERLEAVED = 1 } kda_rope_layout;
+
+typedef struct {
+  int tokens;
+  int Hq, Hk, d;  /* heads of q (>= 1) and of k (>= 0), channels per head         */
+  kda_dtype dtype;
+  int rot;
+  kda_rope_layout layout;
+  float rot_scale;       /* finite                                                */
+  int norm;              /* 1: RMSNorm of each row                                */
+  float eps;             /* >= 0, used with norm                                  */
+  int64_t q_stride, k_stride;         /* of q, k                                  */
+  int64_t q_out_stride, k_out_stride; /* of q_out, k_out; d_q_out, d_k_out        */
+  int64_t dq_stride, dk_stride;       /* of dq, dk (backward)                     */
+} kda_rope_desc;
+
+/*
+ * kda_qk_rope_fwd
+ *   q, k          [tokens, Hq, d], [tokens, Hk, d]
+ *   positions     [tokens] int32, or NULL with rot = 0
+ *   inv_freq      [rot / 2] fp32, or NULL with rot = 0
+ *   q_weight, k_weight  [d] fp32, each or NULL for ones (must be NULL without norm)
+ *   q_out, k_out  as q and k, written; each may be its input with the same stride
+ * Outputs may overlap nothing else (KDA_ERR_ALIAS); rows of one stride that lie
+ * beside each other, as the parts of one projection do, do not overlap.
+ */
+kda_status kda_qk_rope_fwd(const kda_rope_desc *desc, const void *q, const void *k, const int32_t *positions,
+                           const float *inv_freq, const float *q_weight, const float *k_weight, void *q_out,
+                           void *k_out, kda_stream_t stream);
+
+/*
+ * kda_qk_rope_bwd - gradients of L = <d_q_out, q_out> + <d_k_out, k_out>, from the
+ * forward's inputs.  With g the gradient of u, r = (mean x^2 + eps)^-1/2:
+ *     dx = r (g o w - x r^2 mean(g o w o x)),   dw = sum g o x r   (norm; else dx = g)
+ *   dq, dk      as q and k, written; each may be d_q_out / d_k_out with the same stride
+ *   dq_weight, dk_weight  [d] fp32, each or NULL: sums over tokens and heads (of
+ *               absent weights too); NULL without norm
+ *   workspace   kda_qk_rope_bwd_workspace_size bytes, 16-byte aligned (used for
+ *               the weights' gradients only), or NULL: then a call that needs
+ *               some allocates it stream-ordered
+ * Without norm, q and k are not read (and may be NULL).
+ */
+kda_status kda_qk_rope_bwd_workspace_size(const kda_rope_desc *desc, size_t *bytes);
+kda_status kda_qk_rope_bwd(const kda_rope_desc *desc, const void *q, const void *k, const int32_t *positions,
+                           const float *inv_freq, const float *q_weight, const float *k_weight,
+                           const void *d_q_out, const void *d_k_out, void *dq, void *dk, float *dq_weight,
+                           float *dk_weight, void *workspace, size_t workspace_bytes, kda_stream_t stream);
+
+/*
+ * Softmax attention over a paged cache.  Keys and values live in pages of
+ * page_size tokens; page_table[n] lists sequence n's pages in order, and
+ * lens[n] is its length in tokens, the call's own new tokens included (they are
+ * appended first).  New token i of the L_n that sequence n brings stands at
+ * position lens[n] - L_n + i.
+ *
+ * Conventions shared by kda_kv_append and kda_paged_attn
+ *  - k_cache, v_cache  [num_pages, Hk, page_size, d] dtype; each page is dense and
+ *    starts cache_stride elements after the one before (0: dense), so that the
+ *    two may be halves of one buffer.  Hq is a multiple of Hk; heads h * Hq / Hk
+ *    to (h + 1) * Hq / Hk - 1 of the queries share head h of the cache.
+ *  - Token tensors are as kda_qk_rope_fwd's: dense heads of 16, 32, 64 or 128
+ *    channels, a stride from token to token, 16-byte aligned.
+ *  - page_table [N, max_pages], lens [N], cu_seqlens [N + 1] are int32 on the
+ *    device and are read there: captured calls see their values at replay.
+ *    cu_seqlens NULL means B sequences of T new tokens; packed sequences may be
+ *    empty, and rows behind the last one are neither read nor written.
+ *  - Entries of page_table behind a sequence's last page are not read; slots
+ *    behind its length, whatever they hold, have no effect.
+ *  - Validate mode returns KDA_ERR_RANGE for cu_seqlens that do not start at 0
+ *    or that decrease or pass the token count, a length below 0 or above
+ *    max_pages * page_size, or a used page outside [0, num_pages).  Without it
+ *    they are clamped (lengths and cu_seqlens to their ranges; a token whose page is
+ *    outside is not stored, and its key and value are read from the nearest
+ *    page), so that no call reads or writes outside the tensors.
+ *  - A position below 0 (a length below the number of new tokens, as the entries
+ *    that pad a batch have with length 0) is not stored, attends to nothing, and
+ *    gets zeros and a log-sum of -infinity.
+ */
+typedef struct {
+  int B;          /* batch; must be 1 when cu_seqlens is given                   */
+  int T;          /* new tokens per sequence, or of all sequences when packed     */
+  int Hq, Hk, d;
+  int num_seqs;   /* packed: number of sequences N; 0 when cu_seqlens is NULL      */
+  int page_size, num_pages, max_pages;
+  kda_dtype dtype;           /* of every token tensor and of the cache            */
+  int64_t q_stride, k_stride, v_stride; /* of q, k, v                             */
+  int64_t out_stride;        /* of q_out or out                                   */
+  int64_t cache_stride;      /* from page to page                                 */
+  int rot;                   /* kda_kv_append: the rotation and the norm of q, k, */
+  kda_rope_layout layout;    /*   as kda_rope_desc's                              */
+  float rot_scale;
+  int norm;
+  float eps;
+  int causal;                /* kda_paged_attn: 1: keys up to the query's own     */
+                             /*   position; 0: all lens[n] keys                   */
+  float scale;               /*   on the scores; finite, above 0                  */
+  int validate;              /* 1: range-check first (synchronises the stream)    */
+} kda_paged_desc;
+
+/*
+ * kda_kv_append - stores the new tokens' keys and values in the cache; keys are
+ * normed and rotated on the way (kda_qk_rope_fwd's arithmetic, at the tokens'
+ * positions), and so are the queries, where given.
+ *   q             [tokens, Hq, d], or NULL
+ *   k, v          [tokens, Hk, d]
+ *   lens, cu_seqlens, page_table  as above (lengths after the append)
+ *   inv_freq      [rot / 2] fp32, or NULL with rot = 0
+ *   q_weight, k_weight  [d] fp32, each or NULL (must be NULL without norm)
+ *   q_out         as q, written (given exactly when q is); may be q itself
+ *   k_cache, v_cache  written at the new tokens' slots only
+ * Two tokens must not share a slot.
+ */
+kda_status kda_kv_append(const kda_paged_desc *desc, const void *q, const void *k, const void *v,
+                         const int32_t *lens, const int32_t *cu_seqlens, const int32_t *page_table,
+                         const float *inv_freq, const float *q_weight, const float *k_weight, void *q_out,
+                         void *k_cache, void *v_cache, kda_stream_t stream);
+
+/*
+ * kda_paged_attn - attention of the new tokens (one of each sequence when
+ * generating, many in a prefill, or both in one packed call) over the cache:
+ *     out_i = sum_j p_ij v_j,  p_ij = exp(scale q_i . k_j - lse_i)
+ *     lse_i = log sum_j exp(scale q_i . k_j)
+ *   q         [tokens, Hq, d]
+ *   out       [tokens, Hq, d], written
+ *   lse       [tokens, Hq] fp32, or NULL (written): what joins this result to one
+ *             over other keys
+ *   workspace kda_paged_attn_workspace_size bytes, 16-byte aligned, not in use by
+ *             another call in flight; or NULL: allocated stream-ordered
+ * Scores, the softmax's maxima and sums and the output sums are fp32; bf16
+ * probabilities are rounded to bf16 for their product with the values.  A
+ * non-finite key or value reaches the queries that attend to it, and no others.
+ * Results are deterministic.
+ */
+kda_status kda_paged_attn_workspace_size(const kda_paged_desc *desc, size_t *bytes);
+kda_status kda_paged_attn(const kda_paged_desc *desc, const void *q, const void *k_cache, const void *v_cache,
+                          const int32_t *lens, const int32_t *cu_seqlens, const int32_t *page_table, void *out,
+                          float *lse, void *workspace, size_t workspace_bytes, kda_stream_t stream);
 
 /* Static description of a status code (never NULL). */
 const char *kda_status_string(kda_status status);
