@@ -76,13 +76,17 @@ cudaError_t launch_attn_join(const AttnArgs &a, int grid, int R, cudaStream_t s)
   return cudaGetLastError();
 }
 
+// The tensor cores' tiles of 128 rows against products of 16 or 32 rows: by the
+// rows of a (sequence, head) on average.
+static bool many_rows(const AttnArgs &a) { return (long long)a.T_total * a.G > 32LL * a.N && attn_tc_supports(a); }
+
 size_t attn_workspace_bytes(const AttnArgs &a) {
-  return (a.t == KDA_F32 ? attn_f32_floats(a) : attn_mma_floats(a)) * sizeof(float);
+  return (a.t == KDA_F32 ? attn_f32_floats(a) : many_rows(a) ? attn_tc_floats(a) : attn_mma_floats(a)) * sizeof(float);
 }
 
 cudaError_t launch_attn(const AttnArgs &a, cudaStream_t s) {
-  if ((long long)a.T_total == 0) return cudaSuccess;
-  return a.t == KDA_F32 ? launch_attn_f32(a, s) : launch_attn_mma(a, s);
+  if (a.T_total == 0) return cudaSuccess;
+  return a.t == KDA_F32 ? launch_attn_f32(a, s) : many_rows(a) ? launch_attn_tc(a, s) : launch_attn_mma(a, s);
 }
 
 }  // namespace kda

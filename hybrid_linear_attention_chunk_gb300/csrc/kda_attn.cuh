@@ -172,10 +172,13 @@ __device__ __forceinline__ long long key_offset(const AttnArgs &a, int page_id, 
 // Joins the parts of the items that blocks of `grid` began and did not end.
 cudaError_t launch_attn_join(const AttnArgs &a, int grid, int R, cudaStream_t s);
 
-// kda_attn_f32.cu, kda_attn_mma.cu
+// kda_attn_f32.cu, kda_attn_mma.cu, kda_attn_tc.cu
 size_t attn_f32_floats(const AttnArgs &a);
 cudaError_t launch_attn_f32(const AttnArgs &a, cudaStream_t s);
 size_t attn_mma_floats(const AttnArgs &a);
 cudaError_t launch_attn_mma(const AttnArgs &a, cudaStream_t s);
+bool attn_tc_supports(const AttnArgs &a);
+size_t attn_tc_floats(const AttnArgs &a);
+cudaError_t launch_attn_tc(const AttnArgs &a, cudaStream_t s);
 
 }  // namespace kda

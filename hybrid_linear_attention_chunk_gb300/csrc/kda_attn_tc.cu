@@ -1,0 +1,548 @@
+// Attention over a paged cache in bf16 for many query rows to a head of the cache:
+// prefills and chunks, bound by the tensor cores.
+//
+// An item is 256 query rows as two tiles of 128, each with its scores S = Q K^T
+// and its outputs O += P V on tcgen05 with fp32 accumulators in TMEM; P, in bf16,
+// takes the place of its S there and is the second product's operand as it lies.  Two
+// warpgroups hold one row of a tile in each thread, so that the softmax needs no
+// exchange between threads.  While one tile's softmax runs, the tensor cores have the
+// other tile's products.  One warp issues the products, one the copies of keys and values
+// (TMA from the pages, 128 keys at a time), and two go over the values of tiles that some row does not see
+// whole: slots behind the sequence's end are zeroed there, since 0 times what lies in
+// them need not be 0, and values that are not finite are taken out and listed, to be
+// added in the end to the rows that see them.
+//
+// A row's outputs stand relative to a reference that follows its running maximum in steps: while the
+// maximum is less than 2^8 above it, probabilities up to 2^8 are as good in bf16 and
+// fp32, and the outputs need not be rescaled.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <string.h>
+
+#include "kda_attn.cuh"
+#include "kda_sm100.cuh"
+
+namespace kda {
+namespace {
+
+using namespace sm100;
+
+constexpr int kThreads = 384, kRows = 256, kKeys = 128;
+constexpr int kMaxStages = 3;
+constexpr float kSlack = 8.f;  // powers of two between a row's maximum and its reference
+constexpr uint32_t kHalf = 16384;  // 128 rows of 64 channels
+
+enum Bar {
+  B_Q = 0,                        // [2] queries in shared memory
+  B_S = 2,                        // [2] scores in TMEM
+  B_P = 4,                        // [2] probabilities in TMEM, outputs rescaled
+  B_O = 6,                        // [2] the part's outputs are complete
+  B_KFULL = 8,                    // [stages] keys landed
+  B_KEMPTY = B_KFULL + kMaxStages,
+  B_VFULL = B_KEMPTY + kMaxStages,
+  B_VEMPTY = B_VFULL + kMaxStages,
+  B_VOK = B_VEMPTY + kMaxStages,  // values gone over, where they need it
+  B_DRAIN = B_VOK + kMaxStages,
+  B_COUNT
+};
+static_assert(B_COUNT <= 32, "a bit of the watchdog word each");
+
+struct Ctl {
+  uint64_t bar[B_COUNT];
+  uint32_t tmem;
+  int abort;
+  uint32_t odd[4][3][4];  // [part % 4][tile at the end][32 keys]: keys with values that are not finite
+};
+
+template <int D> struct Tc {
+  static constexpr uint32_t kTile = D / 64 * kHalf;
+  static constexpr int kStages = D == 128 ? 2 : 3;
+  static constexpr uint32_t kK = 2 * kTile, kV = kK + kStages * kTile, kCtl = kV + kStages * kTile;
+  static constexpr uint32_t kBytes = kCtl + sizeof(Ctl) + 1024;
+};
+
+struct TcArgs {
+  AttnArgs a;
+  unsigned int *err;
+  int box;  // rows of a copy: a page's, at most 128
+};
+
+struct Waits {
+  Ctl *ctl;
+  unsigned int *err;
+  // By a whole warp; false when any of its lanes gave up.
+  __device__ __forceinline__ bool operator()(int b, uint32_t parity) const {
+    return __all_sync(~0u, mbar_wait(smem_u32(&ctl->bar[b]), parity & 1u, &ctl->abort, err, 1u << b));
+  }
+};
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *m, uint32_t bar, int c0, int c1, int c2,
+                                            int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// What every role derives of a part.
+struct Span {
+  int rows, row0, most, all;  // rows of the (sequence, head); keys that some row sees; that every row sees
+  int n[2];                   // tiles of each 128 rows within the part
+  __device__ __forceinline__ Span(const AttnArgs &a, const AttnPart &p) {
+    rows = p.s.len * a.G;
+    row0 = p.r * kRows;
+    most = attn_end(a, p.s, min(row0 + kRows, rows) - 1);
+    all = attn_end(a, p.s, row0);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int first = row0 + 128 * i;
+      n[i] = 0;
+      if (first < rows) {
+        const int end = attn_end(a, p.s, min(first + 128, rows) - 1);
+        n[i] = max(min(p.t1, max(1, (end + kKeys - 1) / kKeys)) - p.t0, 0);
+      }
+    }
+  }
+  // Whether tile t has keys that some row does not see.
+  __device__ __forceinline__ bool at_end(int t) const { return (t + 1) * kKeys > all; }
+};
+
+// ------------------------------------------------------------------ softmax
+
+template <int D>
+__device__ __forceinline__ void softmax_role(const AttnArgs &a, AttnWalk walk, Ctl *ctl, const Waits &wait,
+                                             unsigned char *smem, int i) {
+  const int grid = gridDim.x, tid = threadIdx.x % 128, qw = tid / 32;
+  const uint32_t tb = ctl->tmem + ((uint32_t)(32 * qw) << 16), ts = tb + 128 * i, to = tb + 256 + 128 * i;
+  const uint32_t qs = smem_u32(smem) + i * Tc<D>::kTile;
+  const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q), *vc = static_cast<const __nv_bfloat16 *>(a.vc);
+  uint32_t seen_s = 0, seen_o = 0;
+  AttnPart p;
+  for (int part = 0; attn_next<kRows, kKeys>(a, walk, p); ++part) {
+    const Span sp(a, p);
+    const int first = sp.row0 + 128 * i;
+    if (first >= sp.rows) continue;
+    const int n = sp.n[i], at = first + tid;
+    const bool mine = at < sp.rows;
+    const int lim = mine ? attn_end(a, p.s, at) : 0, all = attn_end(a, p.s, first);
+    const size_t tok = p.s.bos + at / a.G;
+    const int head = p.h * a.G + at % a.G;
+    float m = -INFINITY, l = 0.f;
+    if (n > 0) {
+      // queries: 16-byte pieces, D / 8 of a row, into the swizzled operand tile (the last product that
+      // read it is complete: this warpgroup has seen its scores)
+#pragma unroll 4
+      for (int x = tid; x < 128 * (D / 8); x += 128) {
+        const int r = x / (D / 8), c = x % (D / 8), rt = first + r;
+        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+        if (rt < sp.rows)
+          w = *reinterpret_cast<const uint4 *>(q + (p.s.bos + rt / a.G) * a.qs + (p.h * a.G + rt % a.G) * D + c * 8);
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(qs + (c / 8) * kHalf + sw128_offset(r, (c % 8) * 8)),
+                     "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(smem_u32(&ctl->bar[B_Q + i]));
+    }
+    for (int j = 0; j < n; ++j) {
+      const int key0 = (p.t0 + j) * kKeys;
+      if (!wait(B_S + i, seen_s++)) return;
+      tc_fence_after();
+      float s[128];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, *reinterpret_cast<float(*)[32]>(s + 32 * c));
+      tmem_wait_ld();
+      if (key0 + kKeys > all) {
+        const int nv = lim - key0;
+#pragma unroll
+        for (int c = 0; c < 128; ++c) s[c] = c < nv ? s[c] : -INFINITY;
+      }
+      float t4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+      for (int c = 4; c < 124; c += 8)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) t4[x] = max3(t4[x], s[c + 2 * x], s[c + 2 * x + 1]);
+      const float top = max3(max3(t4[0], t4[1], fmaxf(s[124], s[125])), max3(t4[2], t4[3], s[126]), s[127]);
+      if (__any_sync(~0u, top * a.scale2 > m * a.scale2 + kSlack)) {
+        const float next = fmaxf(m, top);
+        const float f = next == -INFINITY ? 1.f : fast_exp2((m - next) * a.scale2);
+        l *= f;
+        m = next;
+        if (j > 0) {  // (these scores came after the products that O holds)
+#pragma unroll
+          for (int c = 0; c < D; c += 32) {
+            float o[32];
+            tmem_ld32(to + c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int x = 0; x < 32; ++x) o[x] *= f;
+            tmem_st16(to + c, *reinterpret_cast<float(*)[16]>(o));
+            tmem_st16(to + c + 16, *reinterpret_cast<float(*)[16]>(o + 16));
+          }
+        }
+      }
+      const float r = m == -INFINITY ? 0.f : -m * a.scale2;
+      const Vec<2> scale = pair(a.scale2, a.scale2), ref = pair(r, r);
+      Vec<2> sum = pair(0.f, 0.f);
+#pragma unroll
+      for (int c = 0; c < 128; c += 32) {
+        float w[16];
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+          const Vec<2> e = fma(pair(s[c + 2 * x], s[c + 2 * x + 1]), scale, ref);
+          const float lo = fast_exp2(e.get(0)), hi = fast_exp2(e.get(1));
+          sum = add(sum, pair(lo, hi));
+          const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+          w[x] = __uint_as_float(*reinterpret_cast<const uint32_t *>(&b));
+        }
+        tmem_st16(ts + c / 2, w);
+      }
+      l += sum.get(0) + sum.get(1);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(smem_u32(&ctl->bar[B_P + i]));
+    }
+    if (n > 0) {
+      if (!wait(B_O + i, seen_o++)) return;
+      tc_fence_after();
+    }
+    const bool none = lim == 0;
+    const float inv = 1.f / l;
+    uint32_t any = 0;  // listed keys of the tiles at the end
+    const int end0 = sp.all / kKeys, from = max(p.t0, end0);
+    for (int t = from; t < p.t0 + n; ++t)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) any |= ctl->odd[part & 3][t - end0][x];
+    float *to_part = attn_part_out(a, grid, blockIdx.x, p.slot, kRows, 128 * i + tid);
+#pragma unroll 1
+    for (int c = 0; c < D; c += 32) {
+      float o[32];
+      if (n > 0) {
+        tmem_ld32(to + c, o);
+        tmem_wait_ld();
+      } else {
+#pragma unroll
+        for (int x = 0; x < 32; ++x) o[x] = 0.f;
+      }
+      if (any && mine) {
+        for (int k = from * kKeys; k < min(lim, (p.t0 + n) * kKeys); ++k) {
+          if (!((ctl->odd[part & 3][k / kKeys - end0][k % kKeys / 32] >> (k % 32)) & 1u)) continue;
+          const int id = a.table[(long long)p.n * a.max_pages + k / a.page];
+          const __nv_bfloat16 *v = vc + key_offset(a, id, k % a.page, p.h) + c;
+#pragma unroll
+          for (int x = 0; x < 32; ++x) {
+            const float y = __bfloat162float(v[x]);
+            if (!isfinite(y)) o[x] += y;
+          }
+        }
+      }
+      if (!mine) continue;
+      if (p.whole) {
+        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.o) + tok * a.os + head * D + c;
+#pragma unroll
+        for (int x = 0; x < 32; x += 8) {
+          uint4 w;
+          uint32_t *u = &w.x;
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const __nv_bfloat162 b = none ? __floats2bfloat162_rn(0.f, 0.f)
+                                          : __floats2bfloat162_rn(o[x + 2 * y] * inv, o[x + 2 * y + 1] * inv);
+            u[y] = *reinterpret_cast<const uint32_t *>(&b);
+          }
+          *reinterpret_cast<uint4 *>(out + x) = w;
+        }
+      } else {
+#pragma unroll
+        for (int x = 0; x < 32; x += 4)
+          *reinterpret_cast<float4 *>(to_part + c + x) = make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+      }
+    }
+    tc_fence_before();
+    if (!mine) continue;
+    if (!p.whole) *attn_part_ml(a, grid, blockIdx.x, p.slot, kRows, 128 * i + tid) = make_float2(m * a.scale2, l);
+    else if (a.lse) a.lse[tok * a.Hq + head] = none ? -INFINITY : (m * a.scale2 + log2f(l)) * 0.6931471805599453f;
+  }
+}
+
+// ----------------------------------------------------------------- products
+
+template <int D>
+__device__ __forceinline__ void product_role(const AttnArgs &a, AttnWalk walk, Ctl *ctl, const Waits &wait,
+                                             unsigned char *smem, int lane) {
+  constexpr int S = Tc<D>::kStages;
+  constexpr uint32_t kIdS = idesc_bf16_f32(128, kKeys, 0, 0), kIdO = idesc_bf16_f32(128, D, 0, 1);
+  const uint32_t base = smem_u32(smem), tb = ctl->tmem;
+  auto bar = [&](int b) { return smem_u32(&ctl->bar[b]); };
+  auto scores = [&](int i, uint32_t stage) {  // S_i = Q_i K^T
+    const uint32_t q = base + i * Tc<D>::kTile, k = base + Tc<D>::kK + stage * Tc<D>::kTile;
+    if (lane == 0) {
+#pragma unroll
+      for (int x = 0; x < D / 16; ++x) {
+        const uint32_t off = (x / 4) * kHalf + (x % 4) * 32;
+        mma_bf16_ss(tb + 128 * i, smem_desc_sw128(q + off, 16, 1024), smem_desc_sw128(k + off, 16, 1024), kIdS, x > 0);
+      }
+      mma_commit(bar(B_S + i));
+    }
+    __syncwarp();
+  };
+  uint32_t kc = 0, vcnt = 0, nq[2] = {0, 0}, np[2] = {0, 0};
+  AttnPart p;
+  while (attn_next<kRows, kKeys>(a, walk, p)) {
+    const Span sp(a, p);
+    const int count = p.t1 - p.t0;
+    for (int i = 0; i < 2; ++i)
+      if (sp.n[i] > 0 && !wait(B_Q + i, nq[i]++)) return;
+    if (!wait(B_KFULL + kc % S, kc / S)) return;
+    for (int i = 0; i < 2; ++i)
+      if (sp.n[i] > 0) scores(i, kc % S);
+    if (lane == 0) mma_commit(bar(B_KEMPTY + kc % S));
+    ++kc;
+    for (int j = 0; j < count; ++j) {
+      const uint32_t vs = vcnt % S;
+      if (!wait(B_VFULL + vs, vcnt / S)) return;
+      if (!wait(B_VOK + vs, vcnt / S)) return;
+      if (j + 1 < count && !wait(B_KFULL + kc % S, kc / S)) return;
+      const uint32_t v = base + Tc<D>::kV + vs * Tc<D>::kTile;
+      tc_fence_after();
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (j < sp.n[i]) {
+          if (!wait(B_P + i, np[i]++)) return;
+          tc_fence_after();
+          if (lane == 0) {
+#pragma unroll
+            for (int x = 0; x < kKeys / 16; ++x)
+              mma_bf16_ts(tb + 256 + 128 * i, tb + 128 * i + 8 * x, smem_desc_sw128(v + x * 2048, kHalf, 1024), kIdO,
+                          j > 0 || x > 0);
+            if (j == sp.n[i] - 1) mma_commit(bar(B_O + i));
+          }
+          __syncwarp();
+        }
+        if (i == 1 && lane == 0) mma_commit(bar(B_VEMPTY + vs));
+        __syncwarp();
+        if (j + 1 < sp.n[i]) scores(i, kc % S);
+      }
+      ++vcnt;
+      if (j + 1 < count) {
+        if (lane == 0) mma_commit(bar(B_KEMPTY + kc % S));
+        ++kc;
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------- copies
+
+template <int D>
+__device__ __forceinline__ void copy_role(const TcArgs &args, const CUtensorMap *mk, const CUtensorMap *mv, AttnWalk walk,
+                                          Ctl *ctl, const Waits &wait, unsigned char *smem, int lane) {
+  constexpr int S = Tc<D>::kStages;
+  const AttnArgs &a = args.a;
+  const int box = args.box, boxes = kKeys / box, b = lane % boxes, half = lane / boxes;  // (boxes is a power of two)
+  const uint32_t base = smem_u32(smem), to = half * kHalf + b * box * 128;
+  uint32_t n = 0, issued[2] = {0, 0};  // tiles; copies of keys, of values
+  bool alive = true;
+  AttnPart p;
+  while (alive && attn_next<kRows, kKeys>(a, walk, p)) {
+    const Span sp(a, p);
+    const int32_t *table = a.table + (long long)p.n * a.max_pages;
+    auto page_of = [&](int t) {
+      const int j = t * kKeys + b * box;
+      return t < p.t1 && half < D / 64 && j < sp.most ? min(max(table[j / a.page], 0), a.pages - 1) : -1;
+    };
+    int id = page_of(p.t0);
+    for (int t = p.t0; t < p.t1; ++t) {
+      const int j = t * kKeys + b * box, slot = j % a.page;
+      const uint32_t st = n % S, bytes = __popc(__ballot_sync(~0u, id >= 0)) * box * 128;
+      const int next = page_of(t + 1);
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        const int full = (kv ? B_VFULL : B_KFULL) + st;
+        if (!wait((kv ? B_VEMPTY : B_KEMPTY) + st, n / S + 1)) {
+          alive = false;
+          break;
+        }
+        const uint32_t bar = smem_u32(&ctl->bar[full]);
+        if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+        ++issued[kv];
+        __syncwarp();
+        if (id >= 0) tma_load_4d(base + (kv ? Tc<D>::kV : Tc<D>::kK) + st * Tc<D>::kTile + to, kv ? mv : mk, bar, half * 64, slot, p.h, id);
+      }
+      if (!alive) break;
+      ++n;
+      id = next;
+    }
+  }
+  // copies still in flight after an abort land before the CTA retires
+  volatile int no_abort = 0;
+#pragma unroll
+  for (int kv = 0; kv < 2; ++kv)
+    for (uint32_t x = issued[kv] > S ? issued[kv] - S : 0; x < issued[kv]; ++x)
+      mbar_wait(smem_u32(&ctl->bar[(kv ? B_VFULL : B_KFULL) + x % S]), x / S & 1, &no_abort, args.err, 1u << 31);
+}
+
+// ------------------------------------------------------------ values at the end
+
+__device__ __forceinline__ uint32_t odd_bf16(uint32_t w) {  // mask of the halves that are not finite
+  return ((w & 0x7f80u) == 0x7f80u ? 0xffffu : 0u) | ((w & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u);
+}
+
+template <int D>
+__device__ __forceinline__ void value_role(const AttnArgs &a, AttnWalk walk, Ctl *ctl, const Waits &wait,
+                                           unsigned char *smem, int w, int lane) {
+  constexpr int S = Tc<D>::kStages, kPieces = D / 8, kStep = 32 / kPieces;  // pieces of a row; rows at a time
+  uint32_t n = 0;
+  AttnPart p;
+  for (int part = 0; attn_next<kRows, kKeys>(a, walk, p); ++part) {
+    const Span sp(a, p);
+    for (int t = p.t0; t < p.t1; ++t, ++n) {
+      if (!wait(B_VFULL + n % S, n / S)) return;
+      if (!sp.at_end(t)) {
+        if (lane == 0) mbar_arrive(smem_u32(&ctl->bar[B_VOK + n % S]));
+        continue;
+      }
+      const int valid = sp.most - t * kKeys, c = lane % kPieces;  // rows up to `valid` hold values
+      const uint32_t v = smem_u32(smem) + Tc<D>::kV + n % S * Tc<D>::kTile + (c / 8) * kHalf;
+      uint32_t list[2] = {0u, 0u};
+#pragma unroll 4
+      for (int r0 = 0; r0 < 64; r0 += kStep) {
+        const int r = w * 64 + r0 + lane / kPieces;
+        const uint32_t at = v + sw128_offset(r, (c % 8) * 8);
+        uint4 x;
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at) : "memory");
+        uint32_t o[4] = {odd_bf16(x.x), odd_bf16(x.y), odd_bf16(x.z), odd_bf16(x.w)};
+        const bool odd = r < valid && (o[0] | o[1] | o[2] | o[3]);
+        if (r >= valid) o[0] = o[1] = o[2] = o[3] = ~0u;
+        if (odd || r >= valid)
+          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(x.x & ~o[0]), "r"(x.y & ~o[1]),
+                       "r"(x.z & ~o[2]), "r"(x.w & ~o[3]) : "memory");
+        const uint32_t found = __ballot_sync(~0u, odd);
+        if (found)
+          for (int y = 0; y < kStep; ++y)
+            if ((found >> (y * kPieces)) & ((1u << kPieces) - 1u)) list[(r0 + y) / 32] |= 1u << ((r0 + y) % 32);
+      }
+      if (lane < 2) ctl->odd[part & 3][t - sp.all / kKeys][2 * w + lane] = lane ? list[1] : list[0];
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ctl->bar[B_VOK + n % S]));
+    }
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+                   const __grid_constant__ TcArgs args) {
+  extern __shared__ unsigned char raw[];
+  unsigned char *smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  Ctl *ctl = reinterpret_cast<Ctl *>(smem + Tc<D>::kCtl);
+  const AttnArgs &a = args.a;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, grid = gridDim.x;
+  if (tid == 0) {
+    ctl->abort = 0;
+    for (int b = 0; b < B_COUNT; ++b) {
+      const bool group = (b >= B_Q && b < B_Q + 2) || (b >= B_P && b < B_P + 2);
+      const bool pair = b >= B_VOK && b < B_VOK + kMaxStages;
+      mbar_init(smem_u32(&ctl->bar[b]), group ? 128 : pair ? 2 : 1);
+    }
+    fence_mbar_init();
+    tma_prefetch_desc(&mk);
+    tma_prefetch_desc(&mv);
+  }
+  if (warp == 8) {
+    tmem_alloc(smem_u32(&ctl->tmem), 512);
+    tmem_relinquish();
+  }
+  const AttnWalk walk = attn_walk<kRows, kKeys, kThreads>(a, blockIdx.x, grid);  // (with barriers of the whole block)
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (tid == 0) {  // the record of the item that this block begins and does not end: in its last part
+    AttnWalk w = walk;
+    AttnPart p;
+    AttnRec rec{0, 0, 0, 0};
+    while (attn_next<kRows, kKeys>(a, w, p))
+      if (p.parts) rec = AttnRec{p.n, p.h, p.r, p.parts};
+    reinterpret_cast<AttnRec *>(a.part)[blockIdx.x] = rec;
+  }
+  __syncwarp();
+  const Waits wait{ctl, args.err};
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;" ::: "memory");
+    softmax_role<D>(a, walk, ctl, wait, smem, warp / 4);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;" ::: "memory");
+    if (warp == 8) {
+      product_role<D>(a, walk, ctl, wait, smem, lane);
+      __syncwarp();
+      if (lane == 0) {  // products in flight after an abort
+        volatile int no_abort = 0;
+        mma_commit(smem_u32(&ctl->bar[B_DRAIN]));
+        mbar_wait(smem_u32(&ctl->bar[B_DRAIN]), 0, &no_abort, args.err, 1u << B_DRAIN);
+      }
+    } else if (warp == 9) {
+      copy_role<D>(args, &mk, &mv, walk, ctl, wait, smem, lane);
+    } else {
+      value_role<D>(a, walk, ctl, wait, smem, warp - 10, lane);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(ctl->tmem, 512);
+  }
+}
+
+template <int D> cudaError_t launch_tc(const CUtensorMap &mk, const CUtensorMap &mv, const TcArgs &args, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Tc<D>::kBytes);
+  if (e != cudaSuccess) return e;
+  attn_tc_kernel<D><<<kSms, kThreads, Tc<D>::kBytes, s>>>(mk, mv, args);
+  e = cudaGetLastError();
+  return e == cudaSuccess ? launch_attn_join(args.a, kSms, kRows, s) : e;
+}
+
+// [pages, Hk, page, d] as (channel, slot, head, page); boxes of 64 channels by `box` slots.
+bool encode_cache(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap *m, const void *base, const AttnArgs &a, int box) {
+  memset(m, 0, sizeof(*m));
+  const cuuint64_t dims[4] = {(cuuint64_t)a.d, (cuuint64_t)a.page, (cuuint64_t)a.Hk, (cuuint64_t)a.pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)a.d * 2, (cuuint64_t)a.page * a.d * 2, (cuuint64_t)a.cs * 2};
+  const cuuint32_t boxes[4] = {64u, (cuuint32_t)box, 1u, 1u}, es[4] = {1u, 1u, 1u, 1u};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, boxes, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+// Heads of 64 or 128 channels, pages that tiles of 128 keys are made of, or that are made of such
+// tiles, in boxes of at least 8 slots (a swizzled row group).
+bool attn_tc_supports(const AttnArgs &a) {
+  if (a.t != KDA_BF16 || (a.d != 64 && a.d != 128)) return false;
+  return a.page % 8 == 0 && (a.page < kKeys ? kKeys % a.page == 0 : a.page % kKeys == 0);
+}
+
+size_t attn_tc_floats(const AttnArgs &a) { return attn_part_floats(kSms, kRows, a.d); }
+
+cudaError_t launch_attn_tc(const AttnArgs &a, cudaStream_t s) {
+  auto encode = tensor_map_encoder();
+  if (!encode) return cudaErrorNotSupported;
+  TcArgs args;
+  args.a = a;
+  args.box = a.page < kKeys ? a.page : kKeys;
+  CUtensorMap mk, mv;
+  if (!encode_cache(encode, &mk, a.kc, a, args.box) || !encode_cache(encode, &mv, a.vc, a, args.box))
+    return cudaErrorInvalidValue;
+  const cudaError_t e = tc_watchdog_word(&args.err);
+  if (e != cudaSuccess) return e;
+  return a.d == 128 ? launch_tc<128>(mk, mv, args, s) : launch_tc<64>(mk, mv, args, s);
+}
+
+}  // namespace kda

@@ -1412,7 +1412,9 @@ chunk_tc_kernel(const __grid_constant__ TcMaps maps, TcArgs A) {
   }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
+}  // namespace
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   if (!fn) {
     void *p = nullptr;
@@ -1424,6 +1426,12 @@ PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
   }
   return fn;
 }
+
+cudaError_t tc_watchdog_word(unsigned int **word) {
+  return cudaGetSymbolAddress(reinterpret_cast<void **>(word), g_tc_watchdog);
+}
+
+namespace {
 
 // [T_total, H, 128] row-major tensor; boxes of 64 tokens of one head.
 // Operand layout: bf16, two 64-column boxes with the 128-byte swizzle the MMA
@@ -1461,7 +1469,7 @@ bool chunk_tc_supports(const PrefillArgs &a) {
 
 cudaError_t launch_chunk_tc(const PrefillArgs &a, cudaStream_t s) {
   if (a.N * a.H == 0) return cudaSuccess;
-  auto encode = get_encode();
+  auto encode = tensor_map_encoder();
   if (!encode) return cudaErrorNotSupported;
   const bool z = a.A_log != nullptr, og = a.og != nullptr && a.o != nullptr;
   TcMaps maps;
@@ -1473,8 +1481,8 @@ cudaError_t launch_chunk_tc(const PrefillArgs &a, cudaStream_t s) {
       (og && encode_tok_head(encode, &maps.og, a.og, a.T_total, a.H, false, false) != CUDA_SUCCESS) ||
       (a.o && encode_tok_head(encode, &maps.o, a.o, a.T_total, a.H, false, false) != CUDA_SUCCESS))
     return cudaErrorInvalidValue;
-  void *wd = nullptr;
-  cudaError_t e = cudaGetSymbolAddress(&wd, g_tc_watchdog);
+  unsigned int *wd = nullptr;
+  const cudaError_t e = tc_watchdog_word(&wd);
   if (e != cudaSuccess) return e;
   const int NH = a.N * a.H;
   int dev = 0, sms = 0;
@@ -1484,7 +1492,7 @@ cudaError_t launch_chunk_tc(const PrefillArgs &a, cudaStream_t s) {
   // split M7 for an unsplit launch with at most one chain per SM (measured:
   // batch prefill 0.570 -> 0.555 ms; varlen and the long-sequence plan slower)
   const bool split = a.plan == 0 && a.kinds == 1 && a.nseg == 1 && NH <= sms;
-  TcArgs args{a, reinterpret_cast<unsigned int *>(wd)};
+  TcArgs args{a, wd};
   const int grid = a.plan == 1 ? NH + 2 * NH * (a.P - 2) : a.plan == 2 ? NH * (a.P - 1) : NH * a.nseg * a.kinds;
   if (z) {
     if (og) return launch_variant<true, true, false>(maps, args, grid, s);

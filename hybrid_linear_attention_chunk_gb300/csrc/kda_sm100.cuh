@@ -5,9 +5,17 @@
 #pragma once
 
 #include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
 #include <stdint.h>
 
 namespace kda {
+
+// The driver's tensor-map encoder (nullptr when there is none), and the device
+// word that bounded waits report to (kda_chunk_tc.cu).
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
+cudaError_t tc_watchdog_word(unsigned int **word);
+
 namespace sm100 {
 
 // ------------------------------------------------------------------ basics
