@@ -8,7 +8,8 @@
 // then finish together whatever the lengths are, which only the device knows.  An
 // item that a stretch does not hold whole leaves, for each block that has a part of it, the
 // maxima, sums and unnormalised outputs of that part in the workspace, and a second
-// kernel joins them in order.  A block has two such parts at most: one that goes on
+// kernel joins them in order.  An item counts kStart tiles more than it has, for what it
+// costs to begin and end: blocks whose items are short would otherwise be last.  A block has two such parts at most: one that goes on
 // with an item (slot 0) and one that begins one (slot 1).
 #pragma once
 
@@ -40,7 +41,7 @@ __device__ __forceinline__ float2 *attn_part_ml(const AttnArgs &a, int grid, int
 // Keys that rows up to `row` of a sequence may see: the first `end` ones.
 __device__ __forceinline__ int attn_end(const AttnArgs &a, const PagedSeq &s, int row) {
   if (!a.causal) return s.kv;
-  return min(max(s.kv - s.len + row / a.G + 1, 0), s.kv);
+  return min(max(s.kv - s.len + a.by_G(row) + 1, 0), s.kv);
 }
 
 // Items of a (sequence, head), and tiles of one: at least one, so that rows
@@ -51,31 +52,64 @@ template <int R> __device__ __forceinline__ int attn_items(const AttnArgs &a, co
 template <int R, int KT> __device__ __forceinline__ int attn_tiles(const AttnArgs &a, const PagedSeq &s, int r) {
   return max(1, (attn_end(a, s, min((r + 1) * R, s.len * a.G) - 1) + KT - 1) / KT);
 }
-template <int R, int KT> __device__ __forceinline__ long long attn_head_tiles(const AttnArgs &a, const PagedSeq &s) {
+// sum of floor((k i + b) / m) over 0 <= i < n, for k, b >= 0, by Euclid's algorithm on (k, m).
+__device__ __forceinline__ unsigned long long floor_sum(unsigned long long n, unsigned long long m, unsigned long long k,
+                                                        unsigned long long b) {
+  unsigned long long sum = 0;
+  while (true) {
+    sum += (n * (n - 1) / 2) * (k / m) + n * (b / m);
+    k %= m;
+    b %= m;
+    const unsigned long long top = k * n + b;
+    if (top < m) return sum;
+    n = top / m;
+    b = top % m;
+    const unsigned long long x = m;
+    m = k;
+    k = x;
+  }
+}
+// Tiles of the first n items: whole ones have floor(((kv - len + KT) G + (r + 1) R - 1) / (G KT)) or one.
+template <int R, int KT> __device__ __forceinline__ long long attn_tiles_before(const AttnArgs &a, const PagedSeq &s, int n) {
+  if (n == 0) return 0;
   const int items = attn_items<R>(a, s);
-  if (items == 0) return 0;
-  if (!a.causal) return (long long)items * attn_tiles<R, KT>(a, s, 0);
+  if (!a.causal) return (long long)n * attn_tiles<R, KT>(a, s, 0);
   long long sum = 0;
-  for (int r = 0; r < items; ++r) sum += attn_tiles<R, KT>(a, s, r);
+  if (n == items) {  // the last one may have fewer rows
+    sum = attn_tiles<R, KT>(a, s, --n);
+    if (n == 0) return sum;
+  }
+  const long long m = (long long)a.G * KT, first = (long long)(s.kv - s.len + KT) * a.G + R - 1;
+  const long long low = first >= m ? 0 : min((long long)n, (m - first + R - 1) / R);  // items of one tile at the start
+  sum += low;
+  if (low < n) sum += floor_sum(n - low, m, R, first + low * R);
   return sum;
+}
+// Units of the stretches: an item has its tiles and kStart more.
+template <int R, int KT, int kStart> __device__ __forceinline__ long long attn_units_before(const AttnArgs &a, const PagedSeq &s, int n) {
+  return attn_tiles_before<R, KT>(a, s, n) + (long long)n * kStart;
 }
 
 // Where a block's stretch begins and what is left of it.
 struct AttnWalk {
-  int n, h, r, t;   // sequence, head, rows, tile
+  int n, h, r, u;   // sequence, head, rows, unit of the item
+  PagedSeq s;       // of n
   int block, blocks;  // this block, and those that have a stretch
-  long long left, at, total;  // tiles left; index of the next tile among `total`
+  long long left, at, total;  // units left; index of the next one among `total`
 };
 
 // The stretch of block c of `grid`, by all NT threads of the block.
-template <int R, int KT, int NT>
+template <int R, int KT, int kStart, int NT>
 __device__ __forceinline__ AttnWalk attn_walk(const AttnArgs &a, int c, int grid) {
   __shared__ long long warp_sums[NT / 32];
   __shared__ AttnWalk walk;
   const int tid = threadIdx.x, per = (a.N + NT - 1) / NT;
   const int lo = min(tid * per, a.N), hi = min(lo + per, a.N);
   long long sum = 0;
-  for (int n = lo; n < hi; ++n) sum += attn_head_tiles<R, KT>(a, paged_seq(a, n)) * a.Hk;
+  for (int n = lo; n < hi; ++n) {
+    const PagedSeq s = paged_seq(a, n);
+    sum += attn_units_before<R, KT, kStart>(a, s, attn_items<R>(a, s)) * a.Hk;
+  }
   long long upto = sum;  // sum of this thread and those below, first within the warp
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -94,33 +128,42 @@ __device__ __forceinline__ AttnWalk attn_walk(const AttnArgs &a, int c, int grid
   const int blocks = (int)min(total, (long long)grid);
   const long long begin = c < blocks ? total * c / blocks : 0, end = c < blocks ? total * (c + 1) / blocks : 0;
   if (begin < end && begin >= upto - sum && begin < upto) {
-    long long rest = begin - (upto - sum);
+    // the thread whose sequences hold the first tile: which of them, and how far in
+    long long rest = begin - (upto - sum), head = 1;
     AttnWalk w{};
     for (w.n = lo; w.n < hi; ++w.n) {
-      const PagedSeq s = paged_seq(a, w.n);
-      const long long head = attn_head_tiles<R, KT>(a, s);
-      if (rest < head * a.Hk) {
-        w.h = (int)(rest / head);
-        rest -= w.h * head;
-        for (;; ++w.r) {
-          const int nt = attn_tiles<R, KT>(a, s, w.r);
-          if (rest < nt) break;
-          rest -= nt;
-        }
-        w.t = (int)rest;
-        break;
-      }
+      w.s = paged_seq(a, w.n);
+      head = attn_units_before<R, KT, kStart>(a, w.s, attn_items<R>(a, w.s));
+      if (rest < head * a.Hk) break;
       rest -= head * a.Hk;
     }
+    w.h = (int)(rest / head);
+    w.at = rest - w.h * head;  // within the head, for the search below
     w.block = c;
     w.blocks = blocks;
     w.left = end - begin;
-    w.at = begin;
     w.total = total;
     walk = w;
   }
   __syncthreads();
-  return walk;
+  AttnWalk w = walk;
+  if (w.left > 0) {  // the item: each thread looks at a few
+    const int items = attn_items<R>(a, w.s), each = (items + NT - 1) / NT;
+    const int r0 = min(tid * each, items), r1 = min(r0 + each, items);
+    long long before = attn_units_before<R, KT, kStart>(a, w.s, r0);
+    for (int r = r0; r < r1; ++r) {
+      const int units = attn_tiles<R, KT>(a, w.s, r) + kStart;
+      if (w.at >= before && w.at < before + units) {
+        walk.r = r;
+        walk.u = (int)(w.at - before);
+      }
+      before += units;
+    }
+  }
+  __syncthreads();
+  w = walk;
+  w.at = begin;
+  return w;
 }
 
 // One part of a stretch: tiles [t0, t1) of an item.
@@ -131,37 +174,40 @@ struct AttnPart {
   int slot;     // of the workspace, unless whole
   int parts;    // when it begins an item that it does not end: blocks that hold some of it
 };
-template <int R, int KT>
+template <int R, int KT, int kStart>
 __device__ __forceinline__ bool attn_next(const AttnArgs &a, AttnWalk &w, AttnPart &p) {
-  if (w.left <= 0) return false;
-  p.s = paged_seq(a, w.n);
-  int items = attn_items<R>(a, p.s);
-  while (w.r >= items) {  // past the last item of a head
-    w.r = 0;
-    if (items == 0 || ++w.h >= a.Hk) {
-      w.h = 0;
-      p.s = paged_seq(a, ++w.n);  // (some sequence follows as long as tiles are left)
-      items = attn_items<R>(a, p.s);
+  while (w.left > 0) {
+    int items = attn_items<R>(a, w.s);
+    while (w.r >= items) {  // past the last item of a head
+      w.r = 0;
+      if (items == 0 || ++w.h >= a.Hk) {
+        w.h = 0;
+        w.s = paged_seq(a, ++w.n);  // (some sequence follows as long as units are left)
+        items = attn_items<R>(a, w.s);
+      }
     }
+    const int nt = attn_tiles<R, KT>(a, w.s, w.r), units = nt + kStart;
+    const int take = (int)min(w.left, (long long)units - w.u);
+    p.s = w.s;
+    p.n = w.n;
+    p.h = w.h;
+    p.r = w.r;
+    p.t0 = max(w.u - kStart, 0);
+    p.t1 = max(w.u + take - kStart, 0);
+    p.whole = p.t0 == 0 && p.t1 == nt;
+    p.slot = p.t0 == 0 ? 1 : 0;
+    p.parts = 0;
+    if (p.t0 == 0 && !p.whole) {
+      // up to the block whose stretch holds its last unit; stretch c begins at floor(total c / blocks)
+      p.parts = (int)(((w.at - w.u + units) * w.blocks - 1) / w.total) - w.block + 1;
+    }
+    w.at += take;
+    w.left -= take;
+    w.u = 0;
+    ++w.r;
+    if (p.t1 > p.t0) return true;  // (else the stretch ends within what counts for the item's start)
   }
-  const int nt = attn_tiles<R, KT>(a, p.s, w.r);
-  p.n = w.n;
-  p.h = w.h;
-  p.r = w.r;
-  p.t0 = w.t;
-  p.t1 = (int)min((long long)nt, w.t + w.left);
-  p.whole = p.t0 == 0 && p.t1 == nt;
-  p.slot = p.t0 == 0 ? 1 : 0;
-  p.parts = 0;
-  if (p.t0 == 0 && !p.whole) {
-    // up to the block whose stretch holds its last tile; stretch c begins at floor(total c / blocks)
-    p.parts = (int)(((w.at + nt) * w.blocks - 1) / w.total) - w.block + 1;
-  }
-  w.at += p.t1 - p.t0;
-  w.left -= p.t1 - p.t0;
-  w.t = 0;
-  ++w.r;
-  return true;
+  return false;
 }
 
 // Element offset of (page of key j, slot, head h) in the cache.

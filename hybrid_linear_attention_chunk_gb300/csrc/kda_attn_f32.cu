@@ -9,7 +9,7 @@
 namespace kda {
 namespace {
 
-constexpr int kKeys = 64, kThreads = 256;
+constexpr int kKeys = 64, kThreads = 256, kStart = 1;
 
 template <int D, int R> struct F32Smem {
   static constexpr int kRow = D + 4, kProw = kKeys + 4;  // padded: rows of a quarter warp in distinct banks
@@ -43,10 +43,10 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnArgs a) {
   extern __shared__ float4 smem4[];
   float *Qs = reinterpret_cast<float *>(smem4), *Ks = Qs + R * kRow, *Vs = Ks + kKeys * kRow, *Ps = Vs + kKeys * kRow;
   const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16, grid = gridDim.x;
-  AttnWalk walk = attn_walk<R, kKeys, kThreads>(a, blockIdx.x, grid);
+  AttnWalk walk = attn_walk<R, kKeys, kStart, kThreads>(a, blockIdx.x, grid);
   AttnRec rec{0, 0, 0, 0};
   AttnPart p;
-  while (attn_next<R, kKeys>(a, walk, p)) {
+  while (attn_next<R, kKeys, kStart>(a, walk, p)) {
     if (p.parts) rec = AttnRec{p.n, p.h, p.r, p.parts};
     const float *q = static_cast<const float *>(a.q), *kc = static_cast<const float *>(a.kc),
                 *vc = static_cast<const float *>(a.vc);
@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnArgs a) {
       const int r = i / (D / 4), c = i % (D / 4) * 4, at = row0 + r;
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
       if (at < rows)
-        x = *reinterpret_cast<const float4 *>(q + (p.s.bos + at / a.G) * a.qs + (p.h * a.G + at % a.G) * D + c);
+        x = *reinterpret_cast<const float4 *>(q + (p.s.bos + a.by_G(at)) * a.qs + (p.h * a.G + at - a.by_G(at) * a.G) * D + c);
       *reinterpret_cast<float4 *>(Qs + r * kRow + c) = x;
     }
     int lim[RT];  // keys that each of the thread's rows may see
@@ -135,8 +135,8 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnArgs a) {
     for (int i = 0; i < RT; ++i) {
       const int r = ty * RT + i, at = row0 + r;
       if (at >= rows) continue;
-      const size_t tok = p.s.bos + at / a.G;
-      const int head = p.h * a.G + at % a.G;
+      const size_t tok = p.s.bos + a.by_G(at);
+      const int head = p.h * a.G + at - a.by_G(at) * a.G;
       const bool none = lim[i] == 0;
       float *out = p.whole ? static_cast<float *>(a.o) + tok * a.os + head * D
                            : attn_part_out(a, grid, blockIdx.x, p.slot, R, r);

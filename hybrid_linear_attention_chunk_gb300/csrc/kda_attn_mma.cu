@@ -19,6 +19,7 @@ using sm100::smem_u32;
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kWarpKeys = 16, kKeys = kWarps * kWarpKeys;
 constexpr int kStages = 3;
+constexpr int kStart = 1;  // tiles that an item counts for its start and end
 constexpr int kBlocks = 2;  // of an SM
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool there) {
@@ -72,10 +73,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks) attn_mma_kernel(const AttnA
   const uint32_t ring = smem_u32(smem) + warp * kStages * kStage;
   const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q), *kc = static_cast<const __nv_bfloat16 *>(a.kc),
                       *vc = static_cast<const __nv_bfloat16 *>(a.vc);
-  AttnWalk walk = attn_walk<R, kKeys, kThreads>(a, blockIdx.x, grid);
+  AttnWalk walk = attn_walk<R, kKeys, kStart, kThreads>(a, blockIdx.x, grid);
   AttnRec rec{0, 0, 0, 0};
   AttnPart p;
-  while (attn_next<R, kKeys>(a, walk, p)) {
+  while (attn_next<R, kKeys, kStart>(a, walk, p)) {
     if (p.parts) rec = AttnRec{p.n, p.h, p.r, p.parts};
     const int rows = p.s.len * a.G, row0 = p.r * R, tiles = p.t1 - p.t0;
     const int most = attn_end(a, p.s, min(row0 + R, rows) - 1), all = attn_end(a, p.s, row0);
@@ -116,7 +117,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) attn_mma_kernel(const AttnA
       for (int x = 0; x < 2; ++x) {
         const int at = row0 + t * 16 + x * 8 + g;
         const bool there = at < rows;
-        const __nv_bfloat16 *src = q + (there ? (p.s.bos + at / a.G) * a.qs + (p.h * a.G + at % a.G) * D : 0) + tq * 2;
+        const __nv_bfloat16 *src = q + (there ? (p.s.bos + a.by_G(at)) * a.qs + (p.h * a.G + at - a.by_G(at) * a.G) * D : 0) + tq * 2;
         lim[t][x] = there ? attn_end(a, p.s, at) : 0;
         m[t][x] = -INFINITY;
         l[t][x] = 0.f;
@@ -294,8 +295,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) attn_mma_kernel(const AttnA
         continue;
       }
       const float inv = 1.f / sum;
-      const size_t tok = p.s.bos + at / a.G;
-      const int head = p.h * a.G + at % a.G;
+      const size_t tok = p.s.bos + a.by_G(at);
+      const int head = p.h * a.G + at - a.by_G(at) * a.G;
       *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.o) + tok * a.os + head * D + c) =
           none ? make_uint2(0u, 0u) : make_uint2(bf2(y.x * inv, y.y * inv), bf2(y.z * inv, y.w * inv));
       if (a.lse && c == 0) a.lse[tok * a.Hq + head] = none ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;

@@ -28,6 +28,7 @@ namespace {
 using namespace sm100;
 
 constexpr int kThreads = 384, kRows = 256, kKeys = 128;
+constexpr int kStart = 4;  // tiles that an item counts for its start and end
 constexpr int kMaxStages = 3;
 constexpr float kSlack = 8.f;  // powers of two between a row's maximum and its reference
 constexpr uint32_t kHalf = 16384;  // 128 rows of 64 channels
@@ -124,32 +125,36 @@ __device__ __forceinline__ void softmax_role(const AttnArgs &a, AttnWalk walk, C
   const uint32_t qs = smem_u32(smem) + i * Tc<D>::kTile;
   const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q), *vc = static_cast<const __nv_bfloat16 *>(a.vc);
   uint32_t seen_s = 0, seen_o = 0;
-  AttnPart p;
-  for (int part = 0; attn_next<kRows, kKeys>(a, walk, p); ++part) {
+  // Queries of a part: 16-byte pieces, D / 8 of a row, into the swizzled operand tile.  The last
+  // product that read it is complete once this warpgroup has seen its scores.
+  auto load_queries = [&](const AttnPart &p) {
     const Span sp(a, p);
     const int first = sp.row0 + 128 * i;
-    if (first >= sp.rows) continue;
-    const int n = sp.n[i], at = first + tid;
-    const bool mine = at < sp.rows;
-    const int lim = mine ? attn_end(a, p.s, at) : 0, all = attn_end(a, p.s, first);
-    const size_t tok = p.s.bos + at / a.G;
-    const int head = p.h * a.G + at % a.G;
-    float m = -INFINITY, l = 0.f;
-    if (n > 0) {
-      // queries: 16-byte pieces, D / 8 of a row, into the swizzled operand tile (the last product that
-      // read it is complete: this warpgroup has seen its scores)
+    if (first >= sp.rows || sp.n[i] == 0) return;
 #pragma unroll 4
-      for (int x = tid; x < 128 * (D / 8); x += 128) {
-        const int r = x / (D / 8), c = x % (D / 8), rt = first + r;
-        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-        if (rt < sp.rows)
-          w = *reinterpret_cast<const uint4 *>(q + (p.s.bos + rt / a.G) * a.qs + (p.h * a.G + rt % a.G) * D + c * 8);
-        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(qs + (c / 8) * kHalf + sw128_offset(r, (c % 8) * 8)),
-                     "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
-      }
-      fence_proxy_async_smem();
-      mbar_arrive(smem_u32(&ctl->bar[B_Q + i]));
+    for (int x = tid; x < 128 * (D / 8); x += 128) {
+      const int r = x / (D / 8), c = x % (D / 8), rt = min(first + r, sp.rows - 1), rg = a.by_G(rt);
+      const __nv_bfloat16 *src = q + (p.s.bos + rg) * a.qs + (p.h * a.G + rt - rg * a.G) * D + c * 8;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(qs + (c / 8) * kHalf + sw128_offset(r, (c % 8) * 8)),
+                   "l"(src), "r"(first + r < sp.rows ? 16 : 0) : "memory");
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    fence_proxy_async_smem();
+    mbar_arrive(smem_u32(&ctl->bar[B_Q + i]));
+  };
+  AttnPart p, next;
+  bool more = attn_next<kRows, kKeys, kStart>(a, walk, next);
+  if (more) load_queries(next);
+  for (int part = 0; more; ++part) {
+    p = next;
+    const Span sp(a, p);
+    const int first = sp.row0 + 128 * i;
+    const int n = first < sp.rows ? sp.n[i] : 0, at = first + tid;
+    const bool mine = at < sp.rows;
+    const int lim = mine ? attn_end(a, p.s, at) : 0, all = first < sp.rows ? attn_end(a, p.s, first) : 0;
+    const size_t tok = p.s.bos + a.by_G(at);
+    const int head = p.h * a.G + at - a.by_G(at) * a.G;
+    float m = -INFINITY, l = 0.f;
     for (int j = 0; j < n; ++j) {
       const int key0 = (p.t0 + j) * kKeys;
       if (!wait(B_S + i, seen_s++)) return;
@@ -208,6 +213,10 @@ __device__ __forceinline__ void softmax_role(const AttnArgs &a, AttnWalk walk, C
       tc_fence_before();
       mbar_arrive(smem_u32(&ctl->bar[B_P + i]));
     }
+    // (the next part's first scores are computed while this one's outputs are written)
+    more = attn_next<kRows, kKeys, kStart>(a, walk, next);
+    if (more) load_queries(next);
+    if (first >= sp.rows) continue;
     if (n > 0) {
       if (!wait(B_O + i, seen_o++)) return;
       tc_fence_after();
@@ -272,66 +281,94 @@ __device__ __forceinline__ void softmax_role(const AttnArgs &a, AttnWalk walk, C
 
 // ----------------------------------------------------------------- products
 
+// Products are issued by a whole warp in step, one lane elected in the instruction:
+// what an instruction needs is then uniform, and a product of 64 cycles is not held up by moving its operands.
+// Low words of descriptors are the address / 16 and LBO / 16; the high word is the same for all operands here.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);  // SBO 1024, version, 128-byte swizzle
+template <bool kFirst>
+__device__ __forceinline__ void issue_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred e, p;\n\t.reg .b64 x, y;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 x, {%1, %3};\n\tmov.b64 y, {%2, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(kDescHigh),
+      "r"(idesc), "n"(kFirst ? 0 : 1)
+      : "memory");
+}
+__device__ __forceinline__ void issue_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred e, p;\n\t.reg .b64 y;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 y, {%2, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(kDescHigh),
+      "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void issue_commit(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(~0u, x, 0); }
+
 template <int D>
 __device__ __forceinline__ void product_role(const AttnArgs &a, AttnWalk walk, Ctl *ctl, const Waits &wait,
-                                             unsigned char *smem, int lane) {
-  constexpr int S = Tc<D>::kStages;
+                                             unsigned char *smem) {
+  constexpr uint32_t S = Tc<D>::kStages;
   constexpr uint32_t kIdS = idesc_bf16_f32(128, kKeys, 0, 0), kIdO = idesc_bf16_f32(128, D, 0, 1);
-  const uint32_t base = smem_u32(smem), tb = ctl->tmem;
-  auto bar = [&](int b) { return smem_u32(&ctl->bar[b]); };
-  auto scores = [&](int i, uint32_t stage) {  // S_i = Q_i K^T
-    const uint32_t q = base + i * Tc<D>::kTile, k = base + Tc<D>::kK + stage * Tc<D>::kTile;
-    if (lane == 0) {
+  const uint32_t base = uniform(smem_u32(smem)), tb = uniform(ctl->tmem), bars = uniform(smem_u32(&ctl->bar[0]));
+  uint32_t ks = 0, kp = 0, vs = 0, vp = 0;  // stage and parity of the next keys and values
+  auto scores = [&](int i) {                // S_i = Q_i K^T
+    const uint32_t q = ((base + i * Tc<D>::kTile) >> 4) | 1u << 16;
+    const uint32_t k = uniform(((base + Tc<D>::kK + ks * Tc<D>::kTile) >> 4) | 1u << 16);
+    issue_ss<true>(tb + 128 * i, q, k, kIdS);
 #pragma unroll
-      for (int x = 0; x < D / 16; ++x) {
-        const uint32_t off = (x / 4) * kHalf + (x % 4) * 32;
-        mma_bf16_ss(tb + 128 * i, smem_desc_sw128(q + off, 16, 1024), smem_desc_sw128(k + off, 16, 1024), kIdS, x > 0);
-      }
-      mma_commit(bar(B_S + i));
+    for (int x = 1; x < D / 16; ++x) {
+      const uint32_t off = ((x / 4) * kHalf + (x % 4) * 32) >> 4;
+      issue_ss<false>(tb + 128 * i, q + off, k + off, kIdS);
     }
-    __syncwarp();
+    issue_commit(bars + 8 * (B_S + i));
   };
-  uint32_t kc = 0, vcnt = 0, nq[2] = {0, 0}, np[2] = {0, 0};
+  auto keys_done = [&]() {
+    issue_commit(bars + 8 * (B_KEMPTY + ks));
+    if (++ks == S) ks = 0, kp ^= 1u;
+  };
+  uint32_t nq[2] = {0, 0}, np[2] = {0, 0};
   AttnPart p;
-  while (attn_next<kRows, kKeys>(a, walk, p)) {
+  while (attn_next<kRows, kKeys, kStart>(a, walk, p)) {
     const Span sp(a, p);
-    const int count = p.t1 - p.t0;
-    for (int i = 0; i < 2; ++i)
-      if (sp.n[i] > 0 && !wait(B_Q + i, nq[i]++)) return;
-    if (!wait(B_KFULL + kc % S, kc / S)) return;
-    for (int i = 0; i < 2; ++i)
-      if (sp.n[i] > 0) scores(i, kc % S);
-    if (lane == 0) mma_commit(bar(B_KEMPTY + kc % S));
-    ++kc;
+    const int count = p.t1 - p.t0, n0 = sp.n[0], n1 = sp.n[1];
+    if (n0 > 0 && !wait(B_Q, nq[0]++)) return;
+    if (n1 > 0 && !wait(B_Q + 1, nq[1]++)) return;
+    if (!wait(B_KFULL + ks, kp)) return;
+    tc_fence_after();
+    if (n0 > 0) scores(0);
+    if (n1 > 0) scores(1);
+    keys_done();
+    if (!wait(B_VOK + vs, vp)) return;
     for (int j = 0; j < count; ++j) {
-      const uint32_t vs = vcnt % S;
-      if (!wait(B_VFULL + vs, vcnt / S)) return;
-      if (!wait(B_VOK + vs, vcnt / S)) return;
-      if (j + 1 < count && !wait(B_KFULL + kc % S, kc / S)) return;
-      const uint32_t v = base + Tc<D>::kV + vs * Tc<D>::kTile;
-      tc_fence_after();
+      const uint32_t v = uniform(((base + Tc<D>::kV + vs * Tc<D>::kTile) >> 4) | (kHalf >> 4) << 16);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        if (j < sp.n[i]) {
+        const int n = i ? n1 : n0;
+        if (j < n) {
           if (!wait(B_P + i, np[i]++)) return;
           tc_fence_after();
-          if (lane == 0) {
+          issue_ts(tb + 256 + 128 * i, tb + 128 * i, v, kIdO, j > 0);
 #pragma unroll
-            for (int x = 0; x < kKeys / 16; ++x)
-              mma_bf16_ts(tb + 256 + 128 * i, tb + 128 * i + 8 * x, smem_desc_sw128(v + x * 2048, kHalf, 1024), kIdO,
-                          j > 0 || x > 0);
-            if (j == sp.n[i] - 1) mma_commit(bar(B_O + i));
-          }
-          __syncwarp();
+          for (int x = 1; x < kKeys / 16; ++x) issue_ts(tb + 256 + 128 * i, tb + 128 * i + 8 * x, v + x * (2048 >> 4), kIdO, 1u);
+          if (j == n - 1) issue_commit(bars + 8 * (B_O + i));
         }
-        if (i == 1 && lane == 0) mma_commit(bar(B_VEMPTY + vs));
-        __syncwarp();
-        if (j + 1 < sp.n[i]) scores(i, kc % S);
+        if (i == 1) issue_commit(bars + 8 * (B_VEMPTY + vs));
+        if (j + 1 < count && i == 0 && !wait(B_KFULL + ks, kp)) return;
+        if (j + 1 < n) scores(i);
       }
-      ++vcnt;
+      if (++vs == S) vs = 0, vp ^= 1u;
       if (j + 1 < count) {
-        if (lane == 0) mma_commit(bar(B_KEMPTY + kc % S));
-        ++kc;
+        keys_done();
+        if (!wait(B_VOK + vs, vp)) return;  // (while the last products run)
       }
     }
   }
@@ -349,7 +386,7 @@ __device__ __forceinline__ void copy_role(const TcArgs &args, const CUtensorMap 
   uint32_t n = 0, issued[2] = {0, 0};  // tiles; copies of keys, of values
   bool alive = true;
   AttnPart p;
-  while (alive && attn_next<kRows, kKeys>(a, walk, p)) {
+  while (alive && attn_next<kRows, kKeys, kStart>(a, walk, p)) {
     const Span sp(a, p);
     const int32_t *table = a.table + (long long)p.n * a.max_pages;
     auto page_of = [&](int t) {
@@ -399,7 +436,7 @@ __device__ __forceinline__ void value_role(const AttnArgs &a, AttnWalk walk, Ctl
   constexpr int S = Tc<D>::kStages, kPieces = D / 8, kStep = 32 / kPieces;  // pieces of a row; rows at a time
   uint32_t n = 0;
   AttnPart p;
-  for (int part = 0; attn_next<kRows, kKeys>(a, walk, p); ++part) {
+  for (int part = 0; attn_next<kRows, kKeys, kStart>(a, walk, p); ++part) {
     const Span sp(a, p);
     for (int t = p.t0; t < p.t1; ++t, ++n) {
       if (!wait(B_VFULL + n % S, n / S)) return;
@@ -459,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_u32(&ctl->tmem), 512);
     tmem_relinquish();
   }
-  const AttnWalk walk = attn_walk<kRows, kKeys, kThreads>(a, blockIdx.x, grid);  // (with barriers of the whole block)
+  const AttnWalk walk = attn_walk<kRows, kKeys, kStart, kThreads>(a, blockIdx.x, grid);  // (with barriers of the whole block)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -467,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     AttnWalk w = walk;
     AttnPart p;
     AttnRec rec{0, 0, 0, 0};
-    while (attn_next<kRows, kKeys>(a, w, p))
+    while (attn_next<kRows, kKeys, kStart>(a, w, p))
       if (p.parts) rec = AttnRec{p.n, p.h, p.r, p.parts};
     reinterpret_cast<AttnRec *>(a.part)[blockIdx.x] = rec;
   }
@@ -479,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;" ::: "memory");
     if (warp == 8) {
-      product_role<D>(a, walk, ctl, wait, smem, lane);
+      product_role<D>(a, walk, ctl, wait, smem);
       __syncwarp();
       if (lane == 0) {  // products in flight after an abort
         volatile int no_abort = 0;

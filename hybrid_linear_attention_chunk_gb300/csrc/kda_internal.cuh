@@ -258,6 +258,7 @@ cudaError_t launch_kv_append(const RopeArgs &r, const PagedArgs &p, const void *
 // Attention over a paged cache (kda_attn*.cu).
 struct AttnArgs : PagedArgs {
   int G;                     // query heads that share a head of the cache
+  unsigned g_mul, g_shift;   // x / G = (x g_mul >> 32) >> g_shift for 0 <= x < 2^31 (G > 1)
   const void *q, *kc, *vc;
   void *o;
   float *lse;                // nullable
@@ -265,6 +266,7 @@ struct AttnArgs : PagedArgs {
   float scale2;              // scale / ln 2: scores are powers of two
   bool causal;
   float *part;               // workspace
+  __device__ __forceinline__ int by_G(int x) const { return G == 1 ? x : (int)(__umulhi((unsigned)x, g_mul) >> g_shift); }
 };
 size_t attn_workspace_bytes(const AttnArgs &a);
 cudaError_t launch_attn(const AttnArgs &a, cudaStream_t s);
