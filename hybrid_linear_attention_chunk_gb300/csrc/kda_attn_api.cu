@@ -242,7 +242,7 @@ kda_status kda_qk_rope_bwd_workspace_size(const kda_rope_desc *desc, size_t *byt
   *bytes = 0;
   const kda_status st = rope_sizes(desc);
   if (st != KDA_OK) return st;
-  *bytes = rope_bwd_workspace_bytes(desc->d);
+  *bytes = rope_bwd_workspace_bytes(desc->tokens, desc->Hq, desc->Hk, desc->d);
   return KDA_OK;
 }
 
@@ -274,7 +274,7 @@ kda_status kda_qk_rope_bwd(const kda_rope_desc *desc, const void *q, const void 
   out[4] = flat(workspace, workspace ? workspace_bytes : 0);
   const int same_in[] = {2, 3, -1, -1, -1};
   if (aliased_rows(in, 8, out, 5, same_in)) return KDA_ERR_ALIAS;
-  const size_t full = rope_bwd_workspace_bytes(a.d);
+  const size_t full = rope_bwd_workspace_bytes(a.tokens, a.Hq, a.Hk, a.d);
   if (workspace && workspace_bytes < full) return KDA_ERR_SHAPE;
   a.q = q;
   a.k = k;

@@ -220,7 +220,7 @@ struct RopeBwdIo {
   long long dqs, dks;
   float *dqw, *dkw;
 };
-size_t rope_bwd_workspace_bytes(int d);
+size_t rope_bwd_workspace_bytes(int tokens, int Hq, int Hk, int d);
 cudaError_t launch_rope_fwd(const RopeArgs &a, cudaStream_t s);
 cudaError_t launch_rope_bwd(const RopeArgs &a, const RopeBwdIo &io, float *ws, cudaStream_t s);
 

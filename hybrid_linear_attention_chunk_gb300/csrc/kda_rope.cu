@@ -9,19 +9,24 @@
 //
 // A block takes a few tokens with all their heads.  Its threads first form the
 // sine and cosine of each (token, pair) once, into shared memory, for all the
-// heads: the sine costs more than everything else that a row's lane does.  The
-// angle is position * inv_freq in turns modulo one, a 64-bit product of integers:
-// fp32 would lose 2^-24 of it, all of it at positions of 10^6.
+// heads: the sine costs more than everything else that a row's lane does.  Each group of
+// d / 8 lanes then has one token and every so-many-th of its heads, with the pairs' angles
+// and the weights in registers.  Each lane copies the pieces that it will need kStages rows ahead into
+// shared memory of its own, from before the angles are formed on: HBM latency is all that
+// bounds these kernels otherwise.  The angle is
+// position * inv_freq in turns modulo one, a 64-bit product of integers: fp32
+// would lose 2^-24 of it, all of it at positions of 10^6.
 #include <type_traits>
 
 #include "kda_internal.cuh"
+#include "kda_packed.cuh"
 
 namespace kda {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTokens = 8;   // of a block
-constexpr int kBwdBlocks = 152 * 4;
+constexpr int kMaxTokens = 16;   // of a block
+constexpr int kSms = 152, kBwdBlocks = kSms * 32;
 
 // Row pieces: 4 channels at c0 and 4 at c1.
 struct Piece {
@@ -41,35 +46,66 @@ template <typename T> struct Raw;  // 4 channels as they lie in memory
 template <> struct Raw<float> { using V = float4; };
 template <> struct Raw<__nv_bfloat16> { using V = uint2; };
 
-__device__ __forceinline__ void unpack(float4 r, float *v) { v[0] = r.x; v[1] = r.y; v[2] = r.z; v[3] = r.w; }
-__device__ __forceinline__ void unpack(uint2 r, float *v) {
-  const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&r.x));
-  const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&r.y));
-  v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
+// A lane's 8 channels as its pairs (x, y), two pairs to a register pair: what issues
+// packed fp32 instructions.  (Lanes that are not turned have some order of theirs.)
+struct Eight {
+  Vec<2> x[2], y[2];
+};
+__device__ __forceinline__ float bf_lo(unsigned w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(unsigned w) { return __uint_as_float(w & 0xffff0000u); }
+template <bool kInter> __device__ __forceinline__ Eight unpack(float4 a, float4 b) {
+  if (kInter) return Eight{{pair(a.x, a.z), pair(b.x, b.z)}, {pair(a.y, a.w), pair(b.y, b.w)}};
+  return Eight{{pair(a.x, a.y), pair(a.z, a.w)}, {pair(b.x, b.y), pair(b.z, b.w)}};
 }
-__device__ __forceinline__ void pack(float4 &r, const float *v) { r = make_float4(v[0], v[1], v[2], v[3]); }
-__device__ __forceinline__ void pack(uint2 &r, const float *v) {
-  const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
-  r.x = *reinterpret_cast<const unsigned *>(&a);
-  r.y = *reinterpret_cast<const unsigned *>(&b);
+template <bool kInter> __device__ __forceinline__ Eight unpack(uint2 a, uint2 b) {
+  return unpack<kInter>(make_float4(bf_lo(a.x), bf_hi(a.x), bf_lo(a.y), bf_hi(a.y)),
+                        make_float4(bf_lo(b.x), bf_hi(b.x), bf_lo(b.y), bf_hi(b.y)));
+}
+template <bool kInter> __device__ __forceinline__ void pack(const Eight &v, float4 &a, float4 &b) {
+  if (kInter) {
+    a = make_float4(v.x[0].get(0), v.y[0].get(0), v.x[0].get(1), v.y[0].get(1));
+    b = make_float4(v.x[1].get(0), v.y[1].get(0), v.x[1].get(1), v.y[1].get(1));
+  } else {
+    a = make_float4(v.x[0].get(0), v.x[0].get(1), v.x[1].get(0), v.x[1].get(1));
+    b = make_float4(v.y[0].get(0), v.y[0].get(1), v.y[1].get(0), v.y[1].get(1));
+  }
+}
+__device__ __forceinline__ unsigned bf_pair(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const unsigned *>(&b);
+}
+template <bool kInter> __device__ __forceinline__ void pack(const Eight &v, uint2 &a, uint2 &b) {
+  float4 p, q;
+  pack<kInter>(v, p, q);
+  a = make_uint2(bf_pair(p.x, p.y), bf_pair(p.z, p.w));
+  b = make_uint2(bf_pair(q.x, q.y), bf_pair(q.z, q.w));
+}
+template <typename T, bool kInter> __device__ __forceinline__ void store8(T *row, Piece p, const Eight &v) {
+  typename Raw<T>::V lo, hi;
+  pack<kInter>(v, lo, hi);
+  *reinterpret_cast<typename Raw<T>::V *>(row + p.c0) = lo;
+  *reinterpret_cast<typename Raw<T>::V *>(row + p.c1) = hi;
 }
 
-// A row's 8 channels of this lane.
-template <typename T> struct Eight {
-  typename Raw<T>::V lo, hi;
-  __device__ __forceinline__ void load(const T *row, Piece p) {
-    lo = *reinterpret_cast<const typename Raw<T>::V *>(row + p.c0);
-    hi = *reinterpret_cast<const typename Raw<T>::V *>(row + p.c1);
+// Rows on their way: kN tensors' pieces of each of kStages rows, in a place of its own for each lane.
+template <typename T, int kN> struct Ring {
+  using V = typename Raw<T>::V;
+  static constexpr int kStages = (sizeof(T) == 2 ? 8 : 4) / kN;  // a power of two
+  static constexpr size_t kBytes = (size_t)kStages * kN * 2 * kThreads * sizeof(V);
+  V *mine;  // + threadIdx.x
+  __device__ __forceinline__ V *at(int stage, int n, int piece) const { return mine + ((stage * kN + n) * 2 + piece) * kThreads; }
+  __device__ __forceinline__ void copy(int stage, int n, const T *row, Piece p, bool there) const {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const unsigned dst = (unsigned)__cvta_generic_to_shared(at(stage, n, i));
+      asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(row + (i ? p.c1 : p.c0)), "n"(sizeof(V)),
+                   "r"(there ? (int)sizeof(V) : 0) : "memory");
+    }
   }
-  __device__ __forceinline__ void get(float *v) const {
-    unpack(lo, v);
-    unpack(hi, v + 4);
-  }
-  __device__ __forceinline__ void store(T *row, Piece p, const float *v) {
-    pack(lo, v);
-    pack(hi, v + 4);
-    *reinterpret_cast<typename Raw<T>::V *>(row + p.c0) = lo;
-    *reinterpret_cast<typename Raw<T>::V *>(row + p.c1) = hi;
+  __device__ __forceinline__ void commit() const { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  __device__ __forceinline__ void wait() const { asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory"); }
+  template <bool kInter> __device__ __forceinline__ Eight get(int stage, int n) const {
+    return unpack<kInter>(*at(stage, n, 0), *at(stage, n, 1));
   }
 };
 
@@ -92,27 +128,47 @@ __device__ __forceinline__ float2 angle(unsigned long long turns, int pos, float
   return make_float2(c * scale, s * scale);
 }
 
-// Angles of nt tokens to cs[token][pair].
-__device__ __forceinline__ void fill_angles(float2 *cs, const int *pos, int nt, const RopeArgs &a) {
-  const int half = a.rot / 2;
-  for (int i = threadIdx.x; i < nt * half; i += kThreads) {
-    const int tok = i / half, f = i - tok * half;
-    cs[i] = angle(turns_of(a.freq[f]), pos[tok], a.rot_scale);
+// Angles of nt tokens: rot / 2 cosines of a token, then its sines.  A thread has one pair, of several tokens.
+__device__ __forceinline__ void fill_angles(float *cs, const int *pos, int nt, const RopeArgs &a) {
+  const int half = a.rot / 2, step = kThreads / half, f = threadIdx.x % half;
+  if ((int)threadIdx.x >= step * half) return;
+  const unsigned long long turns = turns_of(a.freq[f]);
+  for (int tok = threadIdx.x / half; tok < nt; tok += step) {
+    const float2 x = angle(turns, pos[tok], a.rot_scale);
+    cs[tok * a.rot + f] = x.x;
+    cs[tok * a.rot + half + f] = x.y;
   }
 }
 
-// (a, b) -> (a cos - b sin, b cos + a sin) of the lane's pairs; kBack turns back.
-template <bool kInter, bool kBack> __device__ __forceinline__ void turn(float *v, const float2 *cs) {
-  const float4 p = reinterpret_cast<const float4 *>(cs)[0], q = reinterpret_cast<const float4 *>(cs)[1];
-  const float c[4] = {p.x, p.z, q.x, q.z}, s[4] = {p.y, p.w, q.y, q.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float &x = v[kInter ? 2 * i : i], &y = v[kInter ? 2 * i + 1 : 4 + i];
-    const float sn = kBack ? -s[i] : s[i], x0 = x;
-    x = x0 * c[i] - y * sn;
-    y = y * c[i] + x0 * sn;
+// The lane's four pairs' cosines and sines.
+struct Turn {
+  Vec<2> c[2], s[2];
+  bool turned;
+  // cs: the token's; kBack turns back
+  template <bool kBack> __device__ __forceinline__ void load(const float *cs, int rot, int l, bool turned_) {
+    turned = turned_;
+    float4 p = make_float4(1.f, 1.f, 1.f, 1.f), q = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (turned) {
+      p = *reinterpret_cast<const float4 *>(cs + 4 * l);
+      q = *reinterpret_cast<const float4 *>(cs + rot / 2 + 4 * l);
+    }
+    c[0] = pair(p.x, p.y);
+    c[1] = pair(p.z, p.w);
+    s[0] = kBack ? pair(-q.x, -q.y) : pair(q.x, q.y);
+    s[1] = kBack ? pair(-q.z, -q.w) : pair(q.z, q.w);
   }
-}
+  // (x, y) -> (x cos - y sin, y cos + x sin)
+  __device__ __forceinline__ void apply(Eight &v) const {
+    if (!turned) return;
+    const Vec<2> minus = pair(-1.f, -1.f);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const Vec<2> x = v.x[i], y = v.y[i];
+      v.x[i] = fma(mul(y, s[i]), minus, mul(x, c[i]));
+      v.y[i] = fma(x, s[i], mul(y, c[i]));
+    }
+  }
+};
 
 template <int L> __device__ __forceinline__ float lane_sum(float x) {
 #pragma unroll
@@ -121,89 +177,140 @@ template <int L> __device__ __forceinline__ float lane_sum(float x) {
 }
 
 // The lane's 8 weights (ones when absent).
-__device__ __forceinline__ void load_weight(const float *w, Piece p, float *v) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = w ? w[(i < 4 ? p.c0 : p.c1 - 4) + i] : 1.f;
+template <bool kInter> __device__ __forceinline__ Eight load_weight(const float *w, Piece p) {
+  float4 a = make_float4(1.f, 1.f, 1.f, 1.f), b = a;
+  if (w) {
+    a = make_float4(w[p.c0], w[p.c0 + 1], w[p.c0 + 2], w[p.c0 + 3]);
+    b = make_float4(w[p.c1], w[p.c1 + 1], w[p.c1 + 2], w[p.c1 + 3]);
+  }
+  return unpack<kInter>(a, b);
 }
 
-// Where rows of a tensor go: row (token, head) is base + at(token) + head * step.
-struct TokenRows {
-  long long first, stride, step;
-  __device__ __forceinline__ long long at(int tok, int head) const { return first + tok * stride + head * step; }
-};
-struct SlotRows {          // slots[token] < 0: not stored
-  const long long *slots;
-  long long step;
-  __device__ __forceinline__ long long at(int tok, int head) const {
-    return slots[tok] < 0 ? -1 : slots[tok] + head * step;
-  }
-};
-
-// Rows of nt tokens of one tensor: x -> norm, rotation -> y, or a copy without kTurn.
-template <typename T, int L, bool kInter, bool kTurn, class To>
-__device__ __forceinline__ void rows_fwd(const RopeArgs &a, const T *x, long long xs, T *y, To to, const float *weight,
-                                         int t0, int nt, int H, const float2 *cs) {
-  constexpr int G = kThreads / L, U = 2;  // rows at a time of a block, of a lane
-  const int l = threadIdx.x % L, g = threadIdx.x / L, total = nt * H, half = a.rot / 2;
-  const Piece p = kTurn ? piece_of<kInter>(l, a.rot) : piece_of<true>(l, 0);
-  float w[8];
-  if (kTurn) load_weight(a.norm ? weight : nullptr, p, w);
-  for (int r0 = 0; r0 < total; r0 += G * U) {  // (the whole warp stays, for its shuffles)
-    Eight<T> e[U];
-    int tok[U], head[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int r = r0 + u * G + g;
-      tok[u] = r < total ? r / H : -1;
-      head[u] = r - tok[u] * H;
-      if (tok[u] >= 0) e[u].load(x + (t0 + tok[u]) * xs + head[u] * (8 * L), p);
-      else e[u].lo = e[u].hi = {};
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float v[8];
-      if (kTurn) {
-        e[u].get(v);
-        if (a.norm) {
-          float ss = 0.f;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
-          const float r = rsqrtf(lane_sum<L>(ss) * (1.f / (8 * L)) + a.eps);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] *= r * w[i];
-        }
-      }
-      if (tok[u] < 0) continue;
-      const long long o = to.at(tok[u], head[u]);
-      if (o < 0) continue;
-      if (kTurn) {
-        if (p.turned) turn<kInter, false>(v, cs + tok[u] * half + 4 * l);
-        e[u].store(y + o, p, v);
-      } else {
-        *reinterpret_cast<typename Raw<T>::V *>(y + o + p.c0) = e[u].lo;
-        *reinterpret_cast<typename Raw<T>::V *>(y + o + p.c1) = e[u].hi;
-      }
-    }
-  }
+__device__ __forceinline__ float sum_of(const Eight &a, const Eight &b) {  // of products
+  const Vec<2> s = fma(a.x[0], b.x[0], mul(a.y[0], b.y[0])), t = fma(a.x[1], b.x[1], mul(a.y[1], b.y[1]));
+  const Vec<2> u = add(s, t);
+  return u.get(0) + u.get(1);
 }
+__device__ __forceinline__ Eight times(const Eight &a, const Eight &b) {
+  return Eight{{mul(a.x[0], b.x[0]), mul(a.x[1], b.x[1])}, {mul(a.y[0], b.y[0]), mul(a.y[1], b.y[1])}};
+}
+__device__ __forceinline__ Eight times(const Eight &a, float f) {
+  const Vec<2> b = pair(f, f);
+  return Eight{{mul(a.x[0], b), mul(a.x[1], b)}, {mul(a.y[0], b), mul(a.y[1], b)}};
+}
+__device__ __forceinline__ Eight add_times(const Eight &a, const Eight &b, float f) {  // a + b f
+  const Vec<2> c = pair(f, f);
+  return Eight{{fma(b.x[0], c, a.x[0]), fma(b.x[1], c, a.x[1])}, {fma(b.y[0], c, a.y[0]), fma(b.y[1], c, a.y[1])}};
+}
+__device__ __forceinline__ Eight add_times(const Eight &a, const Eight &b, const Eight &c) {  // a + b c
+  return Eight{{fma(b.x[0], c.x[0], a.x[0]), fma(b.x[1], c.x[1], a.x[1])},
+               {fma(b.y[0], c.y[0], a.y[0]), fma(b.y[1], c.y[1], a.y[1])}};
+}
+
+// A group's place in its block: one token, and heads h0, h0 + step, ...
+struct Place {
+  int tok, h0, step;
+};
+template <int L> __device__ __forceinline__ Place place_of(int per) {  // per: tokens of a block, a power of two
+  constexpr int G = kThreads / L;
+  const int g = threadIdx.x / L;
+  Place p;
+  p.step = per < G ? G / per : 1;
+  p.tok = g / p.step;
+  p.h0 = g % p.step;
+  return p;
+}
+
+// Rows of up to three tensors of the group's token, one after the other: the queries, the keys
+// and, in the append, the values.
+template <typename T> struct Tensor {
+  const T *x;         // of the token
+  T *y;               // nullptr: nothing to do
+  long long ystep;    // from head to head in y
+  int H;
+};
+template <typename T, int L, bool kInter, int kTensors> struct Rows {
+  Tensor<T> t[kTensors];
+  Place at;
+  Piece p;
+  Ring<T, 1> ring;
+  // the next row to copy: its tensor's, head h of H, of x unless there is nothing to do
+  const T *x;
+  int h, H, tensor = -1, put = 0, got = 0;
+  bool open;
+  __device__ __forceinline__ void next_tensor() {
+    h = at.h0;
+    ++tensor;
+    if (tensor == 0 && t[0].H == 0) tensor = 1;
+    if (tensor == 1 && t[1].H == 0) tensor = 2;
+    if (tensor == 0) x = t[0].x, H = t[0].H, open = t[0].y != nullptr;
+    if (tensor == 1) x = t[1].x, H = t[1].H, open = t[1].y != nullptr;
+    if (kTensors > 2 && tensor == 2) x = t[kTensors - 1].x, H = t[kTensors - 1].H, open = t[kTensors - 1].y != nullptr;
+    x += at.h0 * (8 * L);
+  }
+  __device__ __forceinline__ void issue() {
+    if (tensor < kTensors) {
+      const bool there = open && h < H;
+      ring.copy(put, 0, there ? x : t[0].x, p, there);
+      put = (put + 1) % Ring<T, 1>::kStages;
+      x += at.step * (8 * L);
+      h += at.step;
+      if (h - at.h0 >= H) next_tensor();  // (the same for the whole warp)
+    }
+    ring.commit();
+  }
+  __device__ __forceinline__ void start() {
+    next_tensor();
+#pragma unroll 1
+    for (int i = 0; i < Ring<T, 1>::kStages; ++i) issue();
+  }
+  // Rows of tensor i: x -> norm, rotation -> y, or a copy without kTurn.
+  template <int i, bool kTurn> __device__ __forceinline__ void run(const RopeArgs &a, const float *weight, const Turn &turn) {
+    Eight w;
+    if (kTurn) w = load_weight<kInter>(a.norm ? weight : nullptr, p);
+    T *y = t[i].y + at.h0 * t[i].ystep;
+    const long long step = at.step * t[i].ystep;
+    for (int b = 0; b < t[i].H; b += at.step, y += step) {  // (the same count for the whole warp, for its shuffles)
+      ring.wait();
+      Eight v = ring.template get<kInter>(got, 0);
+      got = (got + 1) % Ring<T, 1>::kStages;
+      issue();
+      if (kTurn) {
+        if (a.norm) v = times(v, times(w, rsqrtf(lane_sum<L>(sum_of(v, v)) * (1.f / (8 * L)) + a.eps)));
+        turn.apply(v);
+      }
+      if (t[i].y && b + at.h0 < t[i].H) store8<T, kInter>(y, p, v);
+    }
+  }
+};
 
 template <typename T, int L, bool kInter>
-__global__ void __launch_bounds__(kThreads) rope_fwd_kernel(const RopeArgs a, int per) {
+__global__ void __launch_bounds__(kThreads, 4) rope_fwd_kernel(const RopeArgs a, int per) {
   extern __shared__ float4 smem4[];
-  float2 *cs = reinterpret_cast<float2 *>(smem4);
+  float *cs = reinterpret_cast<float *>(smem4 + Ring<T, 1>::kBytes / 16);
   __shared__ int pos[kMaxTokens];
-  const int t0 = blockIdx.x * per, nt = min(per, a.tokens - t0);
+  const int t0 = blockIdx.x * per, nt = min(per, a.tokens - t0), l = threadIdx.x % L;
+  Rows<T, L, kInter, 2> rows;
+  rows.at = place_of<L>(per);
+  rows.p = piece_of<kInter>(l, a.rot);
+  rows.ring.mine = reinterpret_cast<typename Raw<T>::V *>(smem4) + threadIdx.x;
+  const bool mine = rows.at.tok < nt;
+  const long long t = t0 + (mine ? rows.at.tok : 0);
+  rows.t[0] = Tensor<T>{static_cast<const T *>(a.q) + t * a.qs, mine ? static_cast<T *>(a.qo) + t * a.qos : nullptr,
+                        8 * L, a.Hq};
+  rows.t[1] = Tensor<T>{static_cast<const T *>(a.k) + t * a.ks, mine ? static_cast<T *>(a.ko) + t * a.kos : nullptr,
+                        8 * L, a.Hk};
+  rows.start();
   if (a.rot) {
     if (threadIdx.x < nt) pos[threadIdx.x] = a.positions[t0 + threadIdx.x];
     __syncthreads();
     fill_angles(cs, pos, nt, a);
     __syncthreads();
   }
-  rows_fwd<T, L, kInter, true>(a, static_cast<const T *>(a.q), a.qs, static_cast<T *>(a.qo),
-                               TokenRows{t0 * a.qos, a.qos, 8 * L}, a.qw, t0, nt, a.Hq, cs);
-  if (a.Hk)
-    rows_fwd<T, L, kInter, true>(a, static_cast<const T *>(a.k), a.ks, static_cast<T *>(a.ko),
-                                 TokenRows{t0 * a.kos, a.kos, 8 * L}, a.kw, t0, nt, a.Hk, cs);
+  Turn turn;
+  turn.load<false>(cs + rows.at.tok * a.rot, a.rot, l, mine && rows.p.turned);
+  rows.template run<0, true>(a, a.qw, turn);
+  rows.template run<1, true>(a, a.kw, turn);
 }
 
 // ------------------------------------------------------------------- append
@@ -244,87 +351,55 @@ __device__ __forceinline__ void place_tokens(const PagedArgs &p, int t0, int nt,
 }
 
 template <typename T, int L, bool kInter>
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(const RopeArgs a, const PagedArgs p, const T *v,
-                                                             long long vs, T *kc, T *vc, int per) {
+__global__ void __launch_bounds__(kThreads, 4) kv_append_kernel(const RopeArgs a, const PagedArgs p, const T *v,
+                                                                long long vs, T *kc, T *vc, int per) {
   extern __shared__ float4 smem4[];
-  float2 *cs = reinterpret_cast<float2 *>(smem4);
+  float *cs = reinterpret_cast<float *>(smem4 + Ring<T, 1>::kBytes / 16);
   __shared__ int pos[kMaxTokens];
-  __shared__ long long slot[kMaxTokens], qrow[kMaxTokens];
-  __shared__ bool mine[kMaxTokens];
-  const int t0 = blockIdx.x * per, nt = min(per, a.tokens - t0);
-  place_tokens(p, t0, nt, pos, slot, mine);
-  if (threadIdx.x < nt) qrow[threadIdx.x] = mine[threadIdx.x] ? (t0 + threadIdx.x) * a.qos : -1;
+  __shared__ long long slot[kMaxTokens];
+  __shared__ bool in[kMaxTokens];
+  const int t0 = blockIdx.x * per, nt = min(per, a.tokens - t0), l = threadIdx.x % L;
+  Rows<T, L, kInter, 3> rows;
+  rows.at = place_of<L>(per);
+  rows.p = piece_of<kInter>(l, a.rot);
+  rows.ring.mine = reinterpret_cast<typename Raw<T>::V *>(smem4) + threadIdx.x;
+  const bool mine = rows.at.tok < nt;
+  const long long t = t0 + (mine ? rows.at.tok : 0), head = (long long)p.page * (8 * L);
+  // (rows of tokens that turn out not to be stored are read all the same: they lie within the tensors)
+  const T *k = static_cast<const T *>(a.k) + t * a.ks;
+  rows.t[0] = Tensor<T>{a.q ? static_cast<const T *>(a.q) + t * a.qs : k,
+                        mine ? static_cast<T *>(a.qo) + t * a.qos : nullptr, 8 * L, a.q ? a.Hq : 0};
+  rows.t[1] = Tensor<T>{k, mine ? kc : nullptr, head, a.Hk};
+  rows.t[2] = Tensor<T>{v + t * vs, mine ? vc : nullptr, head, a.Hk};
+  rows.start();
+  place_tokens(p, t0, nt, pos, slot, in);
   __syncthreads();
   if (a.rot) {
     fill_angles(cs, pos, nt, a);
     __syncthreads();
   }
-  const long long head = (long long)p.page * (8 * L);
-  if (a.q)
-    rows_fwd<T, L, kInter, true>(a, static_cast<const T *>(a.q), a.qs, static_cast<T *>(a.qo), SlotRows{qrow, 8 * L},
-                                 a.qw, t0, nt, a.Hq, cs);
-  rows_fwd<T, L, kInter, true>(a, static_cast<const T *>(a.k), a.ks, kc, SlotRows{slot, head}, a.kw, t0, nt, a.Hk, cs);
-  rows_fwd<T, L, kInter, false>(a, v, vs, vc, SlotRows{slot, head}, nullptr, t0, nt, a.Hk, cs);
+  Turn turn;
+  turn.load<false>(cs + rows.at.tok * a.rot, a.rot, l, mine && rows.p.turned);
+  const bool query = mine && in[rows.at.tok];
+  const long long to = mine ? slot[rows.at.tok] : -1;
+  if (!query) rows.t[0].y = nullptr;
+  rows.t[1].y = to >= 0 ? kc + to : nullptr;
+  rows.t[2].y = to >= 0 ? vc + to : nullptr;
+  rows.template run<0, true>(a, a.qw, turn);
+  rows.template run<1, true>(a, a.kw, turn);
+  rows.template run<2, false>(a, nullptr, turn);
 }
 
 // ----------------------------------------------------------------- backward
 
-// Rows of nt tokens of one tensor: dy -> dx, the lane's weight gradients added to dw.
-template <typename T, int L, bool kInter>
-__device__ __forceinline__ void rows_bwd(const RopeArgs &a, const T *x, long long xs, const T *dy, long long dys, T *dx,
-                                         long long dxs, const float *w, int t0, int nt, int H, const float2 *cs,
-                                         float *dw) {
-  constexpr int G = kThreads / L, U = 2;
-  const int l = threadIdx.x % L, g = threadIdx.x / L, total = nt * H, half = a.rot / 2;
-  const Piece p = piece_of<kInter>(l, a.rot);
-  for (int r0 = 0; r0 < total; r0 += G * U) {
-    Eight<T> ex[U], ey[U];
-    int tok[U], head[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int r = r0 + u * G + g;
-      tok[u] = r < total ? r / H : -1;
-      head[u] = r - tok[u] * H;
-      ex[u].lo = ex[u].hi = ey[u].lo = ey[u].hi = {};
-      if (tok[u] >= 0) {
-        if (a.norm) ex[u].load(x + (t0 + tok[u]) * xs + head[u] * (8 * L), p);
-        ey[u].load(dy + (t0 + tok[u]) * dys + head[u] * (8 * L), p);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float v[8], gr[8];
-      ex[u].get(v);
-      ey[u].get(gr);
-      if (p.turned && tok[u] >= 0) turn<kInter, true>(gr, cs + tok[u] * half + 4 * l);
-      if (a.norm) {
-        float ss = 0.f, dot = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          ss = fmaf(v[i], v[i], ss);
-          dot = fmaf(gr[i] * w[i], v[i], dot);
-        }
-        const float r = rsqrtf(lane_sum<L>(ss) * (1.f / (8 * L)) + a.eps);
-        const float m = lane_sum<L>(dot) * (1.f / (8 * L)) * r * r;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (tok[u] >= 0) dw[i] = fmaf(gr[i], v[i] * r, dw[i]);
-          gr[i] = r * (gr[i] * w[i] - v[i] * m);
-        }
-      }
-      if (tok[u] >= 0) ey[u].store(dx + (t0 + tok[u]) * dxs + head[u] * (8 * L), p, gr);
-    }
-  }
-}
-
 // Sum of dw over the block's rows of lanes, to out[d].
-template <int L, bool kInter>
-__device__ __forceinline__ void block_weight(float *sums, const float *dw, int rot, float *out) {
+template <int L, bool kInter> __device__ __forceinline__ void block_weight(float *sums, const Eight &dw, Piece p, float *out) {
   constexpr int G = kThreads / L, D = 8 * L;
-  const Piece p = piece_of<kInter>(threadIdx.x % L, rot);
+  float4 a, b;
+  pack<kInter>(dw, a, b);
   __syncthreads();  // sums is free
-#pragma unroll
-  for (int i = 0; i < 8; ++i) sums[threadIdx.x / L * D + (i < 4 ? p.c0 : p.c1 - 4) + i] = dw[i];
+  *reinterpret_cast<float4 *>(sums + threadIdx.x / L * D + p.c0) = a;
+  *reinterpret_cast<float4 *>(sums + threadIdx.x / L * D + p.c1) = b;
   __syncthreads();
   for (int c = threadIdx.x; c < D; c += kThreads) {
     float s = 0.f;
@@ -333,56 +408,123 @@ __device__ __forceinline__ void block_weight(float *sums, const float *dw, int r
   }
 }
 
-// Blocks walk over the tokens, so that each leaves one row of weight gradients.
+// Blocks have the tokens of one tensor: the first `q_blocks` q's and the others k's (both
+// at once would hold twice the weights and sums in registers).  Each leaves one row of weight
+// gradients; there are up to kBwdBlocks, which walk over the tokens when these are more.
 template <typename T, int L, bool kInter>
-__global__ void __launch_bounds__(kThreads) rope_bwd_kernel(const RopeArgs a, const RopeBwdIo io, int per, float *part) {
-  __shared__ float4 smem4[kThreads * 2];  // kMaxTokens * 64 angles, then a row of d floats for each d / 8 lanes
-  float2 *cs = reinterpret_cast<float2 *>(smem4);
+__global__ void __launch_bounds__(kThreads, 3) rope_bwd_kernel(const RopeArgs a, const RopeBwdIo io, int per,
+                                                               int q_blocks, float *part) {
+  using R = Ring<T, 2>;
+  extern __shared__ float4 smem4[];  // the ring (and in the end a row of d floats for each d / 8 lanes), angles
+  float *cs = reinterpret_cast<float *>(smem4 + R::kBytes / 16);
   __shared__ int pos[kMaxTokens];
-  float wq[8], wk[8], dwq[8] = {}, dwk[8] = {};
+  const bool isq = (int)blockIdx.x < q_blocks;
+  const int H = isq ? a.Hq : a.Hk, first = isq ? blockIdx.x : blockIdx.x - q_blocks;
+  const long long step = (long long)(isq ? q_blocks : gridDim.x - q_blocks) * per;
+  const T *x = static_cast<const T *>(isq ? a.q : a.k), *dy = static_cast<const T *>(isq ? io.dqo : io.dko);
+  T *dx = static_cast<T *>(isq ? io.dq : io.dk);
+  const long long xs = isq ? a.qs : a.ks, dys = isq ? a.qos : a.kos, dxs = isq ? io.dqs : io.dks;
+  const Place at = place_of<L>(per);
   const Piece p = piece_of<kInter>(threadIdx.x % L, a.rot);
-  load_weight(a.qw, p, wq);
-  load_weight(a.kw, p, wk);
-  for (long long t = (long long)blockIdx.x * per; t < a.tokens; t += (long long)gridDim.x * per) {
+  R ring;
+  ring.mine = reinterpret_cast<typename Raw<T>::V *>(smem4) + threadIdx.x;
+  const Eight w = load_weight<kInter>(isq ? a.qw : a.kw, p);
+  Eight dw = Eight{{pair(0.f, 0.f), pair(0.f, 0.f)}, {pair(0.f, 0.f), pair(0.f, 0.f)}};
+  for (long long t = (long long)first * per; t < a.tokens; t += step) {
     const int t0 = (int)t, nt = min(per, a.tokens - t0);
+    const bool mine = at.tok < nt;
+    const long long tok = t0 + (mine ? at.tok : 0);
+    const T *dyt = dy + tok * dys + (mine ? at.h0 * (8 * L) : 0), *xt = a.norm ? x + tok * xs + (mine ? at.h0 * (8 * L) : 0) : dyt;
+    T *dxt = dx + tok * dxs + at.h0 * (8 * L);
+    int h = 0, put = 0, got = 0;  // the next heads to copy
+    auto issue = [&]() {
+      if (h < H) {
+        const bool there = mine && h + at.h0 < H;
+        const int o = there ? h * (8 * L) : 0;
+        ring.copy(put, 0, xt + o, p, there && a.norm);
+        ring.copy(put, 1, dyt + o, p, there);
+        put = (put + 1) % R::kStages;
+        h += at.step;
+      }
+      ring.commit();
+    };
+#pragma unroll 1
+    for (int i = 0; i < R::kStages; ++i) issue();
     if (a.rot) {
       if (threadIdx.x < nt) pos[threadIdx.x] = a.positions[t0 + threadIdx.x];
       __syncthreads();  // (and the last tokens' angles are read)
       fill_angles(cs, pos, nt, a);
       __syncthreads();
     }
-    rows_bwd<T, L, kInter>(a, static_cast<const T *>(a.q), a.qs, static_cast<const T *>(io.dqo), a.qos,
-                           static_cast<T *>(io.dq), io.dqs, wq, t0, nt, a.Hq, cs, dwq);
-    if (a.Hk)
-      rows_bwd<T, L, kInter>(a, static_cast<const T *>(a.k), a.ks, static_cast<const T *>(io.dko), a.kos,
-                             static_cast<T *>(io.dk), io.dks, wk, t0, nt, a.Hk, cs, dwk);
+    Turn turn;
+    turn.load<true>(cs + at.tok * a.rot, a.rot, threadIdx.x % L, mine && p.turned);
+    for (int b = 0; b < H; b += at.step, dxt += at.step * (8 * L)) {
+      const bool there = mine && b + at.h0 < H;
+      ring.wait();
+      const Eight v = ring.template get<kInter>(got, 0);
+      Eight gr = ring.template get<kInter>(got, 1);
+      got = (got + 1) % R::kStages;
+      issue();
+      turn.apply(gr);
+      if (a.norm) {
+        const Eight gw = times(gr, w);
+        const float r = rsqrtf(lane_sum<L>(sum_of(v, v)) * (1.f / (8 * L)) + a.eps);
+        const float m = lane_sum<L>(sum_of(gw, v)) * (1.f / (8 * L)) * r * r;
+        if (there) dw = add_times(dw, gr, times(v, r));
+        gr = times(add_times(gw, v, -m), r);
+      }
+      if (there) store8<T, kInter>(dxt, p, gr);
+    }
   }
-  if (!part) return;
-  float *sums = reinterpret_cast<float *>(smem4);
-  block_weight<L, kInter>(sums, dwq, a.rot, part + (size_t)blockIdx.x * 16 * L);
-  block_weight<L, kInter>(sums, dwk, a.rot, part + (size_t)blockIdx.x * 16 * L + 8 * L);
+  if (part) block_weight<L, kInter>(reinterpret_cast<float *>(smem4), dw, p, part + (size_t)blockIdx.x * 8 * L);
 }
 
-// Column sums of part[blocks][2 d] in fp64: 32 columns a block, 8 threads to each.
-__global__ void __launch_bounds__(256) rope_weight_kernel(const float *part, int blocks, int d, float *dqw, float *dkw) {
-  __shared__ double s[8][32];
-  const int c = blockIdx.x * 32 + threadIdx.x % 32, y = threadIdx.x / 32;
-  double x = 0.0;
-  for (int b = y; b < blocks; b += 8) x += part[(size_t)b * 2 * d + c];
-  s[y][threadIdx.x % 32] = x;
+// Column sums of part[blocks][d], q's rows first: 8 columns a block, 128 threads to each, which
+// have up to 39 rows each and join them by halves (fp64 would take ten times as long here).
+__global__ void __launch_bounds__(1024) rope_weight_kernel(const float *part, int q_blocks, int blocks, int d,
+                                                           float *dqw, float *dkw) {
+  __shared__ float s[8][128 + 1];
+  const int c0 = blockIdx.x % (d / 8) * 8, c = threadIdx.x % 8, y = threadIdx.x / 8;
+  const bool isq = (int)blockIdx.x < d / 8;
+  float *to = isq ? dqw : dkw;
+  if (!to) return;
+  float x = 0.f;
+#pragma unroll 8
+  for (int b = (isq ? 0 : q_blocks) + y; b < (isq ? q_blocks : blocks); b += 128) x += part[(size_t)b * d + c0 + c];
+  s[c][y] = x;
   __syncthreads();
-  if (y == 0) {
-    for (int i = 1; i < 8; ++i) x += s[i][threadIdx.x];
-    float *to = c < d ? dqw : dkw;
-    if (to) to[c < d ? c : c - d] = (float)x;
-  }
+  const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (w >= 8) return;
+  float sum = (s[w][lane] + s[w][lane + 32]) + (s[w][lane + 64] + s[w][lane + 96]);  // warp w has column w
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+  if (lane == 0) to[c0 + w] = sum;
 }
 
 // Tokens of a block: enough blocks for the SMs first, then up to kMaxTokens, over
 // whose heads a lane's weights and the block's start are spread.
 int tokens_per_block(int tokens) {
-  const int n = tokens / (152 * 4);
-  return n < 1 ? 1 : n > kMaxTokens ? kMaxTokens : n;
+  int n = 1;
+  while (n < kMaxTokens && tokens / (2 * n) >= kSms * 4) n *= 2;
+  return n;
+}
+
+// Blocks of the backward, q's and k's by their shares of the rows.
+struct BwdBlocks {
+  int q, k;
+};
+BwdBlocks bwd_blocks(int tokens, int Hq, int Hk) {
+  const int per = tokens_per_block(tokens);
+  const long long need = ((long long)tokens + per - 1) / per;
+  const int share = (int)((long long)kBwdBlocks * Hq / (Hq + Hk)), q = share > 1 ? share : 1;
+  const int k = Hk ? (kBwdBlocks - q > 1 ? kBwdBlocks - q : 1) : 0;
+  return BwdBlocks{(int)(need < q ? need : q), (int)(need < k ? need : k)};
+}
+
+// A kernel's limit of shared memory is the most that any call needs, so that every call sets the same.
+constexpr size_t kMostAngles = kMaxTokens * kMaxDim * sizeof(float);
+template <typename K> cudaError_t allow_shared(K kernel, size_t bytes) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
 template <typename F> cudaError_t for_shape(const RopeArgs &a, F f) {
@@ -407,14 +549,20 @@ template <typename F> cudaError_t for_shape(const RopeArgs &a, F f) {
 
 }  // namespace
 
-size_t rope_bwd_workspace_bytes(int d) { return (size_t)kBwdBlocks * 2 * d * sizeof(float); }
+size_t rope_bwd_workspace_bytes(int tokens, int Hq, int Hk, int d) {
+  const BwdBlocks b = bwd_blocks(tokens, Hq, Hk);
+  return (size_t)(b.q + b.k + 1) * d * sizeof(float);
+}
 
 cudaError_t launch_rope_fwd(const RopeArgs &a, cudaStream_t s) {
   if (a.tokens == 0) return cudaSuccess;
   const int per = tokens_per_block(a.tokens), grid = (int)(((long long)a.tokens + per - 1) / per);
   return for_shape(a, [&](auto t, auto l, auto inter) {
-    rope_fwd_kernel<decltype(t), decltype(l)::value, decltype(inter)::value>
-        <<<grid, kThreads, per * a.rot * sizeof(float), s>>>(a, per);
+    using T = decltype(t);
+    auto kernel = rope_fwd_kernel<T, decltype(l)::value, decltype(inter)::value>;
+    const cudaError_t e = allow_shared(kernel, Ring<T, 1>::kBytes + kMostAngles);
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, kThreads, Ring<T, 1>::kBytes + per * a.rot * sizeof(float), s>>>(a, per);
     return cudaGetLastError();
   });
 }
@@ -425,27 +573,34 @@ cudaError_t launch_kv_append(const RopeArgs &r, const PagedArgs &p, const void *
   const int per = tokens_per_block(r.tokens), grid = (int)(((long long)r.tokens + per - 1) / per);
   return for_shape(r, [&](auto t, auto l, auto inter) {
     using T = decltype(t);
-    kv_append_kernel<T, decltype(l)::value, decltype(inter)::value>
-        <<<grid, kThreads, per * r.rot * sizeof(float), s>>>(r, p, static_cast<const T *>(v), vs, static_cast<T *>(kc),
-                                                             static_cast<T *>(vc), per);
+    auto kernel = kv_append_kernel<T, decltype(l)::value, decltype(inter)::value>;
+    const cudaError_t e = allow_shared(kernel, Ring<T, 1>::kBytes + kMostAngles);
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, kThreads, Ring<T, 1>::kBytes + per * r.rot * sizeof(float), s>>>(
+        r, p, static_cast<const T *>(v), vs, static_cast<T *>(kc), static_cast<T *>(vc), per);
     return cudaGetLastError();
   });
 }
 
 cudaError_t launch_rope_bwd(const RopeArgs &a, const RopeBwdIo &io, float *ws, cudaStream_t s) {
-  const int per = tokens_per_block(a.tokens);
-  const long long need = ((long long)a.tokens + per - 1) / per;
-  const int grid = (int)(need < kBwdBlocks ? need : kBwdBlocks);
+  const BwdBlocks b = bwd_blocks(a.tokens, a.Hq, a.Hk);
+  const int per = tokens_per_block(a.tokens), q_blocks = b.q, k_blocks = b.k;
   const bool weights = io.dqw || io.dkw;
-  if (grid) {
+  if (q_blocks) {
     const cudaError_t e = for_shape(a, [&](auto t, auto l, auto inter) {
-      rope_bwd_kernel<decltype(t), decltype(l)::value, decltype(inter)::value>
-          <<<grid, kThreads, 0, s>>>(a, io, per, weights ? ws : nullptr);
+      using R = Ring<decltype(t), 2>;
+      auto kernel = rope_bwd_kernel<decltype(t), decltype(l)::value, decltype(inter)::value>;
+      const cudaError_t f = allow_shared(kernel, R::kBytes + kMostAngles);
+      if (f != cudaSuccess) return f;
+      kernel<<<q_blocks + k_blocks, kThreads, R::kBytes + per * a.rot * sizeof(float), s>>>(a, io, per, q_blocks,
+                                                                                        weights ? ws : nullptr);
       return cudaGetLastError();
     });
     if (e != cudaSuccess) return e;
   }
-  if (weights) rope_weight_kernel<<<a.d / 16, 256, 0, s>>>(ws, grid, a.d, io.dqw, io.dkw);
+  if (weights) {
+    rope_weight_kernel<<<a.d / 8 * 2, 1024, 0, s>>>(ws, q_blocks, q_blocks + k_blocks, a.d, io.dqw, io.dkw);
+  }
   return cudaGetLastError();
 }
 

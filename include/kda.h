@@ -591,7 +591,7 @@ kda_status kda_qk_rope_bwd(const kda_rope_desc *desc, const void *q, const void 
  *  - page_table [N, max_pages], lens [N], cu_seqlens [N + 1] are int32 on the
  *    device and are read there: captured calls see their values at replay.
  *    cu_seqlens NULL means B sequences of T new tokens; packed sequences may be
- *    empty, and rows behind the last one are neither read nor written.
+ *    empty, and rows behind the last one have no effect and are not written.
  *  - Entries of page_table behind a sequence's last page are not read; slots
  *    behind its length, whatever they hold, have no effect.
  *  - Validate mode returns KDA_ERR_RANGE for cu_seqlens that do not start at 0

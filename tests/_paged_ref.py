@@ -82,9 +82,13 @@ def turn(x, w, positions, inv_freq, layout="half", rot_scale=1.0, norm=True, eps
     em = (eg * (w * x).abs()).sum(-1, keepdim=True) * r * r / d + 40 * U * mag
     dx = r * (gw - x * m)
     edx = r * (eg * w.abs() + x.abs() * em) + 16 * U * r * (gw.abs() + x.abs() * mag)
-    # rows that one lane sums: a block's tokens times its share of the heads; then 128 lanes
-    lanes = 256 // (d // 8)
-    n = (T // 608 + 8) * (H // lanes + 1) + lanes
+    # Terms that one lane sums: one token of each 16 or fewer (`per`), of every so-many-th such group of tokens,
+    # with up to all its heads; then the block's lanes, and up to 39 blocks and 7 halves.  A tensor has at least
+    # 118 of the 4864 blocks here, where no head stands against more than 40 of the other tensor.
+    per = 1
+    while per < 16 and T // (2 * per) >= 608:
+        per *= 2
+    n = -(-(-(-T // per)) // 118) * H + 256 // (d // 8) + 46
     dw = (g * x * r).sum((0, 1))
     edw = ((eg * x.abs() * r).sum((0, 1)) + (13 + n) * U * (g * x * r).abs().sum((0, 1)))
     return (y, e), (dx, edx), (dw, edw)
