@@ -839,28 +839,49 @@ def _paged_sized(*fields) -> _Sized:
     return _Sized(KdaPagedDesc(*fields))
 
 
-def _rows_arg(name, t, lead, heads, d, dtype, index):
-    """Address and token stride of an optional [..., heads, d] tensor with dense
-    heads, whose tokens lie a fixed distance apart (as the parts of one
-    projection's output do)."""
+def _token_stride(name, t):
+    """Elements from token to token of a [..., heads, d] tensor that is not contiguous
+    but has dense heads and its tokens a fixed distance apart (as the parts of
+    one projection's output do); 0 where there is only one token."""
+    shape, st = t.shape, t.stride()
+    if (st[-1] != 1 and shape[-1] > 1) or (st[-2] != shape[-1] and shape[-2] > 1):
+        raise ValueError(f"{name} must have dense heads")
+    if len(shape) == 3:
+        return st[0] if shape[0] > 1 else 0
+    B, T = shape[:2]
+    if B > 1 and T > 1 and st[0] != T * st[1]:
+        raise ValueError(f"{name} must have its tokens a fixed distance apart")
+    return st[1] if T > 1 else st[0] if B > 1 else 0
+
+
+def _rows(name, t, shape, dtype, index):
+    """Address and token stride of an optional tensor of tokens."""
     if t is None:
         return None, 0
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index:
+        return t.data_ptr() or 256, 0 if t.is_contiguous() else _token_stride(name, t)
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.shape != lead + (heads, d):
-        raise ValueError(f"{name} must have shape {tuple(lead) + (heads, d)}, not {tuple(t.shape)}")
-    if t.get_device() != index:
-        raise ValueError(f"{name} must be on CUDA device {index}, not {t.device}")
-    if t.is_contiguous():
-        return t.data_ptr() or 256, 0
-    st = t.stride()
-    if (st[-1] != 1 and d > 1) or (st[-2] != d and heads > 1):
-        raise ValueError(f"{name} must have dense heads")
-    if len(lead) == 2 and lead[0] > 1 and lead[1] > 1 and st[0] != lead[1] * st[1]:
-        raise ValueError(f"{name} must have its tokens a fixed distance apart")
-    if len(lead) == 2 and lead[1] == 1:
-        return t.data_ptr() or 256, st[0] if lead[0] > 1 else 0
-    return t.data_ptr() or 256, st[len(lead) - 1] if lead[-1] > 1 else 0
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    raise ValueError(f"{name} must be on CUDA device {index}, not {t.device}")
+
+
+def _dense_like(t):
+    """A new contiguous tensor of t's shape and type."""
+    r = torch.empty_like(t)
+    return r if r.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+
+def _heads_shape(name, t, like, heads=None):
+    """Shape of an optional [..., heads, d] tensor with like's tokens and d (its own number of heads unless given)."""
+    if t is None:
+        return None
+    shape = t.shape
+    n = len(like)
+    if len(shape) != n or shape[0] != like[0] or shape[-1] != like[-1] or (n == 4 and shape[1] != like[1]):
+        raise ValueError(f"{name} must have shape {(*like[:-2], heads or 'heads', like[-1])}, not {tuple(shape)}")
+    return shape
 
 
 def _layout(name):
@@ -879,28 +900,24 @@ def _turn_args(inv_freq, q_weight, k_weight, d, index):
                    _arg("k_weight", k_weight, (d,), torch.float32, index))
 
 
-def _rope_call(q, k, positions, inv_freq, q_weight, k_weight, layout, rot_scale, norm, eps, outs):
-    """The sized descriptor and the addresses of inputs, weights and `outs`: pairs
-    (name, tensor) of one more q-like and k-like tensor in turn."""
-    if q.dim() not in (3, 4):
+def _rope_call(q, k, positions, inv_freq, q_weight, k_weight, layout, index):
+    """Checked: q's and k's shapes, the descriptor's fields up to the layout, q's and k's
+    strides, and the addresses of q, k, positions, frequencies and weights."""
+    shape, dt = q.shape, q.dtype
+    if len(shape) not in (3, 4):
         raise ValueError("q must be [tokens, Hq, d] or [B, T, Hq, d]")
-    lead, (Hq, d), index, dt = q.shape[:-2], q.shape[-2:], q.get_device(), q.dtype
-    tokens = lead.numel()
-    Hk = 0 if k is None else k.shape[-2] if k.dim() > 1 else -1
-    pq, sq = _rows_arg("q", q, lead, Hq, d, dt, index)
-    pk, sk = _rows_arg("k", k, lead, Hk, d, dt, index)
+    Hq, d = shape[-2:]
+    ks = _heads_shape("k", k, shape)
+    pq, sq = _rows("q", q, shape, dt, index)
+    pk, sk = _rows("k", k, ks, dt, index)
     rot, turn = _turn_args(inv_freq, q_weight, k_weight, d, index)
-    pos = None if rot == 0 else _arg("positions", positions, lead, torch.int32, index)
-    if rot and positions is None:
-        raise ValueError("a rotation needs positions")
-    there, strides = [], [sq, sk]
-    for i, (name, t) in enumerate(outs):
-        p, s = _rows_arg(name, t, lead, Hk if i % 2 else Hq, d, dt, index)
-        there.append(p)
-        strides.append(s)
-    strides += [0] * (6 - len(strides))
-    sized = _rope_sized(tokens, Hq, Hk, d, _dt(q), rot, _layout(layout), rot_scale, 1 if norm else 0, eps, *strides)
-    return sized, (pq, pk, pos, *turn), there
+    pos = None
+    if rot:
+        if positions is None:
+            raise ValueError("a rotation needs positions")
+        pos = _arg("positions", positions, shape[:-2], torch.int32, index)
+    tokens = shape[0] if len(shape) == 3 else shape[0] * shape[1]
+    return shape, ks, (tokens, Hq, 0 if k is None else ks[-2], d, _dt(q), rot, _layout(layout)), sq, sk, (pq, pk, pos, *turn)
 
 
 def kda_qk_rope_fwd(q, k=None, positions=None, inv_freq=None, q_weight=None, k_weight=None, *, layout="half",
@@ -919,13 +936,19 @@ def kda_qk_rope_fwd(q, k=None, positions=None, inv_freq=None, q_weight=None, k_w
         return _there(lambda: kda_qk_rope_fwd(q, k, positions, inv_freq, q_weight, k_weight, layout=layout,
                                               rot_scale=rot_scale, norm=norm, eps=eps, q_out=q_out, k_out=k_out),
                       index, stream, (q, k, positions, inv_freq, q_weight, k_weight, q_out, k_out))
+    qs, ks, sizes, sq, sk, ins = _rope_call(q, k, positions, inv_freq, q_weight, k_weight, layout, index)
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        q_out = _dense_like(q)
+        pqo, sqo = _new(q_out), 0
+    else:
+        pqo, sqo = _rows("q_out", q_out, qs, q.dtype, index)
     if k_out is None and k is not None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    sized, ins, outs = _rope_call(q, k, positions, inv_freq, q_weight, k_weight, layout, rot_scale, norm, eps,
-                                  (("q_out", q_out), ("k_out", k_out)))
-    st = lib.kda_qk_rope_fwd(sized.ref, *ins, *outs, _current_stream(index))
+        k_out = _dense_like(k)
+        pko, sko = _new(k_out), 0
+    else:
+        pko, sko = _rows("k_out", k_out, ks, q.dtype, index)
+    sized = _rope_sized(*sizes, rot_scale, 1 if norm else 0, eps, sq, sk, sqo, sko, 0, 0)
+    st = lib.kda_qk_rope_fwd(sized.ref, *ins, pqo, pko, _current_stream(index))
     if st:
         _check(st, "kda_qk_rope_fwd")
     return q_out, k_out
@@ -939,65 +962,83 @@ def kda_qk_rope_bwd(d_q_out, d_k_out, q, k=None, positions=None, inv_freq=None, 
     given.  `grads` may pass that dict preallocated (parts of one projection's
     gradient, say): then the weights' gradients that it holds are written."""
     lib = _lib or load()
-    index, f32 = q.get_device(), torch.float32
+    index = q.get_device()
     if _elsewhere(index, stream):
         return _there(lambda: kda_qk_rope_bwd(d_q_out, d_k_out, q, k, positions, inv_freq, q_weight, k_weight,
                                               layout=layout, rot_scale=rot_scale, norm=norm, eps=eps,
                                               workspace=workspace, grads=grads),
                       index, stream, (d_q_out, d_k_out, q, k, positions, inv_freq, q_weight, k_weight, workspace))
+    qs, ks, sizes, sq, sk, ins = _rope_call(q, k, positions, inv_freq, q_weight, k_weight, layout, index)
+    dt = q.dtype
+    (pqo, sqo), (pko, sko) = _rows("d_q_out", d_q_out, qs, dt, index), _rows("d_k_out", d_k_out, ks, dt, index)
     if grads is None:
-        new = lambda like: None if like is None else torch.empty(like.shape, dtype=like.dtype, device=q.device)  # noqa: E731
-        grads = {"d_q": new(q), "d_k": new(k), "d_q_weight": new(q_weight), "d_k_weight": new(k_weight)}
-    get, d = grads.get, q.shape[-1:]
-    weights = (_arg("d_q_weight", get("d_q_weight"), d, f32, index), _arg("d_k_weight", get("d_k_weight"), d, f32, index))
-    sized, ins, outs = _rope_call(q, k, positions, inv_freq, q_weight, k_weight, layout, rot_scale, norm, eps,
-                                  (("d_q_out", d_q_out), ("d_k_out", d_k_out), ("d_q", get("d_q")), ("d_k", get("d_k"))))
-    if workspace is None and any(weights):
+        grads = {"d_q": _dense_like(q), "d_k": None if k is None else _dense_like(k),
+                 "d_q_weight": None if q_weight is None else torch.empty_like(q_weight),
+                 "d_k_weight": None if k_weight is None else torch.empty_like(k_weight)}
+        pdq, pdk, pwq, pwk = [_new(t) for t in grads.values()]
+        sdq = sdk = 0
+    else:
+        get, row = grads.get, qs[-1:]
+        (pdq, sdq), (pdk, sdk) = _rows("d_q", get("d_q"), qs, dt, index), _rows("d_k", get("d_k"), ks, dt, index)
+        pwq = _arg("d_q_weight", get("d_q_weight"), row, torch.float32, index)
+        pwk = _arg("d_k_weight", get("d_k_weight"), row, torch.float32, index)
+    sized = _rope_sized(*sizes, rot_scale, 1 if norm else 0, eps, sq, sk, sqo, sko, sdq, sdk)
+    if workspace is None and (pwq or pwk):
         workspace = torch.empty(sized.size("kda_qk_rope_bwd_workspace_size"), dtype=torch.uint8, device=q.device)
     ws, ws_bytes = _workspace(workspace, index)
-    st = lib.kda_qk_rope_bwd(sized.ref, *ins, *outs, *weights, ws, ws_bytes, _current_stream(index))
+    st = lib.kda_qk_rope_bwd(sized.ref, *ins, pqo, pko, pdq, pdk, pwq, pwk, ws, ws_bytes, _current_stream(index))
     if st:
         _check(st, "kda_qk_rope_bwd")
     return grads
 
 
-def _paged_call(lead, heads, dtype, k_cache, v_cache, page_table, lens, cu_seqlens, index):
-    """Sizes and the addresses of what the append and the attention share: the
-    descriptor's fields up to dtype, the cache's stride, (lens, cu_seqlens, table), caches."""
-    if k_cache.dim() != 4:
-        raise ValueError("k_cache must be [num_pages, Hk, page_size, d]")
-    pages, Hk, page, d = k_cache.shape
-    if page_table.dim() != 2 or lens.dim() != 1:
-        raise ValueError("page_table must be [N, max_pages] and lens [N]")
-    N, max_pages = page_table.shape
-    tokens = lead.numel()
-    if cu_seqlens is None:
-        if N == 0 or tokens % N or (len(lead) == 2 and lead[0] != N):
-            raise ValueError(f"{tuple(lead)} tokens are no batch of {N} sequences")
-        B, T, seqs = N, tokens // N, 0
+def _paged_call(shape, heads, dtype, k_cache, v_cache, page_table, lens, cu_seqlens, index):
+    """Checked: what the append and the attention share, for a tensor of tokens of the given
+    shape.  The descriptor's fields up to dtype, the cache's stride, the addresses of (lens,
+    cu_seqlens, table) and of the caches."""
+    if len(shape) == 3:
+        tokens = shape[0]
+    elif len(shape) == 4:
+        tokens = shape[0] * shape[1]
     else:
-        if len(lead) == 2 and lead[0] != 1:
+        raise ValueError("queries, keys and values must be [tokens, heads, d] or [B, T, heads, d]")
+    cs = k_cache.shape
+    if len(cs) != 4:
+        raise ValueError("k_cache must be [num_pages, Hk, page_size, d]")
+    pages, Hk, page, d = cs
+    ts = page_table.shape
+    if len(ts) != 2 or lens.dim() != 1:
+        raise ValueError("page_table must be [N, max_pages] and lens [N]")
+    N, max_pages = ts
+    if cu_seqlens is None:
+        if N == 0 or tokens % N or (len(shape) == 4 and shape[0] != N):
+            raise ValueError(f"{tuple(shape[:-2])} tokens are no batch of {N} sequences")
+        B, T, seqs, cu = N, tokens // N, 0, None
+    else:
+        if len(shape) == 4 and shape[0] != 1:
             raise ValueError("cu_seqlens needs B = 1")
         B, T, seqs = 1, tokens, N
-    caches, strides = [], []
-    for name, c in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if c.dtype is not dtype:
-            raise TypeError(f"{name} must be {dtype}, not {c.dtype}")
-        if c.shape != k_cache.shape:
-            raise ValueError(f"{name} must have shape {tuple(k_cache.shape)}, not {tuple(c.shape)}")
-        if c.get_device() != index:
-            raise ValueError(f"{name} must be on CUDA device {index}, not {c.device}")
-        st = c.stride()
-        if not c.is_contiguous() and ((st[3] != 1 and d > 1) or (st[2] != d and page > 1) or (st[1] != page * d and Hk > 1)):
-            raise ValueError(f"{name} must have dense pages")
-        caches.append(c.data_ptr() or 256)
-        strides.append(st[0] if pages > 1 else Hk * page * d)
-    if strides[0] != strides[1]:
-        raise ValueError("k_cache and v_cache must have the same distance from page to page")
-    where = (_arg("lens", lens, (N,), torch.int32, index),
-             None if cu_seqlens is None else _arg("cu_seqlens", cu_seqlens, (N + 1,), torch.int32, index),
-             _arg("page_table", page_table, (N, max_pages), torch.int32, index))
-    return (B, T, heads, Hk, d, seqs, page, pages, max_pages, _dt(k_cache)), strides[0], where, caches
+        cu = _arg("cu_seqlens", cu_seqlens, (N + 1,), torch.int32, index)
+    if not (k_cache.dtype is dtype and v_cache.dtype is dtype):
+        raise TypeError(f"the cache must be {dtype}, not {k_cache.dtype} and {v_cache.dtype}")
+    if v_cache.shape != cs:
+        raise ValueError(f"v_cache must have shape {tuple(cs)}, not {tuple(v_cache.shape)}")
+    if k_cache.get_device() != index or v_cache.get_device() != index:
+        raise ValueError(f"the cache must be on CUDA device {index}, not {k_cache.device} and {v_cache.device}")
+    stride = 0
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
+        strides = []
+        for name, c in (("k_cache", k_cache), ("v_cache", v_cache)):
+            st = c.stride()
+            if (st[3] != 1 and d > 1) or (st[2] != d and page > 1) or (st[1] != page * d and Hk > 1):
+                raise ValueError(f"{name} must have dense pages")
+            strides.append(st[0] if pages > 1 else Hk * page * d)
+        stride = strides[0]
+        if stride != strides[1]:
+            raise ValueError("k_cache and v_cache must have the same distance from page to page")
+    where = (_arg("lens", lens, ts[:1], torch.int32, index), cu, _arg("page_table", page_table, ts, torch.int32, index))
+    return (B, T, heads, Hk, d, seqs, page, pages, max_pages, _dt(k_cache)), stride, where, (
+        k_cache.data_ptr() or 256, v_cache.data_ptr() or 256)
 
 
 def kda_kv_append(k, v, k_cache, v_cache, page_table, lens, cu_seqlens=None, *, q=None, inv_freq=None, q_weight=None,
@@ -1019,21 +1060,24 @@ def kda_kv_append(k, v, k_cache, v_cache, page_table, lens, cu_seqlens=None, *, 
                                              rot_scale=rot_scale, norm=norm, eps=eps, q_out=q_out, validate=validate),),
                       index, stream, (k, v, k_cache, v_cache, page_table, lens, cu_seqlens, q, inv_freq, q_weight,
                                       k_weight, q_out))[0]
-    if k.dim() not in (3, 4):
+    shape, dt = k.shape, k.dtype
+    if len(shape) not in (3, 4):
         raise ValueError("k must be [tokens, Hk, d] or [B, T, Hk, d]")
-    lead, (Hk, d), dt = k.shape[:-2], k.shape[-2:], k.dtype
-    Hq = Hk if q is None else q.shape[-2] if q.dim() > 1 else -1
-    sizes, cs, where, caches = _paged_call(lead, Hq, dt, k_cache, v_cache, page_table, lens, cu_seqlens, index)
-    if sizes[3:5] != (Hk, d):
-        raise ValueError(f"k has {Hk} heads of {d}, the cache {sizes[3]} of {sizes[4]}")
+    qs = _heads_shape("q", q, shape)
+    sizes, cs, where, caches = _paged_call(shape, shape[-2] if q is None else qs[-2], dt, k_cache, v_cache, page_table,
+                                           lens, cu_seqlens, index)
+    if sizes[3:5] != shape[-2:]:
+        raise ValueError(f"k has {shape[-2]} heads of {shape[-1]}, the cache {sizes[3]} of {sizes[4]}")
     if q is None and q_out is not None:
         raise ValueError("q_out needs q")
+    (pq, sq), (pk, sk), (pv, sv) = (_rows("q", q, qs, dt, index), _rows("k", k, shape, dt, index),
+                                    _rows("v", v, shape, dt, index))
     if q is not None and q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    (pq, sq), (pk, sk), (pv, sv), (po, so) = (
-        _rows_arg("q", q, lead, Hq, d, dt, index), _rows_arg("k", k, lead, Hk, d, dt, index),
-        _rows_arg("v", v, lead, Hk, d, dt, index), _rows_arg("q_out", q_out, lead, Hq, d, dt, index))
-    rot, turn = _turn_args(inv_freq, q_weight, k_weight, d, index)
+        q_out = _dense_like(q)
+        po, so = _new(q_out), 0
+    else:
+        po, so = _rows("q_out", q_out, qs, dt, index)
+    rot, turn = _turn_args(inv_freq, q_weight, k_weight, shape[-1], index)
     sized = _paged_sized(*sizes, sq, sk, sv, so, cs, rot, _layout(layout), rot_scale, 1 if norm else 0, eps, 1, 1.0,
                          1 if validate else 0)
     st = lib.kda_kv_append(sized.ref, pq, pk, pv, *where, *turn, po, *caches, _current_stream(index))
@@ -1057,23 +1101,30 @@ def kda_paged_attn(q, k_cache, v_cache, page_table, lens, cu_seqlens=None, out=N
         return _there(lambda: kda_paged_attn(q, k_cache, v_cache, page_table, lens, cu_seqlens, out, lse, causal=causal,
                                              scale=scale, want_lse=want_lse, validate=validate, workspace=workspace),
                       index, stream, (q, k_cache, v_cache, page_table, lens, cu_seqlens, out, lse, workspace))
-    if q.dim() not in (3, 4):
-        raise ValueError("q must be [tokens, Hq, d] or [B, T, Hq, d]")
-    lead, (Hq, d), dt = q.shape[:-2], q.shape[-2:], q.dtype
-    sizes, cs, where, caches = _paged_call(lead, Hq, dt, k_cache, v_cache, page_table, lens, cu_seqlens, index)
+    shape, dt = q.shape, q.dtype
+    sizes, cs, where, caches = _paged_call(shape, shape[-2] if len(shape) > 1 else 0, dt, k_cache, v_cache, page_table,
+                                           lens, cu_seqlens, index)
+    d = shape[-1]
     if sizes[4] != d:
         raise ValueError(f"q has heads of {d}, the cache of {sizes[4]}")
+    pq, sq = _rows("q", q, shape, dt, index)
     if out is None:
-        out = torch.empty(q.shape, dtype=dt, device=q.device)
+        out = _dense_like(q)
+        po, so = _new(out), 0
+    else:
+        po, so = _rows("out", out, shape, dt, index)
     if lse is None and want_lse:
-        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
-    (pq, sq), (po, so) = _rows_arg("q", q, lead, Hq, d, dt, index), _rows_arg("out", out, lead, Hq, d, dt, index)
-    pl = _arg("lse", lse, q.shape[:-1], torch.float32, index)
+        lse = torch.empty(shape[:-1], dtype=torch.float32, device=q.device)
+        pl = _new(lse)
+    else:
+        pl = _arg("lse", lse, shape[:-1], torch.float32, index)
     sized = _paged_sized(*sizes, sq, 0, 0, so, cs, 0, 0, 1.0, 0, 0.0, 1 if causal else 0,
                          d ** -0.5 if scale is None else scale, 1 if validate else 0)
     if workspace is None:
         workspace = torch.empty(sized.size("kda_paged_attn_workspace_size"), dtype=torch.uint8, device=q.device)
-    ws, ws_bytes = _workspace(workspace, index)
+        ws, ws_bytes = _new(workspace), workspace.shape[0]
+    else:
+        ws, ws_bytes = _workspace(workspace, index)
     st = lib.kda_paged_attn(sized.ref, pq, *caches, *where, po, pl, ws, ws_bytes, _current_stream(index))
     if st:
         _check(st, "kda_paged_attn")
