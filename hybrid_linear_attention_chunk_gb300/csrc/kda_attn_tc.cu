@@ -36,23 +36,44 @@ constexpr uint32_t kHalf = 16384;  // 128 rows of 64 channels
 enum Bar {
   B_Q = 0,                        // [2] queries in shared memory
   B_S = 2,                        // [2] scores in TMEM
-  B_P = 4,                        // [2] probabilities in TMEM, outputs rescaled
-  B_O = 6,                        // [2] the part's outputs are complete
-  B_KFULL = 8,                    // [stages] keys landed
+  B_P = 4,                        // [2] first half of the probabilities in TMEM, outputs rescaled
+  B_P2 = 6,                       // [2] the second half
+  B_O = 8,                        // [2] the part's outputs are complete
+  B_KFULL = 10,                   // [stages] keys landed
   B_KEMPTY = B_KFULL + kMaxStages,
   B_VFULL = B_KEMPTY + kMaxStages,
   B_VEMPTY = B_VFULL + kMaxStages,
   B_VOK = B_VEMPTY + kMaxStages,  // values gone over, where they need it
   B_DRAIN = B_VOK + kMaxStages,
-  B_COUNT
+  B_FULL,                         // [4] a part is told
+  B_EMPTY = B_FULL + 4,           // [4] every warp is done with a part
+  B_COUNT = B_EMPTY + 4
 };
-static_assert(B_COUNT <= 32, "a bit of the watchdog word each");
+
+// A part, as the copy warp works it out for all: it runs ahead of the others.
+constexpr int kParts = 4;         // told at a time
+struct Part {
+  int n, h;                       // sequence, head of the cache
+  int t0, t1;                     // tiles; t1 = 0: there are no more parts
+  int bos, before, kv;            // first new token, position of it, length
+  int rows, row0;                 // rows of the (sequence, head); of the item
+  int most, all[2];               // keys that some row sees; that every row of each 128 sees
+  int count[2];                   // tiles of each 128 rows within the part
+  int whole, slot;
+  // keys that a row sees
+  __device__ __forceinline__ int end(const AttnArgs &a, int row) const {
+    return a.causal ? min(max(before + a.by_G(row) + 1, 0), kv) : kv;
+  }
+  // whether tile t has keys that some row does not see
+  __device__ __forceinline__ bool at_end(int t) const { return (t + 1) * kKeys > all[0]; }
+};
 
 struct Ctl {
   uint64_t bar[B_COUNT];
   uint32_t tmem;
   int abort;
-  uint32_t odd[4][3][4];  // [part % 4][tile at the end][32 keys]: keys with values that are not finite
+  Part part[kParts];
+  uint32_t odd[kParts][3][4];  // [part % 4][tile at the end][32 keys]: keys with values that are not finite
 };
 
 template <int D> struct Tc {
@@ -73,7 +94,7 @@ struct Waits {
   unsigned int *err;
   // By a whole warp; false when any of its lanes gave up.
   __device__ __forceinline__ bool operator()(int b, uint32_t parity) const {
-    return __all_sync(~0u, mbar_wait(smem_u32(&ctl->bar[b]), parity & 1u, &ctl->abort, err, 1u << b));
+    return __all_sync(~0u, mbar_wait(smem_u32(&ctl->bar[b]), parity & 1u, &ctl->abort, err, 1u << (b & 31)));
   }
 };
 
@@ -86,77 +107,85 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *m, 
       : "memory");
 }
 
+// 32 bytes to global memory: whole sectors where the address allows it.
+__device__ __forceinline__ void store32(void *to, const uint32_t (&w)[8], bool aligned) {
+  if (aligned) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
+  } else {
+    reinterpret_cast<uint4 *>(to)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4 *>(to)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 
-// What every role derives of a part.
-struct Span {
-  int rows, row0, most, all;  // rows of the (sequence, head); keys that some row sees; that every row sees
-  int n[2];                   // tiles of each 128 rows within the part
-  __device__ __forceinline__ Span(const AttnArgs &a, const AttnPart &p) {
-    rows = p.s.len * a.G;
-    row0 = p.r * kRows;
-    most = attn_end(a, p.s, min(row0 + kRows, rows) - 1);
-    all = attn_end(a, p.s, row0);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int first = row0 + 128 * i;
-      n[i] = 0;
-      if (first < rows) {
-        const int end = attn_end(a, p.s, min(first + 128, rows) - 1);
-        n[i] = max(min(p.t1, max(1, (end + kKeys - 1) / kKeys)) - p.t0, 0);
-      }
-    }
+// The parts in turn, for a warp that is told of them.
+struct Parts {
+  Ctl *ctl;
+  Waits wait;
+  int at = 0;
+  // The next part, or nullptr behind the last one or after an abort.
+  __device__ __forceinline__ const Part *next() const {
+    if (!wait(B_FULL + at % kParts, at / kParts)) return nullptr;
+    const Part *p = &ctl->part[at % kParts];
+    return p->t1 ? p : nullptr;
   }
-  // Whether tile t has keys that some row does not see.
-  __device__ __forceinline__ bool at_end(int t) const { return (t + 1) * kKeys > all; }
+  __device__ __forceinline__ void done() {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&ctl->bar[B_EMPTY + at % kParts]));
+    ++at;
+  }
 };
 
 // ------------------------------------------------------------------ softmax
 
 template <int D>
-__device__ __forceinline__ void softmax_role(const AttnArgs &a, AttnWalk walk, Ctl *ctl, const Waits &wait,
-                                             unsigned char *smem, int i) {
+__device__ __forceinline__ void softmax_role(const AttnArgs &a, Ctl *ctl, const Waits &wait, unsigned char *smem, int i) {
   const int grid = gridDim.x, tid = threadIdx.x % 128, qw = tid / 32;
   const uint32_t tb = ctl->tmem + ((uint32_t)(32 * qw) << 16), ts = tb + 128 * i, to = tb + 256 + 128 * i;
   const uint32_t qs = smem_u32(smem) + i * Tc<D>::kTile;
   const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q), *vc = static_cast<const __nv_bfloat16 *>(a.vc);
   uint32_t seen_s = 0, seen_o = 0;
-  // Queries of a part: 16-byte pieces, D / 8 of a row, into the swizzled operand tile.  The last
+  // Queries of a part: asynchronous 16-byte copies, D / 8 of a row, into the swizzled operand tile.  The last
   // product that read it is complete once this warpgroup has seen its scores.
-  auto load_queries = [&](const AttnPart &p) {
-    const Span sp(a, p);
-    const int first = sp.row0 + 128 * i;
-    if (first >= sp.rows || sp.n[i] == 0) return;
+  auto issue_queries = [&](const Part *p) {
+    const int first = p->row0 + 128 * i, rows = p->rows;
+    if (p->count[i] == 0) return false;
+    const __nv_bfloat16 *base = q + p->bos * a.qs + p->h * a.G * D + tid % (D / 8) * 8;
+    const uint32_t dst = qs + (tid % (D / 8) / 8) * kHalf;
 #pragma unroll 4
-    for (int x = tid; x < 128 * (D / 8); x += 128) {
-      const int r = x / (D / 8), c = x % (D / 8), rt = min(first + r, sp.rows - 1), rg = a.by_G(rt);
-      const __nv_bfloat16 *src = q + (p.s.bos + rg) * a.qs + (p.h * a.G + rt - rg * a.G) * D + c * 8;
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(qs + (c / 8) * kHalf + sw128_offset(r, (c % 8) * 8)),
-                   "l"(src), "r"(first + r < sp.rows ? 16 : 0) : "memory");
+    for (int x = 0; x < D / 8; ++x) {
+      const int r = x * (1024 / D) + tid / (D / 8), rt = min(first + r, rows - 1), rg = a.by_G(rt);
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + sw128_offset(r, tid % 8 * 8)),
+                   "l"(base + rg * a.qs + (rt - rg * a.G) * D), "r"(first + r < rows ? 16 : 0) : "memory");
     }
+    return true;
+  };
+  auto land_queries = [&]() {
     asm volatile("cp.async.wait_all;" ::: "memory");
     fence_proxy_async_smem();
     mbar_arrive(smem_u32(&ctl->bar[B_Q + i]));
   };
-  AttnPart p, next;
-  bool more = attn_next<kRows, kKeys, kStart>(a, walk, next);
-  if (more) load_queries(next);
-  for (int part = 0; more; ++part) {
-    p = next;
-    const Span sp(a, p);
-    const int first = sp.row0 + 128 * i;
-    const int n = first < sp.rows ? sp.n[i] : 0, at = first + tid;
-    const bool mine = at < sp.rows;
-    const int lim = mine ? attn_end(a, p.s, at) : 0, all = first < sp.rows ? attn_end(a, p.s, first) : 0;
-    const size_t tok = p.s.bos + a.by_G(at);
-    const int head = p.h * a.G + at - a.by_G(at) * a.G;
+  Parts parts{ctl, wait};
+  const Part *p = parts.next();
+  if (p && issue_queries(p)) land_queries();
+  while (p) {
+    const int first = p->row0 + 128 * i, n = p->count[i];
+    if (first >= p->rows) {
+      parts.done();
+      p = parts.next();
+      if (p && issue_queries(p)) land_queries();
+      continue;
+    }
+    const int lim = first + tid < p->rows ? p->end(a, first + tid) : 0, all = p->all[i], t0 = p->t0;
     float m = -INFINITY, l = 0.f;
     for (int j = 0; j < n; ++j) {
-      const int key0 = (p.t0 + j) * kKeys;
+      const int key0 = (t0 + j) * kKeys;
       if (!wait(B_S + i, seen_s++)) return;
       tc_fence_after();
       float s[128];
@@ -207,28 +236,35 @@ __device__ __forceinline__ void softmax_role(const AttnArgs &a, AttnWalk walk, C
           w[x] = __uint_as_float(*reinterpret_cast<const uint32_t *>(&b));
         }
         tmem_st16(ts + c / 2, w);
+        if (c == 32 || c == 96) {  // half of them: their product starts
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(smem_u32(&ctl->bar[(c == 32 ? B_P : B_P2) + i]));
+        }
       }
       l += sum.get(0) + sum.get(1);
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(smem_u32(&ctl->bar[B_P + i]));
     }
-    // (the next part's first scores are computed while this one's outputs are written)
-    more = attn_next<kRows, kKeys, kStart>(a, walk, next);
-    if (more) load_queries(next);
-    if (first >= sp.rows) continue;
+    // The next part's queries come while the last products run, and its first scores are
+    // computed while this one's outputs are written.
+    Parts ahead = parts;
+    ++ahead.at;
+    const Part *next = ahead.next();
+    const bool queries = next && issue_queries(next);
     if (n > 0) {
       if (!wait(B_O + i, seen_o++)) return;
       tc_fence_after();
     }
-    const bool none = lim == 0;
+    if (queries) land_queries();
+    const int at = first + tid, rg = a.by_G(at), head = p->h * a.G + at - rg * a.G;
+    const size_t tok = p->bos + rg;
+    const bool mine = at < p->rows, none = lim == 0, whole = p->whole;
     const float inv = 1.f / l;
     uint32_t any = 0;  // listed keys of the tiles at the end
-    const int end0 = sp.all / kKeys, from = max(p.t0, end0);
-    for (int t = from; t < p.t0 + n; ++t)
+    const int end0 = p->all[0] / kKeys, from = max(t0, end0), ring = parts.at % kParts;
+    for (int t = from; t < t0 + n; ++t)
 #pragma unroll
-      for (int x = 0; x < 4; ++x) any |= ctl->odd[part & 3][t - end0][x];
-    float *to_part = attn_part_out(a, grid, blockIdx.x, p.slot, kRows, 128 * i + tid);
+      for (int x = 0; x < 4; ++x) any |= ctl->odd[ring][t - end0][x];
+    float *to_part = attn_part_out(a, grid, blockIdx.x, p->slot, kRows, 128 * i + tid);
 #pragma unroll 1
     for (int c = 0; c < D; c += 32) {
       float o[32];
@@ -240,10 +276,10 @@ __device__ __forceinline__ void softmax_role(const AttnArgs &a, AttnWalk walk, C
         for (int x = 0; x < 32; ++x) o[x] = 0.f;
       }
       if (any && mine) {
-        for (int k = from * kKeys; k < min(lim, (p.t0 + n) * kKeys); ++k) {
-          if (!((ctl->odd[part & 3][k / kKeys - end0][k % kKeys / 32] >> (k % 32)) & 1u)) continue;
-          const int id = a.table[(long long)p.n * a.max_pages + k / a.page];
-          const __nv_bfloat16 *v = vc + key_offset(a, id, k % a.page, p.h) + c;
+        for (int k = from * kKeys; k < min(lim, (t0 + n) * kKeys); ++k) {
+          if (!((ctl->odd[ring][k / kKeys - end0][k % kKeys / 32] >> (k % 32)) & 1u)) continue;
+          const int id = a.table[(long long)p->n * a.max_pages + k / a.page];
+          const __nv_bfloat16 *v = vc + key_offset(a, id, k % a.page, p->h) + c;
 #pragma unroll
           for (int x = 0; x < 32; ++x) {
             const float y = __bfloat162float(v[x]);
@@ -252,30 +288,38 @@ __device__ __forceinline__ void softmax_role(const AttnArgs &a, AttnWalk walk, C
         }
       }
       if (!mine) continue;
-      if (p.whole) {
+      if (whole) {
         __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.o) + tok * a.os + head * D + c;
+        const bool aligned = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
 #pragma unroll
-        for (int x = 0; x < 32; x += 8) {
-          uint4 w;
-          uint32_t *u = &w.x;
+        for (int x = 0; x < 32; x += 16) {
+          uint32_t w[8];
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
+          for (int y = 0; y < 8; ++y) {
             const __nv_bfloat162 b = none ? __floats2bfloat162_rn(0.f, 0.f)
                                           : __floats2bfloat162_rn(o[x + 2 * y] * inv, o[x + 2 * y + 1] * inv);
-            u[y] = *reinterpret_cast<const uint32_t *>(&b);
+            w[y] = *reinterpret_cast<const uint32_t *>(&b);
           }
-          *reinterpret_cast<uint4 *>(out + x) = w;
+          store32(out + x, w, aligned);
         }
       } else {
+        const bool aligned = (reinterpret_cast<uintptr_t>(to_part) & 31u) == 0;
 #pragma unroll
-        for (int x = 0; x < 32; x += 4)
-          *reinterpret_cast<float4 *>(to_part + c + x) = make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+        for (int x = 0; x < 32; x += 8) {
+          uint32_t w[8];
+#pragma unroll
+          for (int y = 0; y < 8; ++y) w[y] = __float_as_uint(o[x + y]);
+          store32(to_part + c + x, w, aligned);
+        }
       }
     }
     tc_fence_before();
-    if (!mine) continue;
-    if (!p.whole) *attn_part_ml(a, grid, blockIdx.x, p.slot, kRows, 128 * i + tid) = make_float2(m * a.scale2, l);
-    else if (a.lse) a.lse[tok * a.Hq + head] = none ? -INFINITY : (m * a.scale2 + log2f(l)) * 0.6931471805599453f;
+    if (mine) {
+      if (!whole) *attn_part_ml(a, grid, blockIdx.x, p->slot, kRows, 128 * i + tid) = make_float2(m * a.scale2, l);
+      else if (a.lse) a.lse[tok * a.Hq + head] = none ? -INFINITY : (m * a.scale2 + log2f(l)) * 0.6931471805599453f;
+    }
+    parts.done();
+    p = next;
   }
 }
 
@@ -314,8 +358,7 @@ __device__ __forceinline__ void issue_commit(uint32_t bar) {
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(~0u, x, 0); }
 
 template <int D>
-__device__ __forceinline__ void product_role(const AttnArgs &a, AttnWalk walk, Ctl *ctl, const Waits &wait,
-                                             unsigned char *smem) {
+__device__ __forceinline__ void product_role(Ctl *ctl, const Waits &wait, unsigned char *smem) {
   constexpr uint32_t S = Tc<D>::kStages;
   constexpr uint32_t kIdS = idesc_bf16_f32(128, kKeys, 0, 0), kIdO = idesc_bf16_f32(128, D, 0, 1);
   const uint32_t base = uniform(smem_u32(smem)), tb = uniform(ctl->tmem), bars = uniform(smem_u32(&ctl->bar[0]));
@@ -336,10 +379,10 @@ __device__ __forceinline__ void product_role(const AttnArgs &a, AttnWalk walk, C
     if (++ks == S) ks = 0, kp ^= 1u;
   };
   uint32_t nq[2] = {0, 0}, np[2] = {0, 0};
-  AttnPart p;
-  while (attn_next<kRows, kKeys, kStart>(a, walk, p)) {
-    const Span sp(a, p);
-    const int count = p.t1 - p.t0, n0 = sp.n[0], n1 = sp.n[1];
+  Parts parts{ctl, wait};
+  while (const Part *p = parts.next()) {
+    const int count = p->t1 - p->t0, n0 = p->count[0], n1 = p->count[1];
+    parts.done();
     if (n0 > 0 && !wait(B_Q, nq[0]++)) return;
     if (n1 > 0 && !wait(B_Q + 1, nq[1]++)) return;
     if (!wait(B_KFULL + ks, kp)) return;
@@ -354,11 +397,16 @@ __device__ __forceinline__ void product_role(const AttnArgs &a, AttnWalk walk, C
       for (int i = 0; i < 2; ++i) {
         const int n = i ? n1 : n0;
         if (j < n) {
-          if (!wait(B_P + i, np[i]++)) return;
+          if (!wait(B_P + i, np[i])) return;
           tc_fence_after();
           issue_ts(tb + 256 + 128 * i, tb + 128 * i, v, kIdO, j > 0);
 #pragma unroll
-          for (int x = 1; x < kKeys / 16; ++x) issue_ts(tb + 256 + 128 * i, tb + 128 * i + 8 * x, v + x * (2048 >> 4), kIdO, 1u);
+          for (int x = 1; x < kKeys / 32; ++x) issue_ts(tb + 256 + 128 * i, tb + 128 * i + 8 * x, v + x * (2048 >> 4), kIdO, 1u);
+          if (!wait(B_P2 + i, np[i]++)) return;
+          tc_fence_after();
+#pragma unroll
+          for (int x = kKeys / 32; x < kKeys / 16; ++x)
+            issue_ts(tb + 256 + 128 * i, tb + 128 * i + 8 * x, v + x * (2048 >> 4), kIdO, 1u);
           if (j == n - 1) issue_commit(bars + 8 * (B_O + i));
         }
         if (i == 1) issue_commit(bars + 8 * (B_VEMPTY + vs));
@@ -382,40 +430,60 @@ __device__ __forceinline__ void copy_role(const TcArgs &args, const CUtensorMap 
   constexpr int S = Tc<D>::kStages;
   const AttnArgs &a = args.a;
   const int box = args.box, boxes = kKeys / box, b = lane % boxes, half = lane / boxes;  // (boxes is a power of two)
-  const uint32_t base = smem_u32(smem), to = half * kHalf + b * box * 128;
+  const uint32_t base = smem_u32(smem), to_smem = half * kHalf + b * box * 128;
   uint32_t n = 0, issued[2] = {0, 0};  // tiles; copies of keys, of values
   bool alive = true;
+  AttnRec rec{0, 0, 0, 0};
   AttnPart p;
-  while (alive && attn_next<kRows, kKeys, kStart>(a, walk, p)) {
-    const Span sp(a, p);
+  for (int at = 0; alive; ++at) {
+    const bool more = attn_next<kRows, kKeys, kStart>(a, walk, p);
+    if (!wait(B_EMPTY + at % kParts, at / kParts + 1)) break;
+    const int rows = p.s.len * a.G, row0 = p.r * kRows, most = more ? attn_end(a, p.s, min(row0 + kRows, rows) - 1) : 0;
+    if (lane == 0) {
+      Part *to = &ctl->part[at % kParts];
+      to->t1 = 0;
+      if (more) {
+        if (p.parts) rec = AttnRec{p.n, p.h, p.r, p.parts};
+        *to = Part{p.n, p.h, p.t0, p.t1, p.s.bos, p.s.kv - p.s.len, p.s.kv, rows, row0, most, {0, 0}, {0, 0}, p.whole, p.slot};
+        for (int i = 0; i < 2; ++i) {
+          const int first = row0 + 128 * i;
+          if (first >= rows) continue;
+          const int end = attn_end(a, p.s, min(first + 128, rows) - 1);
+          to->all[i] = attn_end(a, p.s, first);
+          to->count[i] = max(min(p.t1, max(1, (end + kKeys - 1) / kKeys)) - p.t0, 0);
+        }
+      }
+      mbar_arrive(smem_u32(&ctl->bar[B_FULL + at % kParts]));
+    }
+    if (!more) break;
     const int32_t *table = a.table + (long long)p.n * a.max_pages;
     auto page_of = [&](int t) {
       const int j = t * kKeys + b * box;
-      return t < p.t1 && half < D / 64 && j < sp.most ? min(max(table[j / a.page], 0), a.pages - 1) : -1;
+      return t < p.t1 && half < D / 64 && j < most ? min(max(table[j / a.page], 0), a.pages - 1) : -1;
     };
     int id = page_of(p.t0);
-    for (int t = p.t0; t < p.t1; ++t) {
+    for (int t = p.t0; t < p.t1 && alive; ++t) {
       const int j = t * kKeys + b * box, slot = j % a.page;
       const uint32_t st = n % S, bytes = __popc(__ballot_sync(~0u, id >= 0)) * box * 128;
       const int next = page_of(t + 1);
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
-        const int full = (kv ? B_VFULL : B_KFULL) + st;
-        if (!wait((kv ? B_VEMPTY : B_KEMPTY) + st, n / S + 1)) {
+        if (!alive || !wait((kv ? B_VEMPTY : B_KEMPTY) + st, n / S + 1)) {
           alive = false;
-          break;
+          continue;
         }
-        const uint32_t bar = smem_u32(&ctl->bar[full]);
+        const uint32_t bar = smem_u32(&ctl->bar[(kv ? B_VFULL : B_KFULL) + st]);
         if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
         ++issued[kv];
         __syncwarp();
-        if (id >= 0) tma_load_4d(base + (kv ? Tc<D>::kV : Tc<D>::kK) + st * Tc<D>::kTile + to, kv ? mv : mk, bar, half * 64, slot, p.h, id);
+        if (id >= 0)
+          tma_load_4d(base + (kv ? Tc<D>::kV : Tc<D>::kK) + st * Tc<D>::kTile + to_smem, kv ? mv : mk, bar, half * 64, slot, p.h, id);
       }
-      if (!alive) break;
       ++n;
       id = next;
     }
   }
+  if (lane == 0) reinterpret_cast<AttnRec *>(a.part)[blockIdx.x] = rec;
   // copies still in flight after an abort land before the CTA retires
   volatile int no_abort = 0;
 #pragma unroll
@@ -431,44 +499,52 @@ __device__ __forceinline__ uint32_t odd_bf16(uint32_t w) {  // mask of the halve
 }
 
 template <int D>
-__device__ __forceinline__ void value_role(const AttnArgs &a, AttnWalk walk, Ctl *ctl, const Waits &wait,
-                                           unsigned char *smem, int w, int lane) {
+__device__ __forceinline__ void value_role(Ctl *ctl, const Waits &wait, unsigned char *smem, int w, int lane) {
   constexpr int S = Tc<D>::kStages, kPieces = D / 8, kStep = 32 / kPieces;  // pieces of a row; rows at a time
   uint32_t n = 0;
-  AttnPart p;
-  for (int part = 0; attn_next<kRows, kKeys, kStart>(a, walk, p); ++part) {
-    const Span sp(a, p);
-    for (int t = p.t0; t < p.t1; ++t, ++n) {
+  Parts parts{ctl, wait};
+  while (const Part *p = parts.next()) {
+    for (int t = p->t0; t < p->t1; ++t, ++n) {
       if (!wait(B_VFULL + n % S, n / S)) return;
-      if (!sp.at_end(t)) {
+      if (!p->at_end(t)) {
         if (lane == 0) mbar_arrive(smem_u32(&ctl->bar[B_VOK + n % S]));
         continue;
       }
-      const int valid = sp.most - t * kKeys, c = lane % kPieces;  // rows up to `valid` hold values
+      const int valid = p->most - t * kKeys, c = lane % kPieces;  // rows up to `valid` hold values
       const uint32_t v = smem_u32(smem) + Tc<D>::kV + n % S * Tc<D>::kTile + (c / 8) * kHalf;
+      auto at = [&](int r0) { return v + sw128_offset(w * 64 + r0 + lane / kPieces, (c % 8) * 8); };
       uint32_t list[2] = {0u, 0u};
-#pragma unroll 4
+      bool odd = false;
+#pragma unroll 8
       for (int r0 = 0; r0 < 64; r0 += kStep) {
-        const int r = w * 64 + r0 + lane / kPieces;
-        const uint32_t at = v + sw128_offset(r, (c % 8) * 8);
         uint4 x;
-        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at) : "memory");
-        uint32_t o[4] = {odd_bf16(x.x), odd_bf16(x.y), odd_bf16(x.z), odd_bf16(x.w)};
-        const bool odd = r < valid && (o[0] | o[1] | o[2] | o[3]);
-        if (r >= valid) o[0] = o[1] = o[2] = o[3] = ~0u;
-        if (odd || r >= valid)
-          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(x.x & ~o[0]), "r"(x.y & ~o[1]),
-                       "r"(x.z & ~o[2]), "r"(x.w & ~o[3]) : "memory");
-        const uint32_t found = __ballot_sync(~0u, odd);
-        if (found)
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at(r0)) : "memory");
+        odd |= w * 64 + r0 + lane / kPieces < valid && (odd_bf16(x.x) | odd_bf16(x.y) | odd_bf16(x.z) | odd_bf16(x.w));
+      }
+      if (valid < w * 64 + 64)
+        for (int r0 = 0; r0 < 64; r0 += kStep)
+          if (w * 64 + r0 + lane / kPieces >= valid)
+            asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(at(r0)), "r"(0u) : "memory");
+      if (__any_sync(~0u, odd)) {  // seldom
+        for (int r0 = 0; r0 < 64; r0 += kStep) {
+          uint4 x;
+          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at(r0)) : "memory");
+          const uint32_t o[4] = {odd_bf16(x.x), odd_bf16(x.y), odd_bf16(x.z), odd_bf16(x.w)};
+          const bool any = o[0] | o[1] | o[2] | o[3];  // (rows behind the end are zero by now)
+          if (any)
+            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at(r0)), "r"(x.x & ~o[0]), "r"(x.y & ~o[1]),
+                         "r"(x.z & ~o[2]), "r"(x.w & ~o[3]) : "memory");
+          const uint32_t found = __ballot_sync(~0u, any);
           for (int y = 0; y < kStep; ++y)
             if ((found >> (y * kPieces)) & ((1u << kPieces) - 1u)) list[(r0 + y) / 32] |= 1u << ((r0 + y) % 32);
+        }
       }
-      if (lane < 2) ctl->odd[part & 3][t - sp.all / kKeys][2 * w + lane] = lane ? list[1] : list[0];
+      if (lane < 2) ctl->odd[parts.at % kParts][t - p->all[0] / kKeys][2 * w + lane] = lane ? list[1] : list[0];
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&ctl->bar[B_VOK + n % S]));
     }
+    parts.done();
   }
 }
 
@@ -484,9 +560,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     ctl->abort = 0;
     for (int b = 0; b < B_COUNT; ++b) {
-      const bool group = (b >= B_Q && b < B_Q + 2) || (b >= B_P && b < B_P + 2);
-      const bool pair = b >= B_VOK && b < B_VOK + kMaxStages;
-      mbar_init(smem_u32(&ctl->bar[b]), group ? 128 : pair ? 2 : 1);
+      const bool group = (b >= B_Q && b < B_Q + 2) || (b >= B_P && b < B_P2 + 2);
+      const bool pair = b >= B_VOK && b < B_VOK + kMaxStages, empty = b >= B_EMPTY;
+      mbar_init(smem_u32(&ctl->bar[b]), group ? 128 : pair ? 2 : empty ? 11 : 1);  // (11 warps are told of a part)
     }
     fence_mbar_init();
     tma_prefetch_desc(&mk);
@@ -500,23 +576,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (tid == 0) {  // the record of the item that this block begins and does not end: in its last part
-    AttnWalk w = walk;
-    AttnPart p;
-    AttnRec rec{0, 0, 0, 0};
-    while (attn_next<kRows, kKeys, kStart>(a, w, p))
-      if (p.parts) rec = AttnRec{p.n, p.h, p.r, p.parts};
-    reinterpret_cast<AttnRec *>(a.part)[blockIdx.x] = rec;
-  }
-  __syncwarp();
   const Waits wait{ctl, args.err};
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;" ::: "memory");
-    softmax_role<D>(a, walk, ctl, wait, smem, warp / 4);
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;" ::: "memory");
+    softmax_role<D>(a, ctl, wait, smem, warp / 4);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;" ::: "memory");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;" ::: "memory");
     if (warp == 8) {
-      product_role<D>(a, walk, ctl, wait, smem);
+      product_role<D>(ctl, wait, smem);
       __syncwarp();
       if (lane == 0) {  // products in flight after an abort
         volatile int no_abort = 0;
@@ -526,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 9) {
       copy_role<D>(args, &mk, &mv, walk, ctl, wait, smem, lane);
     } else {
-      value_role<D>(a, walk, ctl, wait, smem, warp - 10, lane);
+      value_role<D>(ctl, wait, smem, warp - 10, lane);
     }
   }
   __syncwarp();
