@@ -30,6 +30,9 @@ using namespace sm100;
 constexpr int kThreads = 384, kRows = 256, kKeys = 128;
 constexpr int kStart = 4;  // tiles that an item counts for its start and end
 constexpr int kMaxStages = 3;
+// Heads of 64 channels, whose softmax takes longer than their products, hand on the first half of a tile's
+// probabilities before the second is formed.
+template <int D> constexpr bool kSplit = D == 64;
 constexpr float kSlack = 8.f;  // powers of two between a row's maximum and its reference
 constexpr uint32_t kHalf = 16384;  // 128 rows of 64 channels
 
@@ -144,6 +147,43 @@ struct Parts {
 
 // ------------------------------------------------------------------ softmax
 
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0],"
+      " {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,"
+      "%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+// Probabilities of 64 scores relative to m, in pairs of bf16 to w; returns their sum in two parts.
+__device__ __forceinline__ Vec<2> half_of(const float *s, float scale2, float m, uint32_t (&w)[32]) {
+  const float r = m == -INFINITY ? 0.f : -m * scale2;
+  const Vec<2> scale = pair(scale2, scale2), ref = pair(r, r);
+  Vec<2> sum = pair(0.f, 0.f);
+#pragma unroll
+  for (int x = 0; x < 32; ++x) {
+    const Vec<2> e = fma(pair(s[2 * x], s[2 * x + 1]), scale, ref);
+    const float lo = fast_exp2(e.get(0)), hi = fast_exp2(e.get(1));
+    sum = add(sum, pair(lo, hi));
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    w[x] = *reinterpret_cast<const uint32_t *>(&b);
+  }
+  return sum;
+}
+
+__device__ __forceinline__ float max_of(const float (&s)[128]) {
+  float t[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+  for (int c = 4; c < 124; c += 8)
+#pragma unroll
+    for (int x = 0; x < 4; ++x) t[x] = max3(t[x], s[c + 2 * x], s[c + 2 * x + 1]);
+  return max3(max3(t[0], t[1], fmaxf(s[124], s[125])), max3(t[2], t[3], s[126]), s[127]);
+}
+
 template <int D>
 __device__ __forceinline__ void softmax_role(const AttnArgs &a, Ctl *ctl, const Waits &wait, unsigned char *smem, int i) {
   const int grid = gridDim.x, tid = threadIdx.x % 128, qw = tid / 32;
@@ -192,56 +232,57 @@ __device__ __forceinline__ void softmax_role(const AttnArgs &a, Ctl *ctl, const 
 #pragma unroll
       for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, *reinterpret_cast<float(*)[32]>(s + 32 * c));
       tmem_wait_ld();
+      const int nv = key0 + kKeys > all ? lim - key0 : kKeys;  // keys that the row sees
       if (key0 + kKeys > all) {
-        const int nv = lim - key0;
 #pragma unroll
         for (int c = 0; c < 128; ++c) s[c] = c < nv ? s[c] : -INFINITY;
       }
-      float t4[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-      for (int c = 4; c < 124; c += 8)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) t4[x] = max3(t4[x], s[c + 2 * x], s[c + 2 * x + 1]);
-      const float top = max3(max3(t4[0], t4[1], fmaxf(s[124], s[125])), max3(t4[2], t4[3], s[126]), s[127]);
-      if (__any_sync(~0u, top * a.scale2 > m * a.scale2 + kSlack)) {
+      // The first half's probabilities by the reference as it is, beside the search for the maximum; seldom
+      // this is too far above, then the reference moves and they are formed anew.
+      uint32_t w[32];
+      Vec<2> sum = pair(0.f, 0.f);
+      float top;
+      if (j > 0) {
+        sum = half_of(s, a.scale2, m, w);
+        top = max_of(s);
+      } else {
+        top = max_of(s);
+      }
+      if (j == 0 || __any_sync(~0u, top * a.scale2 > m * a.scale2 + kSlack)) {
         const float next = fmaxf(m, top);
         const float f = next == -INFINITY ? 1.f : fast_exp2((m - next) * a.scale2);
         l *= f;
         m = next;
         if (j > 0) {  // (these scores came after the products that O holds)
 #pragma unroll
-          for (int c = 0; c < D; c += 32) {
-            float o[32];
-            tmem_ld32(to + c, o);
+          for (int c = 0; c < D; c += 16) {
+            float o[16];
+            tmem_ld16(to + c, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int x = 0; x < 32; ++x) o[x] *= f;
-            tmem_st16(to + c, *reinterpret_cast<float(*)[16]>(o));
-            tmem_st16(to + c + 16, *reinterpret_cast<float(*)[16]>(o + 16));
+            for (int x = 0; x < 16; ++x) o[x] *= f;
+            tmem_st16(to + c, o);
           }
         }
-      }
-      const float r = m == -INFINITY ? 0.f : -m * a.scale2;
-      const Vec<2> scale = pair(a.scale2, a.scale2), ref = pair(r, r);
-      Vec<2> sum = pair(0.f, 0.f);
+        float again[64];
 #pragma unroll
-      for (int c = 0; c < 128; c += 32) {
-        float w[16];
+        for (int c = 0; c < 2; ++c) tmem_ld32(ts + 32 * c, *reinterpret_cast<float(*)[32]>(again + 32 * c));
+        tmem_wait_ld();
 #pragma unroll
-        for (int x = 0; x < 16; ++x) {
-          const Vec<2> e = fma(pair(s[c + 2 * x], s[c + 2 * x + 1]), scale, ref);
-          const float lo = fast_exp2(e.get(0)), hi = fast_exp2(e.get(1));
-          sum = add(sum, pair(lo, hi));
-          const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-          w[x] = __uint_as_float(*reinterpret_cast<const uint32_t *>(&b));
-        }
-        tmem_st16(ts + c / 2, w);
-        if (c == 32 || c == 96) {  // half of them: their product starts
-          tmem_wait_st();
-          tc_fence_before();
-          mbar_arrive(smem_u32(&ctl->bar[(c == 32 ? B_P : B_P2) + i]));
-        }
+        for (int c = 0; c < 64; ++c) again[c] = c < nv ? again[c] : -INFINITY;
+        sum = half_of(again, a.scale2, m, w);
       }
+      tmem_st32(ts, w);
+      if (kSplit<D>) {  // their product starts
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(smem_u32(&ctl->bar[B_P + i]));
+      }
+      sum = add(sum, half_of(s + 64, a.scale2, m, w));
+      tmem_st32(ts + 32, w);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(smem_u32(&ctl->bar[(kSplit<D> ? B_P2 : B_P) + i]));
       l += sum.get(0) + sum.get(1);
     }
     // The next part's queries come while the last products run, and its first scores are
@@ -402,8 +443,9 @@ __device__ __forceinline__ void product_role(Ctl *ctl, const Waits &wait, unsign
           issue_ts(tb + 256 + 128 * i, tb + 128 * i, v, kIdO, j > 0);
 #pragma unroll
           for (int x = 1; x < kKeys / 32; ++x) issue_ts(tb + 256 + 128 * i, tb + 128 * i + 8 * x, v + x * (2048 >> 4), kIdO, 1u);
-          if (!wait(B_P2 + i, np[i]++)) return;
-          tc_fence_after();
+          if (kSplit<D> && !wait(B_P2 + i, np[i])) return;
+          ++np[i];
+          if (kSplit<D>) tc_fence_after();
 #pragma unroll
           for (int x = kKeys / 32; x < kKeys / 16; ++x)
             issue_ts(tb + 256 + 128 * i, tb + 128 * i + 8 * x, v + x * (2048 >> 4), kIdO, 1u);
@@ -578,10 +620,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const Waits wait{ctl, args.err};
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;" ::: "memory");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;" ::: "memory");
     softmax_role<D>(a, ctl, wait, smem, warp / 4);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;" ::: "memory");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;" ::: "memory");
     if (warp == 8) {
       product_role<D>(ctl, wait, smem);
       __syncwarp();
