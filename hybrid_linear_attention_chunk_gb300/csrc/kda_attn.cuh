@@ -38,6 +38,11 @@ __device__ __forceinline__ float2 *attn_part_ml(const AttnArgs &a, int grid, int
          ((size_t)(block * 2 + slot) * R + row);
 }
 
+// a / b for a >= 0, b > 0; 64-bit divisions take several times as long as 32-bit ones.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return (unsigned long long)(a | b) >> 32 ? a / b : (long long)((unsigned)a / (unsigned)b);
+}
+
 // Keys that rows up to `row` of a sequence may see: the first `end` ones.
 __device__ __forceinline__ int attn_end(const AttnArgs &a, const PagedSeq &s, int row) {
   if (!a.causal) return s.kv;
@@ -73,6 +78,7 @@ __device__ __forceinline__ unsigned long long floor_sum(unsigned long long n, un
 template <int R, int KT> __device__ __forceinline__ long long attn_tiles_before(const AttnArgs &a, const PagedSeq &s, int n) {
   if (n == 0) return 0;
   const int items = attn_items<R>(a, s);
+  if (items == 1) return attn_tiles<R, KT>(a, s, 0);
   if (!a.causal) return (long long)n * attn_tiles<R, KT>(a, s, 0);
   long long sum = 0;
   if (n == items) {  // the last one may have fewer rows
@@ -80,7 +86,7 @@ template <int R, int KT> __device__ __forceinline__ long long attn_tiles_before(
     if (n == 0) return sum;
   }
   const long long m = (long long)a.G * KT, first = (long long)(s.kv - s.len + KT) * a.G + R - 1;
-  const long long low = first >= m ? 0 : min((long long)n, (m - first + R - 1) / R);  // items of one tile at the start
+  const long long low = first >= m ? 0 : min((long long)n, quotient(m - first + R - 1, R));  // items of one tile at the start
   sum += low;
   if (low < n) sum += floor_sum(n - low, m, R, first + low * R);
   return sum;
@@ -126,7 +132,7 @@ __device__ __forceinline__ AttnWalk attn_walk(const AttnArgs &a, int c, int grid
   }
   // no stretch is empty, so that the parts of an item lie in consecutive blocks
   const int blocks = (int)min(total, (long long)grid);
-  const long long begin = c < blocks ? total * c / blocks : 0, end = c < blocks ? total * (c + 1) / blocks : 0;
+  const long long begin = c < blocks ? quotient(total * c, blocks) : 0, end = c < blocks ? quotient(total * (c + 1), blocks) : 0;
   if (begin < end && begin >= upto - sum && begin < upto) {
     // the thread whose sequences hold the first tile: which of them, and how far in
     long long rest = begin - (upto - sum), head = 1;
@@ -137,7 +143,7 @@ __device__ __forceinline__ AttnWalk attn_walk(const AttnArgs &a, int c, int grid
       if (rest < head * a.Hk) break;
       rest -= head * a.Hk;
     }
-    w.h = (int)(rest / head);
+    w.h = (int)quotient(rest, head);
     w.at = rest - w.h * head;  // within the head, for the search below
     w.block = c;
     w.blocks = blocks;
@@ -199,7 +205,7 @@ __device__ __forceinline__ bool attn_next(const AttnArgs &a, AttnWalk &w, AttnPa
     p.parts = 0;
     if (p.t0 == 0 && !p.whole) {
       // up to the block whose stretch holds its last unit; stretch c begins at floor(total c / blocks)
-      p.parts = (int)(((w.at - w.u + units) * w.blocks - 1) / w.total) - w.block + 1;
+      p.parts = (int)quotient((w.at - w.u + units) * w.blocks - 1, w.total) - w.block + 1;
     }
     w.at += take;
     w.left -= take;
@@ -214,6 +220,10 @@ __device__ __forceinline__ bool attn_next(const AttnArgs &a, AttnWalk &w, AttnPa
 __device__ __forceinline__ long long key_offset(const AttnArgs &a, int page_id, int slot, int h) {
   return min(max(page_id, 0), a.pages - 1) * a.cs + ((long long)h * a.page + slot) * a.d;
 }
+
+// Lets the joining kernel's launch begin while this one runs, and waits there for the end of it.
+__device__ __forceinline__ void attn_let_join() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void attn_wait_for_first() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Joins the parts of the items that blocks of `grid` began and did not end.
 cudaError_t launch_attn_join(const AttnArgs &a, int grid, int R, cudaStream_t s);

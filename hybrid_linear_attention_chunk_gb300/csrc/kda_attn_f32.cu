@@ -4,6 +4,7 @@
 // An item of R = 64 or 16 rows runs over the keys in tiles of 64, by 256 threads as
 // 16 x 16.  Scores: a thread has R / 16 rows and 4 keys, both from shared memory as
 // float4.  Outputs: the same rows and d / 16 channels, probabilities through shared memory.
+// The next tile's keys and values are copied meanwhile (16-byte asynchronous copies into a second buffer).
 #include "kda_attn.cuh"
 
 namespace kda {
@@ -13,7 +14,7 @@ constexpr int kKeys = 64, kThreads = 256, kStart = 1;
 
 template <int D, int R> struct F32Smem {
   static constexpr int kRow = D + 4, kProw = kKeys + 4;  // padded: rows of a quarter warp in distinct banks
-  static constexpr size_t kBytes = ((size_t)(R + 2 * kKeys) * kRow + (size_t)R * kProw) * 4;
+  static constexpr size_t kBytes = ((size_t)(R + 4 * kKeys) * kRow + (size_t)R * kProw) * 4;
 };
 
 // acc += p v of the tile.  With kMask keys that the row may not see are left out,
@@ -22,18 +23,25 @@ template <int D, int RT, int V, bool kMask>
 __device__ __forceinline__ void add_values(float (&o)[RT][V], const float *P, const float *Vs, int tx, const int *lim,
                                            int key0) {
   constexpr int kRow = D + 4, kProw = kKeys + 4;
-#pragma unroll 4
-  for (int k = 0; k < kKeys; ++k) {
-    float p[RT], v[V];
+#pragma unroll 2
+  for (int k0 = 0; k0 < kKeys; k0 += 4) {
+    float4 p4[RT];
 #pragma unroll
-    for (int i = 0; i < RT; ++i) p[i] = P[i * kProw + k];
+    for (int i = 0; i < RT; ++i) p4[i] = *reinterpret_cast<const float4 *>(P + i * kProw + k0);
 #pragma unroll
-    for (int j = 0; j < V; ++j) v[j] = Vs[k * kRow + (V >= 4 ? tx * 4 + (j / 4) * 64 + j % 4 : tx * V + j)];
+    for (int x = 0; x < 4; ++x) {
+      const int k = k0 + x;
+      float v[V];
 #pragma unroll
-    for (int i = 0; i < RT; ++i)
-      if (!kMask || key0 + k < lim[i])
+      for (int j = 0; j < V; ++j) v[j] = Vs[k * kRow + (V >= 4 ? tx * 4 + (j / 4) * 64 + j % 4 : tx * V + j)];
 #pragma unroll
-        for (int j = 0; j < V; ++j) o[i][j] = fmaf(p[i], v[j], o[i][j]);
+      for (int i = 0; i < RT; ++i) {
+        const float p = x == 0 ? p4[i].x : x == 1 ? p4[i].y : x == 2 ? p4[i].z : p4[i].w;
+        if (!kMask || key0 + k < lim[i])
+#pragma unroll
+          for (int j = 0; j < V; ++j) o[i][j] = fmaf(p, v[j], o[i][j]);
+      }
+    }
   }
 }
 
@@ -41,8 +49,9 @@ template <int D, int R>
 __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnArgs a) {
   constexpr int kRow = F32Smem<D, R>::kRow, kProw = F32Smem<D, R>::kProw, RT = R / 16, V = D / 16;
   extern __shared__ float4 smem4[];
-  float *Qs = reinterpret_cast<float *>(smem4), *Ks = Qs + R * kRow, *Vs = Ks + kKeys * kRow, *Ps = Vs + kKeys * kRow;
+  float *Qs = reinterpret_cast<float *>(smem4), *KV = Qs + R * kRow, *Ps = KV + 4 * kKeys * kRow;
   const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16, grid = gridDim.x;
+  attn_let_join();
   AttnWalk walk = attn_walk<R, kKeys, kStart, kThreads>(a, blockIdx.x, grid);
   AttnRec rec{0, 0, 0, 0};
   AttnPart p;
@@ -72,22 +81,30 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnArgs a) {
     }
     const int all = attn_end(a, p.s, row0);            // keys that every row sees
     const int most = attn_end(a, p.s, min(row0 + R, rows) - 1);
+    const int32_t *table = a.table + (long long)p.n * a.max_pages;
+    auto copy_tile = [&](int t) {  // keys, then values, of tile t to buffer t % 2
+      float *to = KV + (t & 1) * 2 * kKeys * kRow;
+#pragma unroll
+      for (int i = 0; i < kKeys * (D / 4) / kThreads; ++i) {
+        const int x = i * kThreads + tid, k = x / (D / 4), c = x % (D / 4) * 4, j = t * kKeys + k;
+        const bool there = j < most;
+        const long long off = there ? key_offset(a, table[j / a.page], j % a.page, p.h) + c : 0;
+        const unsigned dst = (unsigned)__cvta_generic_to_shared(to + k * kRow + c);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(kc + off), "r"(there ? 16 : 0) : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + kKeys * kRow * 4), "l"(vc + off),
+                     "r"(there ? 16 : 0) : "memory");
+      }
+    };
+    copy_tile(p.t0);
+    asm volatile("cp.async.commit_group;" ::: "memory");
     for (int t = p.t0; t < p.t1; ++t) {
       const int key0 = t * kKeys;
-      __syncthreads();  // Ks, Vs, Ps are free (and Qs is there, after the next barrier)
-      for (int i = tid; i < kKeys * (D / 4); i += kThreads) {
-        const int k = i / (D / 4), c = i % (D / 4) * 4, j = key0 + k;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-        if (j < most) {
-          const int id = a.table[(long long)p.n * a.max_pages + j / a.page];
-          const long long off = key_offset(a, id, j % a.page, p.h) + c;
-          x = *reinterpret_cast<const float4 *>(kc + off);
-          y = *reinterpret_cast<const float4 *>(vc + off);
-        }
-        *reinterpret_cast<float4 *>(Ks + k * kRow + c) = x;
-        *reinterpret_cast<float4 *>(Vs + k * kRow + c) = y;
-      }
-      __syncthreads();
+      const float *Ks = KV + (t & 1) * 2 * kKeys * kRow, *Vs = Ks + kKeys * kRow;
+      if (t > p.t0) __syncthreads();  // the other buffer and Ps are free
+      if (t + 1 < p.t1) copy_tile(t + 1);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      __syncthreads();  // tile t (and Qs) is there
       float s[RT][4] = {};
 #pragma unroll 2
       for (int c = 0; c < D; c += 4) {

@@ -73,6 +73,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) attn_mma_kernel(const AttnA
   const uint32_t ring = smem_u32(smem) + warp * kStages * kStage;
   const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q), *kc = static_cast<const __nv_bfloat16 *>(a.kc),
                       *vc = static_cast<const __nv_bfloat16 *>(a.vc);
+  attn_let_join();
   AttnWalk walk = attn_walk<R, kKeys, kStart, kThreads>(a, blockIdx.x, grid);
   AttnRec rec{0, 0, 0, 0};
   AttnPart p;

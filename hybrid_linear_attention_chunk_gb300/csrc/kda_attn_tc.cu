@@ -614,6 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_u32(&ctl->tmem), 512);
     tmem_relinquish();
   }
+  attn_let_join();
   const AttnWalk walk = attn_walk<kRows, kKeys, kStart, kThreads>(a, blockIdx.x, grid);  // (with barriers of the whole block)
   tc_fence_before();
   __syncthreads();
