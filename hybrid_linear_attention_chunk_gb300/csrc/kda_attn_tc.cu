@@ -556,17 +556,22 @@ __device__ __forceinline__ void value_role(Ctl *ctl, const Waits &wait, unsigned
       const uint32_t v = smem_u32(smem) + Tc<D>::kV + n % S * Tc<D>::kTile + (c / 8) * kHalf;
       auto at = [&](int r0) { return v + sw128_offset(w * 64 + r0 + lane / kPieces, (c % 8) * 8); };
       uint32_t list[2] = {0u, 0u};
-      bool odd = false;
+      uint32_t top = 0;  // largest magnitudes of either half of the words, as integers: 0x7f80 and above are not finite
 #pragma unroll 8
       for (int r0 = 0; r0 < 64; r0 += kStep) {
         uint4 x;
         asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at(r0)) : "memory");
-        odd |= w * 64 + r0 + lane / kPieces < valid && (odd_bf16(x.x) | odd_bf16(x.y) | odd_bf16(x.z) | odd_bf16(x.w));
+        const uint32_t m = 0x7fff7fffu;
+        top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & m, x.y & m), __vmaxu2(x.z & m, x.w & m)));
       }
-      if (valid < w * 64 + 64)
+      if (valid < w * 64 + 64) {
         for (int r0 = 0; r0 < 64; r0 += kStep)
           if (w * 64 + r0 + lane / kPieces >= valid)
             asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(at(r0)), "r"(0u) : "memory");
+        __syncwarp();
+      }
+      // (what lies behind the end counts here too, and is zero for the closer look)
+      const bool odd = (top & 0xffffu) >= 0x7f80u || (top >> 16) >= 0x7f80u;
       if (__any_sync(~0u, odd)) {  // seldom
         for (int r0 = 0; r0 < 64; r0 += kStep) {
           uint4 x;
