@@ -82,7 +82,7 @@ cudaError_t launch_attn_join(const AttnArgs &a, int grid, int R, cudaStream_t s)
   early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t c = {};
   c.blockDim = dim3(256);
-  c.gridDim = dim3(grid, R > 32 ? 8 : 4);
+  c.gridDim = dim3(grid, R > 32 ? R / 8 : 4);
   c.stream = s;
   c.attrs = &early;
   c.numAttrs = 1;

@@ -677,7 +677,7 @@ bool encode_cache(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap *m, const v
 // Heads of 64 or 128 channels, pages that tiles of 128 keys are made of, or that are made of such
 // tiles, in boxes of at least 8 slots (a swizzled row group).
 bool attn_tc_supports(const AttnArgs &a) {
-  if (a.t != KDA_BF16 || (a.d != 64 && a.d != 128)) return false;
+  if (a.t != KDA_BF16 || (a.d != 64 && a.d != 128) || a.cs >= 1LL << 39) return false;  // (a tensor map's strides end at 2^40 bytes)
   return a.page % 8 == 0 && (a.page < kKeys ? kKeys % a.page == 0 : a.page % kKeys == 0);
 }
 

@@ -521,10 +521,10 @@ BwdBlocks bwd_blocks(int tokens, int Hq, int Hk) {
   return BwdBlocks{(int)(need < q ? need : q), (int)(need < k ? need : k)};
 }
 
-// A kernel's limit of shared memory is the most that any call needs, so that every call sets the same.
-constexpr size_t kMostAngles = kMaxTokens * kMaxDim * sizeof(float);
-template <typename K> cudaError_t allow_shared(K kernel, size_t bytes) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+// Ring and angles fit the shared memory that a kernel may have without asking.
+template <typename T, int kN> constexpr size_t ring_bytes() {
+  static_assert(Ring<T, kN>::kBytes + kMaxTokens * kMaxDim * sizeof(float) + 1024 <= 48 * 1024, "within the default limit");
+  return Ring<T, kN>::kBytes;
 }
 
 template <typename F> cudaError_t for_shape(const RopeArgs &a, F f) {
@@ -560,9 +560,7 @@ cudaError_t launch_rope_fwd(const RopeArgs &a, cudaStream_t s) {
   return for_shape(a, [&](auto t, auto l, auto inter) {
     using T = decltype(t);
     auto kernel = rope_fwd_kernel<T, decltype(l)::value, decltype(inter)::value>;
-    const cudaError_t e = allow_shared(kernel, Ring<T, 1>::kBytes + kMostAngles);
-    if (e != cudaSuccess) return e;
-    kernel<<<grid, kThreads, Ring<T, 1>::kBytes + per * a.rot * sizeof(float), s>>>(a, per);
+    kernel<<<grid, kThreads, ring_bytes<T, 1>() + per * a.rot * sizeof(float), s>>>(a, per);
     return cudaGetLastError();
   });
 }
@@ -574,9 +572,7 @@ cudaError_t launch_kv_append(const RopeArgs &r, const PagedArgs &p, const void *
   return for_shape(r, [&](auto t, auto l, auto inter) {
     using T = decltype(t);
     auto kernel = kv_append_kernel<T, decltype(l)::value, decltype(inter)::value>;
-    const cudaError_t e = allow_shared(kernel, Ring<T, 1>::kBytes + kMostAngles);
-    if (e != cudaSuccess) return e;
-    kernel<<<grid, kThreads, Ring<T, 1>::kBytes + per * r.rot * sizeof(float), s>>>(
+    kernel<<<grid, kThreads, ring_bytes<T, 1>() + per * r.rot * sizeof(float), s>>>(
         r, p, static_cast<const T *>(v), vs, static_cast<T *>(kc), static_cast<T *>(vc), per);
     return cudaGetLastError();
   });
@@ -588,11 +584,9 @@ cudaError_t launch_rope_bwd(const RopeArgs &a, const RopeBwdIo &io, float *ws, c
   const bool weights = io.dqw || io.dkw;
   if (q_blocks) {
     const cudaError_t e = for_shape(a, [&](auto t, auto l, auto inter) {
-      using R = Ring<decltype(t), 2>;
-      auto kernel = rope_bwd_kernel<decltype(t), decltype(l)::value, decltype(inter)::value>;
-      const cudaError_t f = allow_shared(kernel, R::kBytes + kMostAngles);
-      if (f != cudaSuccess) return f;
-      kernel<<<q_blocks + k_blocks, kThreads, R::kBytes + per * a.rot * sizeof(float), s>>>(a, io, per, q_blocks,
+      using T = decltype(t);
+      auto kernel = rope_bwd_kernel<T, decltype(l)::value, decltype(inter)::value>;
+      kernel<<<q_blocks + k_blocks, kThreads, ring_bytes<T, 2>() + per * a.rot * sizeof(float), s>>>(a, io, per, q_blocks,
                                                                                         weights ? ws : nullptr);
       return cudaGetLastError();
     });

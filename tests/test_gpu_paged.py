@@ -287,6 +287,27 @@ def test_captured_and_replayed(kda, dtype, d, page):
             assert torch.equal(bits(got), bits(out)) and torch.equal(bits(gl), bits(lse))
 
 
+def test_two_calls_at_once(kda):
+    # two streams, each call with a workspace of its own
+    cases = [Case([300, 1, 40], [1700, 2000, 41], 8, 2, 128, 64, BF, seed=1), Case([1] * 9, [3000] * 9, 8, 2, 128, 64, BF, seed=2),
+             Case([500], [900], 6, 3, 64, 16, BF, seed=3), Case([70, 3], [400, 300], 4, 2, 32, 16, F32, seed=4)]
+    want = [c.attend(kda)[0] for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(device=DEV) for _ in cases]
+    got = [[c.attend(kda, stream=s)[0] for c, s in zip(cases, streams)] for _ in range(20)]
+    torch.cuda.synchronize()
+    for turn in got:
+        for g, w in zip(turn, want):
+            assert torch.equal(g, w)
+
+
+def test_groups_of_one_sequence_in_every_kernel(kda):
+    # rows that fill 1, 16, 17, 32, 33, 128, 129, 256 and 257 of a head of the cache, by tokens and by shared heads
+    for G, new in ((1, 1), (16, 1), (17, 1), (4, 8), (3, 11), (1, 128), (43, 3), (2, 128), (1, 257)):
+        for d in (64, 128):
+            Case([new, new], [new + 130, new + 1], 2 * G, 2, d, 16, BF, packed=False).check(kda)
+
+
 def test_side_stream(kda):
     c = Case([300, 1, 40], [700, 2000, 41], 8, 2, 128, 64, BF)
     want, _ = c.attend(kda)
