@@ -28,21 +28,17 @@ namespace {
 using namespace sm100;
 
 constexpr int kThreads = 384, kRows = 256, kKeys = 128;
-constexpr int kStart = 4;  // tiles that an item counts for its start and end
-constexpr int kMaxStages = 3;
-// Heads of 64 channels, whose softmax takes longer than their products, hand on the first half of a tile's
-// probabilities before the second is formed.
-template <int D> constexpr bool kSplit = D == 64;
+constexpr int kStart = 3;  // tiles that an item counts for its start and end
+constexpr int kMaxStages = 4;
 constexpr float kSlack = 8.f;  // powers of two between a row's maximum and its reference
 constexpr uint32_t kHalf = 16384;  // 128 rows of 64 channels
 
 enum Bar {
   B_Q = 0,                        // [2] queries in shared memory
   B_S = 2,                        // [2] scores in TMEM
-  B_P = 4,                        // [2] first half of the probabilities in TMEM, outputs rescaled
-  B_P2 = 6,                       // [2] the second half
-  B_O = 8,                        // [2] the part's outputs are complete
-  B_KFULL = 10,                   // [stages] keys landed
+  B_P = 4,                        // [2] probabilities in TMEM, outputs rescaled
+  B_O = 6,                        // [2] the part's outputs are complete
+  B_KFULL = 8,                    // [stages] keys landed
   B_KEMPTY = B_KFULL + kMaxStages,
   B_VFULL = B_KEMPTY + kMaxStages,
   B_VEMPTY = B_VFULL + kMaxStages,
@@ -81,7 +77,7 @@ struct Ctl {
 
 template <int D> struct Tc {
   static constexpr uint32_t kTile = D / 64 * kHalf;
-  static constexpr int kStages = D == 128 ? 2 : 3;
+  static constexpr int kStages = D == 128 ? 2 : 4;
   static constexpr uint32_t kK = 2 * kTile, kV = kK + kStages * kTile, kCtl = kV + kStages * kTile;
   static constexpr uint32_t kBytes = kCtl + sizeof(Ctl) + 1024;
 };
@@ -273,16 +269,11 @@ __device__ __forceinline__ void softmax_role(const AttnArgs &a, Ctl *ctl, const 
         sum = half_of(again, a.scale2, m, w);
       }
       tmem_st32(ts, w);
-      if (kSplit<D>) {  // their product starts
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(smem_u32(&ctl->bar[B_P + i]));
-      }
       sum = add(sum, half_of(s + 64, a.scale2, m, w));
       tmem_st32(ts + 32, w);
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(smem_u32(&ctl->bar[(kSplit<D> ? B_P2 : B_P) + i]));
+      mbar_arrive(smem_u32(&ctl->bar[B_P + i]));
       l += sum.get(0) + sum.get(1);
     }
     // The next part's queries come while the last products run, and its first scores are
@@ -438,17 +429,11 @@ __device__ __forceinline__ void product_role(Ctl *ctl, const Waits &wait, unsign
       for (int i = 0; i < 2; ++i) {
         const int n = i ? n1 : n0;
         if (j < n) {
-          if (!wait(B_P + i, np[i])) return;
+          if (!wait(B_P + i, np[i]++)) return;
           tc_fence_after();
           issue_ts(tb + 256 + 128 * i, tb + 128 * i, v, kIdO, j > 0);
 #pragma unroll
-          for (int x = 1; x < kKeys / 32; ++x) issue_ts(tb + 256 + 128 * i, tb + 128 * i + 8 * x, v + x * (2048 >> 4), kIdO, 1u);
-          if (kSplit<D> && !wait(B_P2 + i, np[i])) return;
-          ++np[i];
-          if (kSplit<D>) tc_fence_after();
-#pragma unroll
-          for (int x = kKeys / 32; x < kKeys / 16; ++x)
-            issue_ts(tb + 256 + 128 * i, tb + 128 * i + 8 * x, v + x * (2048 >> 4), kIdO, 1u);
+          for (int x = 1; x < kKeys / 16; ++x) issue_ts(tb + 256 + 128 * i, tb + 128 * i + 8 * x, v + x * (2048 >> 4), kIdO, 1u);
           if (j == n - 1) issue_commit(bars + 8 * (B_O + i));
         }
         if (i == 1) issue_commit(bars + 8 * (B_VEMPTY + vs));
@@ -607,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     ctl->abort = 0;
     for (int b = 0; b < B_COUNT; ++b) {
-      const bool group = (b >= B_Q && b < B_Q + 2) || (b >= B_P && b < B_P2 + 2);
+      const bool group = (b >= B_Q && b < B_Q + 2) || (b >= B_P && b < B_P + 2);
       const bool pair = b >= B_VOK && b < B_VOK + kMaxStages, empty = b >= B_EMPTY;
       mbar_init(smem_u32(&ctl->bar[b]), group ? 128 : pair ? 2 : empty ? 11 : 1);  // (11 warps are told of a part)
     }
