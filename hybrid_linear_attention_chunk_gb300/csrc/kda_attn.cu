@@ -6,71 +6,119 @@ namespace {
 
 // A row of an item that several blocks hold parts of:
 //     M = max m_p,  l = sum l_p 2^(m_p - M),  out = sum o_p 2^(m_p - M) / l.
-// A block's 8 warps have 8 / W rows at a time: W of them take a row's parts in turn, and the
-// row is the sum of theirs in the warps' order.  Items of few rows may have a part in every block
-// (one long sequence), which W = 8 reads at once; those of many rows have two or three.
-// The kernel is launched as the first one's blocks end (its launch passes meanwhile) and waits for
-// all of it before it reads anything.
-template <int D, typename T, int W>
-__global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a, int grid, int R) {
-  constexpr int V = D >= 32 ? D / 32 : 1, kLanes = D / V, kRows = 8 / W;
-  __shared__ float2 mls[kRows][W];
-  __shared__ float sum[kRows][W][D];
+// Both kernels below are launched as the first one's blocks end (their launch passes meanwhile) and
+// wait for all of it before they read anything.
+struct Joined {
+  float m = -INFINITY, l = 0.f;
+  // Takes in a part; what has been summed counts `f` and the part `g`.
+  __device__ __forceinline__ void add(float2 x, float &f, float &g) {
+    const float top = fmaxf(m, x.x), ref = top == -INFINITY ? 0.f : top;
+    f = exp2f(m - ref);
+    g = exp2f(x.x - ref);
+    l = l * f + x.y * g;
+    m = top;
+  }
+  __device__ __forceinline__ float log_sum() const { return (m + log2f(l)) * 0.6931471805599453f; }
+};
+
+template <typename T, int V> __device__ __forceinline__ void store_row(T *to, const float (&o)[V], float l, bool none) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const float x = none ? 0.f : o[i] / l;
+    if constexpr (sizeof(T) == 2) to[i] = __float2bfloat16_rn(x);
+    else to[i] = x;
+  }
+}
+
+// Items of many rows, with two or three parts: a warp has four rows at once, a lane D / 32 channels of each.
+template <int D, typename T> __global__ void __launch_bounds__(256) attn_join_rows_kernel(const AttnArgs a, int grid, int R) {
+  constexpr int V = D >= 32 ? D / 32 : 1, kLanes = D / V, kN = 4;
   attn_wait_for_first();
   const AttnRec rec = reinterpret_cast<const AttnRec *>(a.part)[blockIdx.x];
   if (rec.parts == 0) return;
   const PagedSeq s = paged_seq(a, rec.n);
-  const int w = threadIdx.x / 32 % W, lane = threadIdx.x % 32, mine = threadIdx.x / 32 / W;
+  const int lane = threadIdx.x % 32, row0 = (blockIdx.y * 8 + threadIdx.x / 32) * kN;
   const int rows = min(R, s.len * a.G - rec.r * R);
-  for (int row0 = blockIdx.y * kRows; row0 < rows; row0 += gridDim.y * kRows) {
-    const int row = row0 + mine, at = rec.r * R + row;
-    float m = -INFINITY, l = 0.f, o[V] = {};
-    if (row < rows) {
-#pragma unroll 4
-      for (int p = w; p < rec.parts; p += W) {
-        const int block = blockIdx.x + p, slot = p == 0;
-        const float2 x = *attn_part_ml(a, grid, block, slot, R, row);
-        const float *src = attn_part_out(a, grid, block, slot, R, row) + lane * V;
-        float v[V];
+  if (row0 >= rows) return;
+  Joined j[kN];
+  float o[kN][V] = {};
+  for (int p = 0; p < rec.parts; ++p) {
+    const int block = blockIdx.x + p, slot = p == 0;
+    float2 x[kN];
+    float v[kN][V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = lane < kLanes ? src[i] : 0.f;
-        const float top = fmaxf(m, x.x), ref = top == -INFINITY ? 0.f : top;
-        const float f = exp2f(m - ref), g = exp2f(x.x - ref);
-        l = l * f + x.y * g;
+    for (int r = 0; r < kN; ++r) {  // (rows behind the last are not written, but lie in the workspace)
+      x[r] = *attn_part_ml(a, grid, block, slot, R, row0 + r);
+      const float *src = attn_part_out(a, grid, block, slot, R, row0 + r) + lane * V;
 #pragma unroll
-        for (int i = 0; i < V; ++i) o[i] = o[i] * f + v[i] * g;
-        m = top;
-      }
+      for (int i = 0; i < V; ++i) v[r][i] = lane < kLanes ? src[i] : 0.f;
     }
-    __syncthreads();  // the rows before are read
-    if (lane == 0) mls[mine][w] = make_float2(m, l);
-    if (lane < kLanes)
 #pragma unroll
-      for (int i = 0; i < V; ++i) sum[mine][w][lane * V + i] = o[i];
-    __syncthreads();
-    if (row >= rows) continue;
-    const float2 *ml = mls[mine];
-    float top = -INFINITY;
+    for (int r = 0; r < kN; ++r) {
+      float f, g;
+      j[r].add(x[r], f, g);
 #pragma unroll
-    for (int i = 0; i < W; ++i) top = fmaxf(top, ml[i].x);
-    const float ref = top == -INFINITY ? 0.f : top;
-    float all = 0.f;
+      for (int i = 0; i < V; ++i) o[r][i] = o[r][i] * f + v[r][i] * g;
+    }
+  }
 #pragma unroll
-    for (int i = 0; i < W; ++i) all += ml[i].y * exp2f(ml[i].x - ref);
-    const int rg = a.by_G(at), head = rec.h * a.G + at - rg * a.G;
+  for (int r = 0; r < kN; ++r) {
+    if (row0 + r >= rows) break;
+    const int at = rec.r * R + row0 + r, rg = a.by_G(at), head = rec.h * a.G + at - rg * a.G;
     const size_t tok = s.bos + rg;
     const bool none = attn_end(a, s, at) == 0;
-    for (int c = threadIdx.x % (32 * W); c < D; c += 32 * W) {
-      float x = 0.f;
+    if (lane < kLanes) store_row(static_cast<T *>(a.o) + tok * a.os + head * D + lane * V, o[r], j[r].l, none);
+    if (a.lse && lane == 0) a.lse[tok * a.Hq + head] = none ? -INFINITY : j[r].log_sum();
+  }
+}
+
+// Items of few rows may have a part in every block (one long sequence): a block has one row at a time, its 8 warps
+// take the parts in turn, and the row is the sum of theirs in the warps' order.
+template <int D, typename T> __global__ void __launch_bounds__(256) attn_join_parts_kernel(const AttnArgs a, int grid, int R) {
+  constexpr int W = 8, V = D >= 32 ? D / 32 : 1, kLanes = D / V;
+  __shared__ float2 ml[W];
+  __shared__ float sums[W][D];
+  attn_wait_for_first();
+  const AttnRec rec = reinterpret_cast<const AttnRec *>(a.part)[blockIdx.x];
+  if (rec.parts == 0) return;
+  const PagedSeq s = paged_seq(a, rec.n);
+  const int w = threadIdx.x / 32, lane = threadIdx.x % 32, rows = min(R, s.len * a.G - rec.r * R);
+  for (int row = blockIdx.y; row < rows; row += gridDim.y) {
+    Joined j;
+    float o[V] = {};
+#pragma unroll 4
+    for (int p = w; p < rec.parts; p += W) {
+      const int block = blockIdx.x + p, slot = p == 0;
+      const float2 x = *attn_part_ml(a, grid, block, slot, R, row);
+      const float *src = attn_part_out(a, grid, block, slot, R, row) + lane * V;
+      float f, g;
+      j.add(x, f, g);
 #pragma unroll
-      for (int i = 0; i < W; ++i) x += sum[mine][i][c] * exp2f(ml[i].x - ref);
-      x = none ? 0.f : x / all;
-      T *out = static_cast<T *>(a.o) + tok * a.os + head * D + c;
-      if constexpr (sizeof(T) == 2) *out = __float2bfloat16_rn(x);
-      else *out = x;
+      for (int i = 0; i < V; ++i) o[i] = o[i] * f + (lane < kLanes ? src[i] : 0.f) * g;
     }
-    if (a.lse && threadIdx.x % (32 * W) == 0)
-      a.lse[tok * a.Hq + head] = none ? -INFINITY : (top + log2f(all)) * 0.6931471805599453f;
+    __syncthreads();  // the row before is read
+    if (lane == 0) ml[w] = make_float2(j.m, j.l);
+    if (lane < kLanes)
+#pragma unroll
+      for (int i = 0; i < V; ++i) sums[w][lane * V + i] = o[i];
+    __syncthreads();
+    if (threadIdx.x >= kLanes) continue;
+    Joined all;
+    float x[V] = {};
+#pragma unroll
+    for (int i = 0; i < W; ++i) all.m = fmaxf(all.m, ml[i].x);
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const float f = exp2f(ml[i].x - (all.m == -INFINITY ? 0.f : all.m));
+      all.l += ml[i].y * f;
+#pragma unroll
+      for (int c = 0; c < V; ++c) x[c] += sums[i][lane * V + c] * f;
+    }
+    const int at = rec.r * R + row, rg = a.by_G(at), head = rec.h * a.G + at - rg * a.G;
+    const size_t tok = s.bos + rg;
+    const bool none = attn_end(a, s, at) == 0;
+    store_row(static_cast<T *>(a.o) + tok * a.os + head * D + lane * V, x, all.l, none);
+    if (a.lse && lane == 0) a.lse[tok * a.Hq + head] = none ? -INFINITY : all.log_sum();
   }
 }
 
@@ -82,13 +130,13 @@ cudaError_t launch_attn_join(const AttnArgs &a, int grid, int R, cudaStream_t s)
   early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t c = {};
   c.blockDim = dim3(256);
-  c.gridDim = dim3(grid, R > 32 ? R / 8 : 4);
+  c.gridDim = dim3(grid, R > 32 ? R / 32 : 4);
   c.stream = s;
   c.attrs = &early;
   c.numAttrs = 1;
-#define KDA_JOIN(D, T)                                                                  \
-  return R > 32 ? cudaLaunchKernelEx(&c, attn_join_kernel<D, T, 1>, a, grid, R)         \
-                : cudaLaunchKernelEx(&c, attn_join_kernel<D, T, 8>, a, grid, R)
+#define KDA_JOIN(D, T)                                                                 \
+  return R > 32 ? cudaLaunchKernelEx(&c, attn_join_rows_kernel<D, T>, a, grid, R)      \
+                : cudaLaunchKernelEx(&c, attn_join_parts_kernel<D, T>, a, grid, R)
 #define KDA_JOINS(T)                    \
   switch (a.d) {                        \
     case 16: KDA_JOIN(16, T);           \

@@ -5,6 +5,10 @@
 // 16 x 16.  Scores: a thread has R / 16 rows and 4 keys, both from shared memory as
 // float4.  Outputs: the same rows and d / 16 channels, probabilities through shared memory.
 // The next tile's keys and values are copied meanwhile (16-byte asynchronous copies into a second buffer).
+//
+// Bound by instruction issue (57 % of the slots, half of them multiply-adds): 1203 tokens of 5 ragged sequences over
+// 700 on average, 6 heads on 3 of 32, 38 us.  Probabilities are read four keys at a time, so that a product
+// of d / 16 channels is not held up by its loads (50 us before).
 #include "kda_attn.cuh"
 
 namespace kda {

@@ -15,6 +15,14 @@
 // A row's outputs stand relative to a reference that follows its running maximum in steps: while the
 // maximum is less than 2^8 above it, probabilities up to 2^8 are as good in bf16 and
 // fp32, and the outputs need not be rescaled.
+//
+// Measured with heads of 128, 32 on 8: 8192 tokens from an empty cache 356 us and 16 us for the
+// join (1.5 PFLOP/s, tensor pipe 66 % active); 2048 tokens over 65536 in 1360-1570 us (1.4-1.65
+// PFLOP/s, by how the card's power cap falls); heads of 64 about 1.0 PFLOP/s, their products of 64
+// channels being issued no faster than those of 128.  A tile of 128 keys takes about 2900 cycles of
+// its products' 2048: the rest is waits between products (a ready one costs about 100 cycles, five a tile),
+// since the two tiles of scores and outputs fill TMEM and no third product can be in line.  A part costs
+// about 12000 cycles beside its tiles: queries, the first softmax, outputs.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <string.h>
