@@ -150,9 +150,15 @@ cudaError_t launch_attn_join(const AttnArgs &a, int grid, int R, cudaStream_t s)
 #undef KDA_JOIN
 }
 
-// The tensor cores' tiles of 128 rows against products of 16 or 32 rows: by the
-// rows of a (sequence, head) on average.
-static bool many_rows(const AttnArgs &a) { return (long long)a.T_total * a.G > 32LL * a.N && attn_tc_supports(a); }
+// The tensor cores' tiles of 128 rows against products of 16 or 32: by the rows of a
+// (sequence, head) on average, us with tiles / with products of few:
+//     heads of 128   128 x 4 rows over 4000   336 / 325     64 x 20 rows over 2000   110 / 118     64 x 64 rows   115 / 220
+//     heads of 64    128 x 4 rows over 4000   275 / 177     128 x 32 rows over 4000  278 / 242     64 x 64 rows    98 / 144
+// A packed batch of one long chunk among single tokens goes by the same: 256 tokens and a chunk of 2048 over 1000
+// 319 / 615 (36 rows on average), 2047 tokens and that chunk 1834 / 1481 (8 rows).
+static bool many_rows(const AttnArgs &a) {
+  return (long long)a.T_total * a.G > (a.d == 128 ? 16LL : 32LL) * a.N && attn_tc_supports(a);
+}
 
 size_t attn_workspace_bytes(const AttnArgs &a) {
   return (a.t == KDA_F32 ? attn_f32_floats(a) : many_rows(a) ? attn_tc_floats(a) : attn_mma_floats(a)) * sizeof(float);

@@ -601,8 +601,9 @@ kda_status kda_qk_rope_bwd(const kda_rope_desc *desc, const void *q, const void 
  *    outside is not stored, and its key and value are read from the nearest
  *    page), so that no call reads or writes outside the tensors.
  *  - A position below 0 (a length below the number of new tokens, as the entries
- *    that pad a batch have with length 0) is not stored, attends to nothing, and
- *    gets zeros and a log-sum of -infinity.
+ *    that pad a batch have with length 0) is not stored, and under the causal mask
+ *    attends to nothing.  A query without any key gets zeros and a log-sum of
+ *    -infinity.
  */
 typedef struct {
   int B;          /* batch; must be 1 when cu_seqlens is given                   */
