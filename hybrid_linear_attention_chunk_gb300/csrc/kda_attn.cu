@@ -160,13 +160,19 @@ static bool many_rows(const AttnArgs &a) {
   return (long long)a.T_total * a.G > (a.d == 128 ? 16LL : 32LL) * a.N && attn_tc_supports(a);
 }
 
+// fp32: up to 8 rows of a (sequence, head) on average run in items of 4 or 8 by warps of their own.
+static bool few_rows(const AttnArgs &a) { return (long long)a.T_total * a.G <= 8LL * a.N; }
+
 size_t attn_workspace_bytes(const AttnArgs &a) {
-  return (a.t == KDA_F32 ? attn_f32_floats(a) : many_rows(a) ? attn_tc_floats(a) : attn_mma_floats(a)) * sizeof(float);
+  const size_t floats = a.t == KDA_F32 ? (few_rows(a) ? attn_f32_few_floats(a) : attn_f32_floats(a))
+                                       : (many_rows(a) ? attn_tc_floats(a) : attn_mma_floats(a));
+  return floats * sizeof(float);
 }
 
 cudaError_t launch_attn(const AttnArgs &a, cudaStream_t s) {
   if (a.T_total == 0) return cudaSuccess;
-  return a.t == KDA_F32 ? launch_attn_f32(a, s) : many_rows(a) ? launch_attn_tc(a, s) : launch_attn_mma(a, s);
+  if (a.t == KDA_F32) return few_rows(a) ? launch_attn_f32_few(a, s) : launch_attn_f32(a, s);
+  return many_rows(a) ? launch_attn_tc(a, s) : launch_attn_mma(a, s);
 }
 
 }  // namespace kda

@@ -228,7 +228,9 @@ __device__ __forceinline__ void attn_wait_for_first() { asm volatile("griddepcon
 // Joins the parts of the items that blocks of `grid` began and did not end.
 cudaError_t launch_attn_join(const AttnArgs &a, int grid, int R, cudaStream_t s);
 
-// kda_attn_f32.cu, kda_attn_mma.cu, kda_attn_tc.cu
+// kda_attn_f32.cu, kda_attn_f32_few.cu, kda_attn_mma.cu, kda_attn_tc.cu
+size_t attn_f32_few_floats(const AttnArgs &a);
+cudaError_t launch_attn_f32_few(const AttnArgs &a, cudaStream_t s);
 size_t attn_f32_floats(const AttnArgs &a);
 cudaError_t launch_attn_f32(const AttnArgs &a, cudaStream_t s);
 size_t attn_mma_floats(const AttnArgs &a);

@@ -41,16 +41,24 @@ __device__ __forceinline__ void add_values(float (&o)[RT][V], const float *P, co
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
         const float p = x == 0 ? p4[i].x : x == 1 ? p4[i].y : x == 2 ? p4[i].z : p4[i].w;
-        if (!kMask || key0 + k < lim[i])
+        if (kMask && key0 + k >= lim[i]) continue;
+        if constexpr (V >= 2) {
 #pragma unroll
-          for (int j = 0; j < V; ++j) o[i][j] = fmaf(p, v[j], o[i][j]);
+          for (int j = 0; j < V; j += 2) {
+            const Vec<2> y = fma(pair(p, p), pair(v[j], v[j + 1]), pair(o[i][j], o[i][j + 1]));
+            o[i][j] = y.get(0);
+            o[i][j + 1] = y.get(1);
+          }
+        } else {
+          o[i][0] = fmaf(p, v[0], o[i][0]);
+        }
       }
     }
   }
 }
 
 template <int D, int R>
-__global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, F32Smem<D, R>::kBytes > 110 * 1024 ? 1 : 2) attn_f32_kernel(const AttnArgs a) {
   constexpr int kRow = F32Smem<D, R>::kRow, kProw = F32Smem<D, R>::kProw, RT = R / 16, V = D / 16;
   extern __shared__ float4 smem4[];
   float *Qs = reinterpret_cast<float *>(smem4), *KV = Qs + R * kRow, *Ps = KV + 4 * kKeys * kRow;
@@ -109,7 +117,12 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnArgs a) {
       asm volatile("cp.async.commit_group;" ::: "memory");
       asm volatile("cp.async.wait_group 1;" ::: "memory");
       __syncthreads();  // tile t (and Qs) is there
-      float s[RT][4] = {};
+      // even channels' products and odd ones' side by side: two to an instruction, as they lie
+      Vec<2> s2[RT][4];
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s2[i][j] = pair(0.f, 0.f);
 #pragma unroll 2
       for (int c = 0; c < D; c += 4) {
         float4 x[RT], y[4];
@@ -121,8 +134,13 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnArgs a) {
         for (int i = 0; i < RT; ++i)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            s[i][j] = fmaf(x[i].x, y[j].x, fmaf(x[i].y, y[j].y, fmaf(x[i].z, y[j].z, fmaf(x[i].w, y[j].w, s[i][j]))));
+            s2[i][j] = fma(pair(x[i].z, x[i].w), pair(y[j].z, y[j].w), fma(pair(x[i].x, x[i].y), pair(y[j].x, y[j].y), s2[i][j]));
       }
+      float s[RT][4];
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[i][j] = s2[i][j].get(0) + s2[i][j].get(1);
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
         float top = m[i];
