@@ -17,8 +17,10 @@ constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kWarpKeys = 8, kKeys = kWarps * kWarpKeys;
 constexpr int kStages = 3;
 constexpr int kStart = 2;   // tiles that an item counts for its start and end
-constexpr int kBlocks = 2;  // of an SM
-constexpr int kGrid = kSms * kBlocks;
+// Blocks of an SM: as many as shared memory holds for wide heads; narrow ones, whose tiles are small, are bound by the
+// warps' own instructions and take twice as many.
+constexpr int blocks_of(int d) { return d >= 64 ? 2 : 4; }
+int grid_of(int d) { return kSms * blocks_of(d); }
 
 template <int D, int NR> struct FewSmem {
   static constexpr int kStage = 2 * kWarpKeys * D;                 // floats: keys, then values
@@ -41,7 +43,7 @@ template <int N> __device__ __forceinline__ void load_row(const float *p, float 
 }
 
 template <int D, int NR>
-__global__ void __launch_bounds__(kThreads, kBlocks) attn_f32_few_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, blocks_of(D)) attn_f32_few_kernel(const AttnArgs a) {
   using Smem = FewSmem<D, NR>;
   constexpr int CH = D / 16, CV = CH < 4 ? CH : 4;           // channels of a lane's scores, in vectors of CV
   constexpr int VC = D >= 32 ? D / 32 : 1, kLanes = D / VC;  // channels of a lane's outputs
@@ -261,16 +263,16 @@ template <int D, int NR> cudaError_t launch_few(const AttnArgs &a, cudaStream_t 
   constexpr size_t bytes = FewSmem<D, NR>::kBytes;
   cudaError_t e = cudaFuncSetAttribute(attn_f32_few_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
   if (e != cudaSuccess) return e;
-  attn_f32_few_kernel<D, NR><<<kGrid, kThreads, bytes, s>>>(a);
+  attn_f32_few_kernel<D, NR><<<grid_of(D), kThreads, bytes, s>>>(a);
   e = cudaGetLastError();
-  return e == cudaSuccess ? launch_attn_join(a, kGrid, NR, s) : e;
+  return e == cudaSuccess ? launch_attn_join(a, grid_of(D), NR, s) : e;
 }
 
 bool four(const AttnArgs &a) { return (long long)a.T_total * a.G <= 4LL * a.N; }
 
 }  // namespace
 
-size_t attn_f32_few_floats(const AttnArgs &a) { return attn_part_floats(kGrid, four(a) ? 4 : 8, a.d); }
+size_t attn_f32_few_floats(const AttnArgs &a) { return attn_part_floats(grid_of(a.d), four(a) ? 4 : 8, a.d); }
 
 cudaError_t launch_attn_f32_few(const AttnArgs &a, cudaStream_t s) {
   const bool f = four(a);

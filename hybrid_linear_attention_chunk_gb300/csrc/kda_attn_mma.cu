@@ -25,7 +25,9 @@ constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kWarpKeys = 16, kKeys = kWarps * kWarpKeys;
 constexpr int kStages = 3;
 constexpr int kStart = 1;  // tiles that an item counts for its start and end
-constexpr int kBlocks = 2;  // of an SM
+// Blocks of an SM: as many as shared memory holds for wide heads; narrow ones, whose tiles are small, are bound by the
+// warps' own instructions and take twice as many.
+constexpr int blocks_of(int d) { return d >= 64 ? 2 : 4; }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool there) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
@@ -70,7 +72,7 @@ template <int D, int MT> struct MmaSmem {
 };
 
 template <int D, int MT>
-__global__ void __launch_bounds__(kThreads, kBlocks) attn_mma_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, blocks_of(D)) attn_mma_kernel(const AttnArgs a) {
   constexpr int R = 16 * MT, kChunks = Tile<D>::kChunks, kCopies = kWarpKeys * kChunks / 32;
   constexpr uint32_t kStage = MmaSmem<D, MT>::kStage;
   extern __shared__ __align__(128) unsigned char smem[];
@@ -312,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) attn_mma_kernel(const AttnA
   if (tid == 0) reinterpret_cast<AttnRec *>(a.part)[blockIdx.x] = rec;
 }
 
-constexpr int kGrid = kSms * kBlocks;
+int grid_of(int d) { return kSms * blocks_of(d); }
 
 // Up to 16 rows of a (sequence, head) on average, one product of 16 rows, else two.
 bool one_tile(const AttnArgs &a) { return (long long)a.T_total * a.G <= 16LL * a.N; }
@@ -321,14 +323,14 @@ template <int D, int MT> cudaError_t launch_mma(const AttnArgs &a, cudaStream_t 
   constexpr uint32_t bytes = MmaSmem<D, MT>::kBytes;
   cudaError_t e = cudaFuncSetAttribute(attn_mma_kernel<D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
   if (e != cudaSuccess) return e;
-  attn_mma_kernel<D, MT><<<kGrid, kThreads, bytes, s>>>(a);
+  attn_mma_kernel<D, MT><<<grid_of(D), kThreads, bytes, s>>>(a);
   e = cudaGetLastError();
-  return e == cudaSuccess ? launch_attn_join(a, kGrid, 16 * MT, s) : e;
+  return e == cudaSuccess ? launch_attn_join(a, grid_of(D), 16 * MT, s) : e;
 }
 
 }  // namespace
 
-size_t attn_mma_floats(const AttnArgs &a) { return attn_part_floats(kGrid, one_tile(a) ? 16 : 32, a.d); }
+size_t attn_mma_floats(const AttnArgs &a) { return attn_part_floats(grid_of(a.d), one_tile(a) ? 16 : 32, a.d); }
 
 cudaError_t launch_attn_mma(const AttnArgs &a, cudaStream_t s) {
   const bool one = one_tile(a);
