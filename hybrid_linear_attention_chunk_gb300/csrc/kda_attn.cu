@@ -160,8 +160,17 @@ static bool many_rows(const AttnArgs &a) {
   return (long long)a.T_total * a.G > (a.d == 128 ? 16LL : 32LL) * a.N && attn_tc_supports(a);
 }
 
-// fp32: up to 8 rows of a (sequence, head) on average run in items of 4 or 8 by warps of their own.
-static bool few_rows(const AttnArgs &a) { return (long long)a.T_total * a.G <= 8LL * a.N; }
+// fp32: few rows of a (sequence, head) on average run in items of 4 or 8 by warps of their own, more in items of 64 by
+// whole blocks: the first reads a key once for 8 rows, from HBM or L2, the second wastes what an item lacks.  64
+// sequences over 4000, us with few / with 64 rows:
+//     heads of 128   12 rows 193 / 481   24 rows 281 / 481   32 rows 366 / 483   48 rows 532 / 483
+//     heads of 64    12 rows 142 / 247   24 rows 222 / 262   32 rows 270 / 247
+//     heads of 32    12 rows 111 / 156   20 rows 157 / 155   32 rows 204 / 154
+//     heads of 16    12 rows 104 / 113   20 rows 145 / 115
+// and 256 single tokens beside a chunk of 512 over 1000 (12 rows) 225 / 589, 167 / 292, 128 / 184, 119 / 134.
+static bool few_rows(const AttnArgs &a) {
+  return (long long)a.T_total * a.G <= (a.d == 128 ? 32LL : a.d == 64 ? 24LL : 16LL) * a.N;
+}
 
 size_t attn_workspace_bytes(const AttnArgs &a) {
   const size_t floats = a.t == KDA_F32 ? (few_rows(a) ? attn_f32_few_floats(a) : attn_f32_floats(a))

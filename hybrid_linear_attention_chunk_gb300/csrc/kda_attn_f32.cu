@@ -1,24 +1,27 @@
 // Attention over a paged cache in fp32, on CUDA cores: there is no fp32 tensor
 // product, and what tf32 drops would show in the 24 bits of the result.
 //
-// An item of R = 64 or 16 rows runs over the keys in tiles of 64, by 256 threads as
-// 16 x 16.  Scores: a thread has R / 16 rows and 4 keys, both from shared memory as
+// An item of 64 rows runs over the keys in tiles of 64, by 256 threads as
+// 16 x 16.  Scores: a thread has 4 rows and 4 keys, both from shared memory as
 // float4.  Outputs: the same rows and d / 16 channels, probabilities through shared memory.
 // The next tile's keys and values are copied meanwhile (16-byte asynchronous copies into a second buffer).
 //
-// Bound by instruction issue (57 % of the slots, half of them multiply-adds): 1203 tokens of 5 ragged sequences over
-// 700 on average, 6 heads on 3 of 32, 38 us.  Probabilities are read four keys at a time, so that a product
-// of d / 16 channels is not held up by its loads (50 us before).
+// Bound by instruction issue: 1203 tokens of 5 ragged sequences over 700 on average, 6 heads on 3 of 32, 43 us with
+// the join.  Probabilities are read four keys at a time, so that a product of d / 16 channels is not held up by its
+// loads (12 us more before); products are of two channels to an instruction.  Few rows leave most of an item's
+// threads without work and run elsewhere (kda_attn_f32_few.cu).
 #include "kda_attn.cuh"
 
 namespace kda {
 namespace {
 
-constexpr int kKeys = 64, kThreads = 256, kStart = 1;
+constexpr int kRows = 64, kKeys = 64, kThreads = 256, kStart = 1;
+// Blocks of an SM, as many as shared memory holds.
+constexpr int f32_blocks(int d) { return d == 128 ? 1 : 2; }
 
-template <int D, int R> struct F32Smem {
+template <int D> struct F32Smem {
   static constexpr int kRow = D + 4, kProw = kKeys + 4;  // padded: rows of a quarter warp in distinct banks
-  static constexpr size_t kBytes = ((size_t)(R + 4 * kKeys) * kRow + (size_t)R * kProw) * 4;
+  static constexpr size_t kBytes = ((size_t)(kRows + 4 * kKeys) * kRow + (size_t)kRows * kProw) * 4;
 };
 
 // acc += p v of the tile.  With kMask keys that the row may not see are left out,
@@ -57,23 +60,23 @@ __device__ __forceinline__ void add_values(float (&o)[RT][V], const float *P, co
   }
 }
 
-template <int D, int R>
-__global__ void __launch_bounds__(kThreads, F32Smem<D, R>::kBytes > 110 * 1024 ? 1 : 2) attn_f32_kernel(const AttnArgs a) {
-  constexpr int kRow = F32Smem<D, R>::kRow, kProw = F32Smem<D, R>::kProw, RT = R / 16, V = D / 16;
+template <int D>
+__global__ void __launch_bounds__(kThreads, f32_blocks(D)) attn_f32_kernel(const AttnArgs a) {
+  constexpr int kRow = F32Smem<D>::kRow, kProw = F32Smem<D>::kProw, RT = kRows / 16, V = D / 16;
   extern __shared__ float4 smem4[];
-  float *Qs = reinterpret_cast<float *>(smem4), *KV = Qs + R * kRow, *Ps = KV + 4 * kKeys * kRow;
+  float *Qs = reinterpret_cast<float *>(smem4), *KV = Qs + kRows * kRow, *Ps = KV + 4 * kKeys * kRow;
   const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16, grid = gridDim.x;
   attn_let_join();
-  AttnWalk walk = attn_walk<R, kKeys, kStart, kThreads>(a, blockIdx.x, grid);
+  AttnWalk walk = attn_walk<kRows, kKeys, kStart, kThreads>(a, blockIdx.x, grid);
   AttnRec rec{0, 0, 0, 0};
   AttnPart p;
-  while (attn_next<R, kKeys, kStart>(a, walk, p)) {
+  while (attn_next<kRows, kKeys, kStart>(a, walk, p)) {
     if (p.parts) rec = AttnRec{p.n, p.h, p.r, p.parts};
     const float *q = static_cast<const float *>(a.q), *kc = static_cast<const float *>(a.kc),
                 *vc = static_cast<const float *>(a.vc);
-    const int rows = p.s.len * a.G, row0 = p.r * R;
+    const int rows = p.s.len * a.G, row0 = p.r * kRows;
     __syncthreads();  // the part before is done with shared memory
-    for (int i = tid; i < R * (D / 4); i += kThreads) {
+    for (int i = tid; i < kRows * (D / 4); i += kThreads) {
       const int r = i / (D / 4), c = i % (D / 4) * 4, at = row0 + r;
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
       if (at < rows)
@@ -92,7 +95,7 @@ __global__ void __launch_bounds__(kThreads, F32Smem<D, R>::kBytes > 110 * 1024 ?
       for (int j = 0; j < V; ++j) o[i][j] = 0.f;
     }
     const int all = attn_end(a, p.s, row0);            // keys that every row sees
-    const int most = attn_end(a, p.s, min(row0 + R, rows) - 1);
+    const int most = attn_end(a, p.s, min(row0 + kRows, rows) - 1);
     const int32_t *table = a.table + (long long)p.n * a.max_pages;
     auto copy_tile = [&](int t) {  // keys, then values, of tile t to buffer t % 2
       float *to = KV + (t & 1) * 2 * kKeys * kRow;
@@ -178,48 +181,41 @@ __global__ void __launch_bounds__(kThreads, F32Smem<D, R>::kBytes > 110 * 1024 ?
       const int head = p.h * a.G + at - a.by_G(at) * a.G;
       const bool none = lim[i] == 0;
       float *out = p.whole ? static_cast<float *>(a.o) + tok * a.os + head * D
-                           : attn_part_out(a, grid, blockIdx.x, p.slot, R, r);
+                           : attn_part_out(a, grid, blockIdx.x, p.slot, kRows, r);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const int c = V >= 4 ? tx * 4 + (j / 4) * 64 + j % 4 : tx * V + j;
         out[c] = p.whole ? (none ? 0.f : o[i][j] / l[i]) : o[i][j];
       }
       if (tx != 0) continue;
-      if (!p.whole) *attn_part_ml(a, grid, blockIdx.x, p.slot, R, r) = make_float2(m[i], l[i]);
+      if (!p.whole) *attn_part_ml(a, grid, blockIdx.x, p.slot, kRows, r) = make_float2(m[i], l[i]);
       else if (a.lse) a.lse[tok * a.Hq + head] = none ? -INFINITY : (m[i] + log2f(l[i])) * 0.6931471805599453f;
     }
   }
   if (tid == 0) reinterpret_cast<AttnRec *>(a.part)[blockIdx.x] = rec;
 }
 
-// Few rows of a (sequence, head) on average run in items of 16, whose products are
-// not four times too many; the kernel is right for any.
-bool few_rows(const AttnArgs &a) { return (long long)a.T_total * a.G <= 24LL * a.N; }
-template <int D, int R> int f32_grid() { return kSms * (F32Smem<D, R>::kBytes > 110 * 1024 ? 1 : 2); }
+template <int D> int f32_grid() { return kSms * f32_blocks(D); }
 
-template <int D, int R> cudaError_t launch_f32(const AttnArgs &a, cudaStream_t s) {
-  const size_t bytes = F32Smem<D, R>::kBytes;
-  cudaError_t e = cudaFuncSetAttribute(attn_f32_kernel<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+template <int D> cudaError_t launch_f32(const AttnArgs &a, cudaStream_t s) {
+  const size_t bytes = F32Smem<D>::kBytes;
+  cudaError_t e = cudaFuncSetAttribute(attn_f32_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
   if (e != cudaSuccess) return e;
-  attn_f32_kernel<D, R><<<f32_grid<D, R>(), kThreads, bytes, s>>>(a);
+  attn_f32_kernel<D><<<f32_grid<D>(), kThreads, bytes, s>>>(a);
   e = cudaGetLastError();
-  return e == cudaSuccess ? launch_attn_join(a, f32_grid<D, R>(), R, s) : e;
+  return e == cudaSuccess ? launch_attn_join(a, f32_grid<D>(), kRows, s) : e;
 }
 
 }  // namespace
 
-size_t attn_f32_floats(const AttnArgs &a) {
-  const int R = few_rows(a) ? 16 : 64;
-  return attn_part_floats(2 * kSms, R, a.d);
-}
+size_t attn_f32_floats(const AttnArgs &a) { return attn_part_floats(2 * kSms, kRows, a.d); }
 
 cudaError_t launch_attn_f32(const AttnArgs &a, cudaStream_t s) {
-  const bool few = few_rows(a);
   switch (a.d) {
-    case 16: return few ? launch_f32<16, 16>(a, s) : launch_f32<16, 64>(a, s);
-    case 32: return few ? launch_f32<32, 16>(a, s) : launch_f32<32, 64>(a, s);
-    case 64: return few ? launch_f32<64, 16>(a, s) : launch_f32<64, 64>(a, s);
-    default: return few ? launch_f32<128, 16>(a, s) : launch_f32<128, 64>(a, s);
+    case 16: return launch_f32<16>(a, s);
+    case 32: return launch_f32<32>(a, s);
+    case 64: return launch_f32<64>(a, s);
+    default: return launch_f32<128>(a, s);
   }
 }
 

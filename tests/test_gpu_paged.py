@@ -308,6 +308,22 @@ def test_groups_of_one_sequence_in_every_kernel(kda):
             Case([new, new], [new + 130, new + 1], 2 * G, 2, d, 16, BF, packed=False).check(kda)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("d", [16, 32, 64, 128])
+@pytest.mark.parametrize("G", [1, 3, 8, 12])
+def test_a_chunk_among_single_tokens(kda, G, d, dtype):
+    # few rows to a head on average, one chunk of many items; sequences that see nothing, values that are not finite
+    new = [1] * 40 + [97] + [1] * 23
+    lens = [(37 * n) % 300 for n in range(40)] + [530] + [(91 * n) % 170 for n in range(23)]
+    c = Case(new, lens, 2 * G, 2, d, 16, dtype, seed=G)
+    c.check(kda)
+    c.check(kda, causal=False)
+    for j, x in ((450, math.inf), (500, math.nan), (529, -math.inf)):
+        page, slot = c.at(40, j)
+        c.vc[page, :, slot, d // 2] = x
+    c.check(kda)
+
+
 def test_side_stream(kda):
     c = Case([300, 1, 40], [700, 2000, 41], 8, 2, 128, 64, BF)
     want, _ = c.attend(kda)
