@@ -6,9 +6,13 @@
 // float4.  Outputs: the same rows and d / 16 channels, probabilities through shared memory.
 // The next tile's keys and values are copied meanwhile (16-byte asynchronous copies into a second buffer).
 //
-// Bound by instruction issue: 1203 tokens of 5 ragged sequences over 700 on average, 6 heads on 3 of 32, 43 us with
-// the join.  Probabilities are read four keys at a time, so that a product of d / 16 channels is not held up by its
-// loads (12 us more before); products are of two channels to an instruction.  Few rows leave most of an item's
+// 2048 tokens over 8192, 8 heads on 2 of 128: 2038 us (38 TFLOP/s, 0.51 of the CUDA cores' rate); 1203 tokens of 5
+// ragged sequences over 700 on average, 6 heads on 3 of 32, 45 us with the join. Bound by loads from shared memory (60 %
+// of its pipe; a load of 16 bytes takes 2 to 4 of its cycles whatever its lanes share) and the waits for them, with 8
+// warps on an SM. 8 rows and 4 keys a thread load a third less: 0 to 12 % faster on long runs with three blocks of 128
+// threads, 17 % slower on the short ragged one. One barrier a tile, a page looked up once a key and warp: 3 % against
+// three and a division for each copy. Probabilities are read four keys at a time, products are of two channels to
+// an instruction. Few rows leave most of an item's
 // threads without work and run elsewhere (kda_attn_f32_few.cu).
 #include "kda_attn.cuh"
 
@@ -99,11 +103,17 @@ __global__ void __launch_bounds__(kThreads, f32_blocks(D)) attn_f32_kernel(const
     const int32_t *table = a.table + (long long)p.n * a.max_pages;
     auto copy_tile = [&](int t) {  // keys, then values, of tile t to buffer t % 2
       float *to = KV + (t & 1) * 2 * kKeys * kRow;
+      long long at[2];  // where the tile's first 32 keys and its last 32 lie, a lane each
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int j = t * kKeys + i * 32 + tid % 32;
+        at[i] = j < most ? key_offset(a, table[j / a.page], j % a.page, p.h) : 0;
+      }
 #pragma unroll
       for (int i = 0; i < kKeys * (D / 4) / kThreads; ++i) {
         const int x = i * kThreads + tid, k = x / (D / 4), c = x % (D / 4) * 4, j = t * kKeys + k;
         const bool there = j < most;
-        const long long off = there ? key_offset(a, table[j / a.page], j % a.page, p.h) + c : 0;
+        const long long off = __shfl_sync(~0u, k & 32 ? at[1] : at[0], k & 31) + c;  // (a warp's keys are in one half)
         const unsigned dst = (unsigned)__cvta_generic_to_shared(to + k * kRow + c);
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(kc + off), "r"(there ? 16 : 0) : "memory");
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + kKeys * kRow * 4), "l"(vc + off),
@@ -111,15 +121,12 @@ __global__ void __launch_bounds__(kThreads, f32_blocks(D)) attn_f32_kernel(const
       }
     };
     copy_tile(p.t0);
-    asm volatile("cp.async.commit_group;" ::: "memory");
     for (int t = p.t0; t < p.t1; ++t) {
       const int key0 = t * kKeys;
       const float *Ks = KV + (t & 1) * 2 * kKeys * kRow, *Vs = Ks + kKeys * kRow;
-      if (t > p.t0) __syncthreads();  // the other buffer and Ps are free
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncthreads();  // tile t (and Qs) is there, and the other buffer is free
       if (t + 1 < p.t1) copy_tile(t + 1);
-      asm volatile("cp.async.commit_group;" ::: "memory");
-      asm volatile("cp.async.wait_group 1;" ::: "memory");
-      __syncthreads();  // tile t (and Qs) is there
       // even channels' products and odd ones' side by side: two to an instruction, as they lie
       Vec<2> s2[RT][4];
 #pragma unroll
@@ -169,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, f32_blocks(D)) attn_f32_kernel(const
 #pragma unroll
         for (int j = 0; j < V; ++j) o[i][j] *= f;
       }
-      __syncthreads();
+      __syncwarp();  // (a half-warp writes and reads its own rows of Ps)
       if (key0 + kKeys <= all) add_values<D, RT, V, false>(o, Ps + ty * RT * kProw, Vs, tx, lim, key0);
       else add_values<D, RT, V, true>(o, Ps + ty * RT * kProw, Vs, tx, lim, key0);
     }
