@@ -847,11 +847,15 @@ def _token_stride(name, t):
     if (st[-1] != 1 and shape[-1] > 1) or (st[-2] != shape[-1] and shape[-2] > 1):
         raise ValueError(f"{name} must have dense heads")
     if len(shape) == 3:
-        return st[0] if shape[0] > 1 else 0
-    B, T = shape[:2]
-    if B > 1 and T > 1 and st[0] != T * st[1]:
-        raise ValueError(f"{name} must have its tokens a fixed distance apart")
-    return st[1] if T > 1 else st[0] if B > 1 else 0
+        several, stride = shape[0] > 1, st[0]
+    else:
+        B, T = shape[:2]
+        if B > 1 and T > 1 and st[0] != T * st[1]:
+            raise ValueError(f"{name} must have its tokens a fixed distance apart")
+        several, stride = B > 1 or T > 1, st[1] if T > 1 else st[0]
+    if several and not stride:  # (the library takes 0 for dense rows)
+        raise ValueError(f"{name} must have a row of its own for each token, not one for all")
+    return stride if several else 0
 
 
 def _rows(name, t, shape, dtype, index):
@@ -1032,6 +1036,8 @@ def _paged_call(shape, heads, dtype, k_cache, v_cache, page_table, lens, cu_seql
             st = c.stride()
             if (st[3] != 1 and d > 1) or (st[2] != d and page > 1) or (st[1] != page * d and Hk > 1):
                 raise ValueError(f"{name} must have dense pages")
+            if pages > 1 and not st[0]:  # (the library takes 0 for dense pages)
+                raise ValueError(f"{name} must have a place of its own for each page")
             strides.append(st[0] if pages > 1 else Hk * page * d)
         stride = strides[0]
         if stride != strides[1]:

@@ -160,3 +160,28 @@ def test_binding_refuses_before_the_library():
                  lambda: kda.kda_paged_attn(q, q[None], q[None], q, q)):
         with pytest.raises(ValueError, match="CUDA device"):
             call()
+
+
+def test_rows_and_pages_that_share_their_memory_are_refused():
+    # (a stride of 0 is dense to the library: one row that stands for all tokens is not)
+    from hybrid_linear_attention_chunk_gb300 import _lib
+    rows = torch.zeros(12, 3, 16)
+    for t, stride in ((rows, 48), (rows[:1].expand(1, 3, 16), 0), (rows[::2], 96), (rows.view(3, 4, 3, 16), 48),
+                      (rows.view(3, 4, 3, 16)[:, :1], 192), (rows.view(1, 12, 3, 16), 48), (rows[:0], 0)):
+        assert _lib._token_stride("t", t) == stride
+    for t in (rows[:1].expand(12, 3, 16), rows[:1, None].expand(3, 4, 3, 16), rows[:3, None].expand(3, 4, 3, 16),
+              rows[:4].expand(3, 4, 3, 16), rows[:1, None].expand(3, 1, 3, 16), rows[:, :1].expand(12, 3, 16),
+              rows[..., :1].expand(12, 3, 16)):
+        with pytest.raises(ValueError):
+            _lib._token_stride("t", t)
+    pages, one = torch.zeros(5, 2, 8, 16), torch.zeros(1, 2, 8, 16)
+    lens, table = torch.zeros(3, dtype=torch.int32), torch.zeros(3, 4, dtype=torch.int32)
+
+    def call(k, v):
+        return _lib._paged_call((6, 4, 16), 4, torch.float32, k, v, table, lens, None, -1)
+    call(pages, pages)
+    call(one.expand(1, 2, 8, 16), one)
+    for k, v in ((one.expand(5, 2, 8, 16), one.expand(5, 2, 8, 16)), (pages, one.expand(5, 2, 8, 16)),
+                 (one.expand(5, 2, 8, 16), pages), (pages[:, :1].expand(5, 2, 8, 16),) * 2):
+        with pytest.raises(ValueError):
+            call(k, v)
