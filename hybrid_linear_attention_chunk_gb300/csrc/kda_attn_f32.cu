@@ -7,13 +7,13 @@
 // The next tile's keys and values are copied meanwhile (16-byte asynchronous copies into a second buffer).
 //
 // 2048 tokens over 8192, 8 heads on 2 of 128: 2038 us (38 TFLOP/s, 0.51 of the CUDA cores' rate); 1203 tokens of 5
-// ragged sequences over 700 on average, 6 heads on 3 of 32, 45 us with the join. Bound by loads from shared memory (60 %
-// of its pipe; a load of 16 bytes takes 2 to 4 of its cycles whatever its lanes share) and the waits for them, with 8
-// warps on an SM. 8 rows and 4 keys a thread load a third less: 0 to 12 % faster on long runs with three blocks of 128
-// threads, 17 % slower on the short ragged one. One barrier a tile, a page looked up once a key and warp: 3 % against
-// three and a division for each copy. Probabilities are read four keys at a time, products are of two channels to
-// an instruction. Few rows leave most of an item's
-// threads without work and run elsewhere (kda_attn_f32_few.cu).
+// ragged sequences over 700 on average, 6 heads on 3 of 32, 45 us with the join.  Bound by latencies, with 8 warps on
+// an SM for heads of 128: shared memory's pipe is 60 % busy (a load of 16 bytes takes 2 to 4 of its cycles whatever
+// its lanes share) and 38 % of the issue slots are taken.  8 rows and 4 keys a thread load a third less: 0 to 12 %
+// faster on long runs with three blocks of 128 threads, 17 % slower on the short ragged one.  One barrier a tile, a
+// page looked up once a key and warp: 3 % against three and a division for each copy.  Probabilities are read four
+// keys at a time, products are of two channels to an instruction.  Few rows leave most of an item's threads without
+// work and run elsewhere (kda_attn_f32_few.cu).
 #include "kda_attn.cuh"
 
 namespace kda {

@@ -10,7 +10,7 @@
 // maxima, sums and outputs are joined through shared memory.
 //
 // For wide heads two blocks of 4 warps with three tiles each keep 96 to 128 KB in flight on an SM.  128 sequences of 8192 on
-// average, 32 heads on 8 of 128: 642 us for the call, 0.98 of the copy's rate; one of 262144, 16 heads on
+// average, 32 heads on 8 of 128: 642 to 649 us for the call, 0.97 of the copy's rate; one of 262144, 16 heads on
 // 4: 84 us for this kernel, 0.94.  One of 4096 takes 10.6 us, of which 2 find the block's stretch, 2 reach its
 // first keys by way of the page table and 1 joins the warps.
 #include "kda_attn.cuh"
