@@ -12,9 +12,10 @@
 // them need not be 0, and values that are not finite are taken out and listed, to be
 // added in the end to the rows that see them.
 //
-// A row's outputs stand relative to a reference that follows its running maximum in steps: while the
-// maximum is less than 2^8 above it, probabilities up to 2^8 are as good in bf16 and
-// fp32, and the outputs need not be rescaled.
+// A row's outputs stand relative to a reference that follows its running maximum in steps: it is set 2^8 above
+// the maximum, and the outputs need not be rescaled until the maximum is above the reference.  Probabilities are then
+// at most 1, as where the reference is the maximum itself, so that values of up to fp32's range over the number of
+// keys do not overflow the outputs; a factor of 2^-8 costs bf16 and fp32 no bits.
 //
 // Measured with heads of 128, 32 on 8: 8192 tokens from an empty cache 356 us and 16 us for the
 // join (1.5 PFLOP/s, tensor pipe 66 % active); 2048 tokens over 65536 in 1360-1570 us (1.4-1.65
@@ -38,7 +39,7 @@ using namespace sm100;
 constexpr int kThreads = 384, kRows = 256, kKeys = 128;
 constexpr int kStart = 3;  // tiles that an item counts for its start and end
 constexpr int kMaxStages = 4;
-constexpr float kSlack = 8.f;  // powers of two between a row's maximum and its reference
+constexpr float kSlack = 8.f;  // powers of two that a row's reference is set above its maximum
 constexpr uint32_t kHalf = 16384;  // 128 rows of 64 channels
 
 enum Bar {
@@ -163,9 +164,9 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
       : "memory");
 }
 
-// Probabilities of 64 scores relative to m, in pairs of bf16 to w; returns their sum in two parts.
+// Probabilities of 64 scores relative to kSlack powers of two above m, in pairs of bf16 to w; returns their sum in two parts.
 __device__ __forceinline__ Vec<2> half_of(const float *s, float scale2, float m, uint32_t (&w)[32]) {
-  const float r = m == -INFINITY ? 0.f : -m * scale2;
+  const float r = m == -INFINITY ? 0.f : fmaf(-m, scale2, -kSlack);
   const Vec<2> scale = pair(scale2, scale2), ref = pair(r, r);
   Vec<2> sum = pair(0.f, 0.f);
 #pragma unroll
@@ -242,7 +243,7 @@ __device__ __forceinline__ void softmax_role(const AttnArgs &a, Ctl *ctl, const 
         for (int c = 0; c < 128; ++c) s[c] = c < nv ? s[c] : -INFINITY;
       }
       // The first half's probabilities by the reference as it is, beside the search for the maximum; seldom
-      // this is too far above, then the reference moves and they are formed anew.
+      // this is above the reference, then the reference moves and they are formed anew.
       uint32_t w[32];
       Vec<2> sum = pair(0.f, 0.f);
       float top;
@@ -355,8 +356,9 @@ __device__ __forceinline__ void softmax_role(const AttnArgs &a, Ctl *ctl, const 
     }
     tc_fence_before();
     if (mine) {
-      if (!whole) *attn_part_ml(a, grid, blockIdx.x, p->slot, kRows, 128 * i + tid) = make_float2(m * a.scale2, l);
-      else if (a.lse) a.lse[tok * a.Hq + head] = none ? -INFINITY : (m * a.scale2 + log2f(l)) * 0.6931471805599453f;
+      if (!whole) *attn_part_ml(a, grid, blockIdx.x, p->slot, kRows, 128 * i + tid) = make_float2(fmaf(m, a.scale2, kSlack), l);
+      else if (a.lse)  // (l in terms of the maximum, so that the logarithm of a sum of few keys is not the small difference of two)
+        a.lse[tok * a.Hq + head] = none ? -INFINITY : fmaf(m, a.scale2, log2f(l * exp2f(kSlack))) * 0.6931471805599453f;
     }
     parts.done();
     p = next;
