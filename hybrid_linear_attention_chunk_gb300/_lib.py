@@ -539,7 +539,10 @@ def _there(call, index, stream, tensors):
 
 
 class _Sized:
-    """A descriptor, the pointer to it that calls take, and sizes that follow from it."""
+    """A descriptor, the pointer to it that calls take, and sizes that follow from it.
+
+    Kept by its fields, which have to be plain numbers: a tensor of one number equals
+    itself after its value has changed."""
 
     def __init__(self, desc):
         self.desc, self.ref, self.sizes = desc, ctypes.byref(desc), {}
@@ -736,7 +739,7 @@ def _norm_call(y, residual, gate, post_norm, post_weight, scale, pre_weight, pos
     rdt = dt if residual is None else residual.dtype
     code = _dt(y)
     sized = _norm_sized(y.numel() // width, width, code, code if residual is None else _dt(residual),
-                        1 if post_norm else 0, post_eps, pre_eps)
+                        1 if post_norm else 0, float(post_eps), float(pre_eps))
     row = shape[-1:]
     return sized, rdt, (_arg("y", y, shape, dt, index), _arg("residual", residual, shape, rdt, index),
                         _arg("gate", gate, shape, dt, index), _arg("post_weight", post_weight, row, torch.float32, index),
@@ -951,7 +954,7 @@ def kda_qk_rope_fwd(q, k=None, positions=None, inv_freq=None, q_weight=None, k_w
         pko, sko = _new(k_out), 0
     else:
         pko, sko = _rows("k_out", k_out, ks, q.dtype, index)
-    sized = _rope_sized(*sizes, rot_scale, 1 if norm else 0, eps, sq, sk, sqo, sko, 0, 0)
+    sized = _rope_sized(*sizes, float(rot_scale), 1 if norm else 0, float(eps), sq, sk, sqo, sko, 0, 0)
     st = lib.kda_qk_rope_fwd(sized.ref, *ins, pqo, pko, _current_stream(index))
     if st:
         _check(st, "kda_qk_rope_fwd")
@@ -986,7 +989,7 @@ def kda_qk_rope_bwd(d_q_out, d_k_out, q, k=None, positions=None, inv_freq=None, 
         (pdq, sdq), (pdk, sdk) = _rows("d_q", get("d_q"), qs, dt, index), _rows("d_k", get("d_k"), ks, dt, index)
         pwq = _arg("d_q_weight", get("d_q_weight"), row, torch.float32, index)
         pwk = _arg("d_k_weight", get("d_k_weight"), row, torch.float32, index)
-    sized = _rope_sized(*sizes, rot_scale, 1 if norm else 0, eps, sq, sk, sqo, sko, sdq, sdk)
+    sized = _rope_sized(*sizes, float(rot_scale), 1 if norm else 0, float(eps), sq, sk, sqo, sko, sdq, sdk)
     if workspace is None and (pwq or pwk):
         workspace = torch.empty(sized.size("kda_qk_rope_bwd_workspace_size"), dtype=torch.uint8, device=q.device)
     ws, ws_bytes = _workspace(workspace, index)
@@ -1084,8 +1087,8 @@ def kda_kv_append(k, v, k_cache, v_cache, page_table, lens, cu_seqlens=None, *, 
     else:
         po, so = _rows("q_out", q_out, qs, dt, index)
     rot, turn = _turn_args(inv_freq, q_weight, k_weight, shape[-1], index)
-    sized = _paged_sized(*sizes, sq, sk, sv, so, cs, rot, _layout(layout), rot_scale, 1 if norm else 0, eps, 1, 1.0,
-                         1 if validate else 0)
+    sized = _paged_sized(*sizes, sq, sk, sv, so, cs, rot, _layout(layout), float(rot_scale), 1 if norm else 0, float(eps),
+                         1, 1.0, 1 if validate else 0)
     st = lib.kda_kv_append(sized.ref, pq, pk, pv, *where, *turn, po, *caches, _current_stream(index))
     if st:
         _check(st, "kda_kv_append")
@@ -1125,7 +1128,7 @@ def kda_paged_attn(q, k_cache, v_cache, page_table, lens, cu_seqlens=None, out=N
     else:
         pl = _arg("lse", lse, shape[:-1], torch.float32, index)
     sized = _paged_sized(*sizes, sq, 0, 0, so, cs, 0, 0, 1.0, 0, 0.0, 1 if causal else 0,
-                         d ** -0.5 if scale is None else scale, 1 if validate else 0)
+                         d ** -0.5 if scale is None else float(scale), 1 if validate else 0)
     if workspace is None:
         workspace = torch.empty(sized.size("kda_paged_attn_workspace_size"), dtype=torch.uint8, device=q.device)
         ws, ws_bytes = _new(workspace), workspace.shape[0]
