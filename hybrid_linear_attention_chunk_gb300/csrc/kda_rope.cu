@@ -87,11 +87,14 @@ template <bool kInter> __device__ __forceinline__ void pack(const Eight &v, uint
   a = make_uint2(bf_pair(p.x, p.y), bf_pair(p.z, p.w));
   b = make_uint2(bf_pair(q.x, q.y), bf_pair(q.z, q.w));
 }
+template <typename T> __device__ __forceinline__ void store_raw(T *row, Piece p, typename Raw<T>::V lo, typename Raw<T>::V hi) {
+  *reinterpret_cast<typename Raw<T>::V *>(row + p.c0) = lo;
+  *reinterpret_cast<typename Raw<T>::V *>(row + p.c1) = hi;
+}
 template <typename T, bool kInter> __device__ __forceinline__ void store8(T *row, Piece p, const Eight &v) {
   typename Raw<T>::V lo, hi;
   pack<kInter>(v, lo, hi);
-  *reinterpret_cast<typename Raw<T>::V *>(row + p.c0) = lo;
-  *reinterpret_cast<typename Raw<T>::V *>(row + p.c1) = hi;
+  store_raw(row, p, lo, hi);
 }
 
 // Rows on their way: kN tensors' pieces of each of kStages rows, in a place of its own for each lane.
@@ -271,7 +274,7 @@ template <typename T, int L, bool kInter, int kTensors> struct Rows {
 #pragma unroll 1
     for (int i = 0; i < Ring<T, 1>::kStages; ++i) issue();
   }
-  // Rows of tensor i: x -> norm, rotation -> y, or a copy without kTurn.
+  // Rows of tensor i: x -> norm, rotation -> y, or a copy without kTurn (of the bits: a NaN keeps its sign and payload).
   template <int i, bool kTurn> __device__ __forceinline__ void run(const RopeArgs &a, const float *weight, const Turn &turn) {
     Eight w;
     if (kTurn) w = load_weight<kInter>(a.norm ? weight : nullptr, p);
@@ -279,14 +282,20 @@ template <typename T, int L, bool kInter, int kTensors> struct Rows {
     const long long step = at.step * t[i].ystep;
     for (int b = 0; b < t[i].H; b += at.step, y += step) {  // (the same count for the whole warp, for its shuffles)
       ring.wait();
-      Eight v = ring.template get<kInter>(got, 0);
-      got = (got + 1) % Ring<T, 1>::kStages;
-      issue();
-      if (kTurn) {
+      const bool there = t[i].y && b + at.h0 < t[i].H;
+      if constexpr (kTurn) {
+        Eight v = ring.template get<kInter>(got, 0);
+        got = (got + 1) % Ring<T, 1>::kStages;
+        issue();
         if (a.norm) v = times(v, times(w, rsqrtf(lane_sum<L>(sum_of(v, v)) * (1.f / (8 * L)) + a.eps)));
         turn.apply(v);
+        if (there) store8<T, kInter>(y, p, v);
+      } else {
+        const typename Raw<T>::V lo = *ring.at(got, 0, 0), hi = *ring.at(got, 0, 1);
+        got = (got + 1) % Ring<T, 1>::kStages;
+        issue();
+        if (there) store_raw(y, p, lo, hi);
       }
-      if (t[i].y && b + at.h0 < t[i].H) store8<T, kInter>(y, p, v);
     }
   }
 };

@@ -636,7 +636,8 @@ typedef struct {
  *   inv_freq      [rot / 2] fp32, or NULL with rot = 0
  *   q_weight, k_weight  [d] fp32, each or NULL (must be NULL without norm)
  *   q_out         as q, written (given exactly when q is); may be q itself
- *   k_cache, v_cache  written at the new tokens' slots only
+ *   k_cache, v_cache  written at the new tokens' slots only; values are copied as
+ *                 they are, bit for bit
  * Two tokens must not share a slot.
  */
 kda_status kda_kv_append(const kda_paged_desc *desc, const void *q, const void *k, const void *v,
