@@ -130,12 +130,16 @@ __device__ __forceinline__ unsigned long long turns_of(float freq) {
   return (unsigned long long)(x * 18446744073709551616.0) + (unsigned long long)(long long)(y * 18446744073709551616.0);
 }
 
-// cos and sin of position * inv_freq, times scale.
+// cos and sin of position * inv_freq, times scale.  The nearest quarter of a turn is taken out while the angle is an
+// integer: what is left, within an eighth, rounds to fp32 by 2^-27 of a half turn at most, where a whole angle would by 2^-25.
 __device__ __forceinline__ float2 angle(unsigned long long turns, int pos, float scale) {
   const unsigned long long f = turns * (unsigned long long)(long long)pos;  // modulo one turn
+  const unsigned q = (unsigned)((f + (1ull << 61)) >> 62);                  // quarters, modulo 4
+  const int rest = (int)((long long)(f - ((unsigned long long)q << 62)) >> 30);  // of 2^34 a turn, -2^31 to 2^31 - 1
   float s, c;
-  sincospif((float)(int)(f >> 32) * 4.656612873077393e-10f, &s, &c);  // 2^-31: in half turns, -1 to 1
-  return make_float2(c * scale, s * scale);
+  sincospif((float)rest * 1.1641532182693481e-10f, &s, &c);  // 2^-33: in half turns, -1/4 to 1/4
+  const float x = q & 1u ? -s : c, y = q & 1u ? c : s;
+  return q & 2u ? make_float2(-x * scale, -y * scale) : make_float2(x * scale, y * scale);
 }
 
 // Angles of nt tokens: rot / 2 cosines of a token, then its sines.  A thread has one pair, of several tokens.

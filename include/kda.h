@@ -520,9 +520,10 @@ kda_status kda_block_norm_bwd(const kda_norm_desc *desc, const void *y, const vo
  *    heads * d.  Hk may be 0, without any k then.
  *  - positions are any int32 (negative ones turn backwards), inv_freq is fp32
  *    and below 2^16 in magnitude.  position * inv_freq is reduced to a part of a
- *    turn in 64-bit fixed point, to 2^-30 of a turn at any position, and its sine
- *    and cosine are those of fp32.  Arithmetic is fp32 and each output is rounded
- *    once.
+ *    turn in 64-bit fixed point, to 2^-30 of a turn at any position; whole quarters
+ *    of a turn are taken out before the rest is rounded to fp32, and the sine and
+ *    cosine are off by 1.5 x 2^-24 at most.  Arithmetic is fp32 and each output is
+ *    rounded once.
  *  - A non-finite value reaches its own row and, in the backward, the weight's
  *    gradient.  Results are deterministic.
  */
