@@ -159,7 +159,8 @@ kda_status validate_paged(const kda_paged_desc *d, const PagedArgs &a, cudaStrea
 }
 
 kda_status attn_args(const kda_paged_desc *d, AttnArgs *a) {
-  if (!(d->scale > 0.f) || !isfinite(d->scale)) return KDA_ERR_RANGE;
+  a->scale2 = d->scale * 1.4426950408889634f;
+  if (!(d->scale > 0.f) || !isfinite(a->scale2)) return KDA_ERR_RANGE;
   a->G = d->Hq / d->Hk;
   // the multiple of 1 / G by 2^(31 + s), 2^s the power of two at or above G, rounded up: it is off by less than
   // G of 2^(31 + s), so that x < 2^31 times it falls short of the next whole number
@@ -167,7 +168,6 @@ kda_status attn_args(const kda_paged_desc *d, AttnArgs *a) {
   while ((1LL << shift) < a->G) ++shift;
   a->g_shift = shift ? shift - 1 : 0;
   a->g_mul = (unsigned)(((1ULL << (31 + shift)) + a->G - 1) / a->G);
-  a->scale2 = d->scale * 1.4426950408889634f;
   a->causal = d->causal != 0;
   a->q = a->kc = a->vc = nullptr;
   a->o = nullptr;

@@ -623,7 +623,7 @@ typedef struct {
   float eps;
   int causal;                /* kda_paged_attn: 1: keys up to the query's own     */
                              /*   position; 0: all lens[n] keys                   */
-  float scale;               /*   on the scores; finite, above 0                  */
+  float scale;               /*   on the scores; above 0, scale / ln 2 finite     */
   int validate;              /* 1: range-check first (synchronises the stream)    */
 } kda_paged_desc;
 
