@@ -867,6 +867,8 @@ def _rows(name, t, shape, dtype, index):
         return None, 0
     if t.dtype is dtype and t.shape == shape and t.get_device() == index:
         return t.data_ptr() or 256, 0 if t.is_contiguous() else _token_stride(name, t)
+    if shape is None:
+        raise ValueError(f"{name} needs the input that it belongs to")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
     if t.shape != shape:
