@@ -1105,7 +1105,9 @@ def kda_paged_attn(q, k_cache, v_cache, page_table, lens, cu_seqlens=None, out=N
     q: [tokens, Hq, d] (or [B, T, Hq, d]); the cache, page_table, lens and
     cu_seqlens as kda_kv_append's; scale: on the scores (None: d^-1/2); causal:
     keys up to the query's own position, else all.  Returns (out, lse): out as
-    q, lse [.., Hq] fp32 with want_lse (or an `lse` buffer), else None."""
+    q, lse [.., Hq] fp32 with want_lse (or an `lse` buffer), else None.  The
+    tensor-core kernel's waits are bounded: load().kda_device_watchdog tells
+    of one that ran out."""
     lib = _lib or load()
     index = q.get_device()
     if _elsewhere(index, stream):

@@ -17,6 +17,9 @@
 // at most 1, as where the reference is the maximum itself, so that values of up to fp32's range over the number of
 // keys do not overflow the outputs; a factor of 2^-8 costs bf16 and fp32 no bits.
 //
+// Every wait on an mbarrier is bounded (2 s).  On a time-out all warps leave their loops, products and copies in flight
+// are waited for, TMEM is freed and a bit is set in a device word the host can read (kda_device_watchdog).
+//
 // Measured with heads of 128, 32 on 8: 8192 tokens from an empty cache 356 us and 16 us for the
 // join (1.5 PFLOP/s, tensor pipe 66 % active); 2048 tokens over 65536 in 1360-1570 us (1.4-1.65
 // PFLOP/s, by how the card's power cap falls); heads of 64 about 1.0 PFLOP/s, their products of 64
@@ -57,6 +60,21 @@ enum Bar {
   B_EMPTY = B_FULL + 4,           // [4] every warp is done with a part
   B_COUNT = B_EMPTY + 4
 };
+
+// What a wait that runs out reports, by what it waited for: bits of KDA_WATCHDOG_PAGED_ATTN.
+enum Code : unsigned {
+  C_QUERIES = 1u << 16,
+  C_SCORES = 1u << 17,
+  C_PROBS = 1u << 18,
+  C_OUTPUTS = 1u << 19,
+  C_KEYS = 1u << 21,
+  C_VALUES = 1u << 22,
+  C_PART = 1u << 28,
+  C_DRAIN = 1u << 29   // what is in flight after an abort
+};
+static_assert((C_QUERIES | C_SCORES | C_PROBS | C_OUTPUTS | C_KEYS | C_VALUES | C_PART | C_DRAIN) == KDA_WATCHDOG_PAGED_ATTN &&
+                  C_QUERIES + C_SCORES + C_PROBS + C_OUTPUTS + C_KEYS + C_VALUES + C_PART + C_DRAIN == KDA_WATCHDOG_PAGED_ATTN,
+              "a bit to each kind of wait, none shared");
 
 // A part, as the copy warp works it out for all: it runs ahead of the others.
 constexpr int kParts = 4;         // told at a time
@@ -101,8 +119,8 @@ struct Waits {
   Ctl *ctl;
   unsigned int *err;
   // By a whole warp; false when any of its lanes gave up.
-  __device__ __forceinline__ bool operator()(int b, uint32_t parity) const {
-    return __all_sync(~0u, mbar_wait(smem_u32(&ctl->bar[b]), parity & 1u, &ctl->abort, err, 1u << (b & 31)));
+  __device__ __forceinline__ bool operator()(int b, uint32_t parity, Code code) const {
+    return __all_sync(~0u, mbar_wait(smem_u32(&ctl->bar[b]), parity & 1u, &ctl->abort, err, code));
   }
 };
 
@@ -139,7 +157,7 @@ struct Parts {
   int at = 0;
   // The next part, or nullptr behind the last one or after an abort.
   __device__ __forceinline__ const Part *next() const {
-    if (!wait(B_FULL + at % kParts, at / kParts)) return nullptr;
+    if (!wait(B_FULL + at % kParts, at / kParts, C_PART)) return nullptr;
     const Part *p = &ctl->part[at % kParts];
     return p->t1 ? p : nullptr;
   }
@@ -231,7 +249,7 @@ __device__ __forceinline__ void softmax_role(const AttnArgs &a, Ctl *ctl, const 
     float m = -INFINITY, l = 0.f;
     for (int j = 0; j < n; ++j) {
       const int key0 = (t0 + j) * kKeys;
-      if (!wait(B_S + i, seen_s++)) return;
+      if (!wait(B_S + i, seen_s++, C_SCORES)) return;
       tc_fence_after();
       float s[128];
 #pragma unroll
@@ -292,7 +310,7 @@ __device__ __forceinline__ void softmax_role(const AttnArgs &a, Ctl *ctl, const 
     const Part *next = ahead.next();
     const bool queries = next && issue_queries(next);
     if (n > 0) {
-      if (!wait(B_O + i, seen_o++)) return;
+      if (!wait(B_O + i, seen_o++, C_OUTPUTS)) return;
       tc_fence_after();
     }
     if (queries) land_queries();
@@ -425,21 +443,21 @@ __device__ __forceinline__ void product_role(Ctl *ctl, const Waits &wait, unsign
   while (const Part *p = parts.next()) {
     const int count = p->t1 - p->t0, n0 = p->count[0], n1 = p->count[1];
     parts.done();
-    if (n0 > 0 && !wait(B_Q, nq[0]++)) return;
-    if (n1 > 0 && !wait(B_Q + 1, nq[1]++)) return;
-    if (!wait(B_KFULL + ks, kp)) return;
+    if (n0 > 0 && !wait(B_Q, nq[0]++, C_QUERIES)) return;
+    if (n1 > 0 && !wait(B_Q + 1, nq[1]++, C_QUERIES)) return;
+    if (!wait(B_KFULL + ks, kp, C_KEYS)) return;
     tc_fence_after();
     if (n0 > 0) scores(0);
     if (n1 > 0) scores(1);
     keys_done();
-    if (!wait(B_VOK + vs, vp)) return;
+    if (!wait(B_VOK + vs, vp, C_VALUES)) return;
     for (int j = 0; j < count; ++j) {
       const uint32_t v = uniform(((base + Tc<D>::kV + vs * Tc<D>::kTile) >> 4) | (kHalf >> 4) << 16);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int n = i ? n1 : n0;
         if (j < n) {
-          if (!wait(B_P + i, np[i]++)) return;
+          if (!wait(B_P + i, np[i]++, C_PROBS)) return;
           tc_fence_after();
           issue_ts(tb + 256 + 128 * i, tb + 128 * i, v, kIdO, j > 0);
 #pragma unroll
@@ -447,13 +465,13 @@ __device__ __forceinline__ void product_role(Ctl *ctl, const Waits &wait, unsign
           if (j == n - 1) issue_commit(bars + 8 * (B_O + i));
         }
         if (i == 1) issue_commit(bars + 8 * (B_VEMPTY + vs));
-        if (j + 1 < count && i == 0 && !wait(B_KFULL + ks, kp)) return;
+        if (j + 1 < count && i == 0 && !wait(B_KFULL + ks, kp, C_KEYS)) return;
         if (j + 1 < n) scores(i);
       }
       if (++vs == S) vs = 0, vp ^= 1u;
       if (j + 1 < count) {
         keys_done();
-        if (!wait(B_VOK + vs, vp)) return;  // (while the last products run)
+        if (!wait(B_VOK + vs, vp, C_VALUES)) return;  // (while the last products run)
       }
     }
   }
@@ -474,7 +492,7 @@ __device__ __forceinline__ void copy_role(const TcArgs &args, const CUtensorMap 
   AttnPart p;
   for (int at = 0; alive; ++at) {
     const bool more = attn_next<kRows, kKeys, kStart>(a, walk, p);
-    if (!wait(B_EMPTY + at % kParts, at / kParts + 1)) break;
+    if (!wait(B_EMPTY + at % kParts, at / kParts + 1, C_PART)) break;
     const int rows = p.s.len * a.G, row0 = p.r * kRows, most = more ? attn_end(a, p.s, min(row0 + kRows, rows) - 1) : 0;
     if (lane == 0) {
       Part *to = &ctl->part[at % kParts];
@@ -505,7 +523,7 @@ __device__ __forceinline__ void copy_role(const TcArgs &args, const CUtensorMap 
       const int next = page_of(t + 1);
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
-        if (!alive || !wait((kv ? B_VEMPTY : B_KEMPTY) + st, n / S + 1)) {
+        if (!alive || !wait((kv ? B_VEMPTY : B_KEMPTY) + st, n / S + 1, kv ? C_VALUES : C_KEYS)) {
           alive = false;
           continue;
         }
@@ -526,7 +544,7 @@ __device__ __forceinline__ void copy_role(const TcArgs &args, const CUtensorMap 
 #pragma unroll
   for (int kv = 0; kv < 2; ++kv)
     for (uint32_t x = issued[kv] > S ? issued[kv] - S : 0; x < issued[kv]; ++x)
-      mbar_wait(smem_u32(&ctl->bar[(kv ? B_VFULL : B_KFULL) + x % S]), x / S & 1, &no_abort, args.err, 1u << 31);
+      mbar_wait(smem_u32(&ctl->bar[(kv ? B_VFULL : B_KFULL) + x % S]), x / S & 1, &no_abort, args.err, C_DRAIN);
 }
 
 // ------------------------------------------------------------ values at the end
@@ -542,7 +560,7 @@ __device__ __forceinline__ void value_role(Ctl *ctl, const Waits &wait, unsigned
   Parts parts{ctl, wait};
   while (const Part *p = parts.next()) {
     for (int t = p->t0; t < p->t1; ++t, ++n) {
-      if (!wait(B_VFULL + n % S, n / S)) return;
+      if (!wait(B_VFULL + n % S, n / S, C_VALUES)) return;
       if (!p->at_end(t)) {
         if (lane == 0) mbar_arrive(smem_u32(&ctl->bar[B_VOK + n % S]));
         continue;
@@ -631,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) {  // products in flight after an abort
         volatile int no_abort = 0;
         mma_commit(smem_u32(&ctl->bar[B_DRAIN]));
-        mbar_wait(smem_u32(&ctl->bar[B_DRAIN]), 0, &no_abort, args.err, 1u << B_DRAIN);
+        mbar_wait(smem_u32(&ctl->bar[B_DRAIN]), 0, &no_abort, args.err, C_DRAIN);
       }
     } else if (warp == 9) {
       copy_role<D>(args, &mk, &mv, walk, ctl, wait, smem, lane);

@@ -133,6 +133,9 @@ enum Bar : int {
   B_M1 = 0, B_M7, B_VFULL, B_GFULL, B_QK0, B_QK1, B_TB, B_M4,
   B_M56, B_M7S, B_L2, B_TD_C, B_TD_S, B_OG, B_OPS0, B_OPS1, B_COUNT
 };
+// Time-out codes: a bit for each barrier, and 20, 23 .. 27 for what is in flight after an abort.
+static_assert((((1u << B_COUNT) - 1u) | 1u << 20 | 0x1fu << 23) == KDA_WATCHDOG_PREFILL &&
+                  (KDA_WATCHDOG_PREFILL & KDA_WATCHDOG_PAGED_ATTN) == 0, "bits of this kernel alone");
 // B_OPS0 + (c & 1): chunk c's operands are in place (arrived once per chunk of
 // that parity, so a barrier runs at most one phase ahead of its waiter: the
 // next arrival on it needs the q/k copy that is issued only once chunk c's

@@ -660,7 +660,8 @@ kda_status kda_kv_append(const kda_paged_desc *desc, const void *q, const void *
  * Scores, the softmax's maxima and sums and the output sums are fp32; bf16
  * probabilities are rounded to bf16 for their product with the values.  A
  * non-finite key or value reaches the queries that attend to it, and no others.
- * Results are deterministic.
+ * Results are deterministic.  Where a bounded wait inside the kernel runs out the
+ * outputs are undefined, and kda_device_watchdog says so.
  */
 kda_status kda_paged_attn_workspace_size(const kda_paged_desc *desc, size_t *bytes);
 kda_status kda_paged_attn(const kda_paged_desc *desc, const void *q, const void *k_cache, const void *v_cache,
@@ -674,12 +675,17 @@ const char *kda_status_string(kda_status status);
  * or "" (never NULL). */
 const char *kda_last_cuda_error(void);
 
-/* The tensor-core prefill bounds every wait on its internal barriers (2 s).
- * A wait that runs out makes the kernel abandon its work, release what it
- * holds and OR a bit into a per-device word; the outputs of that call are
- * then undefined.  This call waits for the current device to go idle
- * (cudaDeviceSynchronize), stores that word in *flags (0 = no time-out since
- * it was last cleared) and clears it when `clear` is non-zero. */
+/* The tensor-core prefill and the tensor-core kernel of kda_paged_attn (bf16,
+ * many query rows to a head of the cache) bound every wait on their internal
+ * barriers (2 s).  A wait that runs out makes the kernel abandon its work,
+ * release what it holds and OR a bit into a per-device word; the outputs of that
+ * call, which has returned KDA_OK by then, are undefined.  This call waits for the
+ * current device to go idle (cudaDeviceSynchronize), stores that word in *flags
+ * (0 = no time-out since it was last cleared) and clears it when `clear` is
+ * non-zero.  Bits within KDA_WATCHDOG_PREFILL are of the prefill, bits within
+ * KDA_WATCHDOG_PAGED_ATTN of the attention. */
+#define KDA_WATCHDOG_PREFILL 0x0f90ffffu
+#define KDA_WATCHDOG_PAGED_ATTN 0x306f0000u
 kda_status kda_device_watchdog(unsigned int *flags, int clear);
 
 /* Size of the library's built-in scratch array used by kda_chunk_fwd_noalloc:
