@@ -659,7 +659,9 @@ kda_status kda_kv_append(const kda_paged_desc *desc, const void *q, const void *
  *             another call in flight; or NULL: allocated stream-ordered
  * Scores, the softmax's maxima and sums and the output sums are fp32; bf16
  * probabilities are rounded to bf16 for their product with the values.  A
- * non-finite key or value reaches the queries that attend to it, and no others.
+ * non-finite key or value reaches the queries that attend to it, and no others; an
+ * infinite value comes out as an infinity, or as NaN where its probability or a
+ * factor of the running maximum underflows (0 times infinity).
  * Results are deterministic.  Where a bounded wait inside the kernel runs out the
  * outputs are undefined, and kda_device_watchdog says so.
  */
