@@ -30,7 +30,9 @@ template <typename T, int V> __device__ __forceinline__ void store_row(T *to, co
   }
 }
 
-// Items of many rows, with two or three parts: a warp has four rows at once, a lane D / 32 channels of each.
+// Items of many rows: a warp has four rows at once, a lane D / 32 channels of each, and goes over the parts one after the
+// other.  These are two or three where a call has more items than blocks (8192 tokens, 32 heads on 8 of 128: 15 us), and up
+// to one for each block where it has few: 32 rows of one head over 262144 keys are 152 parts, 80 of the call's 121 us.
 template <int D, typename T> __global__ void __launch_bounds__(256) attn_join_rows_kernel(const AttnArgs a, int grid, int R) {
   constexpr int V = D >= 32 ? D / 32 : 1, kLanes = D / V, kN = 4;
   attn_wait_for_first();
@@ -154,8 +156,11 @@ cudaError_t launch_attn_join(const AttnArgs &a, int grid, int R, cudaStream_t s)
 // (sequence, head) on average, us with tiles / with products of few:
 //     heads of 128   128 x 4 rows over 4000   336 / 325     64 x 20 rows over 2000   110 / 118     64 x 64 rows   115 / 220
 //     heads of 64    128 x 4 rows over 4000   275 / 177     128 x 32 rows over 4000  278 / 242     64 x 64 rows    98 / 144
-// A packed batch of one long chunk among single tokens goes by the same: 256 tokens and a chunk of 2048 over 1000
-// 319 / 615 (36 rows on average), 2047 tokens and that chunk 1834 / 1481 (8 rows).
+// A packed batch of one long chunk among single tokens goes by the same, since only the device knows its lengths: 256
+// tokens and a chunk of 2048 over 1000 319 / 615 (36 rows on average), 2047 tokens and that chunk 1834 / 1481 (8 rows).
+// Over short contexts, where the chunk outweighs the single tokens, the average misses it: 2000 tokens (4 rows each) over
+// 16, 256 and 1000 beside a chunk of 4096 from an empty cache (12 rows on average) take 838 / 1620, 1230 / 1615 and 1791 /
+// 2158 with heads of 128, 792 / 1256, 1207 / 1158 and 1688 / 1587 with heads of 64.
 static bool many_rows(const AttnArgs &a) {
   return (long long)a.T_total * a.G > (a.d == 128 ? 16LL : 32LL) * a.N && attn_tc_supports(a);
 }
@@ -168,6 +173,8 @@ static bool many_rows(const AttnArgs &a) {
 //     heads of 32    12 rows 111 / 156   20 rows 157 / 155   32 rows 204 / 154
 //     heads of 16    12 rows 104 / 113   20 rows 145 / 115
 // and 256 single tokens beside a chunk of 512 over 1000 (12 rows) 225 / 589, 167 / 292, 128 / 184, 119 / 134.
+// A third form, items of 16 rows by whole blocks, was faster for narrow heads of 9 to 16 rows (12 rows: heads of 32 96 us,
+// of 16 65) and slower for wide ones (354 against 193), and is not kept.
 static bool few_rows(const AttnArgs &a) {
   return (long long)a.T_total * a.G <= (a.d == 128 ? 32LL : a.d == 64 ? 24LL : 16LL) * a.N;
 }

@@ -18,6 +18,8 @@
 
 namespace kda {
 
+// SMs of the card: the grids, and with them the workspaces' sizes, are whole multiples.  (With fewer SMs blocks would run
+// in a second wave, with the same results.)
 constexpr int kSms = 152;
 
 // The joining record of a block: the item that it begins and does not end.
@@ -57,7 +59,8 @@ template <int R> __device__ __forceinline__ int attn_items(const AttnArgs &a, co
 template <int R, int KT> __device__ __forceinline__ int attn_tiles(const AttnArgs &a, const PagedSeq &s, int r) {
   return max(1, (attn_end(a, s, min((r + 1) * R, s.len * a.G) - 1) + KT - 1) / KT);
 }
-// sum of floor((k i + b) / m) over 0 <= i < n, for k, b >= 0, by Euclid's algorithm on (k, m).
+// sum of floor((k i + b) / m) over 0 <= i < n, for k, b >= 0, by Euclid's algorithm on (k, m): whole multiples come out of
+// the sum, and what is left is the sum over the exchanged k and m (Graham, Knuth, Patashnik, Concrete Mathematics, 3.5).
 __device__ __forceinline__ unsigned long long floor_sum(unsigned long long n, unsigned long long m, unsigned long long k,
                                                         unsigned long long b) {
   unsigned long long sum = 0;

@@ -1,12 +1,13 @@
-// Attention over a paged cache in fp32, on CUDA cores: there is no fp32 tensor
-// product, and what tf32 drops would show in the 24 bits of the result.
+// Attention over a paged cache in fp32, on CUDA cores.  Tensor cores have no fp32 product, and a single tf32 one would
+// show in the 24 bits of the result; operands split in two tf32 parts each, three products to one, would keep them (as
+// the delta rule's backward does), at a rate that is above that of the CUDA cores.  This kernel does not do that.
 //
 // An item of 64 rows runs over the keys in tiles of 64, by 256 threads as
 // 16 x 16.  Scores: a thread has 4 rows and 4 keys, both from shared memory as
 // float4.  Outputs: the same rows and d / 16 channels, probabilities through shared memory.
 // The next tile's keys and values are copied meanwhile (16-byte asynchronous copies into a second buffer).
 //
-// 2048 tokens over 8192, 8 heads on 2 of 128: 2038 us (38 TFLOP/s, 0.51 of the CUDA cores' rate); 1203 tokens of 5
+// 2048 tokens over 8192, 8 heads on 2 of 128: 2030 us (38 TFLOP/s, 0.51 of the CUDA cores' rate); 1203 tokens of 5
 // ragged sequences over 700 on average, 6 heads on 3 of 32, 45 us with the join.  Bound by latencies, with 8 warps on
 // an SM for heads of 128: shared memory's pipe is 60 % busy (a load of 16 bytes takes 2 to 4 of its cycles whatever
 // its lanes share) and 38 % of the issue slots are taken.  8 rows and 4 keys a thread load a third less: 0 to 12 %
@@ -19,7 +20,11 @@
 namespace kda {
 namespace {
 
-constexpr int kRows = 64, kKeys = 64, kThreads = 256, kStart = 1;
+constexpr int kRows = 64, kKeys = 64, kThreads = 256;
+// Tiles that an item counts for its start and end.  0 and 2 against 1: 5 ragged sequences, 6 heads on 3 of 32, 44 and 46
+// against 41 us; 4 x 1024 tokens, 8 heads on 2 of 128, 291 and 287 against 276; 20 x 100 over 300, of 64, 66 and 73 against
+// 73.
+constexpr int kStart = 1;
 // Blocks of an SM, as many as shared memory holds.
 constexpr int f32_blocks(int d) { return d == 128 ? 1 : 2; }
 

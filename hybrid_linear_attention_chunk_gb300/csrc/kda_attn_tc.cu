@@ -20,11 +20,16 @@
 // Every wait on an mbarrier is bounded (2 s).  On a time-out all warps leave their loops, products and copies in flight
 // are waited for, TMEM is freed and a bit is set in a device word the host can read (kda_device_watchdog).
 //
-// Measured with heads of 128, 32 on 8: 8192 tokens from an empty cache 356 us and 16 us for the
-// join (1.5 PFLOP/s, tensor pipe 66 % active); 2048 tokens over 65536 in 1360-1570 us (1.4-1.65
-// PFLOP/s, by how the card's power cap falls); heads of 64 about 1.0 PFLOP/s, their products of 64
-// channels being issued no faster than those of 128.  A tile of 128 keys takes about 2900 cycles of
-// its products' 2048: the rest is waits between products (a ready one costs about 100 cycles, five a tile),
+// P is rounded to bf16 since both operands of the product have one type and V is bf16: 2^-8 of each probability at most,
+// while their sum is of the unrounded ones.  The outputs' error against fp64 grows by it from 0.0016, their own rounding, to
+// 0.0017-0.0025.  A second product with what the rounding leaves out would make the two products three.
+//
+// Measured with heads of 128, 32 on 8: 8192 tokens from an empty cache 371 us and 16 us for the
+// join, 380 together (1.45 PFLOP/s, tensor pipe 67 % active); 2048 tokens over 65536 in 1440 us (tensor pipe 76 %
+// active) while the card's clock holds and 1650 us (1.36 PFLOP/s) when it runs for seconds, at 1.37 kW and 1500 of 2070 MHz.
+// 8192 tokens with heads of 64 take 335 us (0.82 PFLOP/s, tensor pipe 37 % active), 2048 over 65536 1135 us (1.0
+// PFLOP/s): their products of 64 channels are issued no faster than those of 128.  A tile of 128 keys takes about 2900
+// cycles, its products 2048 of them: the rest is waits between products (a ready one costs about 100 cycles, five a tile),
 // since the two tiles of scores and outputs fill TMEM and no third product can be in line.  A part costs
 // about 12000 cycles beside its tiles: queries, the first softmax, outputs.
 #include <cuda.h>
@@ -40,7 +45,9 @@ namespace {
 using namespace sm100;
 
 constexpr int kThreads = 384, kRows = 256, kKeys = 128;
-constexpr int kStart = 3;  // tiles that an item counts for its start and end
+// Tiles that an item counts for its start and end, about 12000 cycles to a tile's 2900.  2 and 4 against 3: 8192 tokens 377
+// and 375 against 372 us, 20 x 300 tokens over 500 116 and 112 against 113, the mixed batch of heads of 64 the same.
+constexpr int kStart = 3;
 constexpr int kMaxStages = 4;
 constexpr float kSlack = 8.f;  // powers of two that a row's reference is set above its maximum
 constexpr uint32_t kHalf = 16384;  // 128 rows of 64 channels

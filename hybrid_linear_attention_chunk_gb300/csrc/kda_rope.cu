@@ -19,8 +19,8 @@
 //
 // Bound by HBM and, close behind, by instruction issue (71 % of the slots), which is why
 // channels are taken two to an fp32 instruction.  32768 tokens x 40 heads of 128 in bf16:
-// forward 110 us (0.90 of the copy's rate on its bytes), backward 164 us (0.90) and 8 us for
-// the weights' sums; append of 16384 tokens x (32 + 2 x 8) heads 69 us (0.86).  Rings of 16 rows
+// forward 112 us (0.88 of the copy's rate on its bytes), backward 166 us (0.89) and 8 us for
+// the weights' sums; append of 16384 tokens x (32 + 2 x 8) heads 71 us (0.84).  Rings of 16 rows
 // instead of 8 leave room for fewer blocks (159 us forward); blocks of 8 tokens instead of
 // 16 take the backward from 172 to 190 us.
 #include <type_traits>
@@ -33,7 +33,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxTokens = 16;   // of a block
-constexpr int kSms = 152, kBwdBlocks = kSms * 32;
+constexpr int kSms = 152, kBwdBlocks = kSms * 32;  // of the card; the backward's blocks, which its workspace's size goes by
 
 // Row pieces: 4 channels at c0 and 4 at c1.
 struct Piece {
