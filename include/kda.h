@@ -657,7 +657,8 @@ kda_status kda_kv_append(const kda_paged_desc *desc, const void *q, const void *
  *             over other keys
  *   workspace kda_paged_attn_workspace_size bytes, 16-byte aligned, not in use by
  *             another call in flight; or NULL: allocated stream-ordered
- * Scores, the softmax's maxima and sums and the output sums are fp32; bf16
+ * Scores, the softmax's maxima and sums and the output sums are fp32, the sums
+ * being of probabilities relative to a row's largest, at most 1 each; bf16
  * probabilities are rounded to bf16 for their product with the values.  A
  * non-finite key or value reaches the queries that attend to it, and no others; an
  * infinite value comes out as an infinity, or as NaN where its probability or a
