@@ -22,7 +22,7 @@
 //
 // P is rounded to bf16 since both operands of the product have one type and V is bf16: 2^-8 of each probability at most,
 // while their sum is of the unrounded ones.  The outputs' error against fp64 grows by it from 0.0016, their own rounding, to
-// 0.0017-0.0025.  A second product with what the rounding leaves out would make the two products three.
+// 0.0018-0.0023.  A second product with what the rounding leaves out would make the two products three.
 //
 // Measured with heads of 128, 32 on 8: 8192 tokens from an empty cache 371 us and 16 us for the
 // join, 380 together (1.45 PFLOP/s, tensor pipe 67 % active); 2048 tokens over 65536 in 1440 us (tensor pipe 76 %

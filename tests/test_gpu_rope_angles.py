@@ -14,7 +14,7 @@ def test_sines_and_cosines(kda, top, layout):
     # that fp64 holds it whole.
     #
     # Bound: the reduced angle is off by 2^-30 of a turn (2 pi 2^-30 = 0.10 U).  What is left of it after whole
-    # eighths are taken out, at most 1/4 of a half turn, rounds to fp32 by 2^-27 of a half turn at most (pi / 8 U =
+    # quarters are taken out, at most 1/4 of a half turn, rounds to fp32 by 2^-27 of a half turn at most (pi / 8 U =
     # 0.40 U).  sincospif is documented to 1 ulp, which is U for results from 1/2 to 1.  In all 1.5 U; an angle that is
     # rounded with all of its half turn before is off by pi / 2 U by that alone.
     T, d = 8192, 16
